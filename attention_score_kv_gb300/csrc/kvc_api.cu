@@ -209,7 +209,7 @@ int check_ws(void* ws, size_t ws_bytes, size_t need) {
 
 }  // namespace kvc
 
-namespace {
+namespace kvc {
 
 // Rows of each head inside a batch element's block of the retained cache:
 // head h fills min(K_l[h], S) rows from out_off[h]; the block is
@@ -243,6 +243,10 @@ int make_layout(int S, int H_kv, const int32_t* K_l, const int64_t* out_off, int
   sp->T = off;
   return KVC_OK;
 }
+
+}  // namespace kvc
+
+namespace {
 
 // Selection parameters from the host budget array and the output layout.
 int make_sel(int S, int H_kv, const int32_t* K_l, const int64_t* out_off, int sink, int recent, SelParams* sp,
@@ -279,17 +283,19 @@ int launch_status(cudaError_t e, const char* what) {
 namespace {
 
 // kvc_compress_layer with an optional event the gather waits on (the values
-// are read by the gather only).
+// are read by the gather only).  cache given: the gather writes the 4-bit
+// cache in the slots out_off, instead of k_out and v_out.
 int compress_layer(int N, int layer, int B, int S, int C, int H_q, int H_kv, int D, int W, const int32_t* K_l,
                    int sink, int recent, int pool_k, int b_s, const kvc_bf16* q_win, const kvc_bf16* k,
                    const kvc_bf16* v, kvc_bf16* k_out, kvc_bf16* v_out, int32_t* pos_out,
-                   const int64_t* out_off, void* ws, size_t ws_bytes, cudaEvent_t v_ready, kvc_stream_t stream) {
+                   const int64_t* out_off, uint8_t* cache, void* ws, size_t ws_bytes, cudaEvent_t v_ready,
+                   kvc_stream_t stream) {
   int rc;
   if (N < 1 || layer < 0 || layer >= N) return set_error(KVC_ERR_INVALID_ARG, "layer %d outside [0, N=%d)", layer, N);
   if ((rc = check_shapes(B, H_q, H_kv, S, D, W)) || (rc = check_bs(b_s)) || (rc = check_pool(pool_k))) return rc;
   if (C < W || C > S) return set_error(KVC_ERR_INVALID_ARG, "chunk C=%d must satisfy W=%d <= C <= S=%d", C, W, S);
   if ((rc = check_ptr(q_win, 16, "q_win")) || (rc = check_ptr(k, 16, "k")) || (rc = check_ptr(v, 16, "v")) ||
-      (rc = check_ptr(k_out, 16, "k_out")) || (rc = check_ptr(v_out, 16, "v_out")) ||
+      (!cache && ((rc = check_ptr(k_out, 16, "k_out")) || (rc = check_ptr(v_out, 16, "v_out")))) ||
       (rc = check_ptr(pos_out, 4, "pos_out")))
     return rc;
   SelParams sp;
@@ -329,9 +335,12 @@ int compress_layer(int N, int layer, int B, int S, int C, int H_q, int H_kv, int
   if (ev) cudaEventRecord(ev[3], st);
   if (v_ready && (rc = launch_status(cudaStreamWaitEvent(st, v_ready, 0), "wait for v_ready")))
     return rc;
-  rc = launch_status(launch_gather(kk, vv, pos_out, B, sp, D, reinterpret_cast<__nv_bfloat16*>(k_out),
-                                   reinterpret_cast<__nv_bfloat16*>(v_out), pos_out, st),
-                     "gather launch");
+  if (cache)
+    rc = launch_status(launch_gather_q4(kk, vv, pos_out, B, sp, D, cache, pos_out, st), "4-bit gather launch");
+  else
+    rc = launch_status(launch_gather(kk, vv, pos_out, B, sp, D, reinterpret_cast<__nv_bfloat16*>(k_out),
+                                     reinterpret_cast<__nv_bfloat16*>(v_out), pos_out, st),
+                       "gather launch");
   if (ev) cudaEventRecord(ev[4], st);
   return rc;
 }
@@ -477,7 +486,7 @@ int kvc_compress_layer(int N, int layer, int B, int S, int C, int H_q, int H_kv,
                        const kvc_bf16* v, kvc_bf16* k_out, kvc_bf16* v_out, int32_t* pos_out,
                        const int64_t* out_off, void* ws, size_t ws_bytes, kvc_stream_t stream) {
   return compress_layer(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, k_out,
-                        v_out, pos_out, out_off, ws, ws_bytes, nullptr, stream);
+                        v_out, pos_out, out_off, nullptr, ws, ws_bytes, nullptr, stream);
 }
 
 int kvc_compress_layer_deferred_v(int N, int layer, int B, int S, int C, int H_q, int H_kv, int D, int W,
@@ -486,7 +495,19 @@ int kvc_compress_layer_deferred_v(int N, int layer, int B, int S, int C, int H_q
                                   kvc_bf16* v_out, int32_t* pos_out, const int64_t* out_off, void* ws,
                                   size_t ws_bytes, kvc_event_t v_ready, kvc_stream_t stream) {
   return compress_layer(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, k_out,
-                        v_out, pos_out, out_off, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready), stream);
+                        v_out, pos_out, out_off, nullptr, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready),
+                        stream);
+}
+
+int kvc_compress_layer_q4(int N, int layer, int B, int S, int C, int H_q, int H_kv, int D, int W, const int32_t* K_l,
+                          int sink, int recent, int pool_k, int b_s, const kvc_bf16* q_win, const kvc_bf16* k,
+                          const kvc_bf16* v, const int64_t* slot_off, uint8_t* cache, int32_t* pos, void* ws,
+                          size_t ws_bytes, kvc_event_t v_ready, kvc_stream_t stream) {
+  int rc;
+  if (H_kv < 1) return set_error(KVC_ERR_INVALID_ARG, "H_kv must be >= 1");
+  if ((rc = check_slots(H_kv, slot_off)) || (rc = check_ptr(cache, 16, "cache"))) return rc;
+  return compress_layer(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, nullptr,
+                        nullptr, pos, slot_off, cache, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready), stream);
 }
 
 int kvc_scan_ranges(int BH, int S, int P, int64_t* starts) {

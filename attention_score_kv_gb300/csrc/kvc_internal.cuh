@@ -101,6 +101,10 @@ int check_bs(int b_s);
 int check_pool(int pool_k);
 int check_ptr(const void* p, size_t align, const char* name);
 int check_ws(void* ws, size_t ws_bytes, size_t need);
+// Rows of each head inside a batch element's block (kvc.h: output layout).
+int make_layout(int S, int H_kv, const int32_t* K_l, const int64_t* out_off, int lo_rows, SelParams* sp);
+// Head slots of the 4-bit cache: multiples of 16 rows, in order.
+int check_slots(int H_kv, const int64_t* slot_off);
 int cuda_error(cudaError_t e, const char* what);
 int num_sms();
 int scan_ctas_target();                             // SM count or the tuning override
@@ -180,6 +184,36 @@ cudaError_t launch_select(int mode, const float* scores, const uint64_t* cand, c
 cudaError_t launch_gather(const __nv_bfloat16* k, const __nv_bfloat16* v, const int32_t* idx, int B,
                           const SelParams& sel, int D, __nv_bfloat16* k_out, __nv_bfloat16* v_out,
                           int32_t* pos_out, cudaStream_t st);
+
+// norm and rotation of queries and keys per head, into the scorer's and the
+// active layer's layouts; values copied along when v is given
+cudaError_t launch_qk_norm_rope(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v, int B, int T,
+                                int H_q, int H_kv, int D, int64_t q_ld, int64_t k_ld, int64_t v_ld, int R, bool inter,
+                                const __nv_bfloat16* qw, const __nv_bfloat16* kw, float eps, const float* inv_freq,
+                                const int32_t* pos, int S, int row0, __nv_bfloat16* q_out, __nv_bfloat16* k_act,
+                                __nv_bfloat16* v_act, cudaStream_t st);
+// the 4-bit retained cache (kvc_q4.cuh): gather into it (sel: kept rows and
+// slots), append T rows at rows[b][h], read rows back (out: rows and layout)
+struct Q4Slots;
+cudaError_t launch_gather_q4(const __nv_bfloat16* k, const __nv_bfloat16* v, const int32_t* idx, int B,
+                             const SelParams& sel, int D, uint8_t* cache, int32_t* pos, cudaStream_t st);
+cudaError_t launch_append_q4(const __nv_bfloat16* k, const __nv_bfloat16* v, const int32_t* pos, int B, int T, int D,
+                             const Q4Slots& slots, const int32_t* rows, uint8_t* cache, int32_t* pos_cache,
+                             cudaStream_t st);
+cudaError_t launch_read_q4(const uint8_t* cache, int B, int D, const Q4Slots& slots, const int32_t* first,
+                           const SelParams& out, __nv_bfloat16* k_out, __nv_bfloat16* v_out, cudaStream_t st);
+// attention over the 4-bit cache: scratch and launches of one call
+struct Q4AttendPlan {
+  int P;             // key ranges
+  int tiles;         // tiles of query rows per KV head
+  int64_t slots;     // partial results per tile: P + B * H_kv
+  size_t off_o;      // offset of the partial outputs in the workspace
+  size_t total;
+};
+Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D);
+cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const int32_t* pos, const int32_t* rows,
+                             int extra, const int32_t* q_pos, int B, int T, int H_q, int D, const Q4Slots& slots,
+                             __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st);
 
 int* status_word_ptr();     // device address of the status word
 void note_launches(int n);  // count kernels issued (measurement)

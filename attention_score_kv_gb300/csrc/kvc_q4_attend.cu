@@ -1,0 +1,473 @@
+// Attention over the 4-bit retained cache (format: kvc_q4.cuh), few query rows
+// per KV head: the decoding step.
+//
+//   o = sum_r p_r v_r / sum_r p_r,  p_r = exp(q.k_r / sqrt(D)) over the rows a query sees
+//
+// One read of the cache bounds it: 9D/8 + 4 bytes a row for 4*G*T*D flops.  So
+// the rows of all (sequence, KV head) pairs are laid end to end, in blocks of
+// 16, and cut into equal ranges, one per CTA, whatever the heads' lengths: a
+// CTA computes its range from the device-held row counts.  A range may end
+// inside a head; each CTA writes per head it touches the running maximum, sum
+// and unnormalised output, and a second kernel joins the parts in order.
+//
+// A warp takes one block at a time.  The codes come in fragment order, so they
+// go from global memory through two conversions straight into mma operands:
+//   S^T (16 rows x 8 queries) = K Q^T,   O^T (D x 8 queries) += V^T P^T,
+// with the queries as the narrow N side (8 columns), so that no row of the
+// matrix instruction is wasted when a KV head has 4 or 5 query heads.  P goes
+// from accumulator to operand layout with movmatrix.
+// Numerics: codes times scales are exact in fp16; q is scaled by a power of
+// two per row into fp16's range (values below 2^-24 of the row's largest round
+// off there); sums, maxima and outputs are fp32; p is rounded to fp16
+// (2^-12 relative; the reference point leaves it below 2^12, and 2^-26 of the
+// largest weight is its smallest step).
+#include <algorithm>
+#include <cmath>
+
+#include "kvc_device.cuh"
+#include "kvc_internal.cuh"
+#include "kvc_q4.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMinBlocks = kWarps;   // blocks of 16 rows a CTA takes at least
+constexpr float kNoRef = -1.7e38f;   // reference of a query that has seen no row
+constexpr float kShift = 4.0f;       // weights are kept as 2^(x - max + kShift)
+constexpr float kSlack = 8.0f;       // the reference moves when a score passes it by more
+
+struct AttendArgs {
+  const __nv_bfloat16* q;
+  const uint8_t* cache;
+  const int32_t *pos, *rows, *q_pos;
+  __nv_bfloat16* out;
+  float* lse;
+  float2* part_ml;                   // [row tiles][slots][8 NT] maximum, sum
+  float* part_o;                     // [row tiles][slots][8 NT][D]
+  int* status;
+  int B, T, H_q, G, extra, P, slots;
+  float scale;                       // log2(e) / sqrt(D)
+  Q4Slots s;
+};
+
+// Blocks that the counted rows of (b, h) fill.
+__device__ __forceinline__ int blocks_of(const AttendArgs& a, int bh, int* n_rows) {
+  const int h = bh % a.s.H_kv;
+  const int64_t cap = a.s.off[h + 1] - a.s.off[h];
+  int64_t n = (int64_t)a.rows[bh] + a.extra;
+  if (n < 0 || n > cap) {
+    record_status(a.status, kStatusBadInput);
+    n = n < 0 ? 0 : cap;
+  }
+  *n_rows = (int)n;
+  return (int)((n + q4::kRows - 1) / q4::kRows);
+}
+
+// Total blocks, and the blocks before item `bh_of` (bh_of < 0: only the total)
+// or, with `at` >= 0, the item whose blocks hold flat block `at`.
+struct Place { int64_t total, before; int bh; };
+__device__ Place find_place(const AttendArgs& a, int64_t at, int want_bh, int* scratch, int64_t* sh) {
+  const int BH = a.B * a.s.H_kv;
+  int64_t run = 0;
+  if (threadIdx.x == 0) sh[0] = 0, sh[1] = -1;
+  __syncthreads();
+  for (int base = 0; base < BH; base += blockDim.x) {
+    const int bh = base + threadIdx.x;
+    int n, tot;
+    const int v = bh < BH ? blocks_of(a, bh, &n) : 0;
+    const int inc = block_inclusive_scan(v, scratch, &tot);
+    const int64_t before = run + inc - v;
+    if (bh < BH && (want_bh >= 0 ? bh == want_bh : (at >= before && at < before + v))) sh[0] = before, sh[1] = bh;
+    run += tot;
+  }
+  __syncthreads();
+  Place p{run, sh[0], (int)sh[1]};
+  __syncthreads();
+  return p;
+}
+
+// Blocks of a CTA's range when N blocks are shared out.
+__device__ __forceinline__ int64_t range_blocks(int64_t N, int P) {
+  const int64_t L = (N + P - 1) / P;
+  return L < kMinBlocks ? kMinBlocks : L;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int N>
+struct Codes { uint32_t w[N]; };
+template <int kB>
+__device__ __forceinline__ Codes<kB / 4> load_codes(const uint8_t* p) {
+  Codes<kB / 4> c;
+  if constexpr (kB == 16) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    c.w[0] = v.x, c.w[1] = v.y, c.w[2] = v.z, c.w[3] = v.w;
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    c.w[0] = v.x, c.w[1] = v.y;
+  }
+  return c;
+}
+
+// What a warp reads of one block.
+template <int D>
+struct BlockData {
+  Codes<D / 32> k[2], v[2];
+  uint32_t ks, vs;
+  int p[2];
+};
+template <int D>
+__device__ __forceinline__ void load_block(BlockData<D>& x, const uint8_t* rec, const int32_t* pos, int lane) {
+  constexpr int kB = D / 8;
+  const int r = lane >> 2, j = lane & 3;
+  x.k[0] = load_codes<kB>(rec + q4::k_codes(D) + lane * kB);
+  x.k[1] = load_codes<kB>(rec + q4::k_codes(D) + 4 * D + lane * kB);
+  x.v[0] = load_codes<kB>(rec + q4::v_codes(D) + lane * kB);
+  x.v[1] = load_codes<kB>(rec + q4::v_codes(D) + 4 * D + lane * kB);
+  if constexpr (D == 128) {
+    x.ks = __ldg(reinterpret_cast<const uint32_t*>(rec + q4::k_scales(D)) + lane);
+    x.vs = __ldg(reinterpret_cast<const uint32_t*>(rec + q4::v_scales(D)) + lane);
+  } else {
+    const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(rec + q4::k_scales(D)) + lane);
+    x.ks = (two & 0xffu) * 0x101u | (two >> 8) * 0x1010000u;
+    x.vs = __ldg(reinterpret_cast<const uint32_t*>(rec + q4::v_scales(D)) + (r >> 1) * 4 + j);
+  }
+  x.p[0] = __ldg(pos + r);
+  x.p[1] = __ldg(pos + r + 8);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int KS = D / 16;         // k-steps of the scores, m-tiles of the output
+  constexpr int kB = D / 8;
+  __shared__ __align__(16) float s_o[kWarps][8][D];
+  __shared__ float2 s_ml[kWarps][8 * NT];
+  __shared__ int s_scan[32];
+  __shared__ int64_t s_place[2];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
+  const int H = a.s.H_kv, R = a.G * a.T, row_base = blockIdx.y * 8 * NT;
+
+  // the CTA's range [f0, f1) of the blocks laid end to end
+  Place pl = find_place(a, -1, -1, s_scan, s_place);
+  const int64_t L = range_blocks(pl.total, a.P);
+  const int64_t f0 = blockIdx.x * L, f1 = min(f0 + L, pl.total);
+  if (f0 >= f1) return;
+  const int64_t total = pl.total;
+  (void)total;
+  pl = find_place(a, f0, -1, s_scan, s_place);
+  int bh = pl.bh;
+  int64_t before = pl.before;
+
+  for (int64_t f = f0; f < f1; ++bh) {
+    int n_rows;
+    const int nb = blocks_of(a, bh, &n_rows);
+    if (nb == 0) continue;
+    const int s0 = (int)(f - before), cnt = (int)min(f1 - f, (int64_t)(nb - s0));
+    f += cnt;
+    before += nb;
+    const int b = bh / H, h = bh - b * H;
+
+    // queries: column n = lane / 4 of each n-tile, quarter j of its dims
+    uint32_t qf[NT][KS][2];
+    float c2[NT][2];                 // factor from accumulator to log2 units, columns 2j and 2j + 1
+    int qp[NT][2];                   // their positions
+    int q_lo = INT32_MAX, q_hi = -1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row_base + nt * 8 + r;
+      const bool live = row < R;
+      uint32_t w[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) w[i] = 0;
+      if (live) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + ((int64_t)bh * R + row) * D + j * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 v = __ldg(p + i);
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+      }
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+      mx = max(mx & 0xffffu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // scale by the power of two that brings the largest value into [1, 2)
+      const uint32_t e = mx >> 7;
+      const uint32_t ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
+      const float down = __uint_as_float((254u - ee) << 23);
+      const float c = __uint_as_float(ee << 23) * a.scale;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          qf[nt][s][y] = pack_half2(__uint_as_float(q4::bf16_of(w, 2 * s + y) << 16) * down,
+                                    __uint_as_float(q4::bf16_of(w, kB + 2 * s + y) << 16) * down);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        c2[nt][y] = __shfl_sync(0xffffffffu, c, (2 * j + y) * 4);
+        const int rr = row_base + nt * 8 + 2 * j + y;
+        qp[nt][y] = rr < R ? a.q_pos[(int64_t)b * a.T + rr % a.T] : -1;
+        if (rr < R) q_lo = min(q_lo, qp[nt][y]), q_hi = max(q_hi, qp[nt][y]);
+      }
+    }
+    q_lo = __reduce_min_sync(0xffffffffu, q_lo);
+    q_hi = __reduce_max_sync(0xffffffffu, q_hi);
+
+    float o[NT][KS][4], ref[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int m = 0; m < KS; ++m)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[nt][m][y] = 0.f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) ref[nt][y] = kNoRef, sum[nt][y] = 0.f;
+    }
+
+    const int64_t row_of_head = (int64_t)b * a.s.off[H] + a.s.off[h];
+    const uint8_t* rec0 = a.cache + row_of_head / q4::kRows * q4::block_bytes(D);
+    const int32_t* pos0 = a.pos + row_of_head;
+    for (int blk = s0 + warp; blk < s0 + cnt; blk += kWarps) {
+      BlockData<D> x;
+      load_block<D>(x, rec0 + (int64_t)blk * q4::block_bytes(D), pos0 + (int64_t)blk * q4::kRows, lane);
+      // ---- scores
+      float acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) acc[nt][y] = 0.f;
+      const uint32_t ks[2] = {q4::scales_to_half2((uint16_t)x.ks), q4::scales_to_half2((uint16_t)(x.ks >> 16))};
+#pragma unroll
+      for (int w = 0; w < kB / 4; ++w) {
+        uint32_t ka[4], kb[4];
+        q4::codes_to_half2(x.k[0].w[w], ka);
+        q4::codes_to_half2(x.k[1].w[w], kb);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) ka[y] = q4::mul_half2(ka[y], ks[0]), kb[y] = q4::mul_half2(kb[y], ks[1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(acc[nt], ka[0], kb[0], ka[1], kb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
+          mma_f16(acc[nt], ka[2], kb[2], ka[3], kb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+        }
+      }
+      // ---- mask: acc[nt][y], acc[nt][2 + y] are rows r, r + 8 against column 2j + y
+      uint32_t vs = x.vs;
+      const bool in0 = blk * q4::kRows + r < n_rows && x.p[0] >= 0, in1 = blk * q4::kRows + r + 8 < n_rows && x.p[1] >= 0;
+      const bool clear = in0 && x.p[0] <= q_lo && in1 && x.p[1] <= q_lo;
+      if (!__all_sync(0xffffffffu, clear)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (!in0 || x.p[0] > qp[nt][y]) acc[nt][y] = -INFINITY;
+            if (!in1 || x.p[1] > qp[nt][y]) acc[nt][2 + y] = -INFINITY;
+          }
+        // a row that no query sees may hold anything: its values count as zeros
+        const uint32_t see0 = __ballot_sync(0xffffffffu, in0 && x.p[0] <= q_hi);
+        const uint32_t see1 = __ballot_sync(0xffffffffu, in1 && x.p[1] <= q_hi);
+        uint32_t keep = 0;           // bytes of vs: rows 2j, 2j + 1, 2j + 8, 2j + 9; lane 4r' speaks for row r'
+        if (see0 >> (8 * j) & 1) keep |= 0x000000ffu;
+        if (see0 >> (8 * j + 4) & 1) keep |= 0x0000ff00u;
+        if (see1 >> (8 * j) & 1) keep |= 0x00ff0000u;
+        if (see1 >> (8 * j + 4) & 1) keep |= 0xff000000u;
+        vs &= keep;
+      }
+      // ---- weights
+      uint32_t pf[NT][2];
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          above |= fmaxf(acc[nt][y], acc[nt][2 + y]) * c2[nt][y] > ref[nt][y] + (kSlack + kShift);
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float m = fmaxf(acc[nt][y], acc[nt][2 + y]) * c2[nt][y];
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float next = fmaxf(ref[nt][y], m - kShift);
+            const float f = ex2(ref[nt][y] - next);
+            ref[nt][y] = next;
+            sum[nt][y] *= f;
+#pragma unroll
+            for (int m2 = 0; m2 < KS; ++m2) o[nt][m2][y] *= f, o[nt][m2][2 + y] *= f;
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          p[y] = ex2(fmaf(acc[nt][y], c2[nt][y & 1], -ref[nt][y & 1]));
+          sum[nt][y & 1] += p[y];
+        }
+        pf[nt][0] = transpose8(pack_half2(p[0], p[1]));
+        pf[nt][1] = transpose8(pack_half2(p[2], p[3]));
+      }
+      // ---- output
+      const uint32_t vs2[2] = {q4::scales_to_half2((uint16_t)vs), q4::scales_to_half2((uint16_t)(vs >> 16))};
+#pragma unroll
+      for (int w = 0; w < kB / 4; ++w) {
+        uint32_t va[4], vb[4];
+        q4::codes_to_half2(x.v[0].w[w], va);
+        q4::codes_to_half2(x.v[1].w[w], vb);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) va[y] = q4::mul_half2(va[y], vs2[0]), vb[y] = q4::mul_half2(vb[y], vs2[1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(o[nt][2 * w], va[0], va[1], vb[0], vb[1], pf[nt][0], pf[nt][1]);
+          mma_f16(o[nt][2 * w + 1], va[2], va[3], vb[2], vb[3], pf[nt][0], pf[nt][1]);
+        }
+      }
+    }
+
+    // ---- join the warps: rows of the range that warp w saw, in warp order
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float v = sum[nt][y];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if (r == 0) s_ml[warp][nt * 8 + 2 * j + y] = make_float2(ref[nt][y], v);
+      }
+    __syncthreads();
+    const int64_t slot = (int64_t)blockIdx.y * a.slots + blockIdx.x + bh;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int col = 2 * j + y;
+        float top = s_ml[0][nt * 8 + col].x;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][nt * 8 + col].x);
+        const float f = ex2(ref[nt][y] - top);
+#pragma unroll
+        for (int m = 0; m < KS; ++m)
+          *reinterpret_cast<float2*>(&s_o[warp][col][r * kB + 2 * m]) = make_float2(o[nt][m][y] * f, o[nt][m][2 + y] * f);
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < 8 * D; i += kThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += (&s_o[w][0][0])[i];
+        a.part_o[(slot * 8 * NT + nt * 8) * D + i] = v;
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x < 8 * NT) {
+      float top = kNoRef, l = 0.f;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][threadIdx.x].x);
+      for (int w = 0; w < kWarps; ++w) l += s_ml[w][threadIdx.x].y * ex2(s_ml[w][threadIdx.x].x - top);
+      a.part_ml[slot * 8 * NT + threadIdx.x] = make_float2(top, l);
+    }
+    __syncthreads();
+  }
+}
+
+// One CTA per (sequence, KV head) and row tile: joins the parts in range order.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) kvc_attend_q4_join_kernel(const __grid_constant__ AttendArgs a) {
+  __shared__ int s_scan[32];
+  __shared__ int64_t s_place[2];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int bh = blockIdx.x, R = a.G * a.T, row_base = blockIdx.y * 8 * NT;
+  const Place pl = find_place(a, -1, bh, s_scan, s_place);
+  const int64_t L = range_blocks(pl.total, a.P);
+  int n_rows;
+  const int nb = blocks_of(a, bh, &n_rows);
+  const int64_t c0 = pl.before / L, c1 = nb > 0 ? (pl.before + nb - 1) / L : c0 - 1;
+  const int64_t slot0 = (int64_t)blockIdx.y * a.slots + bh;
+  for (int i = threadIdx.x; i < 8 * NT * D; i += kThreads) {
+    const int row = i / D, d = i - row * D;
+    if (row_base + row >= R) break;
+    float top = kNoRef;
+    for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, a.part_ml[(slot0 + c) * 8 * NT + row].x);
+    float l = 0.f, v = 0.f;
+    for (int64_t c = c0; c <= c1; ++c) {
+      const float2 ml = a.part_ml[(slot0 + c) * 8 * NT + row];
+      const float f = ex2(ml.x - top);
+      l = fmaf(ml.y, f, l);
+      v = fmaf(a.part_o[((slot0 + c) * 8 * NT + row) * D + d], f, v);
+    }
+    const int64_t at = (int64_t)bh * R + row_base + row;
+    a.out[at * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
+    if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+  }
+}
+
+int tile_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
+
+}  // namespace
+
+Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D) {
+  Q4AttendPlan p{};
+  const int R = H_q / H_kv * T;
+  const int tr = tile_rows(R);
+  p.tiles = (R + tr - 1) / tr;
+  p.P = std::max(num_sms(), 1) * 2;
+  p.slots = (int64_t)p.P + (int64_t)B * H_kv;
+  const size_t rows = (size_t)p.tiles * (size_t)p.slots * (size_t)tr;
+  p.off_o = (rows * sizeof(float2) + 255) / 256 * 256;
+  p.total = p.off_o + rows * D * sizeof(float);
+  return p;
+}
+
+cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const int32_t* pos, const int32_t* rows,
+                             int extra, const int32_t* q_pos, int B, int T, int H_q, int D, const Q4Slots& slots,
+                             __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st) {
+  const int H = slots.H_kv, R = H_q / H * T;
+  const Q4AttendPlan p = plan_attend_q4(B, T, H_q, H, D);
+  AttendArgs a{};
+  a.q = q, a.cache = cache, a.pos = pos, a.rows = rows, a.q_pos = q_pos, a.out = out, a.lse = lse;
+  a.part_ml = static_cast<float2*>(ws);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_o);
+  a.status = status_word_ptr();
+  a.B = B, a.T = T, a.H_q = H_q, a.G = H_q / H, a.extra = extra, a.P = p.P, a.slots = (int)p.slots;
+  a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
+  a.s = slots;
+  void (*scan)(AttendArgs) = nullptr;
+  void (*join)(AttendArgs) = nullptr;
+  const int tr = tile_rows(R);
+  if (D == 128) {
+    scan = tr == 8 ? kvc_attend_q4_kernel<128, 1> : tr == 16 ? kvc_attend_q4_kernel<128, 2> : kvc_attend_q4_kernel<128, 4>;
+    join = tr == 8 ? kvc_attend_q4_join_kernel<128, 1> : tr == 16 ? kvc_attend_q4_join_kernel<128, 2> : kvc_attend_q4_join_kernel<128, 4>;
+  } else {
+    scan = tr == 8 ? kvc_attend_q4_kernel<64, 1> : tr == 16 ? kvc_attend_q4_kernel<64, 2> : kvc_attend_q4_kernel<64, 4>;
+    join = tr == 8 ? kvc_attend_q4_join_kernel<64, 1> : tr == 16 ? kvc_attend_q4_join_kernel<64, 2> : kvc_attend_q4_join_kernel<64, 4>;
+  }
+  cudaError_t e = launch_pdl(scan, dim3(p.P, p.tiles), dim3(kThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(join, dim3(B * H, p.tiles), dim3(kThreads), 0, st, a);
+  note_launches(2);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kvc

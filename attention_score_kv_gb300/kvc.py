@@ -82,6 +82,16 @@ _SIGS = {
     "kvc_budget_pyramid": (_I, [_I, _I, _I, _I32P]),
     "kvc_retained_layout": (_I, [_I, _I, _I32P, _I64P]),
     "kvc_budget_inverse_stability": (_I, [_I, _F64P, _I64, _I, _I, _I32P]),
+    "kvc_qk_norm_rope": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I64, _I64, _I64, _I, _I, _P, _P, ctypes.c_float, _P,
+                              _P, _I, _I, _P, _P, _P, _P]),
+    "kvc_q4_layout": (_I, [_I, _I, _I32P, _I, _I64P]),
+    "kvc_gather_q4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I32P, _I64P, _P, _P, _P]),
+    "kvc_append_q4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I64P, _P, _P, _P, _P]),
+    "kvc_read_q4": (_I, [_P, _I, _I, _I, _I64P, _P, _I32P, _I64P, _P, _P, _P]),
+    "kvc_compress_layer_q4": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I32P, _I, _I, _I, _I, _P, _P, _P, _I64P,
+                                   _P, _P, _P, _SZ, _P, _P]),
+    "kvc_attention_q4_workspace_size": (_SZ, [_I] * 5),
+    "kvc_attention_q4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I64P, _P, _P, _P, _SZ, _P]),
     "kvc_check_status": (_I, [_P]),
     "kvc_set_option": (_I, [_I, _I64]),
 }
@@ -129,6 +139,57 @@ def _i64_or_null(arr):
         return None
     vals = [int(x) for x in (arr.tolist() if hasattr(arr, "tolist") else arr)]
     return (ctypes.c_int64 * len(vals))(*vals)
+
+
+def _bad(msg):
+    raise KvcError(KVC_ERR_INVALID_ARG, msg)
+
+
+def _arg(t, dtype, n, name):
+    """Device pointer of a tensor of at least n elements; a raw pointer or None passes as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype != dtype:
+        _bad(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_contiguous():
+        _bad(f"{name} is not contiguous")
+    if t.numel() < n:
+        _bad(f"{name} holds {t.numel()} elements, needs {n}")
+    if t.get_device() != torch.cuda.current_device():
+        _bad(f"{name} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+def _tokens_arg(t, B, T, n, ld, name):
+    """Device pointer of a strided [B, T, n] projection (or [B, T, H, D], [B*T, n])
+    whose tokens lie ld elements apart."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype != torch.bfloat16:
+        _bad(f"{name} is {t.dtype}, not torch.bfloat16")
+    if t.get_device() != torch.cuda.current_device():
+        _bad(f"{name} is on {t.device}, not on the current CUDA device")
+    tok = t.reshape(B * T, n) if t.is_contiguous() else t.flatten(2) if t.dim() == 4 else t
+    shape = tuple(tok.shape)
+    if tok.data_ptr() != t.data_ptr() or shape not in ((B, T, n), (B * T, n)):
+        _bad(f"{name} must be [{B}, {T}, {n}] with its heads side by side, got {tuple(t.shape)}")
+    st = tok.stride()
+    if (st[-1] != 1 or (shape[-2] > 1 and st[-2] != ld)
+            or (len(shape) == 3 and B > 1 and st[0] != T * ld)):
+        _bad(f"{name} has strides {st}, which is not one token every {ld} elements")
+    return t.data_ptr()
+
+
+def _host(arr, ctype, n, name):
+    """A host array argument: a ctypes array of the right type as it is, others copied; None for None."""
+    if arr is None:
+        return None
+    if not (isinstance(arr, ctypes.Array) and arr._type_ is ctype):
+        vals = [int(x) for x in (arr.tolist() if hasattr(arr, "tolist") else arr)]
+        arr = (ctype * len(vals))(*vals)
+    if len(arr) < n:
+        _bad(f"{name} holds {len(arr)} values, needs {n}")
+    return arr
 
 
 def kvc_last_error() -> str:
@@ -275,6 +336,96 @@ def kvc_budget_inverse_stability(s_stable, total, lo, hi) -> list:
     return list(out)
 
 
+def kvc_qk_norm_rope(q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleaved, q_weight, k_weight, eps,
+                     inv_freq, pos, S, row0, q_out, k_act, v_act, stream=None):
+    """Norm of queries and keys per head and position rotation, into q_out and
+    the active layer's buffers (see include/kvc.h)."""
+    bf, ok = torch.bfloat16, B > 0 and T > 0 and H_q > 0 and H_kv > 0 and D > 0
+    if ok:
+        q, k, v = (_tokens_arg(x, B, T, h * D, ld, nm) for x, h, ld, nm in
+                   ((q, H_q, q_ld, "q"), (k, H_kv, k_ld, "k"), (v, H_kv, v_ld, "v")))
+    _check(_lib.kvc_qk_norm_rope(
+        q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleaved, _arg(q_weight, bf, D, "q_weight"),
+        _arg(k_weight, bf, D, "k_weight"), eps, _arg(inv_freq, torch.float32, R // 2, "inv_freq"),
+        _arg(pos, torch.int32, B * T, "pos"), S, row0, _arg(q_out, bf, B * H_q * T * D, "q_out"),
+        _arg(k_act, bf, B * H_kv * S * D, "k_act"), _arg(v_act, bf, B * H_kv * S * D, "v_act"), _stream(stream)))
+
+
+def kvc_q4_layout(H_kv, S, K_l, extra) -> ctypes.Array:
+    """Slots [H_kv + 1] of a 4-bit cache, as the host array its calls take
+    (a ctypes array: indexable, passed on without a copy)."""
+    out = (_I64 * (H_kv + 1))()
+    _check(_lib.kvc_q4_layout(H_kv, S, _host(K_l, ctypes.c_int32, H_kv, "K_l"), extra, out))
+    return out
+
+
+def _q4_rows(B, H_kv, slot_off):
+    """(slot_off as a host array, rows of all batch elements)."""
+    so = _host(slot_off, _I64, H_kv + 1, "slot_off")
+    return so, B * so[H_kv] if so is not None else 0
+
+
+def kvc_gather_q4(k, v, idx, B, H_kv, S, D, K_l, slot_off, cache, pos, stream=None):
+    bf, i32 = torch.bfloat16, torch.int32
+    so, n = _q4_rows(B, H_kv, slot_off)
+    _check(_lib.kvc_gather_q4(_arg(k, bf, B * H_kv * S * D, "k"), _arg(v, bf, B * H_kv * S * D, "v"),
+                              _arg(idx, i32, n, "idx"), B, H_kv, S, D, _host(K_l, ctypes.c_int32, H_kv, "K_l"), so,
+                              _arg(cache, torch.uint8, n * D * 9 // 8, "cache"), _arg(pos, i32, n, "pos"),
+                              _stream(stream)))
+
+
+def kvc_append_q4(k, v, pos_new, B, H_kv, T, D, slot_off, rows, cache, pos, stream=None):
+    bf, i32 = torch.bfloat16, torch.int32
+    so, n = _q4_rows(B, H_kv, slot_off)
+    _check(_lib.kvc_append_q4(_arg(k, bf, B * H_kv * T * D, "k"), _arg(v, bf, B * H_kv * T * D, "v"),
+                              _arg(pos_new, i32, B * T, "pos_new"), B, H_kv, T, D, so,
+                              _arg(rows, i32, B * H_kv, "rows"), _arg(cache, torch.uint8, n * D * 9 // 8, "cache"),
+                              _arg(pos, i32, n, "pos"), _stream(stream)))
+
+
+def kvc_read_q4(cache, B, H_kv, D, slot_off, first, n_rows, k_out, v_out, stream=None, out_off=None):
+    so, n = _q4_rows(B, H_kv, slot_off)
+    nr = _host(n_rows, ctypes.c_int32, H_kv, "n_rows")
+    oo = _host(out_off, _I64, H_kv + 1, "out_off")
+    t = B * (oo[H_kv] if oo is not None else sum(nr[:H_kv]) if nr is not None else 0) * D
+    _check(_lib.kvc_read_q4(_arg(cache, torch.uint8, n * D * 9 // 8, "cache"), B, H_kv, D, so,
+                            _arg(first, torch.int32, B * H_kv, "first"), nr, oo,
+                            _arg(k_out, torch.bfloat16, t, "k_out"), _arg(v_out, torch.bfloat16, t, "v_out"),
+                            _stream(stream)))
+
+
+def kvc_compress_layer_q4(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, slot_off,
+                          cache, pos, ws, ws_bytes=None, v_ready=None, stream=None):
+    """kvc_compress_layer whose retained rows go into the 4-bit cache."""
+    bf = torch.bfloat16
+    so, n = _q4_rows(B, H_kv, slot_off)
+    _check(_lib.kvc_compress_layer_q4(
+        N, layer, B, S, C, H_q, H_kv, D, W, _host(K_l, ctypes.c_int32, H_kv, "K_l"), sink, recent, pool_k, b_s,
+        _arg(q_win, bf, B * H_q * W * D, "q_win"), _arg(k, bf, B * H_kv * S * D, "k"),
+        _arg(v, bf, B * H_kv * S * D, "v"), so, _arg(cache, torch.uint8, n * D * 9 // 8, "cache"),
+        _arg(pos, torch.int32, n, "pos"), _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _event(v_ready),
+        _stream(stream)))
+
+
+def kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D) -> int:
+    n = _lib.kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D)
+    if n == 0:
+        raise KvcError(KVC_ERR_INVALID_ARG, kvc_last_error())
+    return n
+
+
+def kvc_attention_q4(q, cache, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot_off, out, lse, ws, ws_bytes=None,
+                     stream=None):
+    bf, i32 = torch.bfloat16, torch.int32
+    so, n = _q4_rows(B, H_kv, slot_off)
+    nq = B * H_q * T
+    _check(_lib.kvc_attention_q4(_arg(q, bf, nq * D, "q"), _arg(cache, torch.uint8, n * D * 9 // 8, "cache"),
+                                 _arg(pos, i32, n, "pos"), _arg(rows, i32, B * H_kv, "rows"), extra,
+                                 _arg(q_pos, i32, B * T, "q_pos"), B, T, H_q, H_kv, D, so,
+                                 _arg(out, bf, nq * D, "out"), _arg(lse, torch.float32, nq, "lse"),
+                                 _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
 def kvc_check_status(stream=None) -> None:
     _check(_lib.kvc_check_status(_stream(stream)))
 
@@ -298,6 +449,18 @@ def retained_outputs(B, H_kv, S, D, K_l, device="cuda"):
     v_out = torch.empty((B * T, D), dtype=torch.bfloat16, device=device)
     pos = torch.empty((B * T,), dtype=torch.int32, device=device)
     return k_out, v_out, pos, off
+
+
+def attention_q4_workspace(B, T, H_q, H_kv, D, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of kvc_attention_q4_workspace_size(...) bytes."""
+    return torch.empty(kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D), dtype=torch.uint8, device=device)
+
+
+def q4_cache(B, D, slot_off, device="cuda"):
+    """Allocate (cache, pos) of a 4-bit cache; no row is visible yet (positions -1)."""
+    n = B * slot_off[len(slot_off) - 1]
+    return (torch.empty(n * D * 9 // 8, dtype=torch.uint8, device=device),
+            torch.full((n,), -1, dtype=torch.int32, device=device))
 
 
 # ---------------------------------------------------------------- profiling

@@ -398,6 +398,154 @@ int kvc_budget_inverse_stability(int H_kv, const double* s_stable,
                                  int32_t* K_l_out);
 
 /*
+ * Norm of queries and keys per head with the position rotation in the same
+ * pass: from the projections' output to what kvc_score_* and kvc_compress_layer
+ * read (queries) and to the active layer's buffers (keys, values), as
+ * kvc_append_chunk writes them.  Per head, in fp32 with one rounding at the end:
+ *   y = x / sqrt(mean(x^2) + eps) * weight       (left out where weight is NULL)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin), angle pos * inv_freq[i]
+ * for the R/2 pairs of the first R dims: (a, b) = (i, i + R/2), or (2i, 2i + 1)
+ * with `interleaved`.  Dims from R on are not rotated.
+ *   q, k, v   bf16; token t of batch element b starts at element (b*T + t)*q_ld
+ *             (k_ld, v_ld), its heads of D values side by side: the parts of one
+ *             fused projection are passed with its width as all three strides.
+ *             Strides are multiples of 8 elements, pointers 16-byte aligned.
+ *             v and v_act may both be NULL (no values are copied).
+ *   q_weight, k_weight  [D] bf16, each may be NULL
+ *   inv_freq  [R/2] fp32, device; finite
+ *   pos       [B, T] int32, device, any value; the angle's error is below 1e-6
+ *             rad plus pos * inv_freq * 2^-52 for every position
+ *   q_out     [B, H_q, T, D] out
+ *   k_act, v_act [B, H_kv, S, D]: positions row0 .. row0 + T - 1 of every (b, head)
+ *             are overwritten, the rest is left (a decoding step: S = T, row0 = 0)
+ * R is a multiple of 16 in [0, D] (0: norm only; inv_freq and pos unused);
+ * D is 64 or 128.  Inputs and outputs may not overlap.
+ */
+int kvc_qk_norm_rope(const kvc_bf16* q, const kvc_bf16* k, const kvc_bf16* v,
+                     int B, int T, int H_q, int H_kv, int D, int64_t q_ld,
+                     int64_t k_ld, int64_t v_ld, int R, int interleaved,
+                     const kvc_bf16* q_weight, const kvc_bf16* k_weight,
+                     float eps, const float* inv_freq, const int32_t* pos,
+                     int S, int row0, kvc_bf16* q_out, kvc_bf16* k_act,
+                     kvc_bf16* v_act, kvc_stream_t stream);
+
+/*
+ * The 4-bit retained cache.  It holds a layer's retained rows in 4.5 bits a
+ * value: e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign) with one e4m3 scale
+ * per 16 values of a row's keys or values, so 9*D/8 bytes a row instead of 4*D.
+ * Per group of 16:
+ *   scale = max|x| / 6 rounded to e4m3, code = x / scale rounded to e2m1,
+ * both to nearest even and saturating: a group whose max|x| is above 2688
+ * saturates, one at or below 6 * 2^-10 becomes zeros.  NaN becomes zero and
+ * infinities saturate; both are recorded (kvc_check_status: KVC_ERR_DEVICE).
+ *
+ *   cache     uint8, 16-byte aligned, B * slot_off[H_kv] * 9 * D / 8 bytes:
+ *             blocks of 16 rows, 18*D bytes each, of every batch element.  The
+ *             bytes' order is the library's own; kvc_read_q4 returns values.
+ *   slot_off  HOST int64 [H_kv + 1]: head h owns rows slot_off[h] ..
+ *             slot_off[h+1]-1 of its batch element's slot_off[H_kv] rows.
+ *             Multiples of 16, in order (kvc_q4_layout makes one).
+ *   pos       int32 [B * slot_off[H_kv]]: absolute position of each row; a row
+ *             with a negative position is seen by no query
+ *   rows      int32 [B, H_kv], device: rows that each head holds.  The caller
+ *             keeps it (the gather fills min(K_l, S) rows, an append adds T), so
+ *             that one captured step can be replayed while the cache grows.
+ * Offsets are 64-bit; a slot holds up to 2^30 rows.  D is 64 or 128, H_kv up
+ * to 128.  Calls that write one (b, head)'s rows must not overlap on the GPU.
+ */
+
+/*
+ * Host helper: slots with room for min(K_l[h], S) + extra rows, rounded up to 16.
+ *   slot_off HOST [H_kv + 1] out
+ */
+int kvc_q4_layout(int H_kv, int S, const int32_t* K_l, int extra,
+                  int64_t* slot_off);
+
+/*
+ * kvc_gather into the 4-bit cache: the rows of k and v at the selected positions
+ * are written to rows 0 .. min(K_l[h], S) - 1 of each head's slot.
+ *   k, v   [B, H_kv, S, D] bf16
+ *   idx    int32 positions in [0, S) where the rows go (kvc_select_topk with
+ *          out_off = slot_off writes them); may be the same buffer as pos
+ *   K_l    HOST [H_kv]
+ * The last block's rows behind a head's kept rows are written as zeros; other
+ * rows of the slot, and pos behind the kept rows, are left.  A position
+ * outside [0, S) is recorded (KVC_ERR_DEVICE) and its row is unspecified.
+ */
+int kvc_gather_q4(const kvc_bf16* k, const kvc_bf16* v, const int32_t* idx,
+                  int B, int H_kv, int S, int D, const int32_t* K_l,
+                  const int64_t* slot_off, uint8_t* cache, int32_t* pos,
+                  kvc_stream_t stream);
+
+/*
+ * New tokens join the 4-bit cache: token t of batch element b becomes row
+ * rows[b, h] + t of every head h.  `rows` is not changed.
+ *   k, v     [B, H_kv, T, D] bf16 (kvc_qk_norm_rope with S = T writes them)
+ *   pos_new  [B, T] int32; a negative position marks an absent token (a padded
+ *            batch): its row is written as zeros with position -1
+ * A head without room for T rows, or with a negative count, is left as it was
+ * and recorded (KVC_ERR_DEVICE).  No other row changes.
+ */
+int kvc_append_q4(const kvc_bf16* k, const kvc_bf16* v, const int32_t* pos_new,
+                  int B, int H_kv, int T, int D, const int64_t* slot_off,
+                  const int32_t* rows, uint8_t* cache, int32_t* pos,
+                  kvc_stream_t stream);
+
+/*
+ * Rows of the 4-bit cache as bf16 (the exact values the codes stand for), e.g.
+ * to score and compress them again.
+ *   first    int32 [B, H_kv], device, or NULL for 0: rows first .. first +
+ *            n_rows[h] - 1 of head h are read
+ *   n_rows   HOST [H_kv], each at most its slot's rows
+ *   out_off  HOST [H_kv + 1] or NULL: the output layout of kvc_gather, for
+ *            n_rows rows per head
+ *   k_out, v_out [B * T, D] bf16 out (T the block length of the layout)
+ * Rows outside the slot come out as zeros and are recorded (KVC_ERR_DEVICE).
+ */
+int kvc_read_q4(const uint8_t* cache, int B, int H_kv, int D,
+                const int64_t* slot_off, const int32_t* first,
+                const int32_t* n_rows, const int64_t* out_off, kvc_bf16* k_out,
+                kvc_bf16* v_out, kvc_stream_t stream);
+
+/*
+ * kvc_compress_layer (with kvc_compress_layer_deferred_v's v_ready, which may
+ * be NULL) whose last step is kvc_gather_q4: the retained rows go straight into
+ * the 4-bit cache's slots.  The slots must hold min(K_l[h], S) rows each.
+ */
+int kvc_compress_layer_q4(int N, int layer, int B, int S, int C, int H_q,
+                          int H_kv, int D, int W, const int32_t* K_l, int sink,
+                          int recent, int pool_k, int b_s,
+                          const kvc_bf16* q_win, const kvc_bf16* k,
+                          const kvc_bf16* v, const int64_t* slot_off,
+                          uint8_t* cache, int32_t* pos, void* ws,
+                          size_t ws_bytes, kvc_event_t v_ready,
+                          kvc_stream_t stream);
+
+/*
+ * Attention of T new tokens per sequence over the 4-bit cache (decoding, draft
+ * tokens, a follow-up prompt).  Query head g reads KV head g / G.  Query t of
+ * sequence b sees the rows r < rows[b, h] + extra of head h with
+ * 0 <= pos[r] <= q_pos[b, t]:
+ *   out = sum_r p_r v_r / sum_r p_r, p_r = exp(q.k_r / sqrt(D)); lse = log sum_r p_r
+ *   q      [B, H_q, T, D] bf16        out  [B, H_q, T, D] bf16 out
+ *   q_pos  [B, T] int32, device       lse  [B, H_q, T] fp32 out, or NULL
+ *   extra  rows counted beyond `rows`: T where the new tokens were appended at
+ *          `rows` before this call, so that they see each other causally
+ * A query that sees no row gets zeros and lse -inf.  Rows that no query of the
+ * call sees may hold any bytes.  A count outside the slot is clamped to it and
+ * recorded (KVC_ERR_DEVICE).  No atomics: the same call gives the same bits.
+ *   ws     at least kvc_attention_q4_workspace_size(...) bytes, 256-byte
+ *          aligned, any content; the size does not depend on the rows
+ */
+size_t kvc_attention_q4_workspace_size(int B, int T, int H_q, int H_kv, int D);
+
+int kvc_attention_q4(const kvc_bf16* q, const uint8_t* cache,
+                     const int32_t* pos, const int32_t* rows, int extra,
+                     const int32_t* q_pos, int B, int T, int H_q, int H_kv,
+                     int D, const int64_t* slot_off, kvc_bf16* out, float* lse,
+                     void* ws, size_t ws_bytes, kvc_stream_t stream);
+
+/*
  * Waits for `stream`, then reads and clears the device status word.
  * Returns KVC_OK, or KVC_ERR_DEVICE / KVC_ERR_TIMEOUT with a message.
  */

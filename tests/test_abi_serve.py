@@ -1,0 +1,145 @@
+"""Refusals of the serving entry points: every bad argument is an error before
+anything is launched (no GPU; the pointers are never touched)."""
+
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def K():
+    from attention_score_kv_gb300 import build
+    build.build()
+    import attention_score_kv_gb300.kvc as kvc
+    return kvc
+
+
+ROPE = dict(q=0x1000, k=0x2000, v=0x3000, B=2, T=3, H_q=4, H_kv=2, D=64, q_ld=512, k_ld=512, v_ld=512, R=64,
+            interleaved=0, q_weight=0x4000, k_weight=0x5000, eps=1e-6, inv_freq=0x6000, pos=0x7000, S=8, row0=5,
+            q_out=0x8000, k_act=0x9000, v_act=0xa000, stream=0)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(B=0), -1), (dict(T=0), -1), (dict(H_q=0), -1), (dict(H_kv=0), -1),
+    (dict(D=96), -2), (dict(R=24), -1), (dict(R=80), -1), (dict(R=-16), -1),
+    (dict(interleaved=2), -1),
+    (dict(row0=-1), -1), (dict(row0=6), -1), (dict(S=2, row0=0), -1),
+    (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
+    (dict(q_ld=248), -1), (dict(q_ld=260), -1), (dict(k_ld=120), -1), (dict(v_ld=132), -1),
+    (dict(q=None), -1), (dict(k=0x2008), -1), (dict(v=None), -1), (dict(v_act=None), -1),
+    (dict(q_weight=0x4002), -1), (dict(inv_freq=None), -1), (dict(pos=None), -1), (dict(k_act=None), -1),
+    (dict(B=1 << 20, T=1 << 12, S=1 << 13), -2), (dict(H_q=70000, q_ld=1 << 23), -2),
+])
+def test_norm_rope_refuses(K, over, code):
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_qk_norm_rope(**{**ROPE, **over})
+    assert ei.value.code == code
+
+
+SLOT = [0, 16, 64]
+GATHER = dict(k=0x1000, v=0x2000, idx=0x3000, B=1, H_kv=2, S=100, D=64, K_l=[16, 48], slot_off=SLOT, cache=0x4000,
+              pos=0x5000, stream=0)
+APPEND = dict(k=0x1000, v=0x2000, pos_new=0x3000, B=1, H_kv=2, T=3, D=64, slot_off=SLOT, rows=0x3100, cache=0x4000,
+              pos=0x5000, stream=0)
+READ = dict(cache=0x4000, B=1, H_kv=2, D=64, slot_off=SLOT, first=None, n_rows=[16, 48], k_out=0x1000, v_out=0x2000,
+            stream=0)
+ATTEND = dict(q=0x1000, cache=0x4000, pos=0x5000, rows=0x3100, extra=1, q_pos=0x6000, B=1, T=1, H_q=4, H_kv=2, D=64,
+              slot_off=SLOT, out=0x7000, lse=0x8000, ws=0x10000, ws_bytes=1 << 40, stream=0)
+SLOTS = [
+    (dict(slot_off=[0, 16, 60]), -1),          # not a multiple of 16
+    (dict(slot_off=[-16, 16, 64]), -1),
+    (dict(slot_off=[0, 64, 48]), -1),          # out of order
+    (dict(slot_off=[0, 16, 16 + (1 << 31)]), -2),
+    (dict(slot_off=None), -1),
+    (dict(B=0), -1), (dict(H_kv=0), -1), (dict(D=80), -2), (dict(H_kv=129, slot_off=[0] * 130), -2),
+    (dict(cache=None), -1), (dict(cache=0x4008), -1),
+]
+
+
+@pytest.mark.parametrize("over,code", SLOTS + [
+    (dict(K_l=[17, 48]), -1),                  # slot 0 has 16 rows
+    (dict(K_l=[16, 49]), -1), (dict(K_l=[-1, 4]), -1), (dict(K_l=None), -1),
+    (dict(S=0), -1), (dict(S=(1 << 30) + 1), -2), (dict(idx=None), -1), (dict(v=0x2002), -1), (dict(pos=None), -1),
+])
+def test_gather_refuses(K, over, code):
+    if over.get("H_kv") == 129:
+        over = {**over, "K_l": [0] * 129}
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_gather_q4(**{**GATHER, **over})
+    assert ei.value.code == code
+
+
+@pytest.mark.parametrize("over,code", SLOTS + [
+    (dict(T=0), -1), (dict(T=(1 << 30) + 1), -2), (dict(B=1 << 20, T=1 << 20), -2), (dict(rows=None), -1),
+    (dict(pos_new=None), -1), (dict(k=None), -1), (dict(pos=0x5002), -1),
+])
+def test_append_refuses(K, over, code):
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_append_q4(**{**APPEND, **over})
+    assert ei.value.code == code
+
+
+@pytest.mark.parametrize("over,code", SLOTS + [
+    (dict(n_rows=[17, 48]), -1), (dict(n_rows=[-1, 48]), -1), (dict(n_rows=None), -1),
+    (dict(out_off=[0, 8, 64]), -1), (dict(k_out=None), -1), (dict(v_out=0x2004), -1), (dict(first=0x3002), -1),
+])
+def test_read_refuses(K, over, code):
+    if over.get("H_kv") == 129:
+        over = {**over, "n_rows": [0] * 129}
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_read_q4(**{**READ, **over})
+    assert ei.value.code == code
+
+
+@pytest.mark.parametrize("over,code", SLOTS + [
+    (dict(T=0), -1), (dict(H_q=0), -1), (dict(H_q=5), -1), (dict(extra=-1), -1), (dict(T=1 << 20), -2),
+    (dict(B=1 << 24, H_kv=1, H_q=256, slot_off=[0, 16]), -2),
+    (dict(q=None), -1), (dict(q_pos=None), -1), (dict(out=0x7008), -1), (dict(lse=0x8002), -1), (dict(rows=None), -1),
+])
+def test_attention_refuses(K, over, code):
+    if over.get("H_kv") == 129:
+        over = {**over, "H_q": 129}
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_attention_q4(**{**ATTEND, **over})
+    assert ei.value.code == code
+
+
+@pytest.mark.parametrize("args", [(0, 1, 4, 2, 64), (1, 0, 4, 2, 64), (1, 1, 5, 2, 64), (1, 1, 4, 2, 72)])
+def test_attention_workspace_refuses(K, args):
+    with pytest.raises(K.KvcError):
+        K.kvc_attention_q4_workspace_size(*args)
+
+
+def test_compress_q4_refuses(K):
+    a = dict(N=1, layer=0, B=1, S=512, C=512, H_q=4, H_kv=2, D=64, W=16, K_l=[128, 128], sink=4, recent=16, pool_k=1,
+             b_s=128, q_win=0x1000, k=0x2000, v=0x3000, slot_off=[0, 128, 256], cache=0x4000, pos=0x6000, ws=0x10000,
+             ws_bytes=1 << 30, stream=0)
+    for over, code in [(dict(slot_off=[0, 112, 256]), -1), (dict(slot_off=[0, 130, 260]), -1), (dict(cache=None), -1),
+                       (dict(H_kv=0), -1), (dict(layer=1), -1), (dict(K_l=[19, 128]), -1), (dict(v=None), -1)]:
+        with pytest.raises(K.KvcError) as ei:
+            K.kvc_compress_layer_q4(**{**a, **over})
+        assert ei.value.code == code, over
+
+
+def test_slots(K):
+    so = K.kvc_q4_layout(4, 100, [0, 1, 90, 500], 7)
+    assert list(so) == [0, 16, 32, 144, 256]       # 7, 8, 97 and 107 rows
+    assert isinstance(so, ctypes.Array)
+    for bad in [(0, 100, [], 0), (1, 0, [4], 0), (1, 10, [-1], 0), (1, 10, [4], -1)]:
+        with pytest.raises(K.KvcError) as ei:
+            K.kvc_q4_layout(*bad)
+        assert ei.value.code == -1
+
+
+def test_host_tensors_and_wrong_types_are_refused(K):
+    import torch
+    q = torch.zeros((2, 3, 4 * 64), dtype=torch.bfloat16)
+    with pytest.raises(K.KvcError) as ei:          # wrong type, before any look at the device
+        K.kvc_qk_norm_rope(**{**ROPE, "q": q.float()})
+    assert ei.value.code == -1 and "float32" in str(ei.value)
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_read_q4(**{**READ, "slot_off": [0, 16]})   # too short a host array
+    assert ei.value.code == -1
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_append_q4(**{**APPEND, "pos_new": torch.zeros(2, dtype=torch.int32)})
+    assert ei.value.code == -1 and "pos_new" in str(ei.value)
