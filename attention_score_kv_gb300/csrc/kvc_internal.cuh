@@ -207,7 +207,8 @@ struct Q4AttendPlan {
   int P;             // key ranges
   int tiles;         // tiles of query rows per KV head
   int64_t slots;     // partial results per tile: P + B * H_kv
-  size_t off_o;      // offset of the partial outputs in the workspace
+  size_t off_o;      // offsets in the workspace: partial outputs,
+  size_t off_place;  // the heads' places
   size_t total;
 };
 Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D);

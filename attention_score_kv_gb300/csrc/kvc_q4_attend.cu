@@ -10,8 +10,10 @@
 // inside a head; each CTA writes per head it touches the running maximum, sum
 // and unnormalised output, and a second kernel joins the parts in order.
 //
-// A warp takes one block at a time.  The codes come in fragment order, so they
-// go from global memory through two conversions straight into mma operands:
+// A warp takes one block at a time, and every lane copies its share of the
+// blocks ahead into shared memory asynchronously and reads it back itself, so
+// the copies need no barrier.  The codes come in fragment order, so they go
+// through two conversions straight into mma operands:
 //   S^T (16 rows x 8 queries) = K Q^T,   O^T (D x 8 queries) += V^T P^T,
 // with the queries as the narrow N side (8 columns), so that no row of the
 // matrix instruction is wasted when a KV head has 4 or 5 query heads.  P goes
@@ -46,6 +48,7 @@ struct AttendArgs {
   float* lse;
   float2* part_ml;                   // [row tiles][slots][8 NT] maximum, sum
   float* part_o;                     // [row tiles][slots][8 NT][D]
+  int64_t* place;                    // [B * H_kv] blocks before each head, then all blocks
   int* status;
   int B, T, H_q, G, extra, P, slots;
   float scale;                       // log2(e) / sqrt(D)
@@ -65,33 +68,52 @@ __device__ __forceinline__ int blocks_of(const AttendArgs& a, int bh, int* n_row
   return (int)((n + q4::kRows - 1) / q4::kRows);
 }
 
-// Total blocks, and the blocks before item `bh_of` (bh_of < 0: only the total)
-// or, with `at` >= 0, the item whose blocks hold flat block `at`.
-struct Place { int64_t total, before; int bh; };
-__device__ Place find_place(const AttendArgs& a, int64_t at, int want_bh, int* scratch, int64_t* sh) {
-  const int BH = a.B * a.s.H_kv;
-  int64_t run = 0;
-  if (threadIdx.x == 0) sh[0] = 0, sh[1] = -1;
-  __syncthreads();
-  for (int base = 0; base < BH; base += blockDim.x) {
-    const int bh = base + threadIdx.x;
-    int n, tot;
-    const int v = bh < BH ? blocks_of(a, bh, &n) : 0;
-    const int inc = block_inclusive_scan(v, scratch, &tot);
-    const int64_t before = run + inc - v;
-    if (bh < BH && (want_bh >= 0 ? bh == want_bh : (at >= before && at < before + v))) sh[0] = before, sh[1] = bh;
-    run += tot;
-  }
-  __syncthreads();
-  Place p{run, sh[0], (int)sh[1]};
-  __syncthreads();
-  return p;
-}
-
 // Blocks of a CTA's range when N blocks are shared out.
 __device__ __forceinline__ int64_t range_blocks(int64_t N, int P) {
   const int64_t L = (N + P - 1) / P;
   return L < kMinBlocks ? kMinBlocks : L;
+}
+
+// Where a CTA's range begins: the head that holds its first block, and the
+// blocks before that head.  One scan over the row counts when a CTA's threads
+// can hold them all (kPer each), else one for the total and one for the place.
+// write: this CTA leaves every head's place to the joining kernel.
+struct Place { int64_t total, before; int bh; };
+constexpr int kPer = 4;
+__device__ Place find_place(const AttendArgs& a, int cta, bool write) {
+  __shared__ int scratch[32];
+  __shared__ int64_t sh[2];
+  const int BH = a.B * a.s.H_kv, chunk = kThreads * kPer;
+  Place p{0, 0, -1};
+  for (int round = BH <= chunk ? 1 : 0; round < 2; ++round) {
+    int64_t run = 0;
+    for (int base = 0; base < BH; base += chunk) {
+      int v[kPer], mine = 0, tot, n;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int bh = base + (int)threadIdx.x * kPer + i;
+        v[i] = bh < BH ? blocks_of(a, bh, &n) : 0;
+        mine += v[i];
+      }
+      int64_t before = run + block_inclusive_scan(mine, scratch, &tot) - mine;
+      run += tot;
+      if (round == 0) continue;
+      if (BH <= chunk) p.total = run;
+      const int64_t f0 = cta * range_blocks(p.total, a.P);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int bh = base + (int)threadIdx.x * kPer + i;
+        if (bh < BH && f0 >= before && f0 < before + v[i]) sh[0] = before, sh[1] = bh;
+        if (bh < BH && write) a.place[bh] = before;
+        before += v[i];
+      }
+    }
+    p.total = run;
+  }
+  if (write && threadIdx.x == 0) a.place[BH] = p.total;
+  __syncthreads();
+  if (cta * range_blocks(p.total, a.P) < p.total) p.before = sh[0], p.bh = (int)sh[1];
+  return p;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -111,80 +133,127 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// A stage of a warp's ring: a block's bytes as they are in the cache, and its
+// positions.  Lane 4r + j copies the pieces it reads itself: rows r and r + 8
+// of the keys, slice r of the values' pairs j and j + 4, their scales, and the
+// positions of rows r and r + 8 (four lanes each, the same value).
+constexpr int kStages = 4;
+__host__ __device__ constexpr int stage_bytes(int D) { return q4::block_bytes(D) + 32 * 8; }
+
+template <int D>
+__device__ __forceinline__ void copy_block(uint32_t dst, const uint8_t* rec, const int32_t* pos, int lane) {
+  constexpr int kB = D / 8;
+  const int r = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {      // the keys' two halves, then the values' two halves
+    if constexpr (kB == 16) copy16(dst + i * 4 * D + lane * kB, rec + i * 4 * D + lane * kB);
+    else copy_small<8>(dst + i * 4 * D + lane * kB, rec + i * 4 * D + lane * kB);
+  }
+  if constexpr (D == 128) {
+    copy_small<4>(dst + q4::k_scales(D) + lane * 4, rec + q4::k_scales(D) + lane * 4);
+    copy_small<4>(dst + q4::v_scales(D) + lane * 4, rec + q4::v_scales(D) + lane * 4);
+  } else {
+    // two bytes of key scales a lane: the word of an even lane and the next; both copy it
+    const int kw = (lane >> 1) * 4, vw = ((r >> 1) * 4 + j) * 4;
+    copy_small<4>(dst + q4::k_scales(D) + kw, rec + q4::k_scales(D) + kw);
+    copy_small<4>(dst + q4::v_scales(D) + vw, rec + q4::v_scales(D) + vw);
+  }
+  copy_small<4>(dst + q4::block_bytes(D) + lane * 8, pos + r);
+  copy_small<4>(dst + q4::block_bytes(D) + lane * 8 + 4, pos + r + 8);
+}
+
 template <int N>
 struct Codes { uint32_t w[N]; };
 template <int kB>
 __device__ __forceinline__ Codes<kB / 4> load_codes(const uint8_t* p) {
   Codes<kB / 4> c;
   if constexpr (kB == 16) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
     c.w[0] = v.x, c.w[1] = v.y, c.w[2] = v.z, c.w[3] = v.w;
   } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     c.w[0] = v.x, c.w[1] = v.y;
   }
   return c;
 }
 
-// What a warp reads of one block.
-template <int D>
-struct BlockData {
-  Codes<D / 32> k[2], v[2];
-  uint32_t ks, vs;
-  int p[2];
+// The heads of a range, one after the other.
+struct Segment {
+  int64_t f, before;                 // flat block it starts at; blocks before its head
+  int bh, s0, cnt, n_rows;           // head; first block in the head, blocks; the head's rows
 };
-template <int D>
-__device__ __forceinline__ void load_block(BlockData<D>& x, const uint8_t* rec, const int32_t* pos, int lane) {
-  constexpr int kB = D / 8;
-  const int r = lane >> 2, j = lane & 3;
-  x.k[0] = load_codes<kB>(rec + q4::k_codes(D) + lane * kB);
-  x.k[1] = load_codes<kB>(rec + q4::k_codes(D) + 4 * D + lane * kB);
-  x.v[0] = load_codes<kB>(rec + q4::v_codes(D) + lane * kB);
-  x.v[1] = load_codes<kB>(rec + q4::v_codes(D) + 4 * D + lane * kB);
-  if constexpr (D == 128) {
-    x.ks = __ldg(reinterpret_cast<const uint32_t*>(rec + q4::k_scales(D)) + lane);
-    x.vs = __ldg(reinterpret_cast<const uint32_t*>(rec + q4::v_scales(D)) + lane);
-  } else {
-    const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(rec + q4::k_scales(D)) + lane);
-    x.ks = (two & 0xffu) * 0x101u | (two >> 8) * 0x1010000u;
-    x.vs = __ldg(reinterpret_cast<const uint32_t*>(rec + q4::v_scales(D)) + (r >> 1) * 4 + j);
-  }
-  x.p[0] = __ldg(pos + r);
-  x.p[1] = __ldg(pos + r + 8);
+__device__ __forceinline__ bool segment_at(const AttendArgs& a, int64_t f, int64_t f1, int bh, int64_t before,
+                                           Segment* g) {
+  if (f >= f1) return false;
+  int nb, n_rows;
+  while ((nb = blocks_of(a, bh, &n_rows)) == 0) ++bh;      // f < f1 <= total: a head with rows follows
+  g->f = f;
+  g->before = before;
+  g->bh = bh;
+  g->n_rows = n_rows;
+  g->s0 = (int)(f - before);
+  g->cnt = (int)min(f1 - f, (int64_t)(nb - g->s0));
+  return true;
+}
+__device__ __forceinline__ bool next_segment(const AttendArgs& a, int64_t f1, const Segment& g, Segment* next) {
+  // a segment that does not end the range ends its head
+  return segment_at(a, g.f + g.cnt, f1, g.bh + 1, g.before + g.s0 + g.cnt, next);
 }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int KS = D / 16;         // k-steps of the scores, m-tiles of the output
   constexpr int kB = D / 8;
-  __shared__ __align__(16) float s_o[kWarps][8][D];
+  extern __shared__ __align__(128) uint8_t dyn[];
+  float (*s_o)[8][D] = reinterpret_cast<float (*)[8][D]>(dyn);     // [kWarps][8][D]
   __shared__ float2 s_ml[kWarps][8 * NT];
-  __shared__ int s_scan[32];
-  __shared__ int64_t s_place[2];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
   const int H = a.s.H_kv, R = a.G * a.T, row_base = blockIdx.y * 8 * NT;
+  uint8_t* ring = dyn + kWarps * 8 * D * sizeof(float) + warp * kStages * stage_bytes(D);
+  const uint32_t ring_u = smem_u32(ring);
 
   // the CTA's range [f0, f1) of the blocks laid end to end
-  Place pl = find_place(a, -1, -1, s_scan, s_place);
+  const Place pl = find_place(a, blockIdx.x, blockIdx.x == 0 && blockIdx.y == 0);
   const int64_t L = range_blocks(pl.total, a.P);
   const int64_t f0 = blockIdx.x * L, f1 = min(f0 + L, pl.total);
-  if (f0 >= f1) return;
-  const int64_t total = pl.total;
-  (void)total;
-  pl = find_place(a, f0, -1, s_scan, s_place);
-  int bh = pl.bh;
-  int64_t before = pl.before;
+  Segment g;
+  bool more = segment_at(a, f0, f1, pl.bh, pl.before, &g);
 
-  for (int64_t f = f0; f < f1; ++bh) {
-    int n_rows;
-    const int nb = blocks_of(a, bh, &n_rows);
-    if (nb == 0) continue;
-    const int s0 = (int)(f - before), cnt = (int)min(f1 - f, (int64_t)(nb - s0));
-    f += cnt;
-    before += nb;
-    const int b = bh / H, h = bh - b * H;
+  // block `i` (0, 1, ...) of the warp's share of a segment into its ring; a group is
+  // committed whether or not there is one, so that the waits can count
+  int stage_in = 0, stage_out = 0;
+  const auto fetch = [&](const Segment& x, int i) {
+    const int in = warp + i * kWarps;
+    if (in < x.cnt) {
+      const int b = x.bh / H, h = x.bh - b * H;
+      const int64_t row = (int64_t)b * a.s.off[H] + a.s.off[h] + (int64_t)(x.s0 + in) * q4::kRows;
+      copy_block<D>(ring_u + stage_in * stage_bytes(D), a.cache + row / q4::kRows * q4::block_bytes(D), a.pos + row,
+                    lane);
+    }
+    copies_commit();
+    stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+  };
+  if (more)
+    for (int i = 0; i < kStages - 1; ++i) fetch(g, i);
+
+  while (more) {
+    const int bh = g.bh, n_rows = g.n_rows;
+    const int b = bh / H;
 
     // queries: column n = lane / 4 of each n-tile, quarter j of its dims
     uint32_t qf[NT][KS][2];
@@ -245,24 +314,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
       for (int y = 0; y < 2; ++y) ref[nt][y] = kNoRef, sum[nt][y] = 0.f;
     }
 
-    const int64_t row_of_head = (int64_t)b * a.s.off[H] + a.s.off[h];
-    const uint8_t* rec0 = a.cache + row_of_head / q4::kRows * q4::block_bytes(D);
-    const int32_t* pos0 = a.pos + row_of_head;
-    for (int blk = s0 + warp; blk < s0 + cnt; blk += kWarps) {
-      BlockData<D> x;
-      load_block<D>(x, rec0 + (int64_t)blk * q4::block_bytes(D), pos0 + (int64_t)blk * q4::kRows, lane);
+    const int mine = (g.cnt - warp + kWarps - 1) / kWarps;       // blocks of this warp (may be <= 0)
+    for (int i = 0; i < mine; ++i) {
+      const int blk = g.s0 + warp + i * kWarps;
+      fetch(g, i + kStages - 1);
+      copies_wait<kStages - 1>();
+      const uint8_t* st = ring + stage_out * stage_bytes(D);
+      stage_out = stage_out + 1 == kStages ? 0 : stage_out + 1;
+      uint32_t ksc, vs;
+      if constexpr (D == 128) {
+        ksc = *reinterpret_cast<const uint32_t*>(st + q4::k_scales(D) + lane * 4);
+        vs = *reinterpret_cast<const uint32_t*>(st + q4::v_scales(D) + lane * 4);
+      } else {
+        const uint32_t two = *reinterpret_cast<const uint16_t*>(st + q4::k_scales(D) + lane * 2);
+        ksc = (two & 0xffu) * 0x101u | (two >> 8) * 0x1010000u;
+        vs = *reinterpret_cast<const uint32_t*>(st + q4::v_scales(D) + ((r >> 1) * 4 + j) * 4);
+      }
+      const int2 xp = *reinterpret_cast<const int2*>(st + q4::block_bytes(D) + lane * 8);
       // ---- scores
       float acc[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int y = 0; y < 4; ++y) acc[nt][y] = 0.f;
-      const uint32_t ks[2] = {q4::scales_to_half2((uint16_t)x.ks), q4::scales_to_half2((uint16_t)(x.ks >> 16))};
+      const uint32_t ks[2] = {q4::scales_to_half2((uint16_t)ksc), q4::scales_to_half2((uint16_t)(ksc >> 16))};
+      const Codes<kB / 4> kc0 = load_codes<kB>(st + q4::k_codes(D) + lane * kB);
+      const Codes<kB / 4> kc1 = load_codes<kB>(st + q4::k_codes(D) + 4 * D + lane * kB);
 #pragma unroll
       for (int w = 0; w < kB / 4; ++w) {
         uint32_t ka[4], kb[4];
-        q4::codes_to_half2(x.k[0].w[w], ka);
-        q4::codes_to_half2(x.k[1].w[w], kb);
+        q4::codes_to_half2(kc0.w[w], ka);
+        q4::codes_to_half2(kc1.w[w], kb);
 #pragma unroll
         for (int y = 0; y < 4; ++y) ka[y] = q4::mul_half2(ka[y], ks[0]), kb[y] = q4::mul_half2(kb[y], ks[1]);
 #pragma unroll
@@ -272,20 +354,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
         }
       }
       // ---- mask: acc[nt][y], acc[nt][2 + y] are rows r, r + 8 against column 2j + y
-      uint32_t vs = x.vs;
-      const bool in0 = blk * q4::kRows + r < n_rows && x.p[0] >= 0, in1 = blk * q4::kRows + r + 8 < n_rows && x.p[1] >= 0;
-      const bool clear = in0 && x.p[0] <= q_lo && in1 && x.p[1] <= q_lo;
+      const bool in0 = blk * q4::kRows + r < n_rows && xp.x >= 0, in1 = blk * q4::kRows + r + 8 < n_rows && xp.y >= 0;
+      const bool clear = in0 && xp.x <= q_lo && in1 && xp.y <= q_lo;
       if (!__all_sync(0xffffffffu, clear)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            if (!in0 || x.p[0] > qp[nt][y]) acc[nt][y] = -INFINITY;
-            if (!in1 || x.p[1] > qp[nt][y]) acc[nt][2 + y] = -INFINITY;
+            if (!in0 || xp.x > qp[nt][y]) acc[nt][y] = -INFINITY;
+            if (!in1 || xp.y > qp[nt][y]) acc[nt][2 + y] = -INFINITY;
           }
         // a row that no query sees may hold anything: its values count as zeros
-        const uint32_t see0 = __ballot_sync(0xffffffffu, in0 && x.p[0] <= q_hi);
-        const uint32_t see1 = __ballot_sync(0xffffffffu, in1 && x.p[1] <= q_hi);
+        const uint32_t see0 = __ballot_sync(0xffffffffu, in0 && xp.x <= q_hi);
+        const uint32_t see1 = __ballot_sync(0xffffffffu, in1 && xp.y <= q_hi);
         uint32_t keep = 0;           // bytes of vs: rows 2j, 2j + 1, 2j + 8, 2j + 9; lane 4r' speaks for row r'
         if (see0 >> (8 * j) & 1) keep |= 0x000000ffu;
         if (see0 >> (8 * j + 4) & 1) keep |= 0x0000ff00u;
@@ -330,12 +411,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
         pf[nt][1] = transpose8(pack_half2(p[2], p[3]));
       }
       // ---- output
+      const Codes<kB / 4> vc0 = load_codes<kB>(st + q4::v_codes(D) + lane * kB);
+      const Codes<kB / 4> vc1 = load_codes<kB>(st + q4::v_codes(D) + 4 * D + lane * kB);
       const uint32_t vs2[2] = {q4::scales_to_half2((uint16_t)vs), q4::scales_to_half2((uint16_t)(vs >> 16))};
 #pragma unroll
       for (int w = 0; w < kB / 4; ++w) {
         uint32_t va[4], vb[4];
-        q4::codes_to_half2(x.v[0].w[w], va);
-        q4::codes_to_half2(x.v[1].w[w], vb);
+        q4::codes_to_half2(vc0.w[w], va);
+        q4::codes_to_half2(vc1.w[w], vb);
 #pragma unroll
         for (int y = 0; y < 4; ++y) va[y] = q4::mul_half2(va[y], vs2[0]), vb[y] = q4::mul_half2(vb[y], vs2[1]);
 #pragma unroll
@@ -345,6 +428,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
         }
       }
     }
+
+    // the next head's first blocks come in while this one is joined.  Groups that the
+    // loop's tail committed empty are behind the ones it used; the ring starts afresh.
+    Segment next;
+    more = next_segment(a, f1, g, &next);
+    stage_in = stage_out;
+    if (more)
+      for (int i = 0; i < kStages - 1; ++i) fetch(next, i);
 
     // ---- join the warps: rows of the range that warp w saw, in warp order
 #pragma unroll
@@ -388,39 +479,68 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
       a.part_ml[slot * 8 * NT + threadIdx.x] = make_float2(top, l);
     }
     __syncthreads();
+    g = next;
   }
 }
 
-// One CTA per (sequence, KV head) and row tile: joins the parts in range order.
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) kvc_attend_q4_join_kernel(const __grid_constant__ AttendArgs a) {
-  __shared__ int s_scan[32];
-  __shared__ int64_t s_place[2];
+// One CTA per (sequence, KV head) and query row: joins the parts.  Warp w sums
+// parts w, w + 4, ... in range order, each lane a vector of the row, and the
+// four sums are added in warp order.
+constexpr int kJoinWarps = 4;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(const __grid_constant__ AttendArgs a,
+                                                                             int tile) {
+  constexpr int V = D / 32;          // values of a lane
+  __shared__ float s_v[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
   grid_dep_wait();
   grid_dep_launch();
-  const int bh = blockIdx.x, R = a.G * a.T, row_base = blockIdx.y * 8 * NT;
-  const Place pl = find_place(a, -1, bh, s_scan, s_place);
-  const int64_t L = range_blocks(pl.total, a.P);
-  int n_rows;
-  const int nb = blocks_of(a, bh, &n_rows);
-  const int64_t c0 = pl.before / L, c1 = nb > 0 ? (pl.before + nb - 1) / L : c0 - 1;
-  const int64_t slot0 = (int64_t)blockIdx.y * a.slots + bh;
-  for (int i = threadIdx.x; i < 8 * NT * D; i += kThreads) {
-    const int row = i / D, d = i - row * D;
-    if (row_base + row >= R) break;
-    float top = kNoRef;
-    for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, a.part_ml[(slot0 + c) * 8 * NT + row].x);
-    float l = 0.f, v = 0.f;
-    for (int64_t c = c0; c <= c1; ++c) {
-      const float2 ml = a.part_ml[(slot0 + c) * 8 * NT + row];
-      const float f = ex2(ml.x - top);
-      l = fmaf(ml.y, f, l);
-      v = fmaf(a.part_o[((slot0 + c) * 8 * NT + row) * D + d], f, v);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = a.B * a.s.H_kv;
+  const int R = a.G * a.T, bh = blockIdx.x / R, row = blockIdx.x - bh * R, ty = row / tile, in = row - ty * tile;
+  const int64_t total = a.place[BH], before = a.place[bh];
+  const int64_t after = bh + 1 < BH ? a.place[bh + 1] : total;
+  const int64_t L = range_blocks(total, a.P);
+  const int64_t c0 = before / L;
+  const int n = after > before ? (int)((after - 1) / L - c0 + 1) : 0;
+  const int64_t slot0 = (int64_t)ty * a.slots + bh + c0;
+  const float2* ml = a.part_ml + slot0 * tile + in;
+  const float* po = a.part_o + (slot0 * tile + in) * D + lane * V;
+  float top = kNoRef;
+  for (int c = lane; c < n; c += 32) top = fmaxf(top, ml[(int64_t)c * tile].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float l = 0.f, v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = 0.f;
+#pragma unroll 4
+  for (int c = warp; c < n; c += kJoinWarps) {
+    const float2 x = ml[(int64_t)c * tile];
+    const float f = ex2(x.x - top);
+    l = fmaf(x.y, f, l);
+    const float* p = po + (int64_t)c * tile * D;
+    if constexpr (V == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p);
+      v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]), v[2] = fmaf(y.z, f, v[2]), v[3] = fmaf(y.w, f, v[3]);
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(p);
+      v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]);
     }
-    const int64_t at = (int64_t)bh * R + row_base + row;
-    a.out[at * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
-    if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_v[warp][lane * V + i] = v[i];
+  if (lane == 0) s_ml[warp] = make_float2(0.f, l);
+  __syncthreads();
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum += s_ml[w].y;
+  const int64_t at = blockIdx.x;
+  for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+    float o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) o += s_v[w][d];
+    a.out[at * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 int tile_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
@@ -436,7 +556,8 @@ Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D) {
   p.slots = (int64_t)p.P + (int64_t)B * H_kv;
   const size_t rows = (size_t)p.tiles * (size_t)p.slots * (size_t)tr;
   p.off_o = (rows * sizeof(float2) + 255) / 256 * 256;
-  p.total = p.off_o + rows * D * sizeof(float);
+  p.off_place = p.off_o + rows * D * sizeof(float);
+  p.total = p.off_place + ((size_t)B * H_kv + 1) * sizeof(int64_t);
   return p;
 }
 
@@ -449,23 +570,23 @@ cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const
   a.q = q, a.cache = cache, a.pos = pos, a.rows = rows, a.q_pos = q_pos, a.out = out, a.lse = lse;
   a.part_ml = static_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_o);
+  a.place = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + p.off_place);
   a.status = status_word_ptr();
   a.B = B, a.T = T, a.H_q = H_q, a.G = H_q / H, a.extra = extra, a.P = p.P, a.slots = (int)p.slots;
   a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
   a.s = slots;
-  void (*scan)(AttendArgs) = nullptr;
-  void (*join)(AttendArgs) = nullptr;
   const int tr = tile_rows(R);
-  if (D == 128) {
+  const size_t smem = kWarps * (8 * D * sizeof(float) + kStages * stage_bytes(D));
+  void (*scan)(AttendArgs);
+  if (D == 128)
     scan = tr == 8 ? kvc_attend_q4_kernel<128, 1> : tr == 16 ? kvc_attend_q4_kernel<128, 2> : kvc_attend_q4_kernel<128, 4>;
-    join = tr == 8 ? kvc_attend_q4_join_kernel<128, 1> : tr == 16 ? kvc_attend_q4_join_kernel<128, 2> : kvc_attend_q4_join_kernel<128, 4>;
-  } else {
+  else
     scan = tr == 8 ? kvc_attend_q4_kernel<64, 1> : tr == 16 ? kvc_attend_q4_kernel<64, 2> : kvc_attend_q4_kernel<64, 4>;
-    join = tr == 8 ? kvc_attend_q4_join_kernel<64, 1> : tr == 16 ? kvc_attend_q4_join_kernel<64, 2> : kvc_attend_q4_join_kernel<64, 4>;
-  }
-  cudaError_t e = launch_pdl(scan, dim3(p.P, p.tiles), dim3(kThreads), 0, st, a);
+  cudaError_t e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = launch_pdl(scan, dim3(p.P, p.tiles), dim3(kThreads), smem, st, a);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(join, dim3(B * H, p.tiles), dim3(kThreads), 0, st, a);
+  e = launch_pdl(D == 128 ? kvc_attend_q4_join_kernel<128> : kvc_attend_q4_join_kernel<64>, dim3((unsigned)(B * H * R)),
+                 dim3(kJoinWarps * 32), 0, st, a, tr);
   note_launches(2);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

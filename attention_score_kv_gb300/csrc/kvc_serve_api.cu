@@ -49,7 +49,7 @@ int check_attend(int B, int T, int H_q, int H_kv, int D) {
   if (H_q % H_kv != 0) return set_error(KVC_ERR_INVALID_ARG, "H_q (%d) must be a multiple of H_kv (%d)", H_q, H_kv);
   if ((int64_t)(H_q / H_kv) * T > (1 << 20))
     return set_error(KVC_ERR_UNSUPPORTED, "%lld query rows per KV head: above 2^20", (long long)(H_q / H_kv) * T);
-  if ((int64_t)B * H_q * T > (1LL << 31)) return set_error(KVC_ERR_UNSUPPORTED, "batch too large");
+  if ((int64_t)B * H_q * T > INT32_MAX) return set_error(KVC_ERR_UNSUPPORTED, "batch too large");
   return KVC_OK;
 }
 

@@ -121,8 +121,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the raw handle: a Stream object costs microseconds per call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -146,37 +146,40 @@ def _bad(msg):
 
 
 def _arg(t, dtype, n, name):
-    """Device pointer of a tensor of at least n elements; a raw pointer or None passes as it is."""
-    if t is None or isinstance(t, int):
+    """Device pointer of a contiguous tensor of at least n elements on the current
+    device; a raw pointer or None passes as it is."""
+    if t is None or t.__class__ is int:
         return t
+    if t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == torch._C._cuda_getDevice():
+        return t.data_ptr()
     if t.dtype != dtype:
         _bad(f"{name} is {t.dtype}, not {dtype}")
     if not t.is_contiguous():
         _bad(f"{name} is not contiguous")
     if t.numel() < n:
         _bad(f"{name} holds {t.numel()} elements, needs {n}")
-    if t.get_device() != torch.cuda.current_device():
-        _bad(f"{name} is on {t.device}, not on the current CUDA device")
-    return t.data_ptr()
+    _bad(f"{name} is on {t.device}, not on the current CUDA device")
 
 
 def _tokens_arg(t, B, T, n, ld, name):
     """Device pointer of a strided [B, T, n] projection (or [B, T, H, D], [B*T, n])
     whose tokens lie ld elements apart."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         _bad(f"{name} is {t.dtype}, not torch.bfloat16")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         _bad(f"{name} is on {t.device}, not on the current CUDA device")
-    tok = t.reshape(B * T, n) if t.is_contiguous() else t.flatten(2) if t.dim() == 4 else t
-    shape = tuple(tok.shape)
-    if tok.data_ptr() != t.data_ptr() or shape not in ((B, T, n), (B * T, n)):
+    shape, st = t.shape, t.stride()
+    if len(shape) == 4 and shape[2] * shape[3] == n and (shape[2] == 1 or st[2] == shape[3]):
+        shape, st = (*shape[:2], n), (*st[:2], st[3])     # heads side by side
+    if len(shape) == 2:
+        shape, st = (1, *shape), (0, *st)
+    b, tt, m = shape if len(shape) == 3 else (0, 0, 0)
+    if m != n or b * tt != B * T or (b != B and b != 1):
         _bad(f"{name} must be [{B}, {T}, {n}] with its heads side by side, got {tuple(t.shape)}")
-    st = tok.stride()
-    if (st[-1] != 1 or (shape[-2] > 1 and st[-2] != ld)
-            or (len(shape) == 3 and B > 1 and st[0] != T * ld)):
-        _bad(f"{name} has strides {st}, which is not one token every {ld} elements")
+    if st[2] != 1 or (tt > 1 and st[1] != ld) or (b > 1 and st[0] != tt * ld):
+        _bad(f"{name} has strides {t.stride()}, which is not one token every {ld} elements")
     return t.data_ptr()
 
 
@@ -342,8 +345,9 @@ def kvc_qk_norm_rope(q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleav
     the active layer's buffers (see include/kvc.h)."""
     bf, ok = torch.bfloat16, B > 0 and T > 0 and H_q > 0 and H_kv > 0 and D > 0
     if ok:
-        q, k, v = (_tokens_arg(x, B, T, h * D, ld, nm) for x, h, ld, nm in
-                   ((q, H_q, q_ld, "q"), (k, H_kv, k_ld, "k"), (v, H_kv, v_ld, "v")))
+        q = _tokens_arg(q, B, T, H_q * D, q_ld, "q")
+        k = _tokens_arg(k, B, T, H_kv * D, k_ld, "k")
+        v = _tokens_arg(v, B, T, H_kv * D, v_ld, "v")
     _check(_lib.kvc_qk_norm_rope(
         q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleaved, _arg(q_weight, bf, D, "q_weight"),
         _arg(k_weight, bf, D, "k_weight"), eps, _arg(inv_freq, torch.float32, R // 2, "inv_freq"),
