@@ -48,71 +48,92 @@ struct AttendArgs {
   float* lse;
   float2* part_ml;                   // [row tiles][slots][8 NT] maximum, sum
   float* part_o;                     // [row tiles][slots][8 NT][D]
-  int64_t* place;                    // [B * H_kv] blocks before each head, then all blocks
+  int* place;                        // [B * H_kv] blocks before each head, then all blocks
   int* status;
   int B, T, H_q, G, extra, P, slots;
+  uint32_t inv_h;                    // ceil(2^32 / H_kv): bh / H_kv as a product (bh < 2^24, H_kv <= 128)
   float scale;                       // log2(e) / sqrt(D)
   Q4Slots s;
 };
 
-// Blocks that the counted rows of (b, h) fill.
-__device__ __forceinline__ int blocks_of(const AttendArgs& a, int bh, int* n_rows) {
-  const int h = bh % a.s.H_kv;
-  const int64_t cap = a.s.off[h + 1] - a.s.off[h];
-  int64_t n = (int64_t)a.rows[bh] + a.extra;
-  if (n < 0 || n > cap) {
-    record_status(a.status, kStatusBadInput);
-    n = n < 0 ? 0 : cap;
+// The heads' slots, in shared memory: lanes look up different heads at a time,
+// which the constant bank would serve one after the other.
+struct SlotTable { int64_t off[kMaxHkv]; int cap[kMaxHkv]; };
+__device__ __forceinline__ void fill_slots(const AttendArgs& a, SlotTable& t) {
+  for (int h = threadIdx.x; h < a.s.H_kv; h += blockDim.x) {
+    t.off[h] = a.s.off[h];
+    t.cap[h] = (int)(a.s.off[h + 1] - a.s.off[h]);
   }
-  *n_rows = (int)n;
-  return (int)((n + q4::kRows - 1) / q4::kRows);
 }
+__device__ __forceinline__ int batch_of(const AttendArgs& a, int bh) {
+  // a divisor of 1 has no such product below 2^32
+  return a.s.H_kv == 1 ? bh : (int)__umulhi((uint32_t)bh, a.inv_h);
+}
+// Rows that (sequence, KV head) bh counts; bad: the count does not fit the slot.
+__device__ __forceinline__ int rows_of(const AttendArgs& a, const SlotTable& t, int bh, int held, bool* bad) {
+  const int cap = t.cap[bh - batch_of(a, bh) * a.s.H_kv];
+  const int64_t n = (int64_t)held + a.extra;
+  *bad |= n < 0 || n > cap;
+  return (int)(n < 0 ? 0 : n > cap ? cap : n);
+}
+__device__ __forceinline__ int blocks_of(int n_rows) { return (n_rows + q4::kRows - 1) / q4::kRows; }
 
-// Blocks of a CTA's range when N blocks are shared out.
-__device__ __forceinline__ int64_t range_blocks(int64_t N, int P) {
-  const int64_t L = (N + P - 1) / P;
+// Blocks of a CTA's range when N blocks are shared out.  Block numbers are
+// ints: all of this GPU's memory holds less than 2^28 blocks.
+__device__ __forceinline__ int range_blocks(int N, int P) {
+  const int L = (int)(((uint32_t)N + P - 1) / (uint32_t)P);
   return L < kMinBlocks ? kMinBlocks : L;
 }
 
 // Where a CTA's range begins: the head that holds its first block, and the
-// blocks before that head.  One scan over the row counts when a CTA's threads
-// can hold them all (kPer each), else one for the total and one for the place.
-// write: this CTA leaves every head's place to the joining kernel.
-struct Place { int64_t total, before; int bh; };
-constexpr int kPer = 4;
-__device__ Place find_place(const AttendArgs& a, int cta, bool write) {
-  __shared__ int scratch[32];
-  __shared__ int64_t sh[2];
-  const int BH = a.B * a.s.H_kv, chunk = kThreads * kPer;
-  Place p{0, 0, -1};
-  for (int round = BH <= chunk ? 1 : 0; round < 2; ++round) {
-    int64_t run = 0;
-    for (int base = 0; base < BH; base += chunk) {
-      int v[kPer], mine = 0, tot, n;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int bh = base + (int)threadIdx.x * kPer + i;
-        v[i] = bh < BH ? blocks_of(a, bh, &n) : 0;
-        mine += v[i];
-      }
-      int64_t before = run + block_inclusive_scan(mine, scratch, &tot) - mine;
-      run += tot;
-      if (round == 0) continue;
-      if (BH <= chunk) p.total = run;
-      const int64_t f0 = cta * range_blocks(p.total, a.P);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int bh = base + (int)threadIdx.x * kPer + i;
-        if (bh < BH && f0 >= before && f0 < before + v[i]) sh[0] = before, sh[1] = bh;
-        if (bh < BH && write) a.place[bh] = before;
-        before += v[i];
-      }
-    }
-    p.total = run;
+// blocks before that head.  Each warp adds up its share of the heads; the warp
+// whose share holds the place finds it.
+// write: leave every head's place to the joining kernel, and record counts
+// that do not fit.
+struct Place { int total, before, bh; };
+__device__ __forceinline__ Place find_place(const AttendArgs& a, const SlotTable& t, int cta, bool write) {
+  __shared__ int s_sum[kWarps], s_at[2];
+  const int BH = a.B * a.s.H_kv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = (BH + kThreads - 1) / kThreads * 32;
+  const int i0 = min(warp * share, BH), i1 = min(i0 + share, BH);
+  bool bad = false;
+  int sum = 0, nb0 = 0;
+  for (int base = i0; base < i1; base += 32) {
+    const int i = base + lane;
+    const int nb = i < i1 ? blocks_of(rows_of(a, t, i, __ldg(a.rows + i), &bad)) : 0;
+    if (base == i0) nb0 = nb;
+    sum += nb;
   }
-  if (write && threadIdx.x == 0) a.place[BH] = p.total;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
-  if (cta * range_blocks(p.total, a.P) < p.total) p.before = sh[0], p.bh = (int)sh[1];
+  Place p{0, 0, 0};
+  int run = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    run += w < warp ? s_sum[w] : 0;
+    p.total += s_sum[w];
+  }
+  const int f0 = (int)min((int64_t)cta * range_blocks(p.total, a.P), (int64_t)p.total);
+  if ((f0 >= run && f0 < run + sum) || write)
+    for (int base = i0; base < i1; base += 32) {
+      const int i = base + lane;
+      const int nb = base == i0 ? nb0 : i < i1 ? blocks_of(rows_of(a, t, i, __ldg(a.rows + i), &bad)) : 0;
+      int inc = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const int before = run + inc - nb;
+      if (write && i < i1) a.place[i] = before;
+      if (f0 >= before && f0 < before + nb) s_at[0] = before, s_at[1] = i;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  if (write && threadIdx.x == 0) a.place[BH] = p.total;
+  if (write && bad) record_status(a.status, kStatusBadInput);
+  __syncthreads();
+  if (f0 < p.total) p.before = s_at[0], p.bh = s_at[1];
   return p;
 }
 
@@ -150,7 +171,7 @@ __device__ __forceinline__ void copies_wait() {
 // positions.  Lane 4r + j copies the pieces it reads itself: rows r and r + 8
 // of the keys, slice r of the values' pairs j and j + 4, their scales, and the
 // positions of rows r and r + 8 (four lanes each, the same value).
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 __host__ __device__ constexpr int stage_bytes(int D) { return q4::block_bytes(D) + 32 * 8; }
 
 template <int D>
@@ -192,92 +213,113 @@ __device__ __forceinline__ Codes<kB / 4> load_codes(const uint8_t* p) {
 
 // The heads of a range, one after the other.
 struct Segment {
-  int64_t f, before;                 // flat block it starts at; blocks before its head
-  int bh, s0, cnt, n_rows;           // head; first block in the head, blocks; the head's rows
+  const uint8_t* rec;                // first block of the segment, its rows' positions
+  const int32_t* pos;
+  int f, bh, cnt, s0, n_rows;        // flat block it starts at; head; blocks; first block in the head; the head's rows
 };
-__device__ __forceinline__ bool segment_at(const AttendArgs& a, int64_t f, int64_t f1, int bh, int64_t before,
+template <int D>
+__device__ __forceinline__ bool segment_at(const AttendArgs& a, const SlotTable& t, int f, int f1, int bh, int before,
                                            Segment* g) {
   if (f >= f1) return false;
-  int nb, n_rows;
-  while ((nb = blocks_of(a, bh, &n_rows)) == 0) ++bh;      // f < f1 <= total: a head with rows follows
+  bool bad = false;                  // recorded where the places are found
+  int n;
+  while ((n = rows_of(a, t, bh, __ldg(a.rows + bh), &bad)) == 0) ++bh;     // f < f1 <= total: a head with rows follows
+  const int b = batch_of(a, bh);
   g->f = f;
-  g->before = before;
   g->bh = bh;
-  g->n_rows = n_rows;
-  g->s0 = (int)(f - before);
-  g->cnt = (int)min(f1 - f, (int64_t)(nb - g->s0));
+  g->n_rows = n;
+  g->s0 = f - before;
+  g->cnt = min(f1 - f, blocks_of(n) - g->s0);
+  const int64_t row = (int64_t)b * a.s.off[a.s.H_kv] + t.off[bh - b * a.s.H_kv] + (int64_t)g->s0 * q4::kRows;
+  g->rec = a.cache + row / q4::kRows * q4::block_bytes(D);
+  g->pos = a.pos + row;
   return true;
 }
-__device__ __forceinline__ bool next_segment(const AttendArgs& a, int64_t f1, const Segment& g, Segment* next) {
-  // a segment that does not end the range ends its head
-  return segment_at(a, g.f + g.cnt, f1, g.bh + 1, g.before + g.s0 + g.cnt, next);
-}
+
+// Shared memory: the joint outputs of 8 columns, then the warps' rings.
+// Position d' = 16 m + 2 r + e of a row there holds dim r*D/8 + 2m + e: a lane
+// of the output fragments stores pairs side by side with its neighbours', and
+// rows D + 4 apart keep the four columns of a store on different banks.
+__host__ __device__ constexpr int o_stride(int D) { return D + 4; }
+__host__ __device__ constexpr int o_bytes(int D, int cols) { return kWarps * cols * o_stride(D) * (int)sizeof(float); }
+template <int D>
+__device__ __forceinline__ int dim_of(int at) { return (at >> 1 & 7) * (D / 8) + (at >> 4) * 2 + (at & 1); }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int KS = D / 16;         // k-steps of the scores, m-tiles of the output
   constexpr int kB = D / 8;
   extern __shared__ __align__(128) uint8_t dyn[];
-  float (*s_o)[8][D] = reinterpret_cast<float (*)[8][D]>(dyn);     // [kWarps][8][D]
   __shared__ float2 s_ml[kWarps][8 * NT];
+  __shared__ SlotTable slots;
+  fill_slots(a, slots);
+  __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
-  const int H = a.s.H_kv, R = a.G * a.T, row_base = blockIdx.y * 8 * NT;
-  uint8_t* ring = dyn + kWarps * 8 * D * sizeof(float) + warp * kStages * stage_bytes(D);
+  const int R = a.G * a.T, row_base = blockIdx.y * 8 * NT;
+  const int cols = min(8, R);        // columns of an n-tile that may hold queries
+  float* s_o = reinterpret_cast<float*>(dyn);              // [kWarps][cols][o_stride]
+  uint8_t* ring = dyn + o_bytes(D, cols) + warp * kStages * stage_bytes(D);
   const uint32_t ring_u = smem_u32(ring);
 
   // the CTA's range [f0, f1) of the blocks laid end to end
-  const Place pl = find_place(a, blockIdx.x, blockIdx.x == 0 && blockIdx.y == 0);
-  const int64_t L = range_blocks(pl.total, a.P);
-  const int64_t f0 = blockIdx.x * L, f1 = min(f0 + L, pl.total);
+  const Place pl = find_place(a, slots, blockIdx.x, blockIdx.x == 0 && blockIdx.y == 0);
+  const int L = range_blocks(pl.total, a.P);
+  const int f0 = (int)min((int64_t)blockIdx.x * L, (int64_t)pl.total), f1 = min(f0 + L, pl.total);
   Segment g;
-  bool more = segment_at(a, f0, f1, pl.bh, pl.before, &g);
+  bool more = segment_at<D>(a, slots, f0, f1, pl.bh, pl.before, &g);
 
   // block `i` (0, 1, ...) of the warp's share of a segment into its ring; a group is
   // committed whether or not there is one, so that the waits can count
   int stage_in = 0, stage_out = 0;
   const auto fetch = [&](const Segment& x, int i) {
     const int in = warp + i * kWarps;
-    if (in < x.cnt) {
-      const int b = x.bh / H, h = x.bh - b * H;
-      const int64_t row = (int64_t)b * a.s.off[H] + a.s.off[h] + (int64_t)(x.s0 + in) * q4::kRows;
-      copy_block<D>(ring_u + stage_in * stage_bytes(D), a.cache + row / q4::kRows * q4::block_bytes(D), a.pos + row,
-                    lane);
-    }
+    if (in < x.cnt)
+      copy_block<D>(ring_u + stage_in * stage_bytes(D), x.rec + (int64_t)in * q4::block_bytes(D),
+                    x.pos + (int64_t)in * q4::kRows, lane);
     copies_commit();
     stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
   };
-  if (more)
-    for (int i = 0; i < kStages - 1; ++i) fetch(g, i);
+  bool started = false;
 
   while (more) {
     const int bh = g.bh, n_rows = g.n_rows;
-    const int b = bh / H;
+    const int b = batch_of(a, bh);
 
     // queries: column n = lane / 4 of each n-tile, quarter j of its dims
     uint32_t qf[NT][KS][2];
     float c2[NT][2];                 // factor from accumulator to log2 units, columns 2j and 2j + 1
     int qp[NT][2];                   // their positions
     int q_lo = INT32_MAX, q_hi = -1;
+    uint32_t w[NT][D / 8];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = row_base + nt * 8 + r;
-      const bool live = row < R;
-      uint32_t w[D / 8];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) w[i] = 0;
-      if (live) {
+      for (int i = 0; i < D / 8; ++i) w[nt][i] = 0;
+      if (row < R) {
         const uint4* p = reinterpret_cast<const uint4*>(a.q + ((int64_t)bh * R + row) * D + j * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const uint4 v = __ldg(p + i);
-          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+          w[nt][4 * i] = v.x, w[nt][4 * i + 1] = v.y, w[nt][4 * i + 2] = v.z, w[nt][4 * i + 3] = v.w;
         }
       }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int rr = row_base + nt * 8 + 2 * j + y;
+        qp[nt][y] = rr < R ? __ldg(a.q_pos + (int64_t)b * a.T + rr % a.T) : -1;
+      }
+    }
+    if (!started)                    // behind the queries' loads, which the blocks' traffic would hold up
+      for (int i = 0; i < kStages - 1; ++i) fetch(g, i);
+    started = true;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       uint32_t mx = 0;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+      for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, w[nt][i] & 0x7fff7fffu);
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -290,14 +332,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          qf[nt][s][y] = pack_half2(__uint_as_float(q4::bf16_of(w, 2 * s + y) << 16) * down,
-                                    __uint_as_float(q4::bf16_of(w, kB + 2 * s + y) << 16) * down);
+          qf[nt][s][y] = pack_half2(__uint_as_float(q4::bf16_of(w[nt], 2 * s + y) << 16) * down,
+                                    __uint_as_float(q4::bf16_of(w[nt], kB + 2 * s + y) << 16) * down);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         c2[nt][y] = __shfl_sync(0xffffffffu, c, (2 * j + y) * 4);
-        const int rr = row_base + nt * 8 + 2 * j + y;
-        qp[nt][y] = rr < R ? a.q_pos[(int64_t)b * a.T + rr % a.T] : -1;
-        if (rr < R) q_lo = min(q_lo, qp[nt][y]), q_hi = max(q_hi, qp[nt][y]);
+        if (row_base + nt * 8 + 2 * j + y < R) q_lo = min(q_lo, qp[nt][y]), q_hi = max(q_hi, qp[nt][y]);
       }
     }
     q_lo = __reduce_min_sync(0xffffffffu, q_lo);
@@ -332,11 +372,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
       }
       const int2 xp = *reinterpret_cast<const int2*>(st + q4::block_bytes(D) + lane * 8);
       // ---- scores
-      float acc[NT][4];
+      float acc[NT][4], odd[NT][4];  // two chains of products, half as long
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) acc[nt][y] = 0.f;
+        for (int y = 0; y < 4; ++y) acc[nt][y] = odd[nt][y] = 0.f;
       const uint32_t ks[2] = {q4::scales_to_half2((uint16_t)ksc), q4::scales_to_half2((uint16_t)(ksc >> 16))};
       const Codes<kB / 4> kc0 = load_codes<kB>(st + q4::k_codes(D) + lane * kB);
       const Codes<kB / 4> kc1 = load_codes<kB>(st + q4::k_codes(D) + 4 * D + lane * kB);
@@ -350,9 +390,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_f16(acc[nt], ka[0], kb[0], ka[1], kb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          mma_f16(acc[nt], ka[2], kb[2], ka[3], kb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+          mma_f16(odd[nt], ka[2], kb[2], ka[3], kb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
         }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) acc[nt][y] += odd[nt][y];
       // ---- mask: acc[nt][y], acc[nt][2 + y] are rows r, r + 8 against column 2j + y
       const bool in0 = blk * q4::kRows + r < n_rows && xp.x >= 0, in1 = blk * q4::kRows + r + 8 < n_rows && xp.y >= 0;
       const bool clear = in0 && xp.x <= q_lo && in1 && xp.y <= q_lo;
@@ -432,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
     // the next head's first blocks come in while this one is joined.  Groups that the
     // loop's tail committed empty are behind the ones it used; the ring starts afresh.
     Segment next;
-    more = next_segment(a, f1, g, &next);
+    more = segment_at<D>(a, slots, g.f + g.cnt, f1, bh + 1, g.f + g.cnt, &next);   // it does not end the range: it ends its head
     stage_in = stage_out;
     if (more)
       for (int i = 0; i < kStages - 1; ++i) fetch(next, i);
@@ -455,22 +499,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int col = 2 * j + y;
+        if (col >= cols) continue;
         float top = s_ml[0][nt * 8 + col].x;
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][nt * 8 + col].x);
         const float f = ex2(ref[nt][y] - top);
+        float* to = s_o + (warp * cols + col) * o_stride(D) + 2 * r;
 #pragma unroll
         for (int m = 0; m < KS; ++m)
-          *reinterpret_cast<float2*>(&s_o[warp][col][r * kB + 2 * m]) = make_float2(o[nt][m][y] * f, o[nt][m][2 + y] * f);
+          *reinterpret_cast<float2*>(to + 16 * m) = make_float2(o[nt][m][y] * f, o[nt][m][2 + y] * f);
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < 8 * D; i += kThreads) {
-        float v = 0.f;
+      for (int i = threadIdx.x; i < cols * (D / 4); i += kThreads) {
+        const int col = i / (D / 4), at = i % (D / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += (&s_o[w][0][0])[i];
-        a.part_o[(slot * 8 * NT + nt * 8) * D + i] = v;
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(s_o + (w * cols + col) * o_stride(D) + at);
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        *reinterpret_cast<float4*>(a.part_o + (slot * 8 * NT + nt * 8 + col) * D + at) = v;
       }
-      __syncthreads();
+      if (nt + 1 < NT) __syncthreads();
     }
     if (threadIdx.x < 8 * NT) {
       float top = kNoRef, l = 0.f;
@@ -497,11 +547,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(con
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = a.B * a.s.H_kv;
   const int R = a.G * a.T, bh = blockIdx.x / R, row = blockIdx.x - bh * R, ty = row / tile, in = row - ty * tile;
-  const int64_t total = a.place[BH], before = a.place[bh];
-  const int64_t after = bh + 1 < BH ? a.place[bh + 1] : total;
-  const int64_t L = range_blocks(total, a.P);
-  const int64_t c0 = before / L;
-  const int n = after > before ? (int)((after - 1) / L - c0 + 1) : 0;
+  const int total = a.place[BH], before = a.place[bh], after = a.place[bh + 1];   // place[BH] is the total
+  const int L = range_blocks(total, a.P);
+  const int c0 = before / L;
+  const int n = after > before ? (after - 1) / L - c0 + 1 : 0;
   const int64_t slot0 = (int64_t)ty * a.slots + bh + c0;
   const float2* ml = a.part_ml + slot0 * tile + in;
   const float* po = a.part_o + (slot0 * tile + in) * D + lane * V;
@@ -538,7 +587,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(con
     float o = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) o += s_v[w][d];
-    a.out[at * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+    a.out[at * D + dim_of<D>(d)] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
   }
   if (a.lse && threadIdx.x == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
@@ -557,7 +606,7 @@ Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D) {
   const size_t rows = (size_t)p.tiles * (size_t)p.slots * (size_t)tr;
   p.off_o = (rows * sizeof(float2) + 255) / 256 * 256;
   p.off_place = p.off_o + rows * D * sizeof(float);
-  p.total = p.off_place + ((size_t)B * H_kv + 1) * sizeof(int64_t);
+  p.total = p.off_place + ((size_t)B * H_kv + 1) * sizeof(int);
   return p;
 }
 
@@ -570,13 +619,14 @@ cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const
   a.q = q, a.cache = cache, a.pos = pos, a.rows = rows, a.q_pos = q_pos, a.out = out, a.lse = lse;
   a.part_ml = static_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_o);
-  a.place = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + p.off_place);
+  a.place = reinterpret_cast<int*>(static_cast<char*>(ws) + p.off_place);
   a.status = status_word_ptr();
   a.B = B, a.T = T, a.H_q = H_q, a.G = H_q / H, a.extra = extra, a.P = p.P, a.slots = (int)p.slots;
   a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
+  a.inv_h = (uint32_t)(((1ull << 32) + H - 1) / H);
   a.s = slots;
   const int tr = tile_rows(R);
-  const size_t smem = kWarps * (8 * D * sizeof(float) + kStages * stage_bytes(D));
+  const size_t smem = o_bytes(D, std::min(8, R)) + kWarps * kStages * stage_bytes(D);
   void (*scan)(AttendArgs);
   if (D == 128)
     scan = tr == 8 ? kvc_attend_q4_kernel<128, 1> : tr == 16 ? kvc_attend_q4_kernel<128, 2> : kvc_attend_q4_kernel<128, 4>;
