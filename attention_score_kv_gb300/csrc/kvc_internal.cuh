@@ -212,6 +212,17 @@ struct Q4AttendPlan {
   size_t total;
 };
 Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D);
+// the same for many query rows per KV head, on the tensor cores
+struct Q4TcPlan {
+  int tiles;         // tiles of 128 query rows per KV head
+  int splits;        // CTAs that share a tile's cache rows
+  size_t off_o, total;
+};
+Q4TcPlan plan_attend_q4_tc(int B, int T, int H_q, int H_kv, int D);
+cudaError_t launch_attend_q4_tc(const __nv_bfloat16* q, const uint8_t* cache, const int32_t* pos, const int32_t* rows,
+                                int extra, const int32_t* q_pos, int B, int T, int H_q, int D, const Q4Slots& slots,
+                                __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st);
+bool attend_q4_on_tc(int H_q, int H_kv, int T);     // which of the two a call takes
 cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const int32_t* pos, const int32_t* rows,
                              int extra, const int32_t* q_pos, int B, int T, int H_q, int D, const Q4Slots& slots,
                              __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st);

@@ -1,0 +1,593 @@
+// Attention over the 4-bit retained cache (format: kvc_q4.cuh), many query rows
+// per KV head: a follow-up prompt, long drafts.
+//
+// 128 query rows of a KV head (its G*T rows, head by head) against tiles of 128
+// cache rows, both products on the tensor cores (tcgen05, fp16 operands, fp32
+// accumulators in tensor memory):
+//   S = Q K^T  (Q in tensor memory, K in shared memory)
+//   O += P V   (P in tensor memory, over the scores it came from; V in shared)
+// 4*128*128*D flops a tile against 128*9D/8 bytes of cache: the products bound
+// it, 1024 cycles a tile at D = 128, if nothing else takes longer.  So:
+//  - Q and P come from tensor memory: with both operands in shared memory its
+//    128 bytes a cycle would be the limit before the products are;
+//  - four warps turn codes into fp16 operands (exact, as codes times scales),
+//    each 32 cache rows of a tile, into double-buffered shared tiles, with the
+//    next tile's bytes already on their way into registers;
+//  - eight warps take the softmax: two threads a row, 64 scores each, against a
+//    reference that follows the running maximum only when a score passes it by
+//    2^8, so the output in tensor memory is hardly ever rescaled;
+//  - S is double buffered: the next tile's scores are computed while this one's
+//    weights are.
+// Orders inside a tile are free (the contraction of S runs over dims, that of O
+// over rows), so each operand is written in the order that falls out of the
+// block format and keeps 16-byte stores on different banks:
+//   dims    16-byte chunk c of a K row: codes 4i .. 4i+3 of quarter j (pairs with
+//           the dims D/8 further), c = (D/32) j + i, i ^ 2 in the upper quarters of
+//           D = 128; Q is laid out alike
+//   rows    row k = r + 8s of block x of a warp's two is row 8 (r / 2) + 4x + 2s +
+//           r % 2 of its 32: the four rows of a value pair j, twice, side by side
+//   values  dim y of slice r is row r*D/8 + (y ^ 4 (r % 2)) of V^T
+// Few row tiles leave SMs idle; then the cache rows are split over several CTAs
+// per row tile, whose parts a second kernel joins in order.
+#include <algorithm>
+#include <cmath>
+
+#include "kvc_q4.cuh"
+#include "kvc_scan_common.cuh"
+
+namespace kvc {
+namespace {
+
+using scan::wait_bar;
+using scan::wait_bar_warp;
+
+constexpr int kSoftWarps = 8, kCodeWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kCodeWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kRowsM = 128, kKeys = 128;
+constexpr int kTileBlocks = kKeys / q4::kRows;
+// Positions are read by the softmax of tile i after the products of K have
+// freed the tile's stage.  Tile i + 4's are written when the scores of tile
+// i + 2 are done, which were issued after the weights of tile i were there.
+constexpr int kPosSlots = 4;
+constexpr uint32_t kCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;      // S: two buffers of 128 columns
+constexpr float kNoRef = -1.7e38f, kShift = 4.0f, kSlack = 8.0f;
+
+struct TcArgs {
+  const __nv_bfloat16* q;
+  const uint8_t* cache;
+  const int32_t *pos, *rows, *q_pos;
+  __nv_bfloat16* out;
+  float* lse;
+  float2* part_ml;                   // [row tiles of all heads][splits][128]
+  float* part_o;                     // [..][128][D]
+  int* status;
+  int T, R, extra, tiles, splits;
+  uint32_t wait_limit;
+  float scale;                       // log2(e) / sqrt(D)
+  Q4Slots s;
+};
+
+struct Bars {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, q_full, drain;
+};
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// One lane's share of two blocks: codes of the keys' rows r, r + 8 and of the
+// values' slice r, pairs j and j + 4; scales; positions of the rows.
+template <int D>
+struct TwoBlocks {
+  uint32_t k[2][2][D / 32], v[2][2][D / 32], ks[2], vs[2];
+  int pos[2][2];
+};
+template <int D>
+__device__ __forceinline__ void load_two(TwoBlocks<D>& x, const uint8_t* rec, const int32_t* pos, int n_blocks,
+                                         int lane) {
+  constexpr int kB = D / 8;
+  const int r = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const bool there = b < n_blocks;
+    const uint8_t* p = rec + b * q4::block_bytes(D);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) x.k[b][s][w] = x.v[b][s][w] = 0;
+      x.pos[b][s] = -1;
+      if (there) {
+        if constexpr (kB == 16) {
+          const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + q4::k_codes(D) + s * 4 * D + lane * kB));
+          x.k[b][s][0] = a.x, x.k[b][s][1] = a.y, x.k[b][s][2] = a.z, x.k[b][s][3] = a.w;
+          const uint4 c = __ldg(reinterpret_cast<const uint4*>(p + q4::v_codes(D) + s * 4 * D + lane * kB));
+          x.v[b][s][0] = c.x, x.v[b][s][1] = c.y, x.v[b][s][2] = c.z, x.v[b][s][3] = c.w;
+        } else {
+          const uint2 a = __ldg(reinterpret_cast<const uint2*>(p + q4::k_codes(D) + s * 4 * D + lane * kB));
+          x.k[b][s][0] = a.x, x.k[b][s][1] = a.y;
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(p + q4::v_codes(D) + s * 4 * D + lane * kB));
+          x.v[b][s][0] = c.x, x.v[b][s][1] = c.y;
+        }
+        x.pos[b][s] = __ldg(pos + b * q4::kRows + r + 8 * s);
+      }
+    }
+    x.ks[b] = x.vs[b] = 0;
+    if (there) {
+      if constexpr (D == 128) {
+        x.ks[b] = __ldg(reinterpret_cast<const uint32_t*>(p + q4::k_scales(D)) + lane);
+        x.vs[b] = __ldg(reinterpret_cast<const uint32_t*>(p + q4::v_scales(D)) + lane);
+      } else {
+        const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(p + q4::k_scales(D)) + lane);
+        x.ks[b] = (two & 0xffu) * 0x101u | (two >> 8) * 0x1010000u;
+        x.vs[b] = __ldg(reinterpret_cast<const uint32_t*>(p + q4::v_scales(D)) + (r >> 1) * 4 + j);
+      }
+    }
+  }
+}
+
+// A warp of the code converters: 32 rows of every tile.
+template <int D>
+__device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, int (*s_pos)[kKeys],
+                          uint8_t (*s_mixed)[kCodeWarps], const uint8_t* rec, const int32_t* pos, int n_rows, int t0,
+                          int t1, int q_lo, int q_hi, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps, r = lane >> 2, j = lane & 3;
+  const int n_blocks = (n_rows + q4::kRows - 1) / q4::kRows;
+  const auto load = [&](TwoBlocks<D>& x, int t) {
+    const int blk = t * kTileBlocks + 2 * w;
+    load_two<D>(x, rec + (int64_t)blk * q4::block_bytes(D), pos + (int64_t)blk * q4::kRows, t < t1 ? n_blocks - blk : 0,
+                lane);
+  };
+  TwoBlocks<D> next;
+  load(next, t0);
+  for (int t = t0; t < t1; ++t) {
+    const int i = t - t0, st = i & 1;
+    const uint32_t ph = ((i >> 1) & 1) ^ 1;
+    const TwoBlocks<D> x = next;
+    load(next, t + 1);
+    // what the queries see of the rows
+    uint32_t vs[2];
+    bool clear = true;
+    int seen_pos[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint32_t see[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int row = (t * kTileBlocks + 2 * w + b) * q4::kRows + r + 8 * s;
+        const int p = row < n_rows ? x.pos[b][s] : -1;
+        seen_pos[b][s] = p;
+        clear = clear && p >= 0 && p <= q_lo;
+        see[s] = __ballot_sync(0xffffffffu, p >= 0 && p <= q_hi);
+      }
+      // a row that no query sees may hold anything: its values count as zeros
+      uint32_t keep = 0;
+      if (see[0] >> (8 * j) & 1) keep |= 0x000000ffu;
+      if (see[0] >> (8 * j + 4) & 1) keep |= 0x0000ff00u;
+      if (see[1] >> (8 * j) & 1) keep |= 0x00ff0000u;
+      if (see[1] >> (8 * j + 4) & 1) keep |= 0xff000000u;
+      vs[b] = x.vs[b] & keep;
+    }
+    clear = __all_sync(0xffffffffu, clear);
+    // ---- keys
+    if (!wait_bar_warp(smem_u32(&bars->k_empty[st]), ph, abort_flag, a.status, a.wait_limit)) return;
+    const uint32_t kb = sK + st * (kKeys * D * 2);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t s2 = q4::scales_to_half2((uint16_t)(x.ks[b] >> (16 * s)));
+        const int row = w * 32 + (r >> 1) * 8 + b * 4 + s * 2 + (r & 1);
+        const uint32_t at = kb + (D == 128 ? (j >> 1) * (kKeys * 128) : 0) + row * 128;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t f[4];
+          q4::codes_to_half2(x.k[b][s][c], f);
+          const int chunk = D == 128 ? (j & 1) * 4 + (c ^ (2 * (j >> 1))) : j * 2 + c;
+          store16(at + ((chunk ^ (row & 7)) << 4), q4::mul_half2(f[0], s2), q4::mul_half2(f[1], s2),
+                  q4::mul_half2(f[2], s2), q4::mul_half2(f[3], s2));
+        }
+        if (j == 0) s_pos[i & (kPosSlots - 1)][row] = seen_pos[b][s];
+      }
+    if (lane == 0) s_mixed[i & (kPosSlots - 1)][w] = clear ? 0 : 1;
+    tc::fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(smem_u32(&bars->k_full[st]));
+    // ---- values
+    if (!wait_bar_warp(smem_u32(&bars->v_empty[st]), ph, abort_flag, a.status, a.wait_limit)) return;
+    const uint32_t vb = sV + st * (kKeys * D * 2) + (w >> 1) * (D * 128);
+    const uint32_t chunk = (w & 1) * 4 + j;
+    uint32_t s2[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) s2[b][s] = q4::scales_to_half2((uint16_t)(vs[b] >> (16 * s)));
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t f[2][2][4];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) q4::codes_to_half2(x.v[b][s][c], f[b][s]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = r * (D / 8) + ((4 * c + e) ^ (4 * (r & 1)));
+        store16(vb + row * 128 + ((chunk ^ (row & 7)) << 4), q4::mul_half2(f[0][0][e], s2[0][0]),
+                q4::mul_half2(f[0][1][e], s2[0][1]), q4::mul_half2(f[1][0][e], s2[1][0]),
+                q4::mul_half2(f[1][1][e], s2[1][1]));
+      }
+    }
+    tc::fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(smem_u32(&bars->v_full[st]));
+  }
+}
+
+// The thread that issues the products.  The scores of tile i + 1 go first, so
+// that its softmax can start while the output of tile i is added up.  Products
+// of one thread execute in order: tile i + 1's scores overwrite the weights of
+// tile i - 1 only after those have been used.
+template <int D>
+__device__ void mma_thread(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, uint32_t tmem, int n,
+                           volatile int* abort_flag) {
+  constexpr uint32_t kIdS = tc::idesc_f16(kRowsM, kKeys), kIdO = tc::idesc_f16(kRowsM, D);
+  const auto scores = [&](int i) {
+    const int st = i & 1;
+    if (!wait_bar(smem_u32(&bars->k_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit)) return false;
+    tc::fence_after_sync();
+    const uint32_t kb = sK + st * (kKeys * D * 2);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      tc::mma_bf16_ta(tmem + kColS + st * kKeys, tmem + kColQ + s * 8,
+                      tc::desc_sw128(kb + (s >> 2) * (kKeys * 128) + (s & 3) * 32), kIdS, s > 0);
+    tc::mma_commit(smem_u32(&bars->k_empty[st]));
+    tc::mma_commit(smem_u32(&bars->s_full[st]));
+    return true;
+  };
+  bool ok = wait_bar(smem_u32(&bars->q_full), 0, abort_flag, a.status, a.wait_limit) && scores(0);
+  for (int i = 0; i < n && ok; ++i) {
+    const int st = i & 1;
+    if (i + 1 < n && !scores(i + 1)) break;
+    if (!wait_bar(smem_u32(&bars->v_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit) ||
+        !wait_bar(smem_u32(&bars->p_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit))
+      break;
+    tc::fence_after_sync();
+    const uint32_t vb = sV + st * (kKeys * D * 2);
+#pragma unroll
+    for (int s = 0; s < kKeys / 16; ++s)
+      tc::mma_bf16_ta(tmem + kColO, tmem + kColS + st * kKeys + (s >> 2) * 64 + (s & 3) * 8,
+                      tc::desc_sw128(vb + (s >> 2) * (D * 128) + (s & 3) * 32), kIdO, i > 0 || s > 0);
+    tc::mma_commit(smem_u32(&bars->v_empty[st]));
+    tc::mma_commit(smem_u32(&bars->o_done));
+  }
+  scan::drain_mma(smem_u32(&bars->drain), a.status);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __grid_constant__ TcArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ __align__(16) int s_pos[kPosSlots][kKeys];
+  __shared__ __align__(4) uint8_t s_mixed[kPosSlots][kCodeWarps];  // a row of the warp's 32 that some query does not see
+  __shared__ float s_x[2][2][kRowsM];              // what the two threads of a row tell each other
+
+  const uint32_t sK = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sV = sK + 2 * kKeys * D * 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(smem_u32(&bars.k_full[i]), kCodeWarps);
+      tc::mbar_init(smem_u32(&bars.v_full[i]), kCodeWarps);
+      tc::mbar_init(smem_u32(&bars.k_empty[i]), 1);
+      tc::mbar_init(smem_u32(&bars.v_empty[i]), 1);
+      tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
+      tc::mbar_init(smem_u32(&bars.p_full[i]), kSoftWarps);
+    }
+    tc::mbar_init(smem_u32(&bars.o_done), 1);
+    tc::mbar_init(smem_u32(&bars.q_full), kSoftWarps);
+    tc::mbar_init(smem_u32(&bars.drain), 1);
+    s_abort = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(smem_u32(&s_tmem), kCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  const int H = a.s.H_kv, bh = blockIdx.x / a.tiles, tile = blockIdx.x - bh * a.tiles;
+  const int b = bh / H, h = bh - b * H;
+  const int64_t row0 = (int64_t)b * a.s.off[H] + a.s.off[h];
+  const int64_t cap = a.s.off[h + 1] - a.s.off[h];
+  int64_t held = (int64_t)__ldg(a.rows + bh) + a.extra;
+  if (held < 0 || held > cap) {
+    if (threadIdx.x == 0) record_status(a.status, kStatusBadInput);
+    held = held < 0 ? 0 : cap;
+  }
+  const int n_rows = (int)held;
+  const int key_tiles = (n_rows + kKeys - 1) / kKeys, per = (key_tiles + a.splits - 1) / a.splits;
+  const int t0 = min((int)blockIdx.y * per, key_tiles), t1 = min(t0 + per, key_tiles), n = t1 - t0;
+
+  if (warp >= kSoftWarps && warp < kMmaWarp) {
+    int q_lo = INT32_MAX, q_hi = -1;
+    for (int i = lane; i < kRowsM; i += 32) {
+      const int row = tile * kRowsM + i;
+      if (row < a.R) {
+        const int p = __ldg(a.q_pos + (int64_t)b * a.T + row % a.T);
+        q_lo = min(q_lo, p), q_hi = max(q_hi, p);
+      }
+    }
+    q_lo = __reduce_min_sync(0xffffffffu, q_lo);
+    q_hi = __reduce_max_sync(0xffffffffu, q_hi);
+    code_warp<D>(a, &bars, sK, sV, s_pos, s_mixed, a.cache + row0 / q4::kRows * q4::block_bytes(D), a.pos + row0, n_rows,
+                 t0, t1, q_lo, q_hi, &s_abort);
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && n > 0) mma_thread<D>(a, &bars, sK, sV, tmem, n, &s_abort);
+  } else {
+    // ---- softmax: thread (row, half): dims and scores [half * .., ..)
+    constexpr int kHalfD = D / 2;
+    const int half = warp >> 2, in = (warp & 3) * 32 + lane, row = tile * kRowsM + in;
+    const bool live = row < a.R;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int qp = live ? __ldg(a.q_pos + (int64_t)b * a.T + row % a.T) : -1;
+    float c2;
+    {
+      uint32_t w[kHalfD / 2];
+#pragma unroll
+      for (int i = 0; i < kHalfD / 2; ++i) w[i] = 0;
+      if (live) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.q + ((int64_t)bh * a.R + row) * D + half * kHalfD);
+#pragma unroll
+        for (int i = 0; i < kHalfD / 8; ++i) {
+          const uint4 v = __ldg(p + i);
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+      }
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < kHalfD / 2; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+      mx = max(mx & 0xffffu, mx >> 16);
+      s_x[0][half][in] = __uint_as_float(mx);
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      mx = max(mx, __float_as_uint(s_x[0][half ^ 1][in]));
+      // scale by the power of two that brings the row's largest value into [1, 2)
+      const uint32_t e = mx >> 7, ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
+      const float down = __uint_as_float((254u - ee) << 23);
+      c2 = __uint_as_float(ee << 23) * a.scale;
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj)               // the half's two quarters
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t v[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            v[y] = half2_of(__uint_as_float(q4::bf16_of(w, jj * (D / 4) + 4 * i + y) << 16) * down,
+                            __uint_as_float(q4::bf16_of(w, jj * (D / 4) + D / 8 + 4 * i + y) << 16) * down);
+          const int j = 2 * half + jj;
+          const int chunk = D == 128 ? j * 4 + (i ^ (2 * half)) : j * 2 + i;
+          tc::tmem_st4(tmem + lanes + kColQ + chunk * 4, v);
+        }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(smem_u32(&bars.q_full));
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");       // s_x is free again
+    }
+
+    float ref = kNoRef, sum = 0.f;
+    bool ok = true;                  // a wait that gave up: go on without waiting, so that no barrier is left alone
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      const uint32_t s_at = tmem + lanes + kColS + st * kKeys + half * 64;
+      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.s_full[st]), (i >> 1) & 1, &s_abort, a.status,
+                                                        a.wait_limit));
+      tc::fence_after_sync();
+      float x[64];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) tc::tmem_ld16(s_at + 16 * y, x + 16 * y);
+      const uint32_t mixed = *reinterpret_cast<const uint16_t*>(&s_mixed[i & (kPosSlots - 1)][2 * half]);
+      tc::tmem_wait_ld();
+      tc::reg_fence(x, 64);
+      if (mixed) {
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const int4 p = *reinterpret_cast<const int4*>(&s_pos[i & (kPosSlots - 1)][half * 64 + 4 * y]);
+          if (p.x < 0 || p.x > qp) x[4 * y] = -INFINITY;
+          if (p.y < 0 || p.y > qp) x[4 * y + 1] = -INFINITY;
+          if (p.z < 0 || p.z > qp) x[4 * y + 2] = -INFINITY;
+          if (p.w < 0 || p.w > qp) x[4 * y + 3] = -INFINITY;
+        }
+      }
+      float m = x[0];
+#pragma unroll
+      for (int y = 1; y < 64; ++y) m = fmaxf(m, x[y]);
+      s_x[st][half][in] = m;
+      asm volatile("bar.sync %0, 64;\n" ::"r"(2 + (warp & 3)) : "memory");
+      m = fmaxf(m, s_x[st][half ^ 1][in]) * c2;
+      if (__any_sync(0xffffffffu, m > ref + (kSlack + kShift))) {
+        const float to = fmaxf(ref, m - kShift), f = ex2(ref - to);
+        ref = to;
+        sum *= f;
+        if (i > 0) {
+          ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), (i - 1) & 1, &s_abort, a.status,
+                                                            a.wait_limit));
+          tc::fence_after_sync();
+#pragma unroll
+          for (int y = 0; y < kHalfD / 16; ++y) {
+            float o[16];
+            const uint32_t at = tmem + lanes + kColO + half * kHalfD + 16 * y;
+            tc::tmem_ld16(at, o);
+            tc::tmem_wait_ld();
+            tc::reg_fence(o, 16);
+#pragma unroll
+            for (int z = 0; z < 16; ++z) o[z] *= f;
+            tc::tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t p[16];
+#pragma unroll
+        for (int z = 0; z < 16; ++z) {
+          const float u = ex2(fmaf(x[32 * y + 2 * z], c2, -ref)), v = ex2(fmaf(x[32 * y + 2 * z + 1], c2, -ref));
+          sum += u + v;
+          p[z] = half2_of(u, v);
+        }
+        tc::tmem_st16(s_at + 16 * y, p);
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(smem_u32(&bars.p_full[st]));
+    }
+    // ---- the row: both halves' sums, and this half's dims
+    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    s_x[0][half][in] = sum;
+    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    sum = s_x[0][0][in] + s_x[0][1][in];
+    if (n > 0) {
+      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), (n - 1) & 1, &s_abort, a.status,
+                                                        a.wait_limit));
+      tc::fence_after_sync();
+    }
+    const bool whole = a.splits == 1;
+    const float f = whole ? (sum == 0.f ? 0.f : 1.0f / sum) : 1.f;
+    const int64_t at = (int64_t)bh * a.R + row;
+    const int64_t part = ((int64_t)blockIdx.x * a.splits + blockIdx.y) * kRowsM + in;
+#pragma unroll
+    for (int y = 0; y < kHalfD / 16; ++y) {
+      float o[16];
+      if (n > 0) {
+        tc::tmem_ld16(tmem + lanes + kColO + half * kHalfD + 16 * y, o);
+        tc::tmem_wait_ld();
+        tc::reg_fence(o, 16);
+      }
+      // columns are rows of V^T; the groups of four are swapped where the slice is odd
+      float v[16];
+#pragma unroll
+      for (int z = 0; z < 16; ++z) {
+        const int n_of = half * kHalfD + 16 * y + z;
+        const int odd = D == 128 ? y & 1 : (n_of >> 3) & 1;
+        v[z] = n > 0 && sum != 0.f ? o[z ^ (4 * odd)] * f : 0.f;
+      }
+      const int d0 = half * kHalfD + 16 * y;
+      if (whole) {
+        if (live) {
+          uint32_t w[8];
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            const __nv_bfloat162 c = __floats2bfloat162_rn(v[2 * z], v[2 * z + 1]);
+            w[z] = *reinterpret_cast<const uint32_t*>(&c);
+          }
+          uint4* to = reinterpret_cast<uint4*>(a.out + at * D + d0);
+          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      } else if (live) {
+        float4* to = reinterpret_cast<float4*>(a.part_o + part * D + d0);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) to[z] = make_float4(v[4 * z], v[4 * z + 1], v[4 * z + 2], v[4 * z + 3]);
+      }
+    }
+    if (half == 0 && live) {
+      if (!whole) a.part_ml[part] = make_float2(ref, sum);
+      else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994530942f;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kCols);
+}
+
+// One warp per query row: joins the parts of its splits, in order.
+template <int D>
+__global__ void __launch_bounds__(128) kvc_attend_q4_tc_join_kernel(const __grid_constant__ TcArgs a, int64_t n_rows) {
+  constexpr int V = D / 32;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (at >= n_rows) return;
+  const int64_t bh = at / a.R;
+  const int row = (int)(at - bh * a.R);
+  const int64_t first = ((bh * a.tiles + row / kRowsM) * a.splits) * kRowsM + row % kRowsM;
+  float top = kNoRef;
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_ml[first + (int64_t)s * kRowsM].x);
+  float l = 0.f, v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const int64_t p = first + (int64_t)s * kRowsM;
+    const float2 ml = a.part_ml[p];
+    const float f = ex2(ml.x - top);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = fmaf(a.part_o[p * D + lane * V + i], f, v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) a.out[at * D + lane * V + i] = __float2bfloat16_rn(l == 0.f ? 0.f : v[i] / l);
+  if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+}
+
+}  // namespace
+
+Q4TcPlan plan_attend_q4_tc(int B, int T, int H_q, int H_kv, int D) {
+  Q4TcPlan p{};
+  const int64_t R = (int64_t)(H_q / H_kv) * T;
+  p.tiles = (int)((R + kRowsM - 1) / kRowsM);
+  const int64_t units = (int64_t)B * H_kv * p.tiles;
+  // one wave: as many CTAs as SMs, never more parts than that
+  p.splits = (int)std::max<int64_t>(1, std::max(num_sms(), 1) / units);
+  if (p.splits > 1) {
+    const size_t rows = (size_t)units * p.splits * kRowsM;
+    p.off_o = (rows * sizeof(float2) + 255) / 256 * 256;
+    p.total = p.off_o + rows * D * sizeof(float);
+  }
+  return p;
+}
+
+cudaError_t launch_attend_q4_tc(const __nv_bfloat16* q, const uint8_t* cache, const int32_t* pos, const int32_t* rows,
+                                int extra, const int32_t* q_pos, int B, int T, int H_q, int D, const Q4Slots& slots,
+                                __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st) {
+  const int H = slots.H_kv;
+  const Q4TcPlan p = plan_attend_q4_tc(B, T, H_q, H, D);
+  TcArgs a{};
+  a.q = q, a.cache = cache, a.pos = pos, a.rows = rows, a.q_pos = q_pos, a.out = out, a.lse = lse;
+  a.part_ml = static_cast<float2*>(ws);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_o);
+  a.status = status_word_ptr();
+  a.T = T, a.R = H_q / H * T, a.extra = extra, a.tiles = p.tiles, a.splits = p.splits;
+  a.wait_limit = wait_limit_polls();
+  a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
+  a.s = slots;
+  const size_t smem = 4 * (size_t)kKeys * D * 2 + 1024;
+  auto* kern = D == 128 ? kvc_attend_q4_tc_kernel<128> : kvc_attend_q4_tc_kernel<64>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess)
+    e = launch_pdl(kern, dim3((unsigned)(B * H * p.tiles), p.splits), dim3(kThreads), smem, st, a);
+  note_launches(1);
+  if (e != cudaSuccess) return e;
+  if (p.splits > 1) {
+    const int64_t n = (int64_t)B * H_q * T;
+    e = launch_pdl(D == 128 ? kvc_attend_q4_tc_join_kernel<128> : kvc_attend_q4_tc_join_kernel<64>,
+                   dim3((unsigned)((n + 3) / 4)), dim3(128), 0, st, a, n);
+    note_launches(1);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace kvc

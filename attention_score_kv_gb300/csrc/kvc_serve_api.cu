@@ -11,6 +11,9 @@ using namespace kvc;
 
 namespace kvc {
 
+// Above 64 query rows per KV head the products bound the work, not the cache.
+bool attend_q4_on_tc(int H_q, int H_kv, int T) { return (int64_t)(H_q / H_kv) * T > 64; }
+
 int check_slots(int H_kv, const int64_t* slot_off) {
   if (H_kv > kMaxHkv) return set_error(KVC_ERR_UNSUPPORTED, "H_kv=%d above %d", H_kv, kMaxHkv);
   if (!slot_off) return set_error(KVC_ERR_INVALID_ARG, "slot_off is NULL");
@@ -51,6 +54,11 @@ int check_attend(int B, int T, int H_q, int H_kv, int D) {
     return set_error(KVC_ERR_UNSUPPORTED, "%lld query rows per KV head: above 2^20", (long long)(H_q / H_kv) * T);
   if ((int64_t)B * H_q * T > INT32_MAX) return set_error(KVC_ERR_UNSUPPORTED, "batch too large");
   return KVC_OK;
+}
+
+size_t attend_ws(int B, int T, int H_q, int H_kv, int D) {
+  return attend_q4_on_tc(H_q, H_kv, T) ? plan_attend_q4_tc(B, T, H_q, H_kv, D).total
+                                       : plan_attend_q4(B, T, H_q, H_kv, D).total;
 }
 
 Q4Slots make_slots(int H_kv, const int64_t* slot_off) {
@@ -174,7 +182,7 @@ size_t kvc_attention_q4_workspace_size(int B, int T, int H_q, int H_kv, int D) {
     set_error(KVC_ERR_CUDA, "no CUDA device to size the workspace for");
     return 0;
   }
-  return plan_attend_q4(B, T, H_q, H_kv, D).total;
+  return std::max<size_t>(attend_ws(B, T, H_q, H_kv, D), 256);   // 0 is the error
 }
 
 int kvc_attention_q4(const kvc_bf16* q, const uint8_t* cache, const int32_t* pos, const int32_t* rows, int extra,
@@ -188,8 +196,9 @@ int kvc_attention_q4(const kvc_bf16* q, const uint8_t* cache, const int32_t* pos
       (lse && (rc = check_ptr(lse, 4, "lse"))))
     return rc;
   if (num_sms() <= 0) return set_error(KVC_ERR_CUDA, "no CUDA device");
-  if ((rc = check_ws(ws, ws_bytes, plan_attend_q4(B, T, H_q, H_kv, D).total))) return rc;
-  return done(launch_attend_q4(bf(q), cache, pos, rows, extra, q_pos, B, T, H_q, D, make_slots(H_kv, slot_off), bf(out),
+  if ((rc = check_ws(ws, ws_bytes, attend_ws(B, T, H_q, H_kv, D)))) return rc;
+  auto* launch = attend_q4_on_tc(H_q, H_kv, T) ? launch_attend_q4_tc : launch_attend_q4;
+  return done(launch(bf(q), cache, pos, rows, extra, q_pos, B, T, H_q, D, make_slots(H_kv, slot_off), bf(out),
                                lse, ws, cs(stream)),
               "4-bit attention launch");
 }
