@@ -10,9 +10,9 @@
 // it, 1024 cycles a tile at D = 128, if nothing else takes longer.  So:
 //  - Q and P come from tensor memory: with both operands in shared memory its
 //    128 bytes a cycle would be the limit before the products are;
-//  - four warps turn codes into fp16 operands (exact, as codes times scales),
-//    each 32 cache rows of a tile, into double-buffered shared tiles, with the
-//    next tile's bytes already on their way into registers;
+//  - a warp copies tiles of codes in, and four warps turn them into fp16
+//    operands (exact, as codes times scales), each 32 cache rows of a tile, in
+//    double-buffered shared tiles;
 //  - eight warps take the softmax: two threads a row, 64 scores each, against a
 //    reference that follows the running maximum only when a score passes it by
 //    2^8, so the output in tensor memory is hardly ever rescaled;
@@ -42,14 +42,22 @@ using scan::wait_bar;
 using scan::wait_bar_warp;
 
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kCodeWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kRowsM = 128, kKeys = 128;
 constexpr int kTileBlocks = kKeys / q4::kRows;
-// Positions are read by the softmax of tile i after the products of K have
-// freed the tile's stage.  Tile i + 4's are written when the scores of tile
-// i + 2 are done, which were issued after the weights of tile i were there.
-constexpr int kPosSlots = 4;
+constexpr int kRaw = 3;              // tiles of codes in flight
+// What the queries see of a tile's rows, in the tile's row order.  Tile i's is
+// written when the codes of tile i - 3 have been read, that is after K's stage
+// was free for tile i - 3, so the scores of tile i - 5 were done; those were
+// issued after the weights of tile i - 7 were there, the last reader.
+constexpr int kSeen = 8;
+struct alignas(16) Seen {
+  int pos[kKeys];
+  uint32_t some[4];                  // rows (of two blocks, in cache order) that some query may see
+  uint8_t mixed[4];                  // some query does not see all of these 32
+};
+__host__ __device__ constexpr int raw_bytes(int D) { return kTileBlocks * q4::block_bytes(D); }
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;      // S: two buffers of 128 columns
 constexpr float kNoRef = -1.7e38f, kShift = 4.0f, kSlack = 8.0f;
@@ -70,7 +78,7 @@ struct TcArgs {
 };
 
 struct Bars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, q_full, drain;
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, q_full, drain;
 };
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -81,139 +89,158 @@ __device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, u
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// One lane's share of two blocks: codes of the keys' rows r, r + 8 and of the
-// values' slice r, pairs j and j + 4; scales; positions of the rows.
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The warp that brings in the cache: a tile's blocks as they are, in one copy,
+// and its positions, in the tiles' row order, with what the queries see of them.
 template <int D>
-struct TwoBlocks {
-  uint32_t k[2][2][D / 32], v[2][2][D / 32], ks[2], vs[2];
-  int pos[2][2];
-};
-template <int D>
-__device__ __forceinline__ void load_two(TwoBlocks<D>& x, const uint8_t* rec, const int32_t* pos, int n_blocks,
-                                         int lane) {
-  constexpr int kB = D / 8;
-  const int r = lane >> 2, j = lane & 3;
+__device__ void load_warp(const TcArgs& a, Bars* bars, uint8_t* raw, Seen* seen, const uint8_t* rec,
+                          const int32_t* pos, int n_rows, int t0, int t1, int q_lo, int q_hi,
+                          volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  const int n_blocks = (n_rows + q4::kRows - 1) / q4::kRows;
+  const int n = t1 - t0;
+  // row k of block x of a warp's two, as a place in its 32 (header)
+  const int x = lane >> 4, k = lane & 15;
+  const int place = ((k & 7) >> 1) * 8 + x * 4 + (k >> 3) * 2 + (k & 1);
+  const auto fetch = [&](int t, int (&p)[4]) {
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const bool there = b < n_blocks;
-    const uint8_t* p = rec + b * q4::block_bytes(D);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) x.k[b][s][w] = x.v[b][s][w] = 0;
-      x.pos[b][s] = -1;
-      if (there) {
-        if constexpr (kB == 16) {
-          const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + q4::k_codes(D) + s * 4 * D + lane * kB));
-          x.k[b][s][0] = a.x, x.k[b][s][1] = a.y, x.k[b][s][2] = a.z, x.k[b][s][3] = a.w;
-          const uint4 c = __ldg(reinterpret_cast<const uint4*>(p + q4::v_codes(D) + s * 4 * D + lane * kB));
-          x.v[b][s][0] = c.x, x.v[b][s][1] = c.y, x.v[b][s][2] = c.z, x.v[b][s][3] = c.w;
-        } else {
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(p + q4::k_codes(D) + s * 4 * D + lane * kB));
-          x.k[b][s][0] = a.x, x.k[b][s][1] = a.y;
-          const uint2 c = __ldg(reinterpret_cast<const uint2*>(p + q4::v_codes(D) + s * 4 * D + lane * kB));
-          x.v[b][s][0] = c.x, x.v[b][s][1] = c.y;
-        }
-        x.pos[b][s] = __ldg(pos + b * q4::kRows + r + 8 * s);
-      }
+    for (int w = 0; w < 4; ++w) {
+      const int row = t * kKeys + w * 32 + lane;
+      p[w] = row < n_rows ? __ldg(pos + row) : -1;
     }
-    x.ks[b] = x.vs[b] = 0;
-    if (there) {
-      if constexpr (D == 128) {
-        x.ks[b] = __ldg(reinterpret_cast<const uint32_t*>(p + q4::k_scales(D)) + lane);
-        x.vs[b] = __ldg(reinterpret_cast<const uint32_t*>(p + q4::v_scales(D)) + lane);
-      } else {
-        const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(p + q4::k_scales(D)) + lane);
-        x.ks[b] = (two & 0xffu) * 0x101u | (two >> 8) * 0x1010000u;
-        x.vs[b] = __ldg(reinterpret_cast<const uint32_t*>(p + q4::v_scales(D)) + (r >> 1) * 4 + j);
-      }
+  };
+  int next[4];
+  if (n > 0) fetch(t0, next);
+  int i = 0;
+  for (; i < n; ++i) {
+    const int st = i % kRaw, t = t0 + i;
+    int p[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) p[w] = next[w];
+    if (i + 1 < n) fetch(t + 1, next);
+    if (!__all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars->raw_empty[st]), ((i / kRaw) & 1) ^ 1, abort_flag,
+                                               a.status, a.wait_limit)))
+      break;
+    Seen& s = seen[i % kSeen];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      s.pos[w * 32 + place] = p[w];
+      const bool all = __all_sync(0xffffffffu, p[w] >= 0 && p[w] <= q_lo);
+      const uint32_t some = __ballot_sync(0xffffffffu, p[w] >= 0 && p[w] <= q_hi);
+      if (lane == 0) s.mixed[w] = all ? 0 : 1, s.some[w] = some;
     }
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t bytes = min(kTileBlocks, n_blocks - t * kTileBlocks) * q4::block_bytes(D);
+      const uint32_t bar = smem_u32(&bars->raw_full[st]);
+      tc::mbar_arrive_expect_tx(bar, bytes);
+      tc::bulk_g2s(smem_u32(raw + st * raw_bytes(D)), rec + (int64_t)t * raw_bytes(D), bytes, bar);
+    }
+  }
+  // every copy issued has landed before the CTA may leave
+  for (int y = max(0, i - kRaw); y < i; ++y) scan::drain_wait(smem_u32(&bars->raw_full[y % kRaw]), (y / kRaw) & 1, a.status);
+}
+
+template <int kB>
+__device__ __forceinline__ void read_codes(const uint8_t* p, uint32_t (&w)[kB / 4]) {
+  if constexpr (kB == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
   }
 }
 
-// A warp of the code converters: 32 rows of every tile.
+// A warp of the code converters: 32 rows (two blocks) of every tile.  No load
+// from global memory may be in flight here: the proxy fences would wait for it.
 template <int D>
-__device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, int (*s_pos)[kKeys],
-                          uint8_t (*s_mixed)[kCodeWarps], const uint8_t* rec, const int32_t* pos, int n_rows, int t0,
-                          int t1, int q_lo, int q_hi, volatile int* abort_flag) {
+__device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, const uint8_t* raw, const Seen* seen,
+                          int n, volatile int* abort_flag) {
+  constexpr int kB = D / 8;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps, r = lane >> 2, j = lane & 3;
-  const int n_blocks = (n_rows + q4::kRows - 1) / q4::kRows;
-  const auto load = [&](TwoBlocks<D>& x, int t) {
-    const int blk = t * kTileBlocks + 2 * w;
-    load_two<D>(x, rec + (int64_t)blk * q4::block_bytes(D), pos + (int64_t)blk * q4::kRows, t < t1 ? n_blocks - blk : 0,
-                lane);
-  };
-  TwoBlocks<D> next;
-  load(next, t0);
-  for (int t = t0; t < t1; ++t) {
-    const int i = t - t0, st = i & 1;
+  for (int i = 0; i < n; ++i) {
+    const int st = i & 1, rs = i % kRaw;
     const uint32_t ph = ((i >> 1) & 1) ^ 1;
-    const TwoBlocks<D> x = next;
-    load(next, t + 1);
-    // what the queries see of the rows
-    uint32_t vs[2];
-    bool clear = true;
-    int seen_pos[2][2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t see[2];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int row = (t * kTileBlocks + 2 * w + b) * q4::kRows + r + 8 * s;
-        const int p = row < n_rows ? x.pos[b][s] : -1;
-        seen_pos[b][s] = p;
-        clear = clear && p >= 0 && p <= q_lo;
-        see[s] = __ballot_sync(0xffffffffu, p >= 0 && p <= q_hi);
-      }
-      // a row that no query sees may hold anything: its values count as zeros
-      uint32_t keep = 0;
-      if (see[0] >> (8 * j) & 1) keep |= 0x000000ffu;
-      if (see[0] >> (8 * j + 4) & 1) keep |= 0x0000ff00u;
-      if (see[1] >> (8 * j) & 1) keep |= 0x00ff0000u;
-      if (see[1] >> (8 * j + 4) & 1) keep |= 0xff000000u;
-      vs[b] = x.vs[b] & keep;
-    }
-    clear = __all_sync(0xffffffffu, clear);
+    if (!wait_bar_warp(smem_u32(&bars->raw_full[rs]), (i / kRaw) & 1, abort_flag, a.status, a.wait_limit) ||
+        !wait_bar_warp(smem_u32(&bars->k_empty[st]), ph, abort_flag, a.status, a.wait_limit))
+      return;
+    const uint8_t* rec = raw + rs * raw_bytes(D) + 2 * w * q4::block_bytes(D);
     // ---- keys
-    if (!wait_bar_warp(smem_u32(&bars->k_empty[st]), ph, abort_flag, a.status, a.wait_limit)) return;
     const uint32_t kb = sK + st * (kKeys * D * 2);
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < 2; ++b) {
+      const uint8_t* p = rec + b * q4::block_bytes(D);
+      const uint32_t ks = D == 128 ? *reinterpret_cast<const uint32_t*>(p + q4::k_scales(D) + lane * 4)
+                                   : *reinterpret_cast<const uint16_t*>(p + q4::k_scales(D) + lane * 2);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t s2 = q4::scales_to_half2((uint16_t)(x.ks[b] >> (16 * s)));
+        const uint32_t s2 = q4::scales_to_half2((uint16_t)(D == 128 ? ks >> (16 * s) : (ks >> (8 * s) & 0xffu) * 0x101u));
+        uint32_t code[D / 32];
+        read_codes<kB>(p + q4::k_codes(D) + s * 4 * D + lane * kB, code);
         const int row = w * 32 + (r >> 1) * 8 + b * 4 + s * 2 + (r & 1);
         const uint32_t at = kb + (D == 128 ? (j >> 1) * (kKeys * 128) : 0) + row * 128;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t f[4];
-          q4::codes_to_half2(x.k[b][s][c], f);
+          q4::codes_to_half2(code[c], f);
           const int chunk = D == 128 ? (j & 1) * 4 + (c ^ (2 * (j >> 1))) : j * 2 + c;
           store16(at + ((chunk ^ (row & 7)) << 4), q4::mul_half2(f[0], s2), q4::mul_half2(f[1], s2),
                   q4::mul_half2(f[2], s2), q4::mul_half2(f[3], s2));
         }
-        if (j == 0) s_pos[i & (kPosSlots - 1)][row] = seen_pos[b][s];
       }
-    if (lane == 0) s_mixed[i & (kPosSlots - 1)][w] = clear ? 0 : 1;
+    }
     tc::fence_proxy_async();
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(smem_u32(&bars->k_full[st]));
-    // ---- values
+    // ---- values.  A row that no query sees may hold anything: its values count as zeros
+    uint32_t code[2][2][D / 32], s2[2][2];
+    const uint32_t some = seen[i % kSeen].some[w];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint8_t* p = rec + b * q4::block_bytes(D);
+      uint32_t vs = *reinterpret_cast<const uint32_t*>(p + q4::v_scales(D) + ((D == 128 ? r : r >> 1) * 4 + j) * 4);
+      const uint32_t see = some >> (16 * b + 2 * j);         // rows 2j, 2j + 1 and 2j + 8, 2j + 9 of the block
+      vs &= (see & 1 ? 0x000000ffu : 0u) | (see & 2 ? 0x0000ff00u : 0u) | (see & 0x100 ? 0x00ff0000u : 0u) |
+            (see & 0x200 ? 0xff000000u : 0u);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        s2[b][s] = q4::scales_to_half2((uint16_t)(vs >> (16 * s)));
+        read_codes<kB>(p + q4::v_codes(D) + s * 4 * D + lane * kB, code[b][s]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(smem_u32(&bars->raw_empty[rs]));
     if (!wait_bar_warp(smem_u32(&bars->v_empty[st]), ph, abort_flag, a.status, a.wait_limit)) return;
     const uint32_t vb = sV + st * (kKeys * D * 2) + (w >> 1) * (D * 128);
     const uint32_t chunk = (w & 1) * 4 + j;
-    uint32_t s2[2][2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) s2[b][s] = q4::scales_to_half2((uint16_t)(vs[b] >> (16 * s)));
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t f[2][2][4];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) q4::codes_to_half2(x.v[b][s][c], f[b][s]);
+        for (int s = 0; s < 2; ++s) q4::codes_to_half2(code[b][s][c], f[b][s]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int row = r * (D / 8) + ((4 * c + e) ^ (4 * (r & 1)));
@@ -274,14 +301,18 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   __shared__ Bars bars;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ __align__(16) int s_pos[kPosSlots][kKeys];
-  __shared__ __align__(4) uint8_t s_mixed[kPosSlots][kCodeWarps];  // a row of the warp's 32 that some query does not see
+  __shared__ __align__(16) Seen s_seen[kSeen];
   __shared__ float s_x[2][2][kRowsM];              // what the two threads of a row tell each other
 
   const uint32_t sK = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sV = sK + 2 * kKeys * D * 2;
+  uint8_t* raw = smem_raw + (sV + 2 * kKeys * D * 2 - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      tc::mbar_init(smem_u32(&bars.raw_full[i]), 1);
+      tc::mbar_init(smem_u32(&bars.raw_empty[i]), kCodeWarps);
+    }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(smem_u32(&bars.k_full[i]), kCodeWarps);
       tc::mbar_init(smem_u32(&bars.v_full[i]), kCodeWarps);
@@ -320,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   const int key_tiles = (n_rows + kKeys - 1) / kKeys, per = (key_tiles + a.splits - 1) / a.splits;
   const int t0 = min((int)blockIdx.y * per, key_tiles), t1 = min(t0 + per, key_tiles), n = t1 - t0;
 
-  if (warp >= kSoftWarps && warp < kMmaWarp) {
+  if (warp == kLoadWarp) {
     int q_lo = INT32_MAX, q_hi = -1;
     for (int i = lane; i < kRowsM; i += 32) {
       const int row = tile * kRowsM + i;
@@ -331,8 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     }
     q_lo = __reduce_min_sync(0xffffffffu, q_lo);
     q_hi = __reduce_max_sync(0xffffffffu, q_hi);
-    code_warp<D>(a, &bars, sK, sV, s_pos, s_mixed, a.cache + row0 / q4::kRows * q4::block_bytes(D), a.pos + row0, n_rows,
-                 t0, t1, q_lo, q_hi, &s_abort);
+    load_warp<D>(a, &bars, raw, s_seen, a.cache + row0 / q4::kRows * q4::block_bytes(D), a.pos + row0, n_rows, t0, t1,
+                 q_lo, q_hi, &s_abort);
+  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
+    code_warp<D>(a, &bars, sK, sV, raw, s_seen, n, &s_abort);
   } else if (warp == kMmaWarp) {
     if (lane == 0 && n > 0) mma_thread<D>(a, &bars, sK, sV, tmem, n, &s_abort);
   } else {
@@ -386,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       asm volatile("bar.sync 1, 256;\n" ::: "memory");       // s_x is free again
     }
 
-    float ref = kNoRef, sum = 0.f;
+    float ref = kNoRef;
+    float2 sum2[2] = {};             // the row's sum, in four parts
     bool ok = true;                  // a wait that gave up: go on without waiting, so that no barrier is left alone
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
@@ -397,29 +431,31 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       float x[64];
 #pragma unroll
       for (int y = 0; y < 4; ++y) tc::tmem_ld16(s_at + 16 * y, x + 16 * y);
-      const uint32_t mixed = *reinterpret_cast<const uint16_t*>(&s_mixed[i & (kPosSlots - 1)][2 * half]);
+      const uint32_t mixed = *reinterpret_cast<const uint16_t*>(&s_seen[i % kSeen].mixed[2 * half]);
       tc::tmem_wait_ld();
       tc::reg_fence(x, 64);
       if (mixed) {
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
-          const int4 p = *reinterpret_cast<const int4*>(&s_pos[i & (kPosSlots - 1)][half * 64 + 4 * y]);
+          const int4 p = *reinterpret_cast<const int4*>(&s_seen[i % kSeen].pos[half * 64 + 4 * y]);
           if (p.x < 0 || p.x > qp) x[4 * y] = -INFINITY;
           if (p.y < 0 || p.y > qp) x[4 * y + 1] = -INFINITY;
           if (p.z < 0 || p.z > qp) x[4 * y + 2] = -INFINITY;
           if (p.w < 0 || p.w > qp) x[4 * y + 3] = -INFINITY;
         }
       }
-      float m = x[0];
+      float m = x[0], m1 = x[1];     // two chains of three-input maxima
 #pragma unroll
-      for (int y = 1; y < 64; ++y) m = fmaxf(m, x[y]);
+      for (int y = 2; y < 62; y += 4) m = max3(m, x[y], x[y + 1]), m1 = max3(m1, x[y + 2], x[y + 3]);
+      m = fmaxf(max3(m, x[62], x[63]), m1);
       s_x[st][half][in] = m;
       asm volatile("bar.sync %0, 64;\n" ::"r"(2 + (warp & 3)) : "memory");
       m = fmaxf(m, s_x[st][half ^ 1][in]) * c2;
       if (__any_sync(0xffffffffu, m > ref + (kSlack + kShift))) {
         const float to = fmaxf(ref, m - kShift), f = ex2(ref - to);
         ref = to;
-        sum *= f;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) sum2[y].x *= f, sum2[y].y *= f;
         if (i > 0) {
           ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), (i - 1) & 1, &s_abort, a.status,
                                                             a.wait_limit));
@@ -437,14 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
           }
         }
       }
+      const float2 c22 = make_float2(c2, c2), ref2 = make_float2(-ref, -ref);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         uint32_t p[16];
 #pragma unroll
         for (int z = 0; z < 16; ++z) {
-          const float u = ex2(fmaf(x[32 * y + 2 * z], c2, -ref)), v = ex2(fmaf(x[32 * y + 2 * z + 1], c2, -ref));
-          sum += u + v;
-          p[z] = half2_of(u, v);
+          const float2 e = fma2(make_float2(x[32 * y + 2 * z], x[32 * y + 2 * z + 1]), c22, ref2);
+          const float2 u = make_float2(ex2(e.x), ex2(e.y));
+          sum2[z & 1] = add2(sum2[z & 1], u);
+          p[z] = half2_of(u.x, u.y);
         }
         tc::tmem_st16(s_at + 16 * y, p);
       }
@@ -454,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       if (lane == 0) tc::mbar_arrive(smem_u32(&bars.p_full[st]));
     }
     // ---- the row: both halves' sums, and this half's dims
+    float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     s_x[0][half][in] = sum;
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
@@ -574,7 +613,7 @@ cudaError_t launch_attend_q4_tc(const __nv_bfloat16* q, const uint8_t* cache, co
   a.wait_limit = wait_limit_polls();
   a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
   a.s = slots;
-  const size_t smem = 4 * (size_t)kKeys * D * 2 + 1024;
+  const size_t smem = 4 * (size_t)kKeys * D * 2 + kRaw * (size_t)raw_bytes(D) + 1024;
   auto* kern = D == 128 ? kvc_attend_q4_tc_kernel<128> : kvc_attend_q4_tc_kernel<64>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess)

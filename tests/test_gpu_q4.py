@@ -80,12 +80,12 @@ def attend(K, q, cache, pos, rows, extra, q_pos, B, T, Hq, H, D, so, lse=True):
     return out, ls
 
 
-def check_attention(K, q, cache, pos, rows, extra, q_pos, B, T, Hq, H, D, so, out, lse, heads=None):
+def check_attention(K, q, cache, pos, rows, extra, q_pos, B, T, Hq, H, D, so, out, lse, heads=None, batches=None):
     kk, vv = all_rows(K, cache, B, H, D, so)
     q, out, lse = f64(q), f64(out), f64(lse)
     pos, rows, q_pos = (t.cpu().numpy() for t in (pos.view(B, -1), rows.view(B, H), q_pos.view(B, T)))
     G = Hq // H
-    for b in range(B):
+    for b in batches if batches is not None else range(B):
         for hq in heads if heads is not None else range(Hq):
             h = hq // G
             n = min(max(int(rows[b, h]) + extra, 0), so[h + 1] - so[h])
@@ -313,6 +313,37 @@ def test_attention(K, case, sharp):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
     bare, _ = attend(K, *args, lse=False)
     assert torch.equal(out, bare)
+
+
+# Many query rows, with one CTA per tile of them (more tiles than SMs) and with several; every CTA
+# goes through many tiles of cache rows, and new tokens end in the middle of one.
+LONG = [
+    (20, 66, 8, 8, 64, [700, 130, 1000, 128, 1, 511, 640, 333]),
+    (24, 70, 14, 7, 128, [900, 700, 1200, 65, 1290, 128, 256]),
+    (1, 300, 8, 8, 128, [3000, 2950, 100, 0, 2047, 2048, 2049, 1500]),
+    (2, 130, 6, 2, 64, [9000, 7001]),
+]
+
+
+@pytest.mark.parametrize("case", LONG)
+@pytest.mark.parametrize("sharp", [0.5, 8.0])
+def test_attention_of_many_rows_over_many_tiles(K, case, sharp):
+    B, T, Hq, H, D, n = case
+    so = K.kvc_q4_layout(H, 1 << 20, n, T + 20)
+    cache, pos, _, _ = filled(K, B, H, D, so, n, 131, scale=1.5)
+    rows = np.array(n)[None, :] - np.minimum(np.arange(B)[:, None] % 5, np.array(n))
+    new = 3 * max(n) + np.arange(T)[None, :] + 10 * np.arange(B)[:, None]
+    k, v = rnd(141, B, H, T, D, scale=1.5), rnd(142, B, H, T, D)
+    K.kvc_append_q4(k, v, i32(new), B, H, T, D, so, i32(rows), cache, pos)
+    holes = torch.rand(pos.shape, generator=torch.Generator(device="cuda").manual_seed(7), device="cuda") < 0.01
+    pos[holes] = -1                                      # masked rows in every tile
+    q = rnd(143, B, Hq, T, D, scale=sharp)
+    args = (q, cache, pos, i32(rows), T, i32(new), B, T, Hq, H, D, so)
+    out, lse = attend(K, *args)
+    K.kvc_check_status()
+    check_attention(K, *args, out, lse, batches=sorted({0, B - 1}))
+    again, lse2 = attend(K, *args)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("T", [1, 6, 70])
