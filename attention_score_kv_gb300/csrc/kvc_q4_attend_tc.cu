@@ -259,19 +259,36 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
 // that its softmax can start while the output of tile i is added up.  Products
 // of one thread execute in order: tile i + 1's scores overwrite the weights of
 // tile i - 1 only after those have been used.
+// A product takes the tensor core 64 cycles, and arithmetic on descriptors
+// between products took twice that from the one thread that issues them: they
+// are made once, and steps add constants to them.
+__device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool first) {
+  if (first)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, 0, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.b32 p, 0, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
 template <int D>
 __device__ void mma_thread(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, uint32_t tmem, int n,
                            volatile int* abort_flag) {
   constexpr uint32_t kIdS = tc::idesc_f16(kRowsM, kKeys), kIdO = tc::idesc_f16(kRowsM, D);
+  constexpr uint64_t kStage = kKeys * D * 2 >> 4;              // descriptor units of 16 bytes
+  const uint64_t k0 = tc::desc_sw128(sK), v0 = tc::desc_sw128(sV);
   const auto scores = [&](int i) {
     const int st = i & 1;
     if (!wait_bar(smem_u32(&bars->k_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit)) return false;
     tc::fence_after_sync();
-    const uint32_t kb = sK + st * (kKeys * D * 2);
+    const uint64_t kd = k0 + st * kStage;
+    const uint32_t sd = tmem + kColS + st * kKeys;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
-      tc::mma_bf16_ta(tmem + kColS + st * kKeys, tmem + kColQ + s * 8,
-                      tc::desc_sw128(kb + (s >> 2) * (kKeys * 128) + (s & 3) * 32), kIdS, s > 0);
+      mma_ta(sd, tmem + kColQ + s * 8, kd + (((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4), kIdS, s == 0);
     tc::mma_commit(smem_u32(&bars->k_empty[st]));
     tc::mma_commit(smem_u32(&bars->s_full[st]));
     return true;
@@ -284,11 +301,14 @@ __device__ void mma_thread(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV
         !wait_bar(smem_u32(&bars->p_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit))
       break;
     tc::fence_after_sync();
-    const uint32_t vb = sV + st * (kKeys * D * 2);
+    const uint64_t vd = v0 + st * kStage;
+    const uint32_t pd = tmem + kColS + st * kKeys;
+    if (i == 0) mma_ta(tmem + kColO, pd, vd, kIdO, true);
+    else mma_ta(tmem + kColO, pd, vd, kIdO, false);
 #pragma unroll
-    for (int s = 0; s < kKeys / 16; ++s)
-      tc::mma_bf16_ta(tmem + kColO, tmem + kColS + st * kKeys + (s >> 2) * 64 + (s & 3) * 8,
-                      tc::desc_sw128(vb + (s >> 2) * (D * 128) + (s & 3) * 32), kIdO, i > 0 || s > 0);
+    for (int s = 1; s < kKeys / 16; ++s)
+      mma_ta(tmem + kColO, pd + (s >> 2) * 64 + (s & 3) * 8, vd + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), kIdO,
+             false);
     tc::mma_commit(smem_u32(&bars->v_empty[st]));
     tc::mma_commit(smem_u32(&bars->o_done));
   }
@@ -456,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
         ref = to;
 #pragma unroll
         for (int y = 0; y < 2; ++y) sum2[y].x *= f, sum2[y].y *= f;
-        if (i > 0) {
+        if (i > 0) {                 // the output of tile i - 2 was done before these scores
           ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), (i - 1) & 1, &s_abort, a.status,
                                                             a.wait_limit));
           tc::fence_after_sync();
@@ -498,8 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     sum = s_x[0][0][in] + s_x[0][1][in];
     if (n > 0) {
-      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), (n - 1) & 1, &s_abort, a.status,
-                                                        a.wait_limit));
+      // a parity names the last phase but one as well: the output of tile n - 3 is done
+      // (the scores of tile n - 1 came after it), so wait for the two after that
+      for (int i = max(0, n - 2); i < n; ++i)
+        ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), i & 1, &s_abort, a.status,
+                                                          a.wait_limit));
       tc::fence_after_sync();
     }
     const bool whole = a.splits == 1;
