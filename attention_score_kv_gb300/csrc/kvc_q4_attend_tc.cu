@@ -255,7 +255,7 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
   }
 }
 
-// The thread that issues the products.  The scores of tile i + 1 go first, so
+// The warp that issues the products.  The scores of tile i + 1 go first, so
 // that its softmax can start while the output of tile i is added up.  Products
 // of one thread execute in order: tile i + 1's scores overwrite the weights of
 // tile i - 1 only after those have been used.
@@ -274,45 +274,56 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc)
         : "memory");
 }
+// The whole warp waits (a lane that polls alone costs 300 cycles a wait, the
+// warp together 20 to 90); lane 0 issues.
 template <int D>
-__device__ void mma_thread(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, uint32_t tmem, int n,
-                           volatile int* abort_flag) {
+__device__ void mma_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, uint32_t tmem, int n,
+                         volatile int* abort_flag) {
   constexpr uint32_t kIdS = tc::idesc_f16(kRowsM, kKeys), kIdO = tc::idesc_f16(kRowsM, D);
   constexpr uint64_t kStage = kKeys * D * 2 >> 4;              // descriptor units of 16 bytes
+  const bool issues = (threadIdx.x & 31) == 0;
   const uint64_t k0 = tc::desc_sw128(sK), v0 = tc::desc_sw128(sV);
+  const auto wait = [&](uint64_t* bar, int phase) {
+    return __all_sync(0xffffffffu, wait_bar_warp(smem_u32(bar), phase & 1, abort_flag, a.status, a.wait_limit));
+  };
   const auto scores = [&](int i) {
     const int st = i & 1;
-    if (!wait_bar(smem_u32(&bars->k_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit)) return false;
+    if (!wait(&bars->k_full[st], i >> 1)) return false;
     tc::fence_after_sync();
-    const uint64_t kd = k0 + st * kStage;
-    const uint32_t sd = tmem + kColS + st * kKeys;
+    if (issues) {
+      const uint64_t kd = k0 + st * kStage;
+      const uint32_t sd = tmem + kColS + st * kKeys;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      mma_ta(sd, tmem + kColQ + s * 8, kd + (((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4), kIdS, s == 0);
-    tc::mma_commit(smem_u32(&bars->k_empty[st]));
-    tc::mma_commit(smem_u32(&bars->s_full[st]));
+      for (int s = 0; s < D / 16; ++s)
+        mma_ta(sd, tmem + kColQ + s * 8, kd + (((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4), kIdS, s == 0);
+      tc::mma_commit(smem_u32(&bars->k_empty[st]));
+      tc::mma_commit(smem_u32(&bars->s_full[st]));
+    }
+    __syncwarp();
     return true;
   };
-  bool ok = wait_bar(smem_u32(&bars->q_full), 0, abort_flag, a.status, a.wait_limit) && scores(0);
+  bool ok = wait(&bars->q_full, 0) && scores(0);
   for (int i = 0; i < n && ok; ++i) {
     const int st = i & 1;
     if (i + 1 < n && !scores(i + 1)) break;
-    if (!wait_bar(smem_u32(&bars->v_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit) ||
-        !wait_bar(smem_u32(&bars->p_full[st]), (i >> 1) & 1, abort_flag, a.status, a.wait_limit))
-      break;
+    if (!wait(&bars->v_full[st], i >> 1) || !wait(&bars->p_full[st], i >> 1)) break;
     tc::fence_after_sync();
-    const uint64_t vd = v0 + st * kStage;
-    const uint32_t pd = tmem + kColS + st * kKeys;
-    if (i == 0) mma_ta(tmem + kColO, pd, vd, kIdO, true);
-    else mma_ta(tmem + kColO, pd, vd, kIdO, false);
+    if (issues) {
+      const uint64_t vd = v0 + st * kStage;
+      const uint32_t pd = tmem + kColS + st * kKeys;
+      if (i == 0) mma_ta(tmem + kColO, pd, vd, kIdO, true);
+      else mma_ta(tmem + kColO, pd, vd, kIdO, false);
 #pragma unroll
-    for (int s = 1; s < kKeys / 16; ++s)
-      mma_ta(tmem + kColO, pd + (s >> 2) * 64 + (s & 3) * 8, vd + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), kIdO,
-             false);
-    tc::mma_commit(smem_u32(&bars->v_empty[st]));
-    tc::mma_commit(smem_u32(&bars->o_done));
+      for (int s = 1; s < kKeys / 16; ++s)
+        mma_ta(tmem + kColO, pd + (s >> 2) * 64 + (s & 3) * 8, vd + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), kIdO,
+               false);
+      tc::mma_commit(smem_u32(&bars->v_empty[st]));
+      tc::mma_commit(smem_u32(&bars->o_done));
+    }
+    __syncwarp();
   }
-  scan::drain_mma(smem_u32(&bars->drain), a.status);
+  if (issues) scan::drain_mma(smem_u32(&bars->drain), a.status);
+  __syncwarp();
 }
 
 template <int D>
@@ -387,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   } else if (warp >= kSoftWarps && warp < kMmaWarp) {
     code_warp<D>(a, &bars, sK, sV, raw, s_seen, n, &s_abort);
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && n > 0) mma_thread<D>(a, &bars, sK, sV, tmem, n, &s_abort);
+    if (n > 0) mma_warp<D>(a, &bars, sK, sV, tmem, n, &s_abort);
   } else {
     // ---- softmax: thread (row, half): dims and scores [half * .., ..)
     constexpr int kHalfD = D / 2;
