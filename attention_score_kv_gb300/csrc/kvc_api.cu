@@ -87,6 +87,29 @@ int* status_word_ptr() {
   return g_status_ptr[dev];
 }
 
+cudaError_t allow_smem(const void* kernel, size_t smem) {
+  struct Entry {
+    const void* kernel;
+    int dev;
+    size_t smem;
+  };
+  static std::vector<Entry> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(g_mu);
+  for (Entry& x : known)
+    if (x.kernel == kernel && x.dev == dev) {
+      if (x.smem >= smem) return cudaSuccess;
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e == cudaSuccess) x.smem = smem;
+      return e;
+    }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) known.push_back({kernel, dev, smem});
+  return e;
+}
+
 uint32_t wait_limit_polls() {
   return g_opt_wait_limit > 0 ? (uint32_t)std::min<int64_t>(g_opt_wait_limit, 1LL << 30) : (1u << 22);
 }

@@ -135,6 +135,10 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
+// Lets `kernel` have `smem` bytes of dynamic shared memory on the current
+// device; asks the runtime only the first time, or for more than before.
+cudaError_t allow_smem(const void* kernel, size_t smem);
+
 // --------------------------------------------------------- kernel launchers
 // pass 1: per-slot partial normalisers (log2-domain reference m, Z relative
 // to it).  exact_max: m is the slot's maximum score (the pass-1 results the

@@ -632,7 +632,7 @@ cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const
     scan = tr == 8 ? kvc_attend_q4_kernel<128, 1> : tr == 16 ? kvc_attend_q4_kernel<128, 2> : kvc_attend_q4_kernel<128, 4>;
   else
     scan = tr == 8 ? kvc_attend_q4_kernel<64, 1> : tr == 16 ? kvc_attend_q4_kernel<64, 2> : kvc_attend_q4_kernel<64, 4>;
-  cudaError_t e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(scan), smem);
   if (e == cudaSuccess) e = launch_pdl(scan, dim3(p.P, p.tiles), dim3(kThreads), smem, st, a);
   if (e != cudaSuccess) return e;
   e = launch_pdl(D == 128 ? kvc_attend_q4_join_kernel<128> : kvc_attend_q4_join_kernel<64>, dim3((unsigned)(B * H * R)),

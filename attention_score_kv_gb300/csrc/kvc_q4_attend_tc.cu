@@ -77,8 +77,10 @@ struct TcArgs {
   Q4Slots s;
 };
 
+// s_full: the scores of a tile are there, and so K's stage is free.  o_done: a
+// tile's output is added up, and so V's stage is free.
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done, q_full, drain;
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], q_full, drain;
 };
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -183,11 +185,15 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
     const int st = i & 1, rs = i % kRaw;
     const uint32_t ph = ((i >> 1) & 1) ^ 1;
     if (!wait_bar_warp(smem_u32(&bars->raw_full[rs]), (i / kRaw) & 1, abort_flag, a.status, a.wait_limit) ||
-        !wait_bar_warp(smem_u32(&bars->k_empty[st]), ph, abort_flag, a.status, a.wait_limit))
+        !wait_bar_warp(smem_u32(&bars->s_full[st]), ph, abort_flag, a.status, a.wait_limit))
       return;
     const uint8_t* rec = raw + rs * raw_bytes(D) + 2 * w * q4::block_bytes(D);
     // ---- keys
-    const uint32_t kb = sK + st * (kKeys * D * 2);
+    // place of (block b, half s, chunk c) for this lane: tiles are 1024-aligned, so what
+    // the lane adds and what the step adds are different bits, or swizzle bits to flip
+    const uint32_t k_at = (sK + st * (kKeys * D * 2) + (D == 128 ? (j >> 1) * (kKeys * 128) : 0) +
+                           (w * 32 + (r >> 1) * 8 + (r & 1)) * 128) |
+                          ((D == 128 ? (j & 1) * 4 ^ 2 * (j >> 1) : j * 2) ^ (r & 1)) << 4;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const uint8_t* p = rec + b * q4::block_bytes(D);
@@ -198,14 +204,11 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
         const uint32_t s2 = q4::scales_to_half2((uint16_t)(D == 128 ? ks >> (16 * s) : (ks >> (8 * s) & 0xffu) * 0x101u));
         uint32_t code[D / 32];
         read_codes<kB>(p + q4::k_codes(D) + s * 4 * D + lane * kB, code);
-        const int row = w * 32 + (r >> 1) * 8 + b * 4 + s * 2 + (r & 1);
-        const uint32_t at = kb + (D == 128 ? (j >> 1) * (kKeys * 128) : 0) + row * 128;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t f[4];
           q4::codes_to_half2(code[c], f);
-          const int chunk = D == 128 ? (j & 1) * 4 + (c ^ (2 * (j >> 1))) : j * 2 + c;
-          store16(at + ((chunk ^ (row & 7)) << 4), q4::mul_half2(f[0], s2), q4::mul_half2(f[1], s2),
+          store16(k_at ^ ((b * 4 + s * 2) * 128 | (c ^ (b * 4 + s * 2)) << 4), q4::mul_half2(f[0], s2), q4::mul_half2(f[1], s2),
                   q4::mul_half2(f[2], s2), q4::mul_half2(f[3], s2));
         }
       }
@@ -231,9 +234,9 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(smem_u32(&bars->raw_empty[rs]));
-    if (!wait_bar_warp(smem_u32(&bars->v_empty[st]), ph, abort_flag, a.status, a.wait_limit)) return;
-    const uint32_t vb = sV + st * (kKeys * D * 2) + (w >> 1) * (D * 128);
-    const uint32_t chunk = (w & 1) * 4 + j;
+    if (!wait_bar_warp(smem_u32(&bars->o_done[st]), ph, abort_flag, a.status, a.wait_limit)) return;
+    const uint32_t v_at = (sV + st * (kKeys * D * 2) + (w >> 1) * (D * 128) + r * (D / 8) * 128) |
+                          ((4 * (r & 1)) * 128 | (((w & 1) * 4 + j) ^ (4 * (r & 1))) << 4);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t f[2][2][4];
@@ -243,8 +246,7 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
         for (int s = 0; s < 2; ++s) q4::codes_to_half2(code[b][s][c], f[b][s]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int row = r * (D / 8) + ((4 * c + e) ^ (4 * (r & 1)));
-        store16(vb + row * 128 + ((chunk ^ (row & 7)) << 4), q4::mul_half2(f[0][0][e], s2[0][0]),
+        store16(v_at ^ ((4 * c + e) * 128 | ((4 * c + e) & 7) << 4), q4::mul_half2(f[0][0][e], s2[0][0]),
                 q4::mul_half2(f[0][1][e], s2[0][1]), q4::mul_half2(f[1][0][e], s2[1][0]),
                 q4::mul_half2(f[1][1][e], s2[1][1]));
       }
@@ -296,7 +298,6 @@ __device__ void mma_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, 
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
         mma_ta(sd, tmem + kColQ + s * 8, kd + (((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4), kIdS, s == 0);
-      tc::mma_commit(smem_u32(&bars->k_empty[st]));
       tc::mma_commit(smem_u32(&bars->s_full[st]));
     }
     __syncwarp();
@@ -317,8 +318,7 @@ __device__ void mma_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, 
       for (int s = 1; s < kKeys / 16; ++s)
         mma_ta(tmem + kColO, pd + (s >> 2) * 64 + (s & 3) * 8, vd + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), kIdO,
                false);
-      tc::mma_commit(smem_u32(&bars->v_empty[st]));
-      tc::mma_commit(smem_u32(&bars->o_done));
+      tc::mma_commit(smem_u32(&bars->o_done[st]));
     }
     __syncwarp();
   }
@@ -347,12 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(smem_u32(&bars.k_full[i]), kCodeWarps);
       tc::mbar_init(smem_u32(&bars.v_full[i]), kCodeWarps);
-      tc::mbar_init(smem_u32(&bars.k_empty[i]), 1);
-      tc::mbar_init(smem_u32(&bars.v_empty[i]), 1);
       tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
+      tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
       tc::mbar_init(smem_u32(&bars.p_full[i]), kSoftWarps);
     }
-    tc::mbar_init(smem_u32(&bars.o_done), 1);
     tc::mbar_init(smem_u32(&bars.q_full), kSoftWarps);
     tc::mbar_init(smem_u32(&bars.drain), 1);
     s_abort = 0;
@@ -487,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
         ref = to;
 #pragma unroll
         for (int y = 0; y < 2; ++y) sum2[y].x *= f, sum2[y].y *= f;
-        if (i > 0) {                 // the output of tile i - 2 was done before these scores
-          ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), (i - 1) & 1, &s_abort, a.status,
-                                                            a.wait_limit));
+        if (i > 0) {
+          ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[st ^ 1]), ((i - 1) >> 1) & 1, &s_abort,
+                                                            a.status, a.wait_limit));
           tc::fence_after_sync();
 #pragma unroll
           for (int y = 0; y < kHalfD / 16; ++y) {
@@ -529,11 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     sum = s_x[0][0][in] + s_x[0][1][in];
     if (n > 0) {
-      // a parity names the last phase but one as well: the output of tile n - 3 is done
-      // (the scores of tile n - 1 came after it), so wait for the two after that
-      for (int i = max(0, n - 2); i < n; ++i)
-        ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done), i & 1, &s_abort, a.status,
-                                                          a.wait_limit));
+      // a parity names the last phase but one as well; that one, the output of tile
+      // n - 3, was done before the scores of tile n - 1
+      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, &s_abort,
+                                                        a.status, a.wait_limit));
       tc::fence_after_sync();
     }
     const bool whole = a.splits == 1;
@@ -649,7 +646,7 @@ cudaError_t launch_attend_q4_tc(const __nv_bfloat16* q, const uint8_t* cache, co
   a.s = slots;
   const size_t smem = 4 * (size_t)kKeys * D * 2 + kRaw * (size_t)raw_bytes(D) + 1024;
   auto* kern = D == 128 ? kvc_attend_q4_tc_kernel<128> : kvc_attend_q4_tc_kernel<64>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e == cudaSuccess)
     e = launch_pdl(kern, dim3((unsigned)(B * H * p.tiles), p.splits), dim3(kThreads), smem, st, a);
   note_launches(1);

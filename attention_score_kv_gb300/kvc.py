@@ -47,6 +47,17 @@ if not os.path.exists(LIB_PATH):
                       "`python -m attention_score_kv_gb300.build` (nvcc, sm_103a)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _cur_dev() -> int:
+    """The current CUDA device; -1 without one (raw pointers can still be validated)."""
+    try:
+        return _get_device()
+    except (RuntimeError, AssertionError):
+        return -1
+
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -122,7 +133,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:   # the raw handle: a Stream object costs microseconds per call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_cur_dev())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -145,12 +156,12 @@ def _bad(msg):
     raise KvcError(KVC_ERR_INVALID_ARG, msg)
 
 
-def _arg(t, dtype, n, name):
+def _arg(t, dtype, n, name, dev):
     """Device pointer of a contiguous tensor of at least n elements on the current
-    device; a raw pointer or None passes as it is."""
+    device `dev`; a raw pointer or None passes as it is."""
     if t is None or t.__class__ is int:
         return t
-    if t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == torch._C._cuda_getDevice():
+    if t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev:
         return t.data_ptr()
     if t.dtype != dtype:
         _bad(f"{name} is {t.dtype}, not {dtype}")
@@ -161,14 +172,14 @@ def _arg(t, dtype, n, name):
     _bad(f"{name} is on {t.device}, not on the current CUDA device")
 
 
-def _tokens_arg(t, B, T, n, ld, name):
+def _tokens_arg(t, B, T, n, ld, name, dev):
     """Device pointer of a strided [B, T, n] projection (or [B, T, H, D], [B*T, n])
     whose tokens lie ld elements apart."""
     if t is None or t.__class__ is int:
         return t
     if t.dtype is not torch.bfloat16:
         _bad(f"{name} is {t.dtype}, not torch.bfloat16")
-    if t.get_device() != torch._C._cuda_getDevice():
+    if t.get_device() != dev:
         _bad(f"{name} is on {t.device}, not on the current CUDA device")
     shape, st = t.shape, t.stride()
     if len(shape) == 4 and shape[2] * shape[3] == n and (shape[2] == 1 or st[2] == shape[3]):
@@ -343,16 +354,18 @@ def kvc_qk_norm_rope(q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleav
                      inv_freq, pos, S, row0, q_out, k_act, v_act, stream=None):
     """Norm of queries and keys per head and position rotation, into q_out and
     the active layer's buffers (see include/kvc.h)."""
+    dev = _cur_dev()
     bf, ok = torch.bfloat16, B > 0 and T > 0 and H_q > 0 and H_kv > 0 and D > 0
     if ok:
-        q = _tokens_arg(q, B, T, H_q * D, q_ld, "q")
-        k = _tokens_arg(k, B, T, H_kv * D, k_ld, "k")
-        v = _tokens_arg(v, B, T, H_kv * D, v_ld, "v")
+        q = _tokens_arg(q, B, T, H_q * D, q_ld, "q", dev)
+        k = _tokens_arg(k, B, T, H_kv * D, k_ld, "k", dev)
+        v = _tokens_arg(v, B, T, H_kv * D, v_ld, "v", dev)
     _check(_lib.kvc_qk_norm_rope(
-        q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleaved, _arg(q_weight, bf, D, "q_weight"),
-        _arg(k_weight, bf, D, "k_weight"), eps, _arg(inv_freq, torch.float32, R // 2, "inv_freq"),
-        _arg(pos, torch.int32, B * T, "pos"), S, row0, _arg(q_out, bf, B * H_q * T * D, "q_out"),
-        _arg(k_act, bf, B * H_kv * S * D, "k_act"), _arg(v_act, bf, B * H_kv * S * D, "v_act"), _stream(stream)))
+        q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleaved, _arg(q_weight, bf, D, "q_weight", dev),
+        _arg(k_weight, bf, D, "k_weight", dev), eps, _arg(inv_freq, torch.float32, R // 2, "inv_freq", dev),
+        _arg(pos, torch.int32, B * T, "pos", dev), S, row0, _arg(q_out, bf, B * H_q * T * D, "q_out", dev),
+        _arg(k_act, bf, B * H_kv * S * D, "k_act", dev), _arg(v_act, bf, B * H_kv * S * D, "v_act", dev),
+        _stream(stream)))
 
 
 def kvc_q4_layout(H_kv, S, K_l, extra) -> ctypes.Array:
@@ -370,44 +383,50 @@ def _q4_rows(B, H_kv, slot_off):
 
 
 def kvc_gather_q4(k, v, idx, B, H_kv, S, D, K_l, slot_off, cache, pos, stream=None):
+    dev = _cur_dev()
     bf, i32 = torch.bfloat16, torch.int32
     so, n = _q4_rows(B, H_kv, slot_off)
-    _check(_lib.kvc_gather_q4(_arg(k, bf, B * H_kv * S * D, "k"), _arg(v, bf, B * H_kv * S * D, "v"),
-                              _arg(idx, i32, n, "idx"), B, H_kv, S, D, _host(K_l, ctypes.c_int32, H_kv, "K_l"), so,
-                              _arg(cache, torch.uint8, n * D * 9 // 8, "cache"), _arg(pos, i32, n, "pos"),
+    _check(_lib.kvc_gather_q4(_arg(k, bf, B * H_kv * S * D, "k", dev), _arg(v, bf, B * H_kv * S * D, "v", dev),
+                              _arg(idx, i32, n, "idx", dev), B, H_kv, S, D,
+                              _host(K_l, ctypes.c_int32, H_kv, "K_l"), so,
+                              _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev), _arg(pos, i32, n, "pos", dev),
                               _stream(stream)))
 
 
 def kvc_append_q4(k, v, pos_new, B, H_kv, T, D, slot_off, rows, cache, pos, stream=None):
+    dev = _cur_dev()
     bf, i32 = torch.bfloat16, torch.int32
     so, n = _q4_rows(B, H_kv, slot_off)
-    _check(_lib.kvc_append_q4(_arg(k, bf, B * H_kv * T * D, "k"), _arg(v, bf, B * H_kv * T * D, "v"),
-                              _arg(pos_new, i32, B * T, "pos_new"), B, H_kv, T, D, so,
-                              _arg(rows, i32, B * H_kv, "rows"), _arg(cache, torch.uint8, n * D * 9 // 8, "cache"),
-                              _arg(pos, i32, n, "pos"), _stream(stream)))
+    _check(_lib.kvc_append_q4(_arg(k, bf, B * H_kv * T * D, "k", dev), _arg(v, bf, B * H_kv * T * D, "v", dev),
+                              _arg(pos_new, i32, B * T, "pos_new", dev), B, H_kv, T, D, so,
+                              _arg(rows, i32, B * H_kv, "rows", dev),
+                              _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev),
+                              _arg(pos, i32, n, "pos", dev), _stream(stream)))
 
 
 def kvc_read_q4(cache, B, H_kv, D, slot_off, first, n_rows, k_out, v_out, stream=None, out_off=None):
+    dev = _cur_dev()
     so, n = _q4_rows(B, H_kv, slot_off)
     nr = _host(n_rows, ctypes.c_int32, H_kv, "n_rows")
     oo = _host(out_off, _I64, H_kv + 1, "out_off")
     t = B * (oo[H_kv] if oo is not None else sum(nr[:H_kv]) if nr is not None else 0) * D
-    _check(_lib.kvc_read_q4(_arg(cache, torch.uint8, n * D * 9 // 8, "cache"), B, H_kv, D, so,
-                            _arg(first, torch.int32, B * H_kv, "first"), nr, oo,
-                            _arg(k_out, torch.bfloat16, t, "k_out"), _arg(v_out, torch.bfloat16, t, "v_out"),
+    _check(_lib.kvc_read_q4(_arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev), B, H_kv, D, so,
+                            _arg(first, torch.int32, B * H_kv, "first", dev), nr, oo,
+                            _arg(k_out, torch.bfloat16, t, "k_out", dev), _arg(v_out, torch.bfloat16, t, "v_out", dev),
                             _stream(stream)))
 
 
 def kvc_compress_layer_q4(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, slot_off,
                           cache, pos, ws, ws_bytes=None, v_ready=None, stream=None):
     """kvc_compress_layer whose retained rows go into the 4-bit cache."""
+    dev = _cur_dev()
     bf = torch.bfloat16
     so, n = _q4_rows(B, H_kv, slot_off)
     _check(_lib.kvc_compress_layer_q4(
         N, layer, B, S, C, H_q, H_kv, D, W, _host(K_l, ctypes.c_int32, H_kv, "K_l"), sink, recent, pool_k, b_s,
-        _arg(q_win, bf, B * H_q * W * D, "q_win"), _arg(k, bf, B * H_kv * S * D, "k"),
-        _arg(v, bf, B * H_kv * S * D, "v"), so, _arg(cache, torch.uint8, n * D * 9 // 8, "cache"),
-        _arg(pos, torch.int32, n, "pos"), _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _event(v_ready),
+        _arg(q_win, bf, B * H_q * W * D, "q_win", dev), _arg(k, bf, B * H_kv * S * D, "k", dev),
+        _arg(v, bf, B * H_kv * S * D, "v", dev), so, _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev),
+        _arg(pos, torch.int32, n, "pos", dev), _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _event(v_ready),
         _stream(stream)))
 
 
@@ -420,13 +439,15 @@ def kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D) -> int:
 
 def kvc_attention_q4(q, cache, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot_off, out, lse, ws, ws_bytes=None,
                      stream=None):
+    dev = _cur_dev()
     bf, i32 = torch.bfloat16, torch.int32
     so, n = _q4_rows(B, H_kv, slot_off)
     nq = B * H_q * T
-    _check(_lib.kvc_attention_q4(_arg(q, bf, nq * D, "q"), _arg(cache, torch.uint8, n * D * 9 // 8, "cache"),
-                                 _arg(pos, i32, n, "pos"), _arg(rows, i32, B * H_kv, "rows"), extra,
-                                 _arg(q_pos, i32, B * T, "q_pos"), B, T, H_q, H_kv, D, so,
-                                 _arg(out, bf, nq * D, "out"), _arg(lse, torch.float32, nq, "lse"),
+    _check(_lib.kvc_attention_q4(_arg(q, bf, nq * D, "q", dev),
+                                 _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev),
+                                 _arg(pos, i32, n, "pos", dev), _arg(rows, i32, B * H_kv, "rows", dev), extra,
+                                 _arg(q_pos, i32, B * T, "q_pos", dev), B, T, H_q, H_kv, D, so,
+                                 _arg(out, bf, nq * D, "out", dev), _arg(lse, torch.float32, nq, "lse", dev),
                                  _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)))
 
 
