@@ -5,7 +5,7 @@
 // cache rows, both products on the tensor cores (tcgen05, fp16 operands, fp32
 // accumulators in tensor memory):
 //   S = Q K^T  (Q in tensor memory, K in shared memory)
-//   O += P V   (P in tensor memory, over the scores it came from; V in shared)
+//   O += P V   (P in tensor memory; V in shared)
 // 4*128*128*D flops a tile against 128*9D/8 bytes of cache: the products bound
 // it, 1024 cycles a tile at D = 128, if nothing else takes longer.  So:
 //  - Q and P come from tensor memory: with both operands in shared memory its
@@ -16,8 +16,8 @@
 //  - eight warps take the softmax: two threads a row, 64 scores each, against a
 //    reference that follows the running maximum only when a score passes it by
 //    2^8, so the output in tensor memory is hardly ever rescaled;
-//  - S is double buffered: the next tile's scores are computed while this one's
-//    weights are.
+//  - S is double buffered and free again as soon as the softmax has it in
+//    registers: the next scores are computed while this tile's weights are.
 // Orders inside a tile are free (the contraction of S runs over dims, that of O
 // over rows), so each operand is written in the order that falls out of the
 // block format and keeps 16-byte stores on different banks:
@@ -42,7 +42,7 @@ using scan::wait_bar;
 using scan::wait_bar_warp;
 
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kCodeWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kScoreWarp = kSoftWarps + kCodeWarps, kOutWarp = kScoreWarp + 1, kLoadWarp = kOutWarp + 1;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kRowsM = 128, kKeys = 128;
 constexpr int kTileBlocks = kKeys / q4::kRows;
@@ -50,7 +50,7 @@ constexpr int kRaw = 3;              // tiles of codes in flight
 // What the queries see of a tile's rows, in the tile's row order.  Tile i's is
 // written when the codes of tile i - 3 have been read, that is after K's stage
 // was free for tile i - 3, so the scores of tile i - 5 were done; those were
-// issued after the weights of tile i - 7 were there, the last reader.
+// issued after the softmax of tile i - 7, the last reader, had taken its scores.
 constexpr int kSeen = 8;
 struct alignas(16) Seen {
   int pos[kKeys];
@@ -59,7 +59,7 @@ struct alignas(16) Seen {
 };
 __host__ __device__ constexpr int raw_bytes(int D) { return kTileBlocks * q4::block_bytes(D); }
 constexpr uint32_t kCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;      // S: two buffers of 128 columns
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColP = 448;     // S: two buffers of 128 columns
 constexpr float kNoRef = -1.7e38f, kShift = 4.0f, kSlack = 8.0f;
 
 struct TcArgs {
@@ -77,10 +77,13 @@ struct TcArgs {
   Q4Slots s;
 };
 
-// s_full: the scores of a tile are there, and so K's stage is free.  o_done: a
-// tile's output is added up, and so V's stage is free.
+// s_full: the scores of a tile are there, and so K's stage is free.  s_free: the
+// softmax has them in registers (and has read what is seen of the tile).
+// p_full: the weights are there.  o_done: a tile's output is added up, and so
+// V's stage and the weights' columns are free.
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], q_full, drain;
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], v_full[2], s_full[2], s_free[2], p_full, o_done[2], q_full,
+      drain[2];
 };
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -257,10 +260,6 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
   }
 }
 
-// The warp that issues the products.  The scores of tile i + 1 go first, so
-// that its softmax can start while the output of tile i is added up.  Products
-// of one thread execute in order: tile i + 1's scores overwrite the weights of
-// tile i - 1 only after those have been used.
 // A product takes the tensor core 64 cycles, and arithmetic on descriptors
 // between products took twice that from the one thread that issues them: they
 // are made once, and steps add constants to them.
@@ -276,53 +275,65 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint3
         "r"(a), "l"(b), "r"(idesc)
         : "memory");
 }
-// The whole warp waits (a lane that polls alone costs 300 cycles a wait, the
-// warp together 20 to 90); lane 0 issues.
+// Two warps issue the products, one the scores, one the outputs: between its
+// tiles an issuer spends as long on waits and instruction fetches as its
+// products run, which the other's products cover.  Each waits as a whole (a
+// lane that polls alone costs 300 cycles a wait, the warp together 20 to 90);
+// lane 0 issues.
 template <int D>
-__device__ void mma_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, uint32_t tmem, int n,
-                         volatile int* abort_flag) {
-  constexpr uint32_t kIdS = tc::idesc_f16(kRowsM, kKeys), kIdO = tc::idesc_f16(kRowsM, D);
+__device__ void score_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t tmem, int n, volatile int* abort_flag) {
+  constexpr uint32_t kId = tc::idesc_f16(kRowsM, kKeys);
   constexpr uint64_t kStage = kKeys * D * 2 >> 4;              // descriptor units of 16 bytes
   const bool issues = (threadIdx.x & 31) == 0;
-  const uint64_t k0 = tc::desc_sw128(sK), v0 = tc::desc_sw128(sV);
+  const uint64_t k0 = tc::desc_sw128(sK);
   const auto wait = [&](uint64_t* bar, int phase) {
     return __all_sync(0xffffffffu, wait_bar_warp(smem_u32(bar), phase & 1, abort_flag, a.status, a.wait_limit));
   };
-  const auto scores = [&](int i) {
-    const int st = i & 1;
-    if (!wait(&bars->k_full[st], i >> 1)) return false;
-    tc::fence_after_sync();
-    if (issues) {
-      const uint64_t kd = k0 + st * kStage;
-      const uint32_t sd = tmem + kColS + st * kKeys;
+  if (wait(&bars->q_full, 0)) {
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      if (!wait(&bars->k_full[st], i >> 1) || !wait(&bars->s_free[st], (i >> 1) ^ 1)) break;
+      tc::fence_after_sync();
+      if (issues) {
+        const uint64_t kd = k0 + st * kStage;
+        const uint32_t sd = tmem + kColS + st * kKeys;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        mma_ta(sd, tmem + kColQ + s * 8, kd + (((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4), kIdS, s == 0);
-      tc::mma_commit(smem_u32(&bars->s_full[st]));
+        for (int s = 0; s < D / 16; ++s)
+          mma_ta(sd, tmem + kColQ + s * 8, kd + (((s >> 2) * (kKeys * 128) + (s & 3) * 32) >> 4), kId, s == 0);
+        tc::mma_commit(smem_u32(&bars->s_full[st]));
+      }
+      __syncwarp();
     }
-    __syncwarp();
-    return true;
+  }
+  if (issues) scan::drain_mma(smem_u32(&bars->drain[0]), a.status);
+  __syncwarp();
+}
+template <int D>
+__device__ void out_warp(const TcArgs& a, Bars* bars, uint32_t sV, uint32_t tmem, int n, volatile int* abort_flag) {
+  constexpr uint32_t kId = tc::idesc_f16(kRowsM, D);
+  constexpr uint64_t kStage = kKeys * D * 2 >> 4;
+  const bool issues = (threadIdx.x & 31) == 0;
+  const uint64_t v0 = tc::desc_sw128(sV);
+  const auto wait = [&](uint64_t* bar, int phase) {
+    return __all_sync(0xffffffffu, wait_bar_warp(smem_u32(bar), phase & 1, abort_flag, a.status, a.wait_limit));
   };
-  bool ok = wait(&bars->q_full, 0) && scores(0);
-  for (int i = 0; i < n && ok; ++i) {
+  for (int i = 0; i < n; ++i) {
     const int st = i & 1;
-    if (i + 1 < n && !scores(i + 1)) break;
-    if (!wait(&bars->v_full[st], i >> 1) || !wait(&bars->p_full[st], i >> 1)) break;
+    if (!wait(&bars->v_full[st], i >> 1) || !wait(&bars->p_full, i)) break;
     tc::fence_after_sync();
     if (issues) {
       const uint64_t vd = v0 + st * kStage;
-      const uint32_t pd = tmem + kColS + st * kKeys;
-      if (i == 0) mma_ta(tmem + kColO, pd, vd, kIdO, true);
-      else mma_ta(tmem + kColO, pd, vd, kIdO, false);
+      const uint32_t pd = tmem + kColP, od = tmem + kColO;
+      if (i == 0) mma_ta(od, pd, vd, kId, true);
+      else mma_ta(od, pd, vd, kId, false);
 #pragma unroll
       for (int s = 1; s < kKeys / 16; ++s)
-        mma_ta(tmem + kColO, pd + (s >> 2) * 64 + (s & 3) * 8, vd + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), kIdO,
-               false);
+        mma_ta(od, pd + s * 8, vd + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), kId, false);
       tc::mma_commit(smem_u32(&bars->o_done[st]));
     }
     __syncwarp();
   }
-  if (issues) scan::drain_mma(smem_u32(&bars->drain), a.status);
+  if (issues) scan::drain_mma(smem_u32(&bars->drain[1]), a.status);
   __syncwarp();
 }
 
@@ -349,14 +360,15 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       tc::mbar_init(smem_u32(&bars.v_full[i]), kCodeWarps);
       tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
       tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
-      tc::mbar_init(smem_u32(&bars.p_full[i]), kSoftWarps);
+      tc::mbar_init(smem_u32(&bars.s_free[i]), kSoftWarps);
+      tc::mbar_init(smem_u32(&bars.drain[i]), 1);
     }
+    tc::mbar_init(smem_u32(&bars.p_full), kSoftWarps);
     tc::mbar_init(smem_u32(&bars.q_full), kSoftWarps);
-    tc::mbar_init(smem_u32(&bars.drain), 1);
     s_abort = 0;
     tc::fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc::tmem_alloc(smem_u32(&s_tmem), kCols);
     tc::tmem_relinquish();
   }
@@ -393,10 +405,12 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     q_hi = __reduce_max_sync(0xffffffffu, q_hi);
     load_warp<D>(a, &bars, raw, s_seen, a.cache + row0 / q4::kRows * q4::block_bytes(D), a.pos + row0, n_rows, t0, t1,
                  q_lo, q_hi, &s_abort);
-  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
+  } else if (warp >= kSoftWarps && warp < kScoreWarp) {
     code_warp<D>(a, &bars, sK, sV, raw, s_seen, n, &s_abort);
-  } else if (warp == kMmaWarp) {
-    if (n > 0) mma_warp<D>(a, &bars, sK, sV, tmem, n, &s_abort);
+  } else if (warp == kScoreWarp) {
+    if (n > 0) score_warp<D>(a, &bars, sK, tmem, n, &s_abort);
+  } else if (warp == kOutWarp) {
+    if (n > 0) out_warp<D>(a, &bars, sV, tmem, n, &s_abort);
   } else {
     // ---- softmax: thread (row, half): dims and scores [half * .., ..)
     constexpr int kHalfD = D / 2;
@@ -473,6 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
           if (p.w < 0 || p.w > qp) x[4 * y + 3] = -INFINITY;
         }
       }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(smem_u32(&bars.s_free[st]));
       float m = x[0], m1 = x[1];     // two chains of three-input maxima
 #pragma unroll
       for (int y = 2; y < 62; y += 4) m = max3(m, x[y], x[y + 1]), m1 = max3(m1, x[y + 2], x[y + 3]);
@@ -480,15 +497,31 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       s_x[st][half][in] = m;
       asm volatile("bar.sync %0, 64;\n" ::"r"(2 + (warp & 3)) : "memory");
       m = fmaxf(m, s_x[st][half ^ 1][in]) * c2;
-      if (__any_sync(0xffffffffu, m > ref + (kSlack + kShift))) {
-        const float to = fmaxf(ref, m - kShift), f = ex2(ref - to);
+      const bool move = __any_sync(0xffffffffu, m > ref + (kSlack + kShift));
+      float f = 1.f;
+      if (move) {
+        const float to = fmaxf(ref, m - kShift);
+        f = ex2(ref - to);
         ref = to;
 #pragma unroll
         for (int y = 0; y < 2; ++y) sum2[y].x *= f, sum2[y].y *= f;
-        if (i > 0) {
-          ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[st ^ 1]), ((i - 1) >> 1) & 1, &s_abort,
-                                                            a.status, a.wait_limit));
-          tc::fence_after_sync();
+      }
+      const float2 c22 = make_float2(c2, c2), ref2 = make_float2(-ref, -ref);
+      uint32_t p[32];
+#pragma unroll
+      for (int z = 0; z < 32; ++z) {
+        const float2 e = fma2(make_float2(x[2 * z], x[2 * z + 1]), c22, ref2);
+        const float2 u = make_float2(ex2(e.x), ex2(e.y));
+        sum2[z & 1] = add2(sum2[z & 1], u);
+        p[z] = half2_of(u.x, u.y);
+      }
+      // the weights' columns, and the output for a new reference, are free when the
+      // last tile's output is added up
+      if (i > 0) {
+        ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[st ^ 1]), ((i - 1) >> 1) & 1, &s_abort,
+                                                          a.status, a.wait_limit));
+        tc::fence_after_sync();
+        if (move) {
 #pragma unroll
           for (int y = 0; y < kHalfD / 16; ++y) {
             float o[16];
@@ -502,23 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
           }
         }
       }
-      const float2 c22 = make_float2(c2, c2), ref2 = make_float2(-ref, -ref);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t p[16];
-#pragma unroll
-        for (int z = 0; z < 16; ++z) {
-          const float2 e = fma2(make_float2(x[32 * y + 2 * z], x[32 * y + 2 * z + 1]), c22, ref2);
-          const float2 u = make_float2(ex2(e.x), ex2(e.y));
-          sum2[z & 1] = add2(sum2[z & 1], u);
-          p[z] = half2_of(u.x, u.y);
-        }
-        tc::tmem_st16(s_at + 16 * y, p);
-      }
+      for (int y = 0; y < 2; ++y) tc::tmem_st16(tmem + lanes + kColP + half * 32 + 16 * y, p + 16 * y);
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(smem_u32(&bars.p_full[st]));
+      if (lane == 0) tc::mbar_arrive(smem_u32(&bars.p_full));
     }
     // ---- the row: both halves' sums, and this half's dims
     float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
@@ -527,8 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     sum = s_x[0][0][in] + s_x[0][1][in];
     if (n > 0) {
-      // a parity names the last phase but one as well; that one, the output of tile
-      // n - 3, was done before the scores of tile n - 1
       ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, &s_abort,
                                                         a.status, a.wait_limit));
       tc::fence_after_sync();
@@ -579,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kCols);
+  if (warp == kScoreWarp) tc::tmem_dealloc(tmem, kCols);
 }
 
 // One warp per query row: joins the parts of its splits, in order.
