@@ -47,6 +47,7 @@ constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kRowsM = 128, kKeys = 128;
 constexpr int kTileBlocks = kKeys / q4::kRows;
 constexpr int kRaw = 3;              // tiles of codes in flight
+constexpr int kV = 3;                // stages of V: freed a product later than K's two
 // What the queries see of a tile's rows, in the tile's row order.  Tile i's is
 // written when the codes of tile i - 3 have been read, that is after K's stage
 // was free for tile i - 3, so the scores of tile i - 5 were done; those were
@@ -82,7 +83,7 @@ struct TcArgs {
 // p_full: the weights are there.  o_done: a tile's output is added up, and so
 // V's stage and the weights' columns are free.
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], v_full[2], s_full[2], s_free[2], p_full, o_done[2], q_full,
+  uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], s_full[2], s_free[2], p_full, o_done[kV], q_full,
       drain[2];
 };
 
@@ -92,6 +93,17 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
 }
 __device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Waits of a whole warp for several barriers at once: each look at a barrier
+// takes about as long alone as together with the others.
+__device__ __forceinline__ bool wait3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2,
+                                      volatile int* abort_flag, int* status, uint32_t limit) {
+  const bool d0 = tc::mbar_try_wait(b0, p0), d1 = tc::mbar_try_wait(b1, p1), d2 = tc::mbar_try_wait(b2, p2);
+  if (__all_sync(0xffffffffu, d0 && d1 && d2)) return true;
+  return __all_sync(0xffffffffu, wait_bar_warp(b0, p0, abort_flag, status, limit) &&
+                                     wait_bar_warp(b1, p1, abort_flag, status, limit) &&
+                                     wait_bar_warp(b2, p2, abort_flag, status, limit));
 }
 
 // Two fp32 operations in one instruction.
@@ -185,10 +197,10 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
   constexpr int kB = D / 8;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps, r = lane >> 2, j = lane & 3;
   for (int i = 0; i < n; ++i) {
-    const int st = i & 1, rs = i % kRaw;
+    const int st = i & 1, rs = i % kRaw, vst = i % kV;
     const uint32_t ph = ((i >> 1) & 1) ^ 1;
-    if (!wait_bar_warp(smem_u32(&bars->raw_full[rs]), (i / kRaw) & 1, abort_flag, a.status, a.wait_limit) ||
-        !wait_bar_warp(smem_u32(&bars->s_full[st]), ph, abort_flag, a.status, a.wait_limit))
+    if (!wait3(smem_u32(&bars->raw_full[rs]), (i / kRaw) & 1, smem_u32(&bars->s_full[st]), ph,
+               smem_u32(&bars->o_done[vst]), ((i / kV) & 1) ^ 1, abort_flag, a.status, a.wait_limit))
       return;
     const uint8_t* rec = raw + rs * raw_bytes(D) + 2 * w * q4::block_bytes(D);
     // ---- keys
@@ -216,9 +228,6 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
         }
       }
     }
-    tc::fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(smem_u32(&bars->k_full[st]));
     // ---- values.  A row that no query sees may hold anything: its values count as zeros
     uint32_t code[2][2][D / 32], s2[2][2];
     const uint32_t some = seen[i % kSeen].some[w];
@@ -235,10 +244,7 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
         read_codes<kB>(p + q4::v_codes(D) + s * 4 * D + lane * kB, code[b][s]);
       }
     }
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(smem_u32(&bars->raw_empty[rs]));
-    if (!wait_bar_warp(smem_u32(&bars->o_done[st]), ph, abort_flag, a.status, a.wait_limit)) return;
-    const uint32_t v_at = (sV + st * (kKeys * D * 2) + (w >> 1) * (D * 128) + r * (D / 8) * 128) |
+    const uint32_t v_at = (sV + vst * (kKeys * D * 2) + (w >> 1) * (D * 128) + r * (D / 8) * 128) |
                           ((4 * (r & 1)) * 128 | (((w & 1) * 4 + j) ^ (4 * (r & 1))) << 4);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
@@ -256,7 +262,10 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
     }
     tc::fence_proxy_async();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(smem_u32(&bars->v_full[st]));
+    if (lane == 0) {
+      tc::mbar_arrive(smem_u32(&bars->kv_full[st]));
+      tc::mbar_arrive(smem_u32(&bars->raw_empty[rs]));
+    }
   }
 }
 
@@ -292,7 +301,7 @@ __device__ void score_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t tm
   if (wait(&bars->q_full, 0)) {
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
-      if (!wait(&bars->k_full[st], i >> 1) || !wait(&bars->s_free[st], (i >> 1) ^ 1)) break;
+      if (!wait(&bars->kv_full[st], i >> 1) || !wait(&bars->s_free[st], (i >> 1) ^ 1)) break;
       tc::fence_after_sync();
       if (issues) {
         const uint64_t kd = k0 + st * kStage;
@@ -319,17 +328,17 @@ __device__ void out_warp(const TcArgs& a, Bars* bars, uint32_t sV, uint32_t tmem
   };
   for (int i = 0; i < n; ++i) {
     const int st = i & 1;
-    if (!wait(&bars->v_full[st], i >> 1) || !wait(&bars->p_full, i)) break;
+    if (!wait(&bars->kv_full[st], i >> 1) || !wait(&bars->p_full, i)) break;
     tc::fence_after_sync();
     if (issues) {
-      const uint64_t vd = v0 + st * kStage;
+      const uint64_t vd = v0 + (i % kV) * kStage;
       const uint32_t pd = tmem + kColP, od = tmem + kColO;
       if (i == 0) mma_ta(od, pd, vd, kId, true);
       else mma_ta(od, pd, vd, kId, false);
 #pragma unroll
       for (int s = 1; s < kKeys / 16; ++s)
         mma_ta(od, pd + s * 8, vd + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), kId, false);
-      tc::mma_commit(smem_u32(&bars->o_done[st]));
+      tc::mma_commit(smem_u32(&bars->o_done[i % kV]));
     }
     __syncwarp();
   }
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
 
   const uint32_t sK = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sV = sK + 2 * kKeys * D * 2;
-  uint8_t* raw = smem_raw + (sV + 2 * kKeys * D * 2 - smem_u32(smem_raw));
+  uint8_t* raw = smem_raw + (sV + kV * kKeys * D * 2 - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) {
@@ -356,13 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       tc::mbar_init(smem_u32(&bars.raw_empty[i]), kCodeWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(smem_u32(&bars.k_full[i]), kCodeWarps);
-      tc::mbar_init(smem_u32(&bars.v_full[i]), kCodeWarps);
+      tc::mbar_init(smem_u32(&bars.kv_full[i]), kCodeWarps);
       tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
-      tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
       tc::mbar_init(smem_u32(&bars.s_free[i]), kSoftWarps);
       tc::mbar_init(smem_u32(&bars.drain[i]), 1);
     }
+    for (int i = 0; i < kV; ++i) tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
     tc::mbar_init(smem_u32(&bars.p_full), kSoftWarps);
     tc::mbar_init(smem_u32(&bars.q_full), kSoftWarps);
     s_abort = 0;
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       // the weights' columns, and the output for a new reference, are free when the
       // last tile's output is added up
       if (i > 0) {
-        ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[st ^ 1]), ((i - 1) >> 1) & 1, &s_abort,
+        ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(i - 1) % kV]), ((i - 1) / kV) & 1, &s_abort,
                                                           a.status, a.wait_limit));
         tc::fence_after_sync();
         if (move) {
@@ -549,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     asm volatile("bar.sync 1, 256;\n" ::: "memory");
     sum = s_x[0][0][in] + s_x[0][1][in];
     if (n > 0) {
-      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(n - 1) & 1]), ((n - 1) >> 1) & 1, &s_abort,
+      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(n - 1) % kV]), ((n - 1) / kV) & 1, &s_abort,
                                                         a.status, a.wait_limit));
       tc::fence_after_sync();
     }
@@ -664,7 +672,7 @@ cudaError_t launch_attend_q4_tc(const __nv_bfloat16* q, const uint8_t* cache, co
   a.wait_limit = wait_limit_polls();
   a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
   a.s = slots;
-  const size_t smem = 4 * (size_t)kKeys * D * 2 + kRaw * (size_t)raw_bytes(D) + 1024;
+  const size_t smem = (2 + kV) * (size_t)kKeys * D * 2 + kRaw * (size_t)raw_bytes(D) + 1024;
   auto* kern = D == 128 ? kvc_attend_q4_tc_kernel<128> : kvc_attend_q4_tc_kernel<64>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e == cudaSuccess)
