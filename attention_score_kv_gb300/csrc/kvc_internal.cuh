@@ -209,8 +209,6 @@ cudaError_t launch_read_q4(const uint8_t* cache, int B, int D, const Q4Slots& sl
 // attention over the 4-bit cache: scratch and launches of one call
 struct Q4AttendPlan {
   int P;             // key ranges
-  int tiles;         // tiles of query rows per KV head
-  int64_t slots;     // partial results per tile: P + B * H_kv
   size_t off_o;      // offsets in the workspace: partial outputs,
   size_t off_place;  // the heads' places
   size_t total;

@@ -15,7 +15,7 @@
 // the copies need no barrier.  The codes come in fragment order, so they go
 // through two conversions straight into mma operands:
 //   S^T (16 rows x 8 queries) = K Q^T,   O^T (D x 8 queries) += V^T P^T,
-// with the queries as the narrow N side (8 columns), so that no row of the
+// with up to 8 query rows as the narrow N side, so that no row of the
 // matrix instruction is wasted when a KV head has 4 or 5 query heads.  P goes
 // from accumulator to operand layout with movmatrix.
 // Numerics: codes times scales are exact in fp16; q is scaled by a power of
@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kCols = 8;             // query rows per KV head: the narrow side of the products
 constexpr int kMinBlocks = kWarps;   // blocks of 16 rows a CTA takes at least
 constexpr float kNoRef = -1.7e38f;   // reference of a query that has seen no row
 constexpr float kShift = 4.0f;       // weights are kept as 2^(x - max + kShift)
@@ -46,11 +47,11 @@ struct AttendArgs {
   const int32_t *pos, *rows, *q_pos;
   __nv_bfloat16* out;
   float* lse;
-  float2* part_ml;                   // [row tiles][slots][8 NT] maximum, sum
-  float* part_o;                     // [row tiles][slots][8 NT][D]
+  float2* part_ml;                   // [P + B * H_kv][R] maximum, sum: part of range c and head bh at c + bh
+  float* part_o;                     // [..][R][D], dims in the order of o_stride's comment
   int* place;                        // [B * H_kv] blocks before each head, then all blocks
   int* status;
-  int B, T, H_q, G, extra, P, slots;
+  int B, T, G, extra, P;
   uint32_t inv_h;                    // ceil(2^32 / H_kv): bh / H_kv as a product (bh < 2^24, H_kv <= 128)
   float scale;                       // log2(e) / sqrt(D)
   Q4Slots s;
@@ -236,35 +237,34 @@ __device__ __forceinline__ bool segment_at(const AttendArgs& a, const SlotTable&
   return true;
 }
 
-// Shared memory: the joint outputs of 8 columns, then the warps' rings.
+// Shared memory: the warps' outputs, then their rings.
 // Position d' = 16 m + 2 r + e of a row there holds dim r*D/8 + 2m + e: a lane
 // of the output fragments stores pairs side by side with its neighbours', and
 // rows D + 4 apart keep the four columns of a store on different banks.
 __host__ __device__ constexpr int o_stride(int D) { return D + 4; }
-__host__ __device__ constexpr int o_bytes(int D, int cols) { return kWarps * cols * o_stride(D) * (int)sizeof(float); }
+__host__ __device__ constexpr int o_bytes(int D, int R) { return kWarps * R * o_stride(D) * (int)sizeof(float); }
 template <int D>
 __device__ __forceinline__ int dim_of(int at) { return (at >> 1 & 7) * (D / 8) + (at >> 4) * 2 + (at & 1); }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kernel(const __grid_constant__ AttendArgs a) {
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int KS = D / 16;         // k-steps of the scores, m-tiles of the output
   constexpr int kB = D / 8;
   extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ float2 s_ml[kWarps][8 * NT];
+  __shared__ float2 s_ml[kWarps][kCols];
   __shared__ SlotTable slots;
   fill_slots(a, slots);
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
-  const int R = a.G * a.T, row_base = blockIdx.y * 8 * NT;
-  const int cols = min(8, R);        // columns of an n-tile that may hold queries
-  float* s_o = reinterpret_cast<float*>(dyn);              // [kWarps][cols][o_stride]
-  uint8_t* ring = dyn + o_bytes(D, cols) + warp * kStages * stage_bytes(D);
+  const int R = a.G * a.T;           // query rows, at most kCols
+  float* s_o = reinterpret_cast<float*>(dyn);              // [kWarps][R][o_stride]
+  uint8_t* ring = dyn + o_bytes(D, R) + warp * kStages * stage_bytes(D);
   const uint32_t ring_u = smem_u32(ring);
 
   // the CTA's range [f0, f1) of the blocks laid end to end
-  const Place pl = find_place(a, slots, blockIdx.x, blockIdx.x == 0 && blockIdx.y == 0);
+  const Place pl = find_place(a, slots, blockIdx.x, blockIdx.x == 0);
   const int L = range_blocks(pl.total, a.P);
   const int f0 = (int)min((int64_t)blockIdx.x * L, (int64_t)pl.total), f1 = min(f0 + L, pl.total);
   Segment g;
@@ -287,72 +287,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
     const int bh = g.bh, n_rows = g.n_rows;
     const int b = batch_of(a, bh);
 
-    // queries: column n = lane / 4 of each n-tile, quarter j of its dims
-    uint32_t qf[NT][KS][2];
-    float c2[NT][2];                 // factor from accumulator to log2 units, columns 2j and 2j + 1
-    int qp[NT][2];                   // their positions
-    int q_lo = INT32_MAX, q_hi = -1;
-    uint32_t w[NT][D / 8];
+    // queries: column n = lane / 4, quarter j of its dims
+    uint32_t w[D / 8];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row_base + nt * 8 + r;
+    for (int i = 0; i < D / 8; ++i) w[i] = 0;
+    if (r < R) {
+      const uint4* p = reinterpret_cast<const uint4*>(a.q + ((int64_t)bh * R + r) * D + j * (D / 4));
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) w[nt][i] = 0;
-      if (row < R) {
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + ((int64_t)bh * R + row) * D + j * (D / 4));
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 v = __ldg(p + i);
-          w[nt][4 * i] = v.x, w[nt][4 * i + 1] = v.y, w[nt][4 * i + 2] = v.z, w[nt][4 * i + 3] = v.w;
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int rr = row_base + nt * 8 + 2 * j + y;
-        qp[nt][y] = rr < R ? __ldg(a.q_pos + (int64_t)b * a.T + rr % a.T) : -1;
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 v = __ldg(p + i);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
     }
+    int qp[2];                       // positions of columns 2j and 2j + 1
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      qp[y] = 2 * j + y < R ? __ldg(a.q_pos + (int64_t)b * a.T + (2 * j + y) % a.T) : -1;
     if (!started)                    // behind the queries' loads, which the blocks' traffic would hold up
       for (int i = 0; i < kStages - 1; ++i) fetch(g, i);
     started = true;
+    uint32_t mx = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint32_t mx = 0;
+    for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+    mx = max(mx & 0xffffu, mx >> 16);
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // scale by the power of two that brings the row's largest value into [1, 2)
+    const uint32_t e = mx >> 7, ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
+    const float down = __uint_as_float((254u - ee) << 23);
+    const float c = __uint_as_float(ee << 23) * a.scale;
+    uint32_t qf[KS][2];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, w[nt][i] & 0x7fff7fffu);
-      mx = max(mx & 0xffffu, mx >> 16);
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // scale by the power of two that brings the largest value into [1, 2)
-      const uint32_t e = mx >> 7;
-      const uint32_t ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
-      const float down = __uint_as_float((254u - ee) << 23);
-      const float c = __uint_as_float(ee << 23) * a.scale;
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+      for (int y = 0; y < 2; ++y)
+        qf[s][y] = pack_half2(__uint_as_float(q4::bf16_of(w, 2 * s + y) << 16) * down,
+                              __uint_as_float(q4::bf16_of(w, kB + 2 * s + y) << 16) * down);
+    float c2[2];                     // factor from accumulator to log2 units, columns 2j and 2j + 1
+    int q_lo = INT32_MAX, q_hi = -1;
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          qf[nt][s][y] = pack_half2(__uint_as_float(q4::bf16_of(w[nt], 2 * s + y) << 16) * down,
-                                    __uint_as_float(q4::bf16_of(w[nt], kB + 2 * s + y) << 16) * down);
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        c2[nt][y] = __shfl_sync(0xffffffffu, c, (2 * j + y) * 4);
-        if (row_base + nt * 8 + 2 * j + y < R) q_lo = min(q_lo, qp[nt][y]), q_hi = max(q_hi, qp[nt][y]);
-      }
+    for (int y = 0; y < 2; ++y) {
+      c2[y] = __shfl_sync(0xffffffffu, c, (2 * j + y) * 4);
+      if (2 * j + y < R) q_lo = min(q_lo, qp[y]), q_hi = max(q_hi, qp[y]);
     }
     q_lo = __reduce_min_sync(0xffffffffu, q_lo);
     q_hi = __reduce_max_sync(0xffffffffu, q_hi);
 
-    float o[NT][KS][4], ref[NT][2], sum[NT][2];
+    float o[KS][4], ref[2] = {kNoRef, kNoRef}, sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int m = 0; m < KS; ++m)
 #pragma unroll
-      for (int m = 0; m < KS; ++m)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) o[nt][m][y] = 0.f;
-#pragma unroll
-      for (int y = 0; y < 2; ++y) ref[nt][y] = kNoRef, sum[nt][y] = 0.f;
-    }
+      for (int y = 0; y < 4; ++y) o[m][y] = 0.f;
 
     const int mine = (g.cnt - warp + kWarps - 1) / kWarps;       // blocks of this warp (may be <= 0)
     for (int i = 0; i < mine; ++i) {
@@ -371,43 +356,32 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
         vs = *reinterpret_cast<const uint32_t*>(st + q4::v_scales(D) + ((r >> 1) * 4 + j) * 4);
       }
       const int2 xp = *reinterpret_cast<const int2*>(st + q4::block_bytes(D) + lane * 8);
-      // ---- scores
-      float acc[NT][4], odd[NT][4];  // two chains of products, half as long
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) acc[nt][y] = odd[nt][y] = 0.f;
+      // ---- scores, in two chains of products, half as long
+      float acc[4] = {}, odd[4] = {};
       const uint32_t ks[2] = {q4::scales_to_half2((uint16_t)ksc), q4::scales_to_half2((uint16_t)(ksc >> 16))};
       const Codes<kB / 4> kc0 = load_codes<kB>(st + q4::k_codes(D) + lane * kB);
       const Codes<kB / 4> kc1 = load_codes<kB>(st + q4::k_codes(D) + 4 * D + lane * kB);
 #pragma unroll
-      for (int w = 0; w < kB / 4; ++w) {
+      for (int x = 0; x < kB / 4; ++x) {
         uint32_t ka[4], kb[4];
-        q4::codes_to_half2(kc0.w[w], ka);
-        q4::codes_to_half2(kc1.w[w], kb);
+        q4::codes_to_half2(kc0.w[x], ka);
+        q4::codes_to_half2(kc1.w[x], kb);
 #pragma unroll
         for (int y = 0; y < 4; ++y) ka[y] = q4::mul_half2(ka[y], ks[0]), kb[y] = q4::mul_half2(kb[y], ks[1]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(acc[nt], ka[0], kb[0], ka[1], kb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          mma_f16(odd[nt], ka[2], kb[2], ka[3], kb[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
-        }
+        mma_f16(acc, ka[0], kb[0], ka[1], kb[1], qf[2 * x][0], qf[2 * x][1]);
+        mma_f16(odd, ka[2], kb[2], ka[3], kb[3], qf[2 * x + 1][0], qf[2 * x + 1][1]);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int y = 0; y < 4; ++y) acc[y] += odd[y];
+      // ---- mask: acc[y], acc[2 + y] are rows r, r + 8 against column 2j + y
+      const int row = blk * q4::kRows + r;
+      const bool in0 = row < n_rows && xp.x >= 0, in1 = row + 8 < n_rows && xp.y >= 0;
+      if (!__all_sync(0xffffffffu, in0 && xp.x <= q_lo && in1 && xp.y <= q_lo)) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) acc[nt][y] += odd[nt][y];
-      // ---- mask: acc[nt][y], acc[nt][2 + y] are rows r, r + 8 against column 2j + y
-      const bool in0 = blk * q4::kRows + r < n_rows && xp.x >= 0, in1 = blk * q4::kRows + r + 8 < n_rows && xp.y >= 0;
-      const bool clear = in0 && xp.x <= q_lo && in1 && xp.y <= q_lo;
-      if (!__all_sync(0xffffffffu, clear)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if (!in0 || xp.x > qp[nt][y]) acc[nt][y] = -INFINITY;
-            if (!in1 || xp.y > qp[nt][y]) acc[nt][2 + y] = -INFINITY;
-          }
+        for (int y = 0; y < 2; ++y) {
+          if (!in0 || xp.x > qp[y]) acc[y] = -INFINITY;
+          if (!in1 || xp.y > qp[y]) acc[2 + y] = -INFINITY;
+        }
         // a row that no query sees may hold anything: its values count as zeros
         const uint32_t see0 = __ballot_sync(0xffffffffu, in0 && xp.x <= q_hi);
         const uint32_t see1 = __ballot_sync(0xffffffffu, in1 && xp.y <= q_hi);
@@ -419,57 +393,44 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
         vs &= keep;
       }
       // ---- weights
-      uint32_t pf[NT][2];
       bool above = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          above |= fmaxf(acc[nt][y], acc[nt][2 + y]) * c2[nt][y] > ref[nt][y] + (kSlack + kShift);
+      for (int y = 0; y < 2; ++y) above |= fmaxf(acc[y], acc[2 + y]) * c2[y] > ref[y] + (kSlack + kShift);
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int y = 0; y < 2; ++y) {
+          float m = fmaxf(acc[y], acc[2 + y]) * c2[y];
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          const float next = fmaxf(ref[y], m - kShift);
+          const float f = ex2(ref[y] - next);
+          ref[y] = next;
+          sum[y] *= f;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float m = fmaxf(acc[nt][y], acc[nt][2 + y]) * c2[nt][y];
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float next = fmaxf(ref[nt][y], m - kShift);
-            const float f = ex2(ref[nt][y] - next);
-            ref[nt][y] = next;
-            sum[nt][y] *= f;
-#pragma unroll
-            for (int m2 = 0; m2 < KS; ++m2) o[nt][m2][y] *= f, o[nt][m2][2 + y] *= f;
-          }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          p[y] = ex2(fmaf(acc[nt][y], c2[nt][y & 1], -ref[nt][y & 1]));
-          sum[nt][y & 1] += p[y];
+          for (int m2 = 0; m2 < KS; ++m2) o[m2][y] *= f, o[m2][2 + y] *= f;
         }
-        pf[nt][0] = transpose8(pack_half2(p[0], p[1]));
-        pf[nt][1] = transpose8(pack_half2(p[2], p[3]));
       }
+      float p[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        p[y] = ex2(fmaf(acc[y], c2[y & 1], -ref[y & 1]));
+        sum[y & 1] += p[y];
+      }
+      const uint32_t pf0 = transpose8(pack_half2(p[0], p[1])), pf1 = transpose8(pack_half2(p[2], p[3]));
       // ---- output
       const Codes<kB / 4> vc0 = load_codes<kB>(st + q4::v_codes(D) + lane * kB);
       const Codes<kB / 4> vc1 = load_codes<kB>(st + q4::v_codes(D) + 4 * D + lane * kB);
       const uint32_t vs2[2] = {q4::scales_to_half2((uint16_t)vs), q4::scales_to_half2((uint16_t)(vs >> 16))};
 #pragma unroll
-      for (int w = 0; w < kB / 4; ++w) {
+      for (int x = 0; x < kB / 4; ++x) {
         uint32_t va[4], vb[4];
-        q4::codes_to_half2(vc0.w[w], va);
-        q4::codes_to_half2(vc1.w[w], vb);
+        q4::codes_to_half2(vc0.w[x], va);
+        q4::codes_to_half2(vc1.w[x], vb);
 #pragma unroll
         for (int y = 0; y < 4; ++y) va[y] = q4::mul_half2(va[y], vs2[0]), vb[y] = q4::mul_half2(vb[y], vs2[1]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(o[nt][2 * w], va[0], va[1], vb[0], vb[1], pf[nt][0], pf[nt][1]);
-          mma_f16(o[nt][2 * w + 1], va[2], va[3], vb[2], vb[3], pf[nt][0], pf[nt][1]);
-        }
+        mma_f16(o[2 * x], va[0], va[1], vb[0], vb[1], pf0, pf1);
+        mma_f16(o[2 * x + 1], va[2], va[3], vb[2], vb[3], pf0, pf1);
       }
     }
 
@@ -481,52 +442,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
     if (more)
       for (int i = 0; i < kStages - 1; ++i) fetch(next, i);
 
-    // ---- join the warps: rows of the range that warp w saw, in warp order
+    // ---- join the warps, in warp order
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float v = sum[nt][y];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (r == 0) s_ml[warp][nt * 8 + 2 * j + y] = make_float2(ref[nt][y], v);
-      }
-    __syncthreads();
-    const int64_t slot = (int64_t)blockIdx.y * a.slots + blockIdx.x + bh;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int col = 2 * j + y;
-        if (col >= cols) continue;
-        float top = s_ml[0][nt * 8 + col].x;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][nt * 8 + col].x);
-        const float f = ex2(ref[nt][y] - top);
-        float* to = s_o + (warp * cols + col) * o_stride(D) + 2 * r;
-#pragma unroll
-        for (int m = 0; m < KS; ++m)
-          *reinterpret_cast<float2*>(to + 16 * m) = make_float2(o[nt][m][y] * f, o[nt][m][2 + y] * f);
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < cols * (D / 4); i += kThreads) {
-        const int col = i / (D / 4), at = i % (D / 4) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(s_o + (w * cols + col) * o_stride(D) + at);
-          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        }
-        *reinterpret_cast<float4*>(a.part_o + (slot * 8 * NT + nt * 8 + col) * D + at) = v;
-      }
-      if (nt + 1 < NT) __syncthreads();
+    for (int y = 0; y < 2; ++y) {
+      float v = sum[y];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      if (r == 0) s_ml[warp][2 * j + y] = make_float2(ref[y], v);
     }
-    if (threadIdx.x < 8 * NT) {
+    __syncthreads();
+    const int64_t slot = (int64_t)blockIdx.x + bh;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int col = 2 * j + y;
+      if (col >= R) continue;
+      float top = s_ml[0][col].x;
+#pragma unroll
+      for (int x = 1; x < kWarps; ++x) top = fmaxf(top, s_ml[x][col].x);
+      const float f = ex2(ref[y] - top);
+      float* to = s_o + (warp * R + col) * o_stride(D) + 2 * r;
+#pragma unroll
+      for (int m = 0; m < KS; ++m) *reinterpret_cast<float2*>(to + 16 * m) = make_float2(o[m][y] * f, o[m][2 + y] * f);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
+      const int col = i / (D / 4), at = i % (D / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) {
+        const float4 z = *reinterpret_cast<const float4*>(s_o + (x * R + col) * o_stride(D) + at);
+        v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
+      }
+      *reinterpret_cast<float4*>(a.part_o + (slot * R + col) * D + at) = v;
+    }
+    if (threadIdx.x < R) {
       float top = kNoRef, l = 0.f;
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][threadIdx.x].x);
-      for (int w = 0; w < kWarps; ++w) l += s_ml[w][threadIdx.x].y * ex2(s_ml[w][threadIdx.x].x - top);
-      a.part_ml[slot * 8 * NT + threadIdx.x] = make_float2(top, l);
+      for (int x = 0; x < kWarps; ++x) top = fmaxf(top, s_ml[x][threadIdx.x].x);
+      for (int x = 0; x < kWarps; ++x) l += s_ml[x][threadIdx.x].y * ex2(s_ml[x][threadIdx.x].x - top);
+      a.part_ml[slot * R + threadIdx.x] = make_float2(top, l);
     }
     __syncthreads();
     g = next;
@@ -538,24 +492,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kvc_attend_q4_kerne
 // four sums are added in warp order.
 constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(const __grid_constant__ AttendArgs a,
-                                                                             int tile) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int V = D / 32;          // values of a lane
   __shared__ float s_v[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = a.B * a.s.H_kv;
-  const int R = a.G * a.T, bh = blockIdx.x / R, row = blockIdx.x - bh * R, ty = row / tile, in = row - ty * tile;
+  const int R = a.G * a.T, bh = blockIdx.x / R, row = blockIdx.x - bh * R;
   const int total = a.place[BH], before = a.place[bh], after = a.place[bh + 1];   // place[BH] is the total
   const int L = range_blocks(total, a.P);
   const int c0 = before / L;
   const int n = after > before ? (after - 1) / L - c0 + 1 : 0;
-  const int64_t slot0 = (int64_t)ty * a.slots + bh + c0;
-  const float2* ml = a.part_ml + slot0 * tile + in;
-  const float* po = a.part_o + (slot0 * tile + in) * D + lane * V;
+  const int64_t slot0 = bh + c0;
+  const float2* ml = a.part_ml + slot0 * R + row;
+  const float* po = a.part_o + (slot0 * R + row) * D + lane * V;
   float top = kNoRef;
-  for (int c = lane; c < n; c += 32) top = fmaxf(top, ml[(int64_t)c * tile].x);
+  for (int c = lane; c < n; c += 32) top = fmaxf(top, ml[(int64_t)c * R].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float l = 0.f, v[V];
@@ -563,10 +516,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(con
   for (int i = 0; i < V; ++i) v[i] = 0.f;
 #pragma unroll 4
   for (int c = warp; c < n; c += kJoinWarps) {
-    const float2 x = ml[(int64_t)c * tile];
+    const float2 x = ml[(int64_t)c * R];
     const float f = ex2(x.x - top);
     l = fmaf(x.y, f, l);
-    const float* p = po + (int64_t)c * tile * D;
+    const float* p = po + (int64_t)c * R * D;
     if constexpr (V == 4) {
       const float4 y = *reinterpret_cast<const float4*>(p);
       v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]), v[2] = fmaf(y.z, f, v[2]), v[3] = fmaf(y.w, f, v[3]);
@@ -592,18 +545,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(con
   if (a.lse && threadIdx.x == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
-int tile_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
-
 }  // namespace
+
+bool attend_q4_on_tc(int H_q, int H_kv, int T) { return (int64_t)(H_q / H_kv) * T > kCols; }
 
 Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D) {
   Q4AttendPlan p{};
-  const int R = H_q / H_kv * T;
-  const int tr = tile_rows(R);
-  p.tiles = (R + tr - 1) / tr;
   p.P = std::max(num_sms(), 1) * 2;
-  p.slots = (int64_t)p.P + (int64_t)B * H_kv;
-  const size_t rows = (size_t)p.tiles * (size_t)p.slots * (size_t)tr;
+  const size_t rows = ((size_t)p.P + (size_t)B * H_kv) * (size_t)(H_q / H_kv * T);
   p.off_o = (rows * sizeof(float2) + 255) / 256 * 256;
   p.off_place = p.off_o + rows * D * sizeof(float);
   p.total = p.off_place + ((size_t)B * H_kv + 1) * sizeof(int);
@@ -621,22 +570,17 @@ cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_o);
   a.place = reinterpret_cast<int*>(static_cast<char*>(ws) + p.off_place);
   a.status = status_word_ptr();
-  a.B = B, a.T = T, a.H_q = H_q, a.G = H_q / H, a.extra = extra, a.P = p.P, a.slots = (int)p.slots;
+  a.B = B, a.T = T, a.G = H_q / H, a.extra = extra, a.P = p.P;
   a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
   a.inv_h = (uint32_t)(((1ull << 32) + H - 1) / H);
   a.s = slots;
-  const int tr = tile_rows(R);
-  const size_t smem = o_bytes(D, std::min(8, R)) + kWarps * kStages * stage_bytes(D);
-  void (*scan)(AttendArgs);
-  if (D == 128)
-    scan = tr == 8 ? kvc_attend_q4_kernel<128, 1> : tr == 16 ? kvc_attend_q4_kernel<128, 2> : kvc_attend_q4_kernel<128, 4>;
-  else
-    scan = tr == 8 ? kvc_attend_q4_kernel<64, 1> : tr == 16 ? kvc_attend_q4_kernel<64, 2> : kvc_attend_q4_kernel<64, 4>;
+  const size_t smem = o_bytes(D, R) + kWarps * kStages * stage_bytes(D);
+  auto* scan = D == 128 ? kvc_attend_q4_kernel<128> : kvc_attend_q4_kernel<64>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(scan), smem);
-  if (e == cudaSuccess) e = launch_pdl(scan, dim3(p.P, p.tiles), dim3(kThreads), smem, st, a);
+  if (e == cudaSuccess) e = launch_pdl(scan, dim3(p.P), dim3(kThreads), smem, st, a);
   if (e != cudaSuccess) return e;
   e = launch_pdl(D == 128 ? kvc_attend_q4_join_kernel<128> : kvc_attend_q4_join_kernel<64>, dim3((unsigned)(B * H * R)),
-                 dim3(kJoinWarps * 32), 0, st, a, tr);
+                 dim3(kJoinWarps * 32), 0, st, a);
   note_launches(2);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -359,6 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   const uint32_t sV = sK + 2 * kKeys * D * 2;
   uint8_t* raw = smem_raw + (sV + kV * kKeys * D * 2 - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.x / a.tiles, tile = blockIdx.x - bh * a.tiles;
+  // warps of the softmax that have query rows; nothing reads what the products make of
+  // the others' rows, whatever tensor memory holds there
+  const int live_quarters = min(4, (a.R - tile * kRowsM + 31) / 32), live_warps = 2 * live_quarters;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) {
       tc::mbar_init(smem_u32(&bars.raw_full[i]), 1);
@@ -367,12 +371,12 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(smem_u32(&bars.kv_full[i]), kCodeWarps);
       tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
-      tc::mbar_init(smem_u32(&bars.s_free[i]), kSoftWarps);
+      tc::mbar_init(smem_u32(&bars.s_free[i]), live_warps);
       tc::mbar_init(smem_u32(&bars.drain[i]), 1);
     }
     for (int i = 0; i < kV; ++i) tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
-    tc::mbar_init(smem_u32(&bars.p_full), kSoftWarps);
-    tc::mbar_init(smem_u32(&bars.q_full), kSoftWarps);
+    tc::mbar_init(smem_u32(&bars.p_full), live_warps);
+    tc::mbar_init(smem_u32(&bars.q_full), live_warps);
     s_abort = 0;
     tc::fence_barrier_init();
   }
@@ -387,8 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   grid_dep_wait();
   grid_dep_launch();
 
-  const int H = a.s.H_kv, bh = blockIdx.x / a.tiles, tile = blockIdx.x - bh * a.tiles;
-  const int b = bh / H, h = bh - b * H;
+  const int H = a.s.H_kv, b = bh / H, h = bh - b * H;
   const int64_t row0 = (int64_t)b * a.s.off[H] + a.s.off[h];
   const int64_t cap = a.s.off[h + 1] - a.s.off[h];
   int64_t held = (int64_t)__ldg(a.rows + bh) + a.extra;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     if (n > 0) score_warp<D>(a, &bars, sK, tmem, n, &s_abort);
   } else if (warp == kOutWarp) {
     if (n > 0) out_warp<D>(a, &bars, sV, tmem, n, &s_abort);
-  } else {
+  } else if ((warp & 3) < live_quarters) {
     // ---- softmax: thread (row, half): dims and scores [half * .., ..)
     constexpr int kHalfD = D / 2;
     const int half = warp >> 2, in = (warp & 3) * 32 + lane, row = tile * kRowsM + in;
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       for (int i = 0; i < kHalfD / 2; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
       mx = max(mx & 0xffffu, mx >> 16);
       s_x[0][half][in] = __uint_as_float(mx);
-      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      asm volatile("bar.sync 1, %0;\n" ::"r"(live_warps * 32) : "memory");
       mx = max(mx, __float_as_uint(s_x[0][half ^ 1][in]));
       // scale by the power of two that brings the row's largest value into [1, 2)
       const uint32_t e = mx >> 7, ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(smem_u32(&bars.q_full));
-      asm volatile("bar.sync 1, 256;\n" ::: "memory");       // s_x is free again
+      asm volatile("bar.sync 1, %0;\n" ::"r"(live_warps * 32) : "memory");       // s_x is free again
     }
 
     float ref = kNoRef;
@@ -552,9 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     }
     // ---- the row: both halves' sums, and this half's dims
     float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    asm volatile("bar.sync 1, %0;\n" ::"r"(live_warps * 32) : "memory");
     s_x[0][half][in] = sum;
-    asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    asm volatile("bar.sync 1, %0;\n" ::"r"(live_warps * 32) : "memory");
     sum = s_x[0][0][in] + s_x[0][1][in];
     if (n > 0) {
       ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(n - 1) % kV]), ((n - 1) / kV) & 1, &s_abort,
@@ -610,34 +613,69 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   if (warp == kScoreWarp) tc::tmem_dealloc(tmem, kCols);
 }
 
-// One warp per query row: joins the parts of its splits, in order.
-template <int D>
+// Joins the parts of a query row's splits.  WPR warps share a row, each summing
+// every WPR-th part in order, and their sums are added in warp order; a CTA of
+// four warps holds 4 / WPR rows.
+template <int D, int WPR>
 __global__ void __launch_bounds__(128) kvc_attend_q4_tc_join_kernel(const __grid_constant__ TcArgs a, int64_t n_rows) {
   constexpr int V = D / 32;
+  __shared__ float s_v[4][D + 1];
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (at >= n_rows) return;
-  const int64_t bh = at / a.R;
-  const int row = (int)(at - bh * a.R);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = warp % WPR;
+  const int64_t at = (int64_t)blockIdx.x * (4 / WPR) + warp / WPR;
+  const bool on = at < n_rows;
+  const int64_t bh = on ? at / a.R : 0;
+  const int row = on ? (int)(at - bh * a.R) : 0;
   const int64_t first = ((bh * a.tiles + row / kRowsM) * a.splits) * kRowsM + row % kRowsM;
   float top = kNoRef;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_ml[first + (int64_t)s * kRowsM].x);
+  for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_ml[first + (int64_t)s * kRowsM].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float l = 0.f, v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = me; s < a.splits; s += WPR) {
     const int64_t p = first + (int64_t)s * kRowsM;
     const float2 ml = a.part_ml[p];
     const float f = ex2(ml.x - top);
     l = fmaf(ml.y, f, l);
+    const float* o = a.part_o + p * D + lane * V;
+    float y[V];
+    if constexpr (V == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(o);
+    else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(o);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = fmaf(a.part_o[p * D + lane * V + i], f, v[i]);
+    for (int i = 0; i < V; ++i) v[i] = fmaf(y[i], f, v[i]);
   }
+  if constexpr (WPR > 1) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) a.out[at * D + lane * V + i] = __float2bfloat16_rn(l == 0.f ? 0.f : v[i] / l);
+    for (int i = 0; i < V; ++i) s_v[warp][lane * V + i] = v[i];
+    if (lane == 0) s_v[warp][D] = l;
+    __syncthreads();
+    if (me > 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      l += s_v[warp + w][D];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += s_v[warp + w][lane * V + i];
+    }
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = l == 0.f ? 0.f : v[i] / l;
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const __nv_bfloat162 c = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&c);
+  }
+  __nv_bfloat16* o = a.out + at * D + lane * V;
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(o) = w[0];
   if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
 }
 
@@ -668,7 +706,11 @@ cudaError_t launch_attend_q4_tc(const __nv_bfloat16* q, const uint8_t* cache, co
   a.part_ml = static_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_o);
   a.status = status_word_ptr();
-  a.T = T, a.R = H_q / H * T, a.extra = extra, a.tiles = p.tiles, a.splits = p.splits;
+  a.T = T, a.R = H_q / H * T, a.extra = extra, a.tiles = p.tiles;
+  // no more splits than leave two tiles to each in the longest slot
+  int64_t longest = 0;
+  for (int h = 0; h < H; ++h) longest = std::max(longest, slots.off[h + 1] - slots.off[h]);
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(p.splits, (longest + 2 * kKeys - 1) / (2 * kKeys)));
   a.wait_limit = wait_limit_polls();
   a.scale = (float)(1.4426950408889634 / std::sqrt((double)D));
   a.s = slots;
@@ -676,13 +718,15 @@ cudaError_t launch_attend_q4_tc(const __nv_bfloat16* q, const uint8_t* cache, co
   auto* kern = D == 128 ? kvc_attend_q4_tc_kernel<128> : kvc_attend_q4_tc_kernel<64>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e == cudaSuccess)
-    e = launch_pdl(kern, dim3((unsigned)(B * H * p.tiles), p.splits), dim3(kThreads), smem, st, a);
+    e = launch_pdl(kern, dim3((unsigned)(B * H * p.tiles), a.splits), dim3(kThreads), smem, st, a);
   note_launches(1);
   if (e != cudaSuccess) return e;
-  if (p.splits > 1) {
+  if (a.splits > 1) {
     const int64_t n = (int64_t)B * H_q * T;
-    e = launch_pdl(D == 128 ? kvc_attend_q4_tc_join_kernel<128> : kvc_attend_q4_tc_join_kernel<64>,
-                   dim3((unsigned)((n + 3) / 4)), dim3(128), 0, st, a, n);
+    const bool wide = a.splits > 8;                // many parts of few rows: four warps a row
+    auto* join = D == 128 ? (wide ? kvc_attend_q4_tc_join_kernel<128, 4> : kvc_attend_q4_tc_join_kernel<128, 1>)
+                          : (wide ? kvc_attend_q4_tc_join_kernel<64, 4> : kvc_attend_q4_tc_join_kernel<64, 1>);
+    e = launch_pdl(join, dim3((unsigned)(wide ? n : (n + 3) / 4)), dim3(128), 0, st, a, n);
     note_launches(1);
   }
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -11,9 +11,6 @@ using namespace kvc;
 
 namespace kvc {
 
-// Above 64 query rows per KV head the products bound the work, not the cache.
-bool attend_q4_on_tc(int H_q, int H_kv, int T) { return (int64_t)(H_q / H_kv) * T > 64; }
-
 int check_slots(int H_kv, const int64_t* slot_off) {
   if (H_kv > kMaxHkv) return set_error(KVC_ERR_UNSUPPORTED, "H_kv=%d above %d", H_kv, kMaxHkv);
   if (!slot_off) return set_error(KVC_ERR_INVALID_ARG, "slot_off is NULL");
