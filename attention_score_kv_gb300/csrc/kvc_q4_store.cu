@@ -44,15 +44,41 @@ __device__ __forceinline__ uint32_t group_max(uint32_t* w, bool* bad) {
   return m;
 }
 
-template <int N>
+// Rows of the bf16 tensors.  WIDE: 32 bytes an access, a whole sector each, for
+// tensors that start on 32 bytes (16-byte accesses move every sector twice).
+template <int N, bool WIDE>
 __device__ __forceinline__ void load_vecs(const __nv_bfloat16* p, uint32_t* w) {
+  if constexpr (WIDE && N >= 8) {
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    w[4 * i] = v.x;
-    w[4 * i + 1] = v.y;
-    w[4 * i + 2] = v.z;
-    w[4 * i + 3] = v.w;
+    for (int i = 0; i < N / 8; ++i)
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                   : "=r"(w[8 * i]), "=r"(w[8 * i + 1]), "=r"(w[8 * i + 2]), "=r"(w[8 * i + 3]), "=r"(w[8 * i + 4]),
+                     "=r"(w[8 * i + 5]), "=r"(w[8 * i + 6]), "=r"(w[8 * i + 7])
+                   : "l"(p + 16 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  }
+}
+template <int N, bool WIDE>
+__device__ __forceinline__ void store_vecs(__nv_bfloat16* p, const uint32_t* w) {
+  if constexpr (WIDE && N >= 8) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+      asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};\n" ::"r"(w[8 * i]), "r"(w[8 * i + 1]),
+                   "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]), "r"(w[8 * i + 6]),
+                   "r"(w[8 * i + 7]), "l"(p + 16 * i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   }
 }
 
@@ -76,7 +102,7 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* w) {
 // block and, for kWrite, the element offset of its values in k and v.  A warp
 // owns the whole block, so the nibbles that two rows share in a value byte are
 // read and written by one lane.
-template <int D, typename Src>
+template <int D, bool WIDE, typename Src>
 __device__ void store_block(uint8_t* rec, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                             Src src, bool* bad) {
   constexpr int kB = D / 8;                 // code bytes of a lane and row
@@ -89,7 +115,7 @@ __device__ void store_block(uint8_t* rec, const __nv_bfloat16* __restrict__ k, c
     const int64_t at = src(row, &what);
     if (what == kLeave) continue;
     uint32_t w[D / 8];
-    if (what == kWrite) load_vecs<D / 8>(k + at + j * (D / 4), w);
+    if (what == kWrite) load_vecs<D / 8, WIDE>(k + at + j * (D / 4), w);
     else
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) w[i] = 0;
@@ -131,7 +157,7 @@ __device__ void store_block(uint8_t* rec, const __nv_bfloat16* __restrict__ k, c
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int64_t at = src(8 * s + 2 * j + e, &what[e]);
-      if (what[e] == kWrite) load_vecs<D / 16>(v + at + r * (D / 8), w[e]);
+      if (what[e] == kWrite) load_vecs<D / 16, WIDE>(v + at + r * (D / 8), w[e]);
       else
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) w[e][i] = 0;
@@ -196,7 +222,7 @@ struct GatherArgs {
   int64_t off[kMaxHkv];
 };
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kvc_gather_q4_kernel(const __grid_constant__ GatherArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -220,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) kvc_gather_q4_kernel(const __grid_co
     *what = row < n ? kWrite : kZero;
     return (base + pr) * D;
   };
-  store_block<D>(a.cache + (at0 / q4::kRows) * q4::block_bytes(D), a.k, a.v, src, &bad);
+  store_block<D, WIDE>(a.cache + (at0 / q4::kRows) * q4::block_bytes(D), a.k, a.v, src, &bad);
   if (bad) record_status(a.status, kStatusBadInput);
 }
 
@@ -234,7 +260,7 @@ struct AppendArgs {
   Q4Slots slots;
 };
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kvc_append_q4_kernel(const __grid_constant__ AppendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -267,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) kvc_append_q4_kernel(const __grid_co
     *what = (t < 0 || t >= a.T) ? kLeave : pr < 0 ? kZero : kWrite;
     return (bh * a.T + t) * D;
   };
-  store_block<D>(a.cache + (at0 / q4::kRows) * q4::block_bytes(D), a.k, a.v, src, &bad);
+  store_block<D, WIDE>(a.cache + (at0 / q4::kRows) * q4::block_bytes(D), a.k, a.v, src, &bad);
   if (bad) record_status(a.status, kStatusBadInput);
 }
 
@@ -289,7 +315,7 @@ __device__ __forceinline__ uint32_t half2_to_bf16x2(uint32_t h) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kvc_read_q4_kernel(const __grid_constant__ ReadArgs a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -317,9 +343,9 @@ __global__ void __launch_bounds__(kThreads) kvc_read_q4_kernel(const __grid_cons
   for (int s = 0; s < 2; ++s) {                     // keys: row r + 8s, quarter j
     const int row = r + 8 * s;
     if (!wanted(row)) continue;
-    uint32_t lo[kB / 2], hi[kB / 2];                // dims b and D/8 + b of the quarter, as bf16 pairs
+    uint32_t dims[kB], *lo = dims, *hi = dims + kB / 2;       // dims b and D/8 + b of the quarter, as bf16 pairs
 #pragma unroll
-    for (int x = 0; x < kB / 2; ++x) lo[x] = hi[x] = 0;
+    for (int x = 0; x < kB; ++x) dims[x] = 0;
     if (there) {
       uint32_t c[kB / 4];
       load_bytes<kB>(rec + q4::k_codes(D) + row * (D / 2) + j * kB, c);
@@ -341,12 +367,7 @@ __global__ void __launch_bounds__(kThreads) kvc_read_q4_kernel(const __grid_cons
         lo[2 * x + 1] = __byte_perm(f[2], f[3], 0x5410), hi[2 * x + 1] = __byte_perm(f[2], f[3], 0x7632);
       }
     }
-    uint4* o = reinterpret_cast<uint4*>(a.k_out + (o0 + row) * D + j * (D / 4));
-#pragma unroll
-    for (int x = 0; x < kB / 8; ++x) {
-      o[x] = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
-      o[kB / 8 + x] = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-    }
+    store_vecs<kB, WIDE>(a.k_out + (o0 + row) * D + j * (D / 4), dims);
   }
 #pragma unroll
   for (int s = 0; s < 2; ++s) {                     // values: slice r, rows 8s + 2j and the next
@@ -372,14 +393,14 @@ __global__ void __launch_bounds__(kThreads) kvc_read_q4_kernel(const __grid_cons
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (!wanted(row + e)) continue;
-      const uint32_t* w = e ? odd : even;
-      uint4* o = reinterpret_cast<uint4*>(a.v_out + (o0 + row + e) * D + r * (D / 8));
-#pragma unroll
-      for (int x = 0; x < kB / 8; ++x) o[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+      store_vecs<kB / 2, WIDE>(a.v_out + (o0 + row + e) * D + r * (D / 8), e ? odd : even);
     }
   }
 }
 
+bool wide(const void* a, const void* b) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 31) == 0;
+}
 dim3 grid_for(int64_t warps) { return dim3((unsigned)((warps + kWarps - 1) / kWarps)); }
 
 }  // namespace
@@ -396,7 +417,8 @@ cudaError_t launch_gather_q4(const __nv_bfloat16* k, const __nv_bfloat16* v, con
   }
   a.warps = (int64_t)B * a.blk0[sel.H_kv];
   if (a.warps == 0) return cudaSuccess;
-  cudaError_t e = launch_pdl(D == 128 ? kvc_gather_q4_kernel<128> : kvc_gather_q4_kernel<64>, grid_for(a.warps),
+  cudaError_t e = launch_pdl(wide(k, v) ? (D == 128 ? kvc_gather_q4_kernel<128, true> : kvc_gather_q4_kernel<64, true>)
+                                      : (D == 128 ? kvc_gather_q4_kernel<128, false> : kvc_gather_q4_kernel<64, false>), grid_for(a.warps),
                              dim3(kThreads), 0, st, a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -410,7 +432,8 @@ cudaError_t launch_append_q4(const __nv_bfloat16* k, const __nv_bfloat16* v, con
   a.status = status_word_ptr();
   a.B = B, a.T = T, a.nb = (T + q4::kRows - 2) / q4::kRows + 1;
   a.slots = slots;
-  cudaError_t e = launch_pdl(D == 128 ? kvc_append_q4_kernel<128> : kvc_append_q4_kernel<64>,
+  cudaError_t e = launch_pdl(wide(k, v) ? (D == 128 ? kvc_append_q4_kernel<128, true> : kvc_append_q4_kernel<64, true>)
+                                      : (D == 128 ? kvc_append_q4_kernel<128, false> : kvc_append_q4_kernel<64, false>),
                              grid_for((int64_t)B * slots.H_kv * a.nb), dim3(kThreads), 0, st, a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -431,7 +454,8 @@ cudaError_t launch_read_q4(const uint8_t* cache, int B, int D, const Q4Slots& sl
   }
   a.warps = (int64_t)B * a.blk0[slots.H_kv];
   if (a.warps == 0) return cudaSuccess;
-  cudaError_t e = launch_pdl(D == 128 ? kvc_read_q4_kernel<128> : kvc_read_q4_kernel<64>, grid_for(a.warps),
+  cudaError_t e = launch_pdl(wide(k_out, v_out) ? (D == 128 ? kvc_read_q4_kernel<128, true> : kvc_read_q4_kernel<64, true>)
+                                      : (D == 128 ? kvc_read_q4_kernel<128, false> : kvc_read_q4_kernel<64, false>), grid_for(a.warps),
                              dim3(kThreads), 0, st, a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();

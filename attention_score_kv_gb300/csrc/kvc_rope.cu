@@ -26,7 +26,8 @@ namespace kvc {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kMaxTok = 4;           // tokens of a CTA
+constexpr int kMaxTok = 16;          // tokens of a CTA
+constexpr int kUnits = 3;            // lane shares a thread has in flight
 
 struct RopeArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -64,100 +65,110 @@ __global__ void __launch_bounds__(kRopeThreads) kvc_qk_norm_rope_kernel(const __
   grid_dep_launch();
   constexpr int LPH = D / 16;        // lanes of a head
   __shared__ float2 turn[kMaxTok][D / 2];
-  const int64_t tok0 = (int64_t)blockIdx.x * a.tok;
-  const int n_tok = (int)min((int64_t)a.tok, a.n_tok - tok0);
+  const uint32_t tok0 = blockIdx.x * (uint32_t)a.tok;
+  const int n_tok = (int)min((uint32_t)a.tok, (uint32_t)a.n_tok - tok0);
   const int half = a.R / 2;
-  for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
-    const int t = i / half, f = i - t * half;
-    const double u = (double)a.inv_freq[f] * 0.15915494309189533577;       // 1 / (2 pi)
-    const uint64_t frac = (uint64_t)((u - floor(u)) * 18446744073709551616.0);
-    const uint64_t at = (uint64_t)(int64_t)a.pos[tok0 + t] * frac;
-    float s, c;
-    sincospif((float)(int32_t)(at >> 32) * (1.0f / 2147483648.0f), &s, &c);
-    turn[t][f] = make_float2(c, s);
-  }
-  __syncthreads();
-
-  const int heads = a.H_q + 2 * a.H_kv;
-  const int units = n_tok * heads * LPH;
+  const uint32_t heads = a.H_q + 2 * a.H_kv;
+  const uint32_t units = n_tok * heads * LPH;
   const int l = threadIdx.x % LPH;   // kRopeThreads is a multiple of LPH
   const int rot = a.R / 16;          // lanes that hold rotated pairs
   // chunks of 8 values: lanes below `rot` hold l and l + rot, the others two of the rest
   const int c0 = l < rot ? l : 2 * l, c1 = l < rot ? l + rot : 2 * l + 1;
-  for (int u0 = 0; u0 < units; u0 += kRopeThreads) {
-    const int u = u0 + threadIdx.x;
-    const bool live = u < units;
-    const int hd = live ? u / LPH : 0;
-    const int t = hd / heads, h = hd - t * heads;
-    const int64_t tok = tok0 + t;
-    const int64_t b = tok / a.T, tt = tok - b * a.T;
-    const __nv_bfloat16* src;
-    __nv_bfloat16* dst;
-    const __nv_bfloat16* w = nullptr;
-    bool copy = false;
-    if (h < a.H_q) {
-      src = a.q + tok * a.q_ld + (int64_t)h * D;
-      dst = a.q_out + ((b * a.H_q + h) * a.T + tt) * D;
-      w = a.qw;
-    } else if (h < a.H_q + a.H_kv) {
-      const int g = h - a.H_q;
-      src = a.k + tok * a.k_ld + (int64_t)g * D;
-      dst = a.k_act + ((b * a.H_kv + g) * a.S + a.row0 + tt) * D;
-      w = a.kw;
-    } else {
-      const int g = h - a.H_q - a.H_kv;
-      copy = true;
-      src = a.v ? a.v + tok * a.v_ld + (int64_t)g * D : nullptr;
-      dst = a.v_act + ((b * a.H_kv + g) * a.S + a.row0 + tt) * D;
-    }
-    const bool on = live && src != nullptr;
-    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-    if (on) {
-      x0 = *reinterpret_cast<const uint4*>(src + c0 * 8);
-      x1 = *reinterpret_cast<const uint4*>(src + c1 * 8);
-    }
-    float y[16];
-    unpack8(x0, y);
-    unpack8(x1, y + 8);
-    float ss = 0.f;
+
+  for (uint32_t u0 = 0; u0 < units; u0 += kRopeThreads * kUnits) {
+    uint4 x[kUnits][2];
+    __nv_bfloat16* dst[kUnits];
+    int kind[kUnits], tok[kUnits];   // 0: query, 1: key, 2: value, -1: nothing
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-    for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!on) continue;
-    if (!copy) {
-      if (w) {
-        const float rms = rsqrtf(ss * (1.0f / D) + a.eps);
-        float g[16];
-        unpack8(*reinterpret_cast<const uint4*>(w + c0 * 8), g);
-        unpack8(*reinterpret_cast<const uint4*>(w + c1 * 8), g + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = y[i] * rms * g[i];
+    for (int i = 0; i < kUnits; ++i) {
+      const uint32_t u = u0 + i * kRopeThreads + threadIdx.x;
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+      kind[i] = -1, tok[i] = 0, dst[i] = nullptr;
+      if (u >= units) continue;
+      const uint32_t hd = u / LPH, t = hd / heads, h = hd - t * heads;
+      const uint32_t at = tok0 + t, b = at / (uint32_t)a.T, tt = at - b * a.T;
+      const __nv_bfloat16* src;
+      tok[i] = t;
+      if (h < (uint32_t)a.H_q) {
+        kind[i] = 0;
+        src = a.q + at * a.q_ld + (int64_t)h * D;
+        dst[i] = a.q_out + (((int64_t)b * a.H_q + h) * a.T + tt) * D;
+      } else if (h < (uint32_t)(a.H_q + a.H_kv)) {
+        const uint32_t g = h - a.H_q;
+        kind[i] = 1;
+        src = a.k + at * a.k_ld + (int64_t)g * D;
+        dst[i] = a.k_act + (((int64_t)b * a.H_kv + g) * a.S + a.row0 + tt) * D;
+      } else {
+        if (!a.v) continue;
+        const uint32_t g = h - a.H_q - a.H_kv;
+        kind[i] = 2;
+        src = a.v + at * a.v_ld + (int64_t)g * D;
+        dst[i] = a.v_act + (((int64_t)b * a.H_kv + g) * a.S + a.row0 + tt) * D;
       }
-      if (l < rot) {
-        if constexpr (INTER) {
+      x[i][0] = *reinterpret_cast<const uint4*>(src + c0 * 8);
+      x[i][1] = *reinterpret_cast<const uint4*>(src + c1 * 8);
+    }
+    if (u0 == 0) {                   // behind the first loads
+      for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
+        const int t = i / half, f = i - t * half;
+        const double u = (double)a.inv_freq[f] * 0.15915494309189533577;       // 1 / (2 pi)
+        const uint64_t frac = (uint64_t)((u - floor(u)) * 18446744073709551616.0);
+        const uint64_t at = (uint64_t)(int64_t)a.pos[tok0 + t] * frac;
+        float s, c;
+        sincospif((float)(int32_t)(at >> 32) * (1.0f / 2147483648.0f), &s, &c);
+        turn[t][f] = make_float2(c, s);
+      }
+      __syncthreads();
+    }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 cs = turn[t][(i < 4 ? c0 : c1) * 4 + (i & 3)];
-            const float p = y[2 * i], r = y[2 * i + 1];
-            y[2 * i] = p * cs.x - r * cs.y;
-            y[2 * i + 1] = r * cs.x + p * cs.y;
-          }
-        } else {
+    for (int i = 0; i < kUnits; ++i) {
+      if (kind[i] == 0 || kind[i] == 1) {        // the lanes of a head agree
+        float y[16];
+        unpack8(x[i][0], y);
+        unpack8(x[i][1], y + 8);
+        const __nv_bfloat16* w = kind[i] == 0 ? a.qw : a.kw;
+        if (w) {
+          float ss = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 cs = turn[t][c0 * 8 + i];
-            const float p = y[i], r = y[8 + i];
-            y[i] = p * cs.x - r * cs.y;
-            y[8 + i] = r * cs.x + p * cs.y;
+          for (int z = 0; z < 16; ++z) ss = fmaf(y[z], y[z], ss);
+          const uint32_t head_lanes = ((1u << LPH) - 1) << ((threadIdx.x & 31) / LPH * LPH);
+#pragma unroll
+          for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(head_lanes, ss, o);
+          const float rms = rsqrtf(ss * (1.0f / D) + a.eps);
+          float g[16];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w + c0 * 8)), g);
+          unpack8(__ldg(reinterpret_cast<const uint4*>(w + c1 * 8)), g + 8);
+#pragma unroll
+          for (int z = 0; z < 16; ++z) y[z] = y[z] * rms * g[z];
+        }
+        if (l < rot) {
+          const float2* cs = turn[tok[i]];
+          if constexpr (INTER) {
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const float2 t = cs[(z < 4 ? c0 : c1) * 4 + (z & 3)];
+              const float p = y[2 * z], r = y[2 * z + 1];
+              y[2 * z] = p * t.x - r * t.y;
+              y[2 * z + 1] = r * t.x + p * t.y;
+            }
+          } else {
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              const float2 t = cs[c0 * 8 + z];
+              const float p = y[z], r = y[8 + z];
+              y[z] = p * t.x - r * t.y;
+              y[8 + z] = r * t.x + p * t.y;
+            }
           }
         }
+        x[i][0] = pack8(y);
+        x[i][1] = pack8(y + 8);
       }
-      x0 = pack8(y);
-      x1 = pack8(y + 8);
+      if (kind[i] >= 0) {
+        *reinterpret_cast<uint4*>(dst[i] + c0 * 8) = x[i][0];
+        *reinterpret_cast<uint4*>(dst[i] + c1 * 8) = x[i][1];
+      }
     }
-    *reinterpret_cast<uint4*>(dst + c0 * 8) = x0;
-    *reinterpret_cast<uint4*>(dst + c1 * 8) = x1;
   }
 }
 
@@ -172,6 +183,12 @@ cudaError_t launch_qk_norm_rope(const __nv_bfloat16* q, const __nv_bfloat16* k, 
              row0, S, T, H_q, H_kv, R, 1, eps};
   auto* kern = D == 128 ? (inter ? kvc_qk_norm_rope_kernel<128, true> : kvc_qk_norm_rope_kernel<128, false>)
                         : (inter ? kvc_qk_norm_rope_kernel<64, true> : kvc_qk_norm_rope_kernel<64, false>);
+  // tokens of a CTA: what its threads can have in flight, as long as two CTAs an SM
+  // are left; a token's angles are worked out once for all of its heads
+  const int per_tok = (H_q + 2 * H_kv) * (D / 16);
+  const int64_t full = std::max<int64_t>(1, kRopeThreads * kUnits / per_tok);
+  const int64_t spread = (a.n_tok + 2 * std::max(num_sms(), 1) - 1) / (2 * std::max(num_sms(), 1));
+  a.tok = (int)std::min<int64_t>({full, spread, kMaxTok});
   const int64_t grid = (a.n_tok + a.tok - 1) / a.tok;
   cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), dim3(kRopeThreads), 0, st, a);
   note_launches(1);

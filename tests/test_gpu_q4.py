@@ -180,6 +180,34 @@ def test_gather(K, B, H, S, D, K_l, extra):
             assert torch.all(pc[b, so[h] + n:so[h + 1]] == -9)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_tensors_that_start_on_16_bytes(K, D):
+    """Gather, append and read on tensors that start on an odd multiple of 16 bytes."""
+    def shifted(t):
+        x = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")[8:].view(t.shape)
+        assert x.data_ptr() % 32 == 16
+        return x.copy_(t)
+
+    B, H, S, n, T = 2, 2, 90, [70, 33], 3
+    so = K.kvc_q4_layout(H, S, n, 20)
+    k, v = rnd(1, B, H, S, D, scale=2), rnd(2, B, H, S, D)
+    kt, vt, pt = rnd(3, B, H, T, D), rnd(4, B, H, T, D), i32([[500, 501, 502]] * B)
+    idx = torch.arange(so[H], device="cuda", dtype=torch.int32).repeat(B) % S
+    rows = i32([n] * B)
+    got = []
+    for f in (lambda t: t, shifted):
+        cache, pos = K.q4_cache(B, D, so)
+        cache.zero_()
+        K.kvc_gather_q4(f(k), f(v), idx, B, H, S, D, n, so, cache, pos)
+        K.kvc_append_q4(f(kt), f(vt), pt, B, H, T, D, so, rows, cache, pos)
+        ko, vo = (f(torch.zeros((B * (sum(n) + 2 * T), D), dtype=torch.bfloat16, device="cuda")) for _ in range(2))
+        K.kvc_read_q4(cache, B, H, D, so, None, [x + T for x in n], ko, vo)
+        got.append((cache, pos, ko, vo))
+    K.kvc_check_status()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert np.array_equal(f64(got[0][2][n[0]:n[0] + T]), O.held(f64(kt)[0, 0]))
+
+
 def test_gather_records_a_position_outside(K):
     k = rnd(1, 1, 1, 20, 64)
     for bad in (-1, 20, 2 ** 31 - 1):
