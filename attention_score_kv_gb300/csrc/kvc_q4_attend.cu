@@ -48,7 +48,7 @@ struct AttendArgs {
   __nv_bfloat16* out;
   float* lse;
   float2* part_ml;                   // [P + B * H_kv][R] maximum, sum: part of range c and head bh at c + bh
-  float* part_o;                     // [..][R][D], dims in the order of o_stride's comment
+  float* part_o;                     // [..][R][D], dims in the order of dim_of
   int* place;                        // [B * H_kv] blocks before each head, then all blocks
   int* status;
   int B, T, G, extra, P;
@@ -437,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid
     // the next head's first blocks come in while this one is joined.  Groups that the
     // loop's tail committed empty are behind the ones it used; the ring starts afresh.
     Segment next;
-    more = segment_at<D>(a, slots, g.f + g.cnt, f1, bh + 1, g.f + g.cnt, &next);   // it does not end the range: it ends its head
+    // a segment that does not end the range ends its head
+    more = segment_at<D>(a, slots, g.f + g.cnt, f1, bh + 1, g.f + g.cnt, &next);
     stage_in = stage_out;
     if (more)
       for (int i = 0; i < kStages - 1; ++i) fetch(next, i);

@@ -175,7 +175,8 @@ __device__ void load_warp(const TcArgs& a, Bars* bars, uint8_t* raw, Seen* seen,
     }
   }
   // every copy issued has landed before the CTA may leave
-  for (int y = max(0, i - kRaw); y < i; ++y) scan::drain_wait(smem_u32(&bars->raw_full[y % kRaw]), (y / kRaw) & 1, a.status);
+  for (int y = max(0, i - kRaw); y < i; ++y)
+    scan::drain_wait(smem_u32(&bars->raw_full[y % kRaw]), (y / kRaw) & 1, a.status);
 }
 
 template <int kB>
@@ -216,15 +217,16 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
                                    : *reinterpret_cast<const uint16_t*>(p + q4::k_scales(D) + lane * 2);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const uint32_t s2 = q4::scales_to_half2((uint16_t)(D == 128 ? ks >> (16 * s) : (ks >> (8 * s) & 0xffu) * 0x101u));
+        const uint32_t two = D == 128 ? ks >> (16 * s) : (ks >> (8 * s) & 0xffu) * 0x101u;
+        const uint32_t s2 = q4::scales_to_half2((uint16_t)two);
         uint32_t code[D / 32];
         read_codes<kB>(p + q4::k_codes(D) + s * 4 * D + lane * kB, code);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t f[4];
           q4::codes_to_half2(code[c], f);
-          store16(k_at ^ ((b * 4 + s * 2) * 128 | (c ^ (b * 4 + s * 2)) << 4), q4::mul_half2(f[0], s2), q4::mul_half2(f[1], s2),
-                  q4::mul_half2(f[2], s2), q4::mul_half2(f[3], s2));
+          store16(k_at ^ ((b * 4 + s * 2) * 128 | (c ^ (b * 4 + s * 2)) << 4), q4::mul_half2(f[0], s2),
+                  q4::mul_half2(f[1], s2), q4::mul_half2(f[2], s2), q4::mul_half2(f[3], s2));
         }
       }
     }
@@ -275,12 +277,14 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
 __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool first) {
   if (first)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, 0, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "{\n .reg .pred p;\n setp.ne.b32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.eq.b32 p, 0, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "{\n .reg .pred p;\n setp.eq.b32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc)
         : "memory");
 }
@@ -475,12 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
 
     float ref = kNoRef;
     float2 sum2[2] = {};             // the row's sum, in four parts
+    const auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, wait_bar_warp(smem_u32(bar), phase & 1, &s_abort, a.status, a.wait_limit));
+    };
     bool ok = true;                  // a wait that gave up: go on without waiting, so that no barrier is left alone
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       const uint32_t s_at = tmem + lanes + kColS + st * kKeys + half * 64;
-      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.s_full[st]), (i >> 1) & 1, &s_abort, a.status,
-                                                        a.wait_limit));
+      ok = ok && wait(&bars.s_full[st], i >> 1);
       tc::fence_after_sync();
       float x[64];
 #pragma unroll
@@ -529,8 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       // the weights' columns, and the output for a new reference, are free when the
       // last tile's output is added up
       if (i > 0) {
-        ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(i - 1) % kV]), ((i - 1) / kV) & 1, &s_abort,
-                                                          a.status, a.wait_limit));
+        ok = ok && wait(&bars.o_done[(i - 1) % kV], (i - 1) / kV);
         tc::fence_after_sync();
         if (move) {
 #pragma unroll
@@ -560,8 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     asm volatile("bar.sync 1, %0;\n" ::"r"(live_warps * 32) : "memory");
     sum = s_x[0][0][in] + s_x[0][1][in];
     if (n > 0) {
-      ok = ok && __all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars.o_done[(n - 1) % kV]), ((n - 1) / kV) & 1, &s_abort,
-                                                        a.status, a.wait_limit));
+      ok = ok && wait(&bars.o_done[(n - 1) % kV], (n - 1) / kV);
       tc::fence_after_sync();
     }
     const bool whole = a.splits == 1;

@@ -417,9 +417,10 @@ cudaError_t launch_gather_q4(const __nv_bfloat16* k, const __nv_bfloat16* v, con
   }
   a.warps = (int64_t)B * a.blk0[sel.H_kv];
   if (a.warps == 0) return cudaSuccess;
-  cudaError_t e = launch_pdl(wide(k, v) ? (D == 128 ? kvc_gather_q4_kernel<128, true> : kvc_gather_q4_kernel<64, true>)
-                                      : (D == 128 ? kvc_gather_q4_kernel<128, false> : kvc_gather_q4_kernel<64, false>), grid_for(a.warps),
-                             dim3(kThreads), 0, st, a);
+  const bool w = wide(k, v);
+  auto* kern = D == 128 ? (w ? kvc_gather_q4_kernel<128, true> : kvc_gather_q4_kernel<128, false>)
+                        : (w ? kvc_gather_q4_kernel<64, true> : kvc_gather_q4_kernel<64, false>);
+  cudaError_t e = launch_pdl(kern, grid_for(a.warps), dim3(kThreads), 0, st, a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -432,8 +433,10 @@ cudaError_t launch_append_q4(const __nv_bfloat16* k, const __nv_bfloat16* v, con
   a.status = status_word_ptr();
   a.B = B, a.T = T, a.nb = (T + q4::kRows - 2) / q4::kRows + 1;
   a.slots = slots;
-  cudaError_t e = launch_pdl(wide(k, v) ? (D == 128 ? kvc_append_q4_kernel<128, true> : kvc_append_q4_kernel<64, true>)
-                                      : (D == 128 ? kvc_append_q4_kernel<128, false> : kvc_append_q4_kernel<64, false>),
+  const bool w = wide(k, v);
+  auto* kern = D == 128 ? (w ? kvc_append_q4_kernel<128, true> : kvc_append_q4_kernel<128, false>)
+                        : (w ? kvc_append_q4_kernel<64, true> : kvc_append_q4_kernel<64, false>);
+  cudaError_t e = launch_pdl(kern,
                              grid_for((int64_t)B * slots.H_kv * a.nb), dim3(kThreads), 0, st, a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -450,13 +453,15 @@ cudaError_t launch_read_q4(const uint8_t* cache, int B, int D, const Q4Slots& sl
     a.n_rows[h] = n;
     a.out_off[h] = out.off[h];
     // an unaligned start may touch one block more
-    a.blk0[h + 1] = a.blk0[h] + (n == 0 ? 0 : first ? (n + q4::kRows - 2) / q4::kRows + 1 : (n + q4::kRows - 1) / q4::kRows);
+    const int blocks = first ? (n + q4::kRows - 2) / q4::kRows + 1 : (n + q4::kRows - 1) / q4::kRows;
+    a.blk0[h + 1] = a.blk0[h] + (n == 0 ? 0 : blocks);
   }
   a.warps = (int64_t)B * a.blk0[slots.H_kv];
   if (a.warps == 0) return cudaSuccess;
-  cudaError_t e = launch_pdl(wide(k_out, v_out) ? (D == 128 ? kvc_read_q4_kernel<128, true> : kvc_read_q4_kernel<64, true>)
-                                      : (D == 128 ? kvc_read_q4_kernel<128, false> : kvc_read_q4_kernel<64, false>), grid_for(a.warps),
-                             dim3(kThreads), 0, st, a);
+  const bool w = wide(k_out, v_out);
+  auto* kern = D == 128 ? (w ? kvc_read_q4_kernel<128, true> : kvc_read_q4_kernel<128, false>)
+                        : (w ? kvc_read_q4_kernel<64, true> : kvc_read_q4_kernel<64, false>);
+  cudaError_t e = launch_pdl(kern, grid_for(a.warps), dim3(kThreads), 0, st, a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

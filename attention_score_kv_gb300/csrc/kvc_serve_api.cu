@@ -18,9 +18,10 @@ int check_slots(int H_kv, const int64_t* slot_off) {
   for (int h = 0; h <= H_kv; ++h) {
     const int64_t o = slot_off[h];
     if (o < lo || o % q4::kRows != 0)
-      return set_error(KVC_ERR_INVALID_ARG, "slot_off[%d]=%lld must be a multiple of %d, at least %lld", h, (long long)o,
-                       q4::kRows, (long long)lo);
-    if (o - lo > (1 << 30)) return set_error(KVC_ERR_UNSUPPORTED, "a slot of %lld rows: above 2^30", (long long)(o - lo));
+      return set_error(KVC_ERR_INVALID_ARG, "slot_off[%d]=%lld must be a multiple of %d, at least %lld", h,
+                       (long long)o, q4::kRows, (long long)lo);
+    if (o - lo > (1 << 30))
+      return set_error(KVC_ERR_UNSUPPORTED, "a slot of %lld rows: above 2^30", (long long)(o - lo));
     if (o > (int64_t)INT32_MAX * q4::kRows)
       return set_error(KVC_ERR_UNSUPPORTED, "slot_off[%d]=%lld: too many rows", h, (long long)o);
     lo = o;
@@ -94,8 +95,8 @@ int kvc_qk_norm_rope(const kvc_bf16* q, const kvc_bf16* k, const kvc_bf16* v, in
     return rc;
   if ((v == nullptr) != (v_act == nullptr)) return set_error(KVC_ERR_INVALID_ARG, "v and v_act go together");
   if (v && ((rc = check_ptr(v, 16, "v")) || (rc = check_ptr(v_act, 16, "v_act")))) return rc;
-  if ((q_weight && (rc = check_ptr(q_weight, 16, "q_weight"))) || (k_weight && (rc = check_ptr(k_weight, 16, "k_weight"))))
-    return rc;
+  if (q_weight && (rc = check_ptr(q_weight, 16, "q_weight"))) return rc;
+  if (k_weight && (rc = check_ptr(k_weight, 16, "k_weight"))) return rc;
   if (R > 0 && ((rc = check_ptr(inv_freq, 4, "inv_freq")) || (rc = check_ptr(pos, 4, "pos")))) return rc;
   if (q_ld < (int64_t)H_q * D || k_ld < (int64_t)H_kv * D || (v && v_ld < (int64_t)H_kv * D) || q_ld % 8 || k_ld % 8 ||
       (v && v_ld % 8))
@@ -150,7 +151,8 @@ int kvc_append_q4(const kvc_bf16* k, const kvc_bf16* v, const int32_t* pos_new, 
   if ((rc = check_ptr(k, 16, "k")) || (rc = check_ptr(v, 16, "v")) || (rc = check_ptr(pos_new, 4, "pos_new")) ||
       (rc = check_ptr(rows, 4, "rows")) || (rc = check_ptr(cache, 16, "cache")) || (rc = check_ptr(pos, 4, "pos")))
     return rc;
-  return done(launch_append_q4(bf(k), bf(v), pos_new, B, T, D, make_slots(H_kv, slot_off), rows, cache, pos, cs(stream)),
+  return done(launch_append_q4(bf(k), bf(v), pos_new, B, T, D, make_slots(H_kv, slot_off), rows, cache, pos,
+                               cs(stream)),
               "4-bit append launch");
 }
 

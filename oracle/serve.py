@@ -31,10 +31,9 @@ def quantise(x):
     a = np.abs(g)
     sb = nearest_even(np.minimum(a.max(-1) / 6.0, 448.0), E4M3)
     s = E4M3[sb][..., None]
-    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
-        # x / s against the borders between codes, as exact products
-        mag = nearest_even(np.minimum(np.where(s > 0, a, 0.0), 6.0 * np.maximum(s, 1.0 / 512)) / np.where(s > 0, s, 1.0),
-                           E2M1)
+    # the quotient of an 8-bit and a 4-bit value is a border between codes only where it is exact
+    some = s > 0
+    mag = nearest_even(np.where(some, np.minimum(a, 6.0 * s), 0.0) / np.where(some, s, 1.0), E2M1)
     code = mag + 8 * np.signbit(g)
     return code.reshape(*code.shape[:-2], 16 * code.shape[-2]).astype(np.uint8), sb.astype(np.uint8)
 

@@ -91,7 +91,8 @@ def check_attention(K, q, cache, pos, rows, extra, q_pos, B, T, Hq, H, D, so, ou
             n = min(max(int(rows[b, h]) + extra, 0), so[h + 1] - so[h])
             k, v, p = kk[b, so[h]:so[h] + n], vv[b, so[h]:so[h] + n], pos[b, so[h]:so[h] + n]
             seen = (p >= 0) & (p <= q_pos[b].max())
-            ref, rl, mag = O.attention(q[b, hq], np.where(seen[:, None], k, 0), np.where(seen[:, None], v, 0), p, q_pos[b])
+            k, v = np.where(seen[:, None], k, 0), np.where(seen[:, None], v, 0)
+            ref, rl, mag = O.attention(q[b, hq], k, v, p, q_pos[b])
             A = 0.0 if not seen.any() else float((np.abs(q[b, hq]) @ np.abs(k[seen]).T).max()) / math.sqrt(D)
             vmax = np.abs(v[seen]).max() if seen.any() else 0.0
             tol = 2.0 ** -8 * np.abs(ref) + 2 * (2.0 ** -11 + A * 2.0 ** -18) * mag + n * 2.0 ** -29 * vmax
@@ -148,7 +149,8 @@ def test_values_that_are_not_finite(K, D):
 
 
 @pytest.mark.parametrize("B,H,S,D,K_l,extra", [
-    (1, 1, 1, 128, [1], 0), (2, 3, 40, 64, [0, 17, 400], 5), (3, 2, 300, 128, [299, 16], 33), (2, 5, 77, 128, [1, 15, 16, 31, 33], 0),
+    (1, 1, 1, 128, [1], 0), (2, 3, 40, 64, [0, 17, 400], 5), (3, 2, 300, 128, [299, 16], 33),
+    (2, 5, 77, 128, [1, 15, 16, 31, 33], 0),
 ])
 def test_gather(K, B, H, S, D, K_l, extra):
     so = K.kvc_q4_layout(H, S, K_l, extra)
@@ -220,7 +222,8 @@ def test_gather_records_a_position_outside(K):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("T,first", [(1, 0), (1, 1), (1, 15), (1, 16), (2, 7), (3, 14), (5, 31), (16, 8), (17, 0), (33, 15), (40, 1)])
+@pytest.mark.parametrize("T,first", [(1, 0), (1, 1), (1, 15), (1, 16), (2, 7), (3, 14), (5, 31), (16, 8), (17, 0),
+                                     (33, 15), (40, 1)])
 def test_append_writes_its_rows_and_no_other(K, D, T, first):
     B, H = 2, 3
     so = [0, 80, 80 + 96, 80 + 96 + 80]
@@ -263,7 +266,8 @@ def test_append_without_room_leaves_the_head(K):
     with pytest.raises(K.KvcError):
         K.kvc_check_status()
     after = all_rows(K, cache, B, H, D, so)
-    assert np.array_equal(after[0][0, 29:32], O.held(f64(k)[0, 0])) and np.array_equal(after[0][0, 32:], before[0][0, 32:])
+    assert np.array_equal(after[0][0, 29:32], O.held(f64(k)[0, 0]))
+    assert np.array_equal(after[0][0, 32:], before[0][0, 32:])
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -281,7 +285,8 @@ def test_read_ranges(K, D):
         for h in range(H):
             r = so[h] + first[b, h]
             want_k[b, oo[h]:oo[h] + n[h]], want_v[b, oo[h]:oo[h] + n[h]] = kk[b, r:r + n[h]], vv[b, r:r + n[h]]
-    assert np.array_equal(f64(ko).reshape(want_k.shape), want_k) and np.array_equal(f64(vo).reshape(want_v.shape), want_v)
+    assert np.array_equal(f64(ko).reshape(want_k.shape), want_k)
+    assert np.array_equal(f64(vo).reshape(want_v.shape), want_v)
 
 
 def test_read_outside_a_slot_gives_zeros(K):
@@ -462,6 +467,31 @@ def test_many_heads_and_long_rows(K, B, Hq, H, T):
     check_attention(K, *args, *attend(K, *args))
 
 
+def test_a_wait_that_gives_up_is_reported(K):
+    """With a limit of one poll the many-row kernel's waits may give up: the call ends all the
+    same, a wait that did give up is reported, and the next call is right."""
+    B, T, H, Hq, D, n = 4, 40, 8, 32, 128, [6000] * 8
+    so = K.kvc_q4_layout(H, 1 << 20, n, 0)
+    cache, pos, _, _ = filled(K, B, H, D, so, n, 96)
+    q, qp = rnd(97, B, Hq, T, D), i32(np.full((B, T), 1 << 20))
+    args = (q, cache, pos, i32([n] * B), 0, qp, B, T, Hq, H, D, so)
+    for limit in (1, 1, 1, 0):
+        K.kvc_set_option(K.KVC_OPT_WAIT_LIMIT, limit)
+        try:
+            out, lse = attend(K, *args)
+            gave_up = False
+            try:
+                K.kvc_check_status()
+            except K.KvcError as e:
+                assert e.code == K.KVC_ERR_TIMEOUT
+                gave_up = True
+        finally:
+            K.kvc_set_option(K.KVC_OPT_WAIT_LIMIT, 0)
+        assert limit or not gave_up
+        if not gave_up:
+            check_attention(K, *args, out, lse, heads=[0, 31], batches=[0, 3])
+
+
 def test_offsets_past_32_bits(K):
     """A slot of 2^25 rows, 4.8 GB: append and attention at its far end."""
     D, cap = 128, 1 << 25
@@ -471,7 +501,7 @@ def test_offsets_past_32_bits(K):
     k, v, q = rnd(1, 1, 1, 40, D), rnd(2, 1, 1, 40, D), rnd(3, 1, 4, 1, D)
     rows = i32([[cap - 43]])
     K.kvc_append_q4(k, v, i32([np.arange(40)]), 1, 1, 40, D, so, rows, cache, pos)
-    ko, vo = torch.empty((40, D), dtype=torch.bfloat16, device="cuda"), torch.empty((40, D), dtype=torch.bfloat16, device="cuda")
+    ko, vo = (torch.empty((40, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     K.kvc_read_q4(cache, 1, 1, D, so, rows, [40], ko, vo)
     out, lse = attend(K, q, cache, pos, rows, 43, i32([[30]]), 1, 1, 4, 1, D, so)
     K.kvc_check_status()

@@ -97,7 +97,7 @@ def test_negative_positions_turn_the_other_way(K):
     D, inv = 64, torch.tensor([0.7 ** i for i in range(32)], device="cuda")
     x = torch.randn((1, 1, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
     for p in (-1, -100000, -2 ** 31, 2 ** 31 - 1):
-        q, k = torch.empty((1, 1, 1, D), dtype=torch.bfloat16, device="cuda"), torch.empty((1, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+        q, k = (torch.empty((1, 1, 1, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
         pos = torch.tensor([[p]], dtype=torch.int32, device="cuda")
         K.kvc_qk_norm_rope(x, x, None, 1, 1, 1, 1, D, D, D, D, D, 0, None, None, 0.0, inv, pos, 1, 0, q, k, None)
         check_heads(f64(q), f64(x)[:, :, None], None, 0.0, f64(inv), np.array([[p]]), D, False)
@@ -117,7 +117,8 @@ def test_extreme_values(K):
     k = torch.empty((1, 1, 1, D), dtype=torch.bfloat16, device="cuda")
     pos = torch.tensor([[11]], dtype=torch.int32, device="cuda")
     inv = torch.full((D // 2,), 0.1, device="cuda")
-    K.kvc_qk_norm_rope(x, x[..., :D], None, 1, 1, 4, 1, D, 4 * D, 4 * D, D, D, 0, w, w, 1e-6, inv, pos, 1, 0, q, k, None)
+    K.kvc_qk_norm_rope(x, x[..., :D], None, 1, 1, 4, 1, D, 4 * D, 4 * D, D, D, 0, w, w, 1e-6, inv, pos, 1, 0, q, k,
+                       None)
     assert torch.all(q[0, 0] == 0) and torch.isnan(q[0, 2]).all() and torch.isfinite(q[0, 3]).all()
     assert torch.isnan(q[0, 1, 0, 5]) and torch.all(k == 0)
 
