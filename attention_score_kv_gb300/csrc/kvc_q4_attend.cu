@@ -91,35 +91,36 @@ __device__ __forceinline__ int range_blocks(int N, int P) {
 // whose share holds the place finds it.
 // write: leave every head's place to the joining kernel, and record counts
 // that do not fit.
-struct Place { int total, before, bh; };
+struct Place { int total, L, before, bh, n_rows; };    // L: blocks of a range
 __device__ __forceinline__ Place find_place(const AttendArgs& a, const SlotTable& t, int cta, bool write) {
-  __shared__ int s_sum[kWarps], s_at[2];
+  __shared__ int s_sum[kWarps], s_at[3];
   const int BH = a.B * a.s.H_kv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = (BH + kThreads - 1) / kThreads * 32;
   const int i0 = min(warp * share, BH), i1 = min(i0 + share, BH);
   bool bad = false;
-  int sum = 0, nb0 = 0;
+  int sum = 0, n0 = 0;
   for (int base = i0; base < i1; base += 32) {
     const int i = base + lane;
-    const int nb = i < i1 ? blocks_of(rows_of(a, t, i, __ldg(a.rows + i), &bad)) : 0;
-    if (base == i0) nb0 = nb;
-    sum += nb;
+    const int n = i < i1 ? rows_of(a, t, i, __ldg(a.rows + i), &bad) : 0;
+    if (base == i0) n0 = n;
+    sum += blocks_of(n);
   }
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
-  Place p{0, 0, 0};
+  Place p{};
   int run = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     run += w < warp ? s_sum[w] : 0;
     p.total += s_sum[w];
   }
-  const int f0 = (int)min((int64_t)cta * range_blocks(p.total, a.P), (int64_t)p.total);
+  p.L = range_blocks(p.total, a.P);
+  const int f0 = (int)min((int64_t)cta * p.L, (int64_t)p.total);
   if ((f0 >= run && f0 < run + sum) || write)
     for (int base = i0; base < i1; base += 32) {
       const int i = base + lane;
-      const int nb = base == i0 ? nb0 : i < i1 ? blocks_of(rows_of(a, t, i, __ldg(a.rows + i), &bad)) : 0;
+      const int n = base == i0 ? n0 : i < i1 ? rows_of(a, t, i, __ldg(a.rows + i), &bad) : 0, nb = blocks_of(n);
       int inc = nb;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -128,13 +129,13 @@ __device__ __forceinline__ Place find_place(const AttendArgs& a, const SlotTable
       }
       const int before = run + inc - nb;
       if (write && i < i1) a.place[i] = before;
-      if (f0 >= before && f0 < before + nb) s_at[0] = before, s_at[1] = i;
+      if (f0 >= before && f0 < before + nb) s_at[0] = before, s_at[1] = i, s_at[2] = n;
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
   if (write && threadIdx.x == 0) a.place[BH] = p.total;
   if (write && bad) record_status(a.status, kStatusBadInput);
   __syncthreads();
-  if (f0 < p.total) p.before = s_at[0], p.bh = s_at[1];
+  if (f0 < p.total) p.before = s_at[0], p.bh = s_at[1], p.n_rows = s_at[2];
   return p;
 }
 
@@ -219,21 +220,30 @@ struct Segment {
   int f, bh, cnt, s0, n_rows;        // flat block it starts at; head; blocks; first block in the head; the head's rows
 };
 template <int D>
-__device__ __forceinline__ bool segment_at(const AttendArgs& a, const SlotTable& t, int f, int f1, int bh, int before,
-                                           Segment* g) {
+__device__ __forceinline__ Segment segment_of(const AttendArgs& a, const SlotTable& t, int f, int f1, int bh, int before,
+                                              int n_rows) {
+  const int b = batch_of(a, bh);
+  Segment g;
+  g.f = f;
+  g.bh = bh;
+  g.n_rows = n_rows;
+  g.s0 = f - before;
+  g.cnt = min(f1 - f, blocks_of(n_rows) - g.s0);
+  const int64_t row = (int64_t)b * a.s.off[a.s.H_kv] + t.off[bh - b * a.s.H_kv] + (int64_t)g.s0 * q4::kRows;
+  g.rec = a.cache + row / q4::kRows * q4::block_bytes(D);
+  g.pos = a.pos + row;
+  return g;
+}
+// The next one: a segment that does not end the range ends its head.
+template <int D>
+__device__ __forceinline__ bool next_segment(const AttendArgs& a, const SlotTable& t, int f1, const Segment& g,
+                                             Segment* next) {
+  const int f = g.f + g.cnt;
   if (f >= f1) return false;
   bool bad = false;                  // recorded where the places are found
-  int n;
+  int n, bh = g.bh + 1;
   while ((n = rows_of(a, t, bh, __ldg(a.rows + bh), &bad)) == 0) ++bh;     // f < f1 <= total: a head with rows follows
-  const int b = batch_of(a, bh);
-  g->f = f;
-  g->bh = bh;
-  g->n_rows = n;
-  g->s0 = f - before;
-  g->cnt = min(f1 - f, blocks_of(n) - g->s0);
-  const int64_t row = (int64_t)b * a.s.off[a.s.H_kv] + t.off[bh - b * a.s.H_kv] + (int64_t)g->s0 * q4::kRows;
-  g->rec = a.cache + row / q4::kRows * q4::block_bytes(D);
-  g->pos = a.pos + row;
+  *next = segment_of<D>(a, t, f, f1, bh, f, n);
   return true;
 }
 
@@ -254,21 +264,26 @@ __global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid
   __shared__ float2 s_ml[kWarps][kCols];
   __shared__ SlotTable slots;
   fill_slots(a, slots);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
+  const int R = a.G * a.T;           // query rows, at most kCols
+  // what does not depend on the previous grid comes before the wait for it: the tokens of
+  // columns 2j and 2j + 1, and the arguments' first loads
+  const int t_of[2] = {2 * j % a.T, (2 * j + 1) % a.T};
+  asm volatile("" ::"l"(a.q), "l"(a.cache), "l"(a.pos), "l"(a.rows), "l"(a.q_pos), "l"(a.part_ml), "l"(a.part_o),
+               "l"(a.place), "r"(a.extra), "r"(a.P), "r"(a.inv_h), "f"(a.scale));
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
-  const int R = a.G * a.T;           // query rows, at most kCols
   float* s_o = reinterpret_cast<float*>(dyn);              // [kWarps][R][o_stride]
   uint8_t* ring = dyn + o_bytes(D, R) + warp * kStages * stage_bytes(D);
   const uint32_t ring_u = smem_u32(ring);
 
   // the CTA's range [f0, f1) of the blocks laid end to end
   const Place pl = find_place(a, slots, blockIdx.x, blockIdx.x == 0);
-  const int L = range_blocks(pl.total, a.P);
-  const int f0 = (int)min((int64_t)blockIdx.x * L, (int64_t)pl.total), f1 = min(f0 + L, pl.total);
+  const int f0 = (int)min((int64_t)blockIdx.x * pl.L, (int64_t)pl.total), f1 = min(f0 + pl.L, pl.total);
   Segment g;
-  bool more = segment_at<D>(a, slots, f0, f1, pl.bh, pl.before, &g);
+  bool more = f0 < f1;
+  if (more) g = segment_of<D>(a, slots, f0, f1, pl.bh, pl.before, pl.n_rows);
 
   // block `i` (0, 1, ...) of the warp's share of a segment into its ring; a group is
   // committed whether or not there is one, so that the waits can count
@@ -302,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid
     int qp[2];                       // positions of columns 2j and 2j + 1
 #pragma unroll
     for (int y = 0; y < 2; ++y)
-      qp[y] = 2 * j + y < R ? __ldg(a.q_pos + (int64_t)b * a.T + (2 * j + y) % a.T) : -1;
+      qp[y] = 2 * j + y < R ? __ldg(a.q_pos + (int64_t)b * a.T + t_of[y]) : -1;
     if (!started)                    // behind the queries' loads, which the blocks' traffic would hold up
       for (int i = 0; i < kStages - 1; ++i) fetch(g, i);
     started = true;
@@ -437,8 +452,7 @@ __global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid
     // the next head's first blocks come in while this one is joined.  Groups that the
     // loop's tail committed empty are behind the ones it used; the ring starts afresh.
     Segment next;
-    // a segment that does not end the range ends its head
-    more = segment_at<D>(a, slots, g.f + g.cnt, f1, bh + 1, g.f + g.cnt, &next);
+    more = next_segment<D>(a, slots, f1, g, &next);
     stage_in = stage_out;
     if (more)
       for (int i = 0; i < kStages - 1; ++i) fetch(next, i);
