@@ -502,19 +502,20 @@ __global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid
   }
 }
 
-// One CTA per (sequence, KV head) and query row: joins the parts.  Warp w sums
-// parts w, w + 4, ... in range order, each lane a vector of the row, and the
-// four sums are added in warp order.
-constexpr int kJoinWarps = 4;
+// One CTA per (sequence, KV head) and query row: joins the parts.  Warp w goes
+// through parts w, w + 4, ... in range order, each lane with a vector of the
+// row, against a maximum of its own (so that a part's sum and output are
+// loaded together), and the four are joined in warp order.
+constexpr int kJoinWarps = 4, kJoinAhead = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int V = D / 32;          // values of a lane
   __shared__ float s_v[kJoinWarps][D];
   __shared__ float2 s_ml[kJoinWarps];
-  grid_dep_wait();
-  grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = a.B * a.s.H_kv;
   const int R = a.G * a.T, bh = blockIdx.x / R, row = blockIdx.x - bh * R;
+  grid_dep_wait();
+  grid_dep_launch();
   const int total = a.place[BH], before = a.place[bh], after = a.place[bh + 1];   // place[BH] is the total
   const int L = range_blocks(total, a.P);
   const int c0 = before / L;
@@ -522,42 +523,59 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(con
   const int64_t slot0 = bh + c0;
   const float2* ml = a.part_ml + slot0 * R + row;
   const float* po = a.part_o + (slot0 * R + row) * D + lane * V;
-  float top = kNoRef;
-  for (int c = lane; c < n; c += 32) top = fmaxf(top, ml[(int64_t)c * R].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float l = 0.f, v[V];
+  float top = kNoRef, l = 0.f, v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = 0.f;
-#pragma unroll 4
-  for (int c = warp; c < n; c += kJoinWarps) {
-    const float2 x = ml[(int64_t)c * R];
-    const float f = ex2(x.x - top);
-    l = fmaf(x.y, f, l);
-    const float* p = po + (int64_t)c * R * D;
-    if constexpr (V == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(p);
-      v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]), v[2] = fmaf(y.z, f, v[2]), v[3] = fmaf(y.w, f, v[3]);
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(p);
-      v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]);
+  for (int c = warp; c < n; c += kJoinWarps * kJoinAhead) {
+    float2 x[kJoinAhead];
+    float y[kJoinAhead][V];
+#pragma unroll
+    for (int z = 0; z < kJoinAhead; ++z) {
+      const int cz = c + z * kJoinWarps;
+      x[z] = make_float2(kNoRef, 0.f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[z][i] = 0.f;
+      if (cz < n) {
+        x[z] = ml[(int64_t)cz * R];
+        const float* p = po + (int64_t)cz * R * D;
+        if constexpr (V == 4) *reinterpret_cast<float4*>(y[z]) = *reinterpret_cast<const float4*>(p);
+        else *reinterpret_cast<float2*>(y[z]) = *reinterpret_cast<const float2*>(p);
+      }
+    }
+    float next = top;
+#pragma unroll
+    for (int z = 0; z < kJoinAhead; ++z) next = fmaxf(next, x[z].x);
+    const float f0 = ex2(top - next);
+    top = next;
+    l *= f0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] *= f0;
+#pragma unroll
+    for (int z = 0; z < kJoinAhead; ++z) {
+      const float f = ex2(x[z].x - top);
+      l = fmaf(x[z].y, f, l);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = fmaf(y[z][i], f, v[i]);
     }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) s_v[warp][lane * V + i] = v[i];
-  if (lane == 0) s_ml[warp] = make_float2(0.f, l);
+  if (lane == 0) s_ml[warp] = make_float2(top, l);
   __syncthreads();
-  float sum = 0.f;
+  float f[kJoinWarps];
+  top = kNoRef, l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) sum += s_ml[w].y;
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_ml[w].x);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) f[w] = ex2(s_ml[w].x - top), l = fmaf(s_ml[w].y, f[w], l);
   const int64_t at = blockIdx.x;
   for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
     float o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) o += s_v[w][d];
-    a.out[at * D + dim_of<D>(d)] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+    for (int w = 0; w < kJoinWarps; ++w) o = fmaf(s_v[w][d], f[w], o);
+    a.out[at * D + dim_of<D>(d)] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  if (a.lse && threadIdx.x == 0) a.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
 }
 
 }  // namespace
