@@ -37,6 +37,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCols = 8;             // query rows per KV head: the narrow side of the products
 constexpr int kMinBlocks = kWarps;   // blocks of 16 rows a CTA takes at least
+constexpr int kCluster = 8;          // CTAs of a cluster that takes a head,
+constexpr int kClusterBlocks = 128;  // with at most so many blocks each
 constexpr float kNoRef = -1.7e38f;   // reference of a query that has seen no row
 constexpr float kShift = 4.0f;       // weights are kept as 2^(x - max + kShift)
 constexpr float kSlack = 8.0f;       // the reference moves when a score passes it by more
@@ -247,6 +249,14 @@ __device__ __forceinline__ bool next_segment(const AttendArgs& a, const SlotTabl
   return true;
 }
 
+// Block `in` of a segment (if it has one) into a stage of the warp's ring.
+template <int D>
+__device__ __forceinline__ void fetch_block(const Segment& x, int in, uint32_t stage, int lane) {
+  if (in < x.cnt)
+    copy_block<D>(stage, x.rec + (int64_t)in * q4::block_bytes(D), x.pos + (int64_t)in * q4::kRows, lane);
+  copies_commit();
+}
+
 // Shared memory: the warps' outputs, then their rings.
 // Position d' = 16 m + 2 r + e of a row there holds dim r*D/8 + 2m + e: a lane
 // of the output fragments stores pairs side by side with its neighbours', and
@@ -256,24 +266,245 @@ __host__ __device__ constexpr int o_bytes(int D, int R) { return kWarps * R * o_
 template <int D>
 __device__ __forceinline__ int dim_of(int at) { return (at >> 1 & 7) * (D / 8) + (at >> 4) * 2 + (at & 1); }
 
+// What a warp has of a head: output fragments (columns 2j and 2j + 1 of dims
+// dim_of), and per column the reference and the sum.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid_constant__ AttendArgs a) {
+struct Acc {
+  float o[D / 16][4], ref[2], sum[2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[m][y] = 0.f;
+    ref[0] = ref[1] = kNoRef;
+    sum[0] = sum[1] = 0.f;
+  }
+};
+
+// The warp's share of a segment: blocks warp, warp + 8, ...  start() and fetch(g,
+// i) copy blocks ahead into the warp's ring.
+template <int D, typename Start, typename Fetch>
+__device__ __forceinline__ void attend_segment(const AttendArgs& a, const Segment& g, int b, const int (&t_of)[2],
+                                               const uint8_t* ring, int& stage_out, Start start, Fetch fetch,
+                                               Acc<D>& acc_out) {
   constexpr int KS = D / 16;         // k-steps of the scores, m-tiles of the output
   constexpr int kB = D / 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
+  const int R = a.G * a.T, bh = g.bh, n_rows = g.n_rows;
+  auto& o = acc_out.o;
+  auto& ref = acc_out.ref;
+  auto& sum = acc_out.sum;
+  acc_out.clear();
+  // queries: column n = lane / 4, quarter j of its dims
+  uint32_t w[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) w[i] = 0;
+  if (r < R) {
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + ((int64_t)bh * R + r) * D + j * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = __ldg(p + i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  int qp[2];                       // positions of columns 2j and 2j + 1
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    qp[y] = 2 * j + y < R ? __ldg(a.q_pos + (int64_t)b * a.T + t_of[y]) : -1;
+  start();                         // behind the queries' loads, which the blocks' traffic would hold up
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+  mx = max(mx & 0xffffu, mx >> 16);
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  // scale by the power of two that brings the row's largest value into [1, 2)
+  const uint32_t e = mx >> 7, ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
+  const float down = __uint_as_float((254u - ee) << 23);
+  const float c = __uint_as_float(ee << 23) * a.scale;
+  uint32_t qf[KS][2];
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      qf[s][y] = pack_half2(__uint_as_float(q4::bf16_of(w, 2 * s + y) << 16) * down,
+                            __uint_as_float(q4::bf16_of(w, kB + 2 * s + y) << 16) * down);
+  float c2[2];                     // factor from accumulator to log2 units, columns 2j and 2j + 1
+  int q_lo = INT32_MAX, q_hi = -1;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    c2[y] = __shfl_sync(0xffffffffu, c, (2 * j + y) * 4);
+    if (2 * j + y < R) q_lo = min(q_lo, qp[y]), q_hi = max(q_hi, qp[y]);
+  }
+  q_lo = __reduce_min_sync(0xffffffffu, q_lo);
+  q_hi = __reduce_max_sync(0xffffffffu, q_hi);
+
+  const int mine = (g.cnt - warp + kWarps - 1) / kWarps;       // blocks of this warp (may be <= 0)
+  for (int i = 0; i < mine; ++i) {
+    const int blk = g.s0 + warp + i * kWarps;
+    fetch(g, i + kStages - 1);
+    copies_wait<kStages - 1>();
+    const uint8_t* st = ring + stage_out * stage_bytes(D);
+    stage_out = stage_out + 1 == kStages ? 0 : stage_out + 1;
+    uint32_t ksc, vs;
+    if constexpr (D == 128) {
+      ksc = *reinterpret_cast<const uint32_t*>(st + q4::k_scales(D) + lane * 4);
+      vs = *reinterpret_cast<const uint32_t*>(st + q4::v_scales(D) + lane * 4);
+    } else {
+      const uint32_t two = *reinterpret_cast<const uint16_t*>(st + q4::k_scales(D) + lane * 2);
+      ksc = (two & 0xffu) * 0x101u | (two >> 8) * 0x1010000u;
+      vs = *reinterpret_cast<const uint32_t*>(st + q4::v_scales(D) + ((r >> 1) * 4 + j) * 4);
+    }
+    const int2 xp = *reinterpret_cast<const int2*>(st + q4::block_bytes(D) + lane * 8);
+    // ---- scores, in two chains of products, half as long
+    float acc[4] = {}, odd[4] = {};
+    const uint32_t ks[2] = {q4::scales_to_half2((uint16_t)ksc), q4::scales_to_half2((uint16_t)(ksc >> 16))};
+    const Codes<kB / 4> kc0 = load_codes<kB>(st + q4::k_codes(D) + lane * kB);
+    const Codes<kB / 4> kc1 = load_codes<kB>(st + q4::k_codes(D) + 4 * D + lane * kB);
+#pragma unroll
+    for (int x = 0; x < kB / 4; ++x) {
+      uint32_t ka[4], kb[4];
+      q4::codes_to_half2(kc0.w[x], ka);
+      q4::codes_to_half2(kc1.w[x], kb);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) ka[y] = q4::mul_half2(ka[y], ks[0]), kb[y] = q4::mul_half2(kb[y], ks[1]);
+      mma_f16(acc, ka[0], kb[0], ka[1], kb[1], qf[2 * x][0], qf[2 * x][1]);
+      mma_f16(odd, ka[2], kb[2], ka[3], kb[3], qf[2 * x + 1][0], qf[2 * x + 1][1]);
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) acc[y] += odd[y];
+    // ---- mask: acc[y], acc[2 + y] are rows r, r + 8 against column 2j + y
+    const int row = blk * q4::kRows + r;
+    const bool in0 = row < n_rows && xp.x >= 0, in1 = row + 8 < n_rows && xp.y >= 0;
+    if (!__all_sync(0xffffffffu, in0 && xp.x <= q_lo && in1 && xp.y <= q_lo)) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (!in0 || xp.x > qp[y]) acc[y] = -INFINITY;
+        if (!in1 || xp.y > qp[y]) acc[2 + y] = -INFINITY;
+      }
+      // a row that no query sees may hold anything: its values count as zeros
+      const uint32_t see0 = __ballot_sync(0xffffffffu, in0 && xp.x <= q_hi);
+      const uint32_t see1 = __ballot_sync(0xffffffffu, in1 && xp.y <= q_hi);
+      uint32_t keep = 0;           // bytes of vs: rows 2j, 2j + 1, 2j + 8, 2j + 9; lane 4r' speaks for row r'
+      if (see0 >> (8 * j) & 1) keep |= 0x000000ffu;
+      if (see0 >> (8 * j + 4) & 1) keep |= 0x0000ff00u;
+      if (see1 >> (8 * j) & 1) keep |= 0x00ff0000u;
+      if (see1 >> (8 * j + 4) & 1) keep |= 0xff000000u;
+      vs &= keep;
+    }
+    // ---- weights
+    bool above = false;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) above |= fmaxf(acc[y], acc[2 + y]) * c2[y] > ref[y] + (kSlack + kShift);
+    if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float m = fmaxf(acc[y], acc[2 + y]) * c2[y];
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        const float next = fmaxf(ref[y], m - kShift);
+        const float f = ex2(ref[y] - next);
+        ref[y] = next;
+        sum[y] *= f;
+#pragma unroll
+        for (int m2 = 0; m2 < KS; ++m2) o[m2][y] *= f, o[m2][2 + y] *= f;
+      }
+    }
+    float p[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      p[y] = ex2(fmaf(acc[y], c2[y & 1], -ref[y & 1]));
+      sum[y & 1] += p[y];
+    }
+    const uint32_t pf0 = transpose8(pack_half2(p[0], p[1])), pf1 = transpose8(pack_half2(p[2], p[3]));
+    // ---- output
+    const Codes<kB / 4> vc0 = load_codes<kB>(st + q4::v_codes(D) + lane * kB);
+    const Codes<kB / 4> vc1 = load_codes<kB>(st + q4::v_codes(D) + 4 * D + lane * kB);
+    const uint32_t vs2[2] = {q4::scales_to_half2((uint16_t)vs), q4::scales_to_half2((uint16_t)(vs >> 16))};
+#pragma unroll
+    for (int x = 0; x < kB / 4; ++x) {
+      uint32_t va[4], vb[4];
+      q4::codes_to_half2(vc0.w[x], va);
+      q4::codes_to_half2(vc1.w[x], vb);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) va[y] = q4::mul_half2(va[y], vs2[0]), vb[y] = q4::mul_half2(vb[y], vs2[1]);
+      mma_f16(o[2 * x], va[0], va[1], vb[0], vb[1], pf0, pf1);
+      mma_f16(o[2 * x + 1], va[2], va[3], vb[2], vb[3], pf0, pf1);
+    }
+  }
+}
+
+// Joins the CTA's warps, in warp order, into sum_o [R][D] and sum_ml [R]: shared
+// or global memory.
+template <int D>
+__device__ __forceinline__ void join_warps(const Acc<D>& x, int R, float2 (*s_ml)[kCols], float* s_o, float* sum_o,
+                                           float2* sum_ml) {
+  constexpr int KS = D / 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    float v = x.sum[y];
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if (r == 0) s_ml[warp][2 * j + y] = make_float2(x.ref[y], v);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int col = 2 * j + y;
+    if (col >= R) continue;
+    float top = s_ml[0][col].x;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][col].x);
+    const float f = ex2(x.ref[y] - top);
+    float* to = s_o + (warp * R + col) * o_stride(D) + 2 * r;
+#pragma unroll
+    for (int m = 0; m < KS; ++m)
+      *reinterpret_cast<float2*>(to + 16 * m) = make_float2(x.o[m][y] * f, x.o[m][2 + y] * f);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
+    const int col = i / (D / 4), at = i % (D / 4) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 z = *reinterpret_cast<const float4*>(s_o + (w * R + col) * o_stride(D) + at);
+      v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
+    }
+    *reinterpret_cast<float4*>(sum_o + col * D + at) = v;
+  }
+  if (threadIdx.x < R) {
+    float top = kNoRef, l = 0.f;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][threadIdx.x].x);
+    for (int w = 0; w < kWarps; ++w) l += s_ml[w][threadIdx.x].y * ex2(s_ml[w][threadIdx.x].x - top);
+    sum_ml[threadIdx.x] = make_float2(top, l);
+  }
+}
+
+// What does not depend on the previous grid comes before the wait for it: the
+// tokens of columns 2j and 2j + 1, and the arguments' first loads.
+__device__ __forceinline__ void begin(const AttendArgs& a, int (&t_of)[2]) {
+  const int j = threadIdx.x & 3;
+  t_of[0] = 2 * j % a.T, t_of[1] = (2 * j + 1) % a.T;
+  asm volatile("" ::"l"(a.q), "l"(a.cache), "l"(a.pos), "l"(a.rows), "l"(a.q_pos), "l"(a.part_ml), "l"(a.part_o),
+               "l"(a.place), "r"(a.extra), "r"(a.P), "r"(a.inv_h), "f"(a.scale));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ float2 s_ml[kWarps][kCols];
   __shared__ SlotTable slots;
   fill_slots(a, slots);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
-  const int R = a.G * a.T;           // query rows, at most kCols
-  // what does not depend on the previous grid comes before the wait for it: the tokens of
-  // columns 2j and 2j + 1, and the arguments' first loads
-  const int t_of[2] = {2 * j % a.T, (2 * j + 1) % a.T};
-  asm volatile("" ::"l"(a.q), "l"(a.cache), "l"(a.pos), "l"(a.rows), "l"(a.q_pos), "l"(a.part_ml), "l"(a.part_o),
-               "l"(a.place), "r"(a.extra), "r"(a.P), "r"(a.inv_h), "f"(a.scale));
+  int t_of[2];
+  begin(a, t_of);
   __syncthreads();
   grid_dep_wait();
   grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int R = a.G * a.T;           // query rows, at most kCols
   float* s_o = reinterpret_cast<float*>(dyn);              // [kWarps][R][o_stride]
   uint8_t* ring = dyn + o_bytes(D, R) + warp * kStages * stage_bytes(D);
   const uint32_t ring_u = smem_u32(ring);
@@ -289,166 +520,18 @@ __global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid
   // committed whether or not there is one, so that the waits can count
   int stage_in = 0, stage_out = 0;
   const auto fetch = [&](const Segment& x, int i) {
-    const int in = warp + i * kWarps;
-    if (in < x.cnt)
-      copy_block<D>(ring_u + stage_in * stage_bytes(D), x.rec + (int64_t)in * q4::block_bytes(D),
-                    x.pos + (int64_t)in * q4::kRows, lane);
-    copies_commit();
+    fetch_block<D>(x, warp + i * kWarps, ring_u + stage_in * stage_bytes(D), lane);
     stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
   };
   bool started = false;
-
-  while (more) {
-    const int bh = g.bh, n_rows = g.n_rows;
-    const int b = batch_of(a, bh);
-
-    // queries: column n = lane / 4, quarter j of its dims
-    uint32_t w[D / 8];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) w[i] = 0;
-    if (r < R) {
-      const uint4* p = reinterpret_cast<const uint4*>(a.q + ((int64_t)bh * R + r) * D + j * (D / 4));
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 v = __ldg(p + i);
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-      }
-    }
-    int qp[2];                       // positions of columns 2j and 2j + 1
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-      qp[y] = 2 * j + y < R ? __ldg(a.q_pos + (int64_t)b * a.T + t_of[y]) : -1;
-    if (!started)                    // behind the queries' loads, which the blocks' traffic would hold up
+  const auto start = [&] {
+    if (!started)
       for (int i = 0; i < kStages - 1; ++i) fetch(g, i);
     started = true;
-    uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
-    mx = max(mx & 0xffffu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // scale by the power of two that brings the row's largest value into [1, 2)
-    const uint32_t e = mx >> 7, ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
-    const float down = __uint_as_float((254u - ee) << 23);
-    const float c = __uint_as_float(ee << 23) * a.scale;
-    uint32_t qf[KS][2];
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        qf[s][y] = pack_half2(__uint_as_float(q4::bf16_of(w, 2 * s + y) << 16) * down,
-                              __uint_as_float(q4::bf16_of(w, kB + 2 * s + y) << 16) * down);
-    float c2[2];                     // factor from accumulator to log2 units, columns 2j and 2j + 1
-    int q_lo = INT32_MAX, q_hi = -1;
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      c2[y] = __shfl_sync(0xffffffffu, c, (2 * j + y) * 4);
-      if (2 * j + y < R) q_lo = min(q_lo, qp[y]), q_hi = max(q_hi, qp[y]);
-    }
-    q_lo = __reduce_min_sync(0xffffffffu, q_lo);
-    q_hi = __reduce_max_sync(0xffffffffu, q_hi);
-
-    float o[KS][4], ref[2] = {kNoRef, kNoRef}, sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int m = 0; m < KS; ++m)
-#pragma unroll
-      for (int y = 0; y < 4; ++y) o[m][y] = 0.f;
-
-    const int mine = (g.cnt - warp + kWarps - 1) / kWarps;       // blocks of this warp (may be <= 0)
-    for (int i = 0; i < mine; ++i) {
-      const int blk = g.s0 + warp + i * kWarps;
-      fetch(g, i + kStages - 1);
-      copies_wait<kStages - 1>();
-      const uint8_t* st = ring + stage_out * stage_bytes(D);
-      stage_out = stage_out + 1 == kStages ? 0 : stage_out + 1;
-      uint32_t ksc, vs;
-      if constexpr (D == 128) {
-        ksc = *reinterpret_cast<const uint32_t*>(st + q4::k_scales(D) + lane * 4);
-        vs = *reinterpret_cast<const uint32_t*>(st + q4::v_scales(D) + lane * 4);
-      } else {
-        const uint32_t two = *reinterpret_cast<const uint16_t*>(st + q4::k_scales(D) + lane * 2);
-        ksc = (two & 0xffu) * 0x101u | (two >> 8) * 0x1010000u;
-        vs = *reinterpret_cast<const uint32_t*>(st + q4::v_scales(D) + ((r >> 1) * 4 + j) * 4);
-      }
-      const int2 xp = *reinterpret_cast<const int2*>(st + q4::block_bytes(D) + lane * 8);
-      // ---- scores, in two chains of products, half as long
-      float acc[4] = {}, odd[4] = {};
-      const uint32_t ks[2] = {q4::scales_to_half2((uint16_t)ksc), q4::scales_to_half2((uint16_t)(ksc >> 16))};
-      const Codes<kB / 4> kc0 = load_codes<kB>(st + q4::k_codes(D) + lane * kB);
-      const Codes<kB / 4> kc1 = load_codes<kB>(st + q4::k_codes(D) + 4 * D + lane * kB);
-#pragma unroll
-      for (int x = 0; x < kB / 4; ++x) {
-        uint32_t ka[4], kb[4];
-        q4::codes_to_half2(kc0.w[x], ka);
-        q4::codes_to_half2(kc1.w[x], kb);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) ka[y] = q4::mul_half2(ka[y], ks[0]), kb[y] = q4::mul_half2(kb[y], ks[1]);
-        mma_f16(acc, ka[0], kb[0], ka[1], kb[1], qf[2 * x][0], qf[2 * x][1]);
-        mma_f16(odd, ka[2], kb[2], ka[3], kb[3], qf[2 * x + 1][0], qf[2 * x + 1][1]);
-      }
-#pragma unroll
-      for (int y = 0; y < 4; ++y) acc[y] += odd[y];
-      // ---- mask: acc[y], acc[2 + y] are rows r, r + 8 against column 2j + y
-      const int row = blk * q4::kRows + r;
-      const bool in0 = row < n_rows && xp.x >= 0, in1 = row + 8 < n_rows && xp.y >= 0;
-      if (!__all_sync(0xffffffffu, in0 && xp.x <= q_lo && in1 && xp.y <= q_lo)) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          if (!in0 || xp.x > qp[y]) acc[y] = -INFINITY;
-          if (!in1 || xp.y > qp[y]) acc[2 + y] = -INFINITY;
-        }
-        // a row that no query sees may hold anything: its values count as zeros
-        const uint32_t see0 = __ballot_sync(0xffffffffu, in0 && xp.x <= q_hi);
-        const uint32_t see1 = __ballot_sync(0xffffffffu, in1 && xp.y <= q_hi);
-        uint32_t keep = 0;           // bytes of vs: rows 2j, 2j + 1, 2j + 8, 2j + 9; lane 4r' speaks for row r'
-        if (see0 >> (8 * j) & 1) keep |= 0x000000ffu;
-        if (see0 >> (8 * j + 4) & 1) keep |= 0x0000ff00u;
-        if (see1 >> (8 * j) & 1) keep |= 0x00ff0000u;
-        if (see1 >> (8 * j + 4) & 1) keep |= 0xff000000u;
-        vs &= keep;
-      }
-      // ---- weights
-      bool above = false;
-#pragma unroll
-      for (int y = 0; y < 2; ++y) above |= fmaxf(acc[y], acc[2 + y]) * c2[y] > ref[y] + (kSlack + kShift);
-      if (__any_sync(0xffffffffu, above)) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float m = fmaxf(acc[y], acc[2 + y]) * c2[y];
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          const float next = fmaxf(ref[y], m - kShift);
-          const float f = ex2(ref[y] - next);
-          ref[y] = next;
-          sum[y] *= f;
-#pragma unroll
-          for (int m2 = 0; m2 < KS; ++m2) o[m2][y] *= f, o[m2][2 + y] *= f;
-        }
-      }
-      float p[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        p[y] = ex2(fmaf(acc[y], c2[y & 1], -ref[y & 1]));
-        sum[y & 1] += p[y];
-      }
-      const uint32_t pf0 = transpose8(pack_half2(p[0], p[1])), pf1 = transpose8(pack_half2(p[2], p[3]));
-      // ---- output
-      const Codes<kB / 4> vc0 = load_codes<kB>(st + q4::v_codes(D) + lane * kB);
-      const Codes<kB / 4> vc1 = load_codes<kB>(st + q4::v_codes(D) + 4 * D + lane * kB);
-      const uint32_t vs2[2] = {q4::scales_to_half2((uint16_t)vs), q4::scales_to_half2((uint16_t)(vs >> 16))};
-#pragma unroll
-      for (int x = 0; x < kB / 4; ++x) {
-        uint32_t va[4], vb[4];
-        q4::codes_to_half2(vc0.w[x], va);
-        q4::codes_to_half2(vc1.w[x], vb);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) va[y] = q4::mul_half2(va[y], vs2[0]), vb[y] = q4::mul_half2(vb[y], vs2[1]);
-        mma_f16(o[2 * x], va[0], va[1], vb[0], vb[1], pf0, pf1);
-        mma_f16(o[2 * x + 1], va[2], va[3], vb[2], vb[3], pf0, pf1);
-      }
-    }
-
+  };
+  while (more) {
+    Acc<D> acc;
+    attend_segment<D>(a, g, batch_of(a, g.bh), t_of, ring, stage_out, start, fetch, acc);
     // the next head's first blocks come in while this one is joined.  Groups that the
     // loop's tail committed empty are behind the ones it used; the ring starts afresh.
     Segment next;
@@ -456,50 +539,92 @@ __global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_kernel(const __grid
     stage_in = stage_out;
     if (more)
       for (int i = 0; i < kStages - 1; ++i) fetch(next, i);
-
-    // ---- join the warps, in warp order
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      float v = sum[y];
-      v += __shfl_xor_sync(0xffffffffu, v, 4);
-      v += __shfl_xor_sync(0xffffffffu, v, 8);
-      v += __shfl_xor_sync(0xffffffffu, v, 16);
-      if (r == 0) s_ml[warp][2 * j + y] = make_float2(ref[y], v);
-    }
-    __syncthreads();
-    const int64_t slot = (int64_t)blockIdx.x + bh;
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int col = 2 * j + y;
-      if (col >= R) continue;
-      float top = s_ml[0][col].x;
-#pragma unroll
-      for (int x = 1; x < kWarps; ++x) top = fmaxf(top, s_ml[x][col].x);
-      const float f = ex2(ref[y] - top);
-      float* to = s_o + (warp * R + col) * o_stride(D) + 2 * r;
-#pragma unroll
-      for (int m = 0; m < KS; ++m) *reinterpret_cast<float2*>(to + 16 * m) = make_float2(o[m][y] * f, o[m][2 + y] * f);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
-      const int col = i / (D / 4), at = i % (D / 4) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) {
-        const float4 z = *reinterpret_cast<const float4*>(s_o + (x * R + col) * o_stride(D) + at);
-        v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
-      }
-      *reinterpret_cast<float4*>(a.part_o + (slot * R + col) * D + at) = v;
-    }
-    if (threadIdx.x < R) {
-      float top = kNoRef, l = 0.f;
-      for (int x = 0; x < kWarps; ++x) top = fmaxf(top, s_ml[x][threadIdx.x].x);
-      for (int x = 0; x < kWarps; ++x) l += s_ml[x][threadIdx.x].y * ex2(s_ml[x][threadIdx.x].x - top);
-      a.part_ml[slot * R + threadIdx.x] = make_float2(top, l);
-    }
+    const int64_t part = ((int64_t)blockIdx.x + g.bh) * R;
+    join_warps<D>(acc, R, s_ml, s_o, a.part_o + part * D, a.part_ml + part);
     __syncthreads();
     g = next;
   }
+}
+
+// Few and short heads: a cluster of CTAs per head, each with an equal share of
+// its blocks, which join their parts through each other's shared memory: one
+// launch, no partial results in memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t of_rank(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float remote(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) kvc_attend_q4_cluster_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ float2 s_ml[kWarps][kCols];
+  __shared__ __align__(16) float s_sum[kCols * D];
+  __shared__ float2 s_sum_ml[kCols];
+  int t_of[2];
+  begin(a, t_of);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = a.G * a.T, H = a.s.H_kv;
+  const int bh = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = bh / H, h = bh - b * H;
+  const int64_t cap = a.s.off[h + 1] - a.s.off[h], row0 = (int64_t)b * a.s.off[H] + a.s.off[h];
+  float* s_o = reinterpret_cast<float*>(dyn);
+  uint8_t* ring = dyn + o_bytes(D, R) + warp * kStages * stage_bytes(D);
+  const uint32_t ring_u = smem_u32(ring);
+  grid_dep_wait();
+  grid_dep_launch();
+  int64_t n = (int64_t)__ldg(a.rows + bh) + a.extra;
+  if (n < 0 || n > cap) {
+    if (rank == 0 && threadIdx.x == 0) record_status(a.status, kStatusBadInput);
+    n = n < 0 ? 0 : cap;
+  }
+  const int nb = blocks_of((int)n), per = (nb + kCluster - 1) / kCluster;
+  Segment g;
+  g.f = 0;
+  g.bh = bh;
+  g.n_rows = (int)n;
+  g.s0 = min(rank * per, nb);
+  g.cnt = min(per, nb - g.s0);
+  g.rec = a.cache + (row0 / q4::kRows + g.s0) * q4::block_bytes(D);
+  g.pos = a.pos + row0 + (int64_t)g.s0 * q4::kRows;
+  int stage_in = 0, stage_out = 0;
+  const auto fetch = [&](const Segment& x, int i) {
+    fetch_block<D>(x, warp + i * kWarps, ring_u + stage_in * stage_bytes(D), lane);
+    stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+  };
+  const auto start = [&] {
+    for (int i = 0; i < kStages - 1; ++i) fetch(g, i);
+  };
+  Acc<D> acc;
+  attend_segment<D>(a, g, b, t_of, ring, stage_out, start, fetch, acc);
+  join_warps<D>(acc, R, s_ml, s_o, s_sum, s_sum_ml);
+  cluster_sync();
+  for (int i = rank * kThreads + threadIdx.x; i < R * D; i += kCluster * kThreads) {
+    const int row = i / D, d = i % D;
+    float m[kCluster], l[kCluster], v[kCluster], top = kNoRef, sum = 0.f, o = 0.f;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      const uint32_t ml = of_rank(&s_sum_ml[row], c);
+      m[c] = remote(ml), l[c] = remote(ml + 4), v[c] = remote(of_rank(&s_sum[i], c));
+    }
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) top = fmaxf(top, m[c]);
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      const float f = ex2(m[c] - top);
+      sum = fmaf(l[c], f, sum);
+      o = fmaf(v[c], f, o);
+    }
+    const int64_t at = (int64_t)bh * R + row;
+    a.out[at * D + dim_of<D>(d)] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+    if (a.lse && d == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  }
+  cluster_sync();                    // nobody leaves while its part is read
 }
 
 // One CTA per (sequence, KV head) and query row: joins the parts.  Warp w goes
@@ -582,6 +707,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(con
 
 bool attend_q4_on_tc(int H_q, int H_kv, int T) { return (int64_t)(H_q / H_kv) * T > kCols; }
 
+// Whether clusters take the heads: while two CTAs an SM hold them all and the
+// longest slot leaves no CTA more than kClusterBlocks blocks.  One launch instead
+// of two, and no partial results: 8 heads of 1024, 4096 and 13000 rows take 4.9,
+// 6.3 and 10.6 us instead of 8.0, 10.2 and 14.0; 32 heads of 4096 and 9830 rows 8.7
+// and 15.0 instead of 12.8 and 17.7.  Ranges are even where heads are not: 32
+// unequal heads of up to 16.6K rows take 18.2 us in ranges, 19.0 in clusters, and
+// 8 heads of 40000 rows 19.6 and 24.6.  Clusters of 16 were slower (8 heads of
+// 4096 rows 7.0, 16 heads 11.7 against 8.0), but for one long head alone.
+static bool in_clusters(int BH, const Q4Slots& slots) {
+  int64_t longest = 0;
+  for (int h = 0; h < slots.H_kv; ++h) longest = std::max(longest, slots.off[h + 1] - slots.off[h]);
+  return (int64_t)BH * kCluster <= 2 * (int64_t)num_sms() &&
+         longest <= (int64_t)kCluster * kClusterBlocks * q4::kRows;
+}
+
 Q4AttendPlan plan_attend_q4(int B, int T, int H_q, int H_kv, int D) {
   Q4AttendPlan p{};
   p.P = std::max(num_sms(), 1) * 2;
@@ -608,6 +748,28 @@ cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const
   a.inv_h = (uint32_t)(((1ull << 32) + H - 1) / H);
   a.s = slots;
   const size_t smem = o_bytes(D, R) + kWarps * kStages * stage_bytes(D);
+  if (in_clusters(B * H, slots)) {
+    auto* kern = D == 128 ? kvc_attend_q4_cluster_kernel<128> : kvc_attend_q4_cluster_kernel<64>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(B * H * kCluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    note_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
   auto* scan = D == 128 ? kvc_attend_q4_kernel<128> : kvc_attend_q4_kernel<64>;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(scan), smem);
   if (e == cudaSuccess) e = launch_pdl(scan, dim3(p.P), dim3(kThreads), smem, st, a);
