@@ -322,6 +322,12 @@ ATT = [
     (1, 130, 6, 2, 128, [140, 1000]),
     (1, 300, 3, 1, 64, [777]),
     (70, 1, 4, 2, 128, [40, 90]),
+    # more heads than clusters hold, heads without rows among them, and a slot too long for a cluster
+    (41, 2, 8, 2, 64, [0, 129]),
+    (40, 1, 5, 1, 128, [3]),
+    (20, 1, 14, 2, 128, [17, 700]),
+    (1, 1, 8, 2, 128, [17000, 5]),
+    (1, 2, 6, 2, 64, [33, 20000]),
 ]
 
 
@@ -452,6 +458,17 @@ def test_counts_outside_the_slot_are_clamped_and_recorded(K):
             K.kvc_check_status()
         assert ei.value.code == K.KVC_ERR_DEVICE
         check_attention(K, *args, out, lse)
+    # the same for many heads, and for many query rows
+    for B, T in (40, 1), (1, 9):
+        cache, pos, _, _ = filled(K, B, H, D, so, [32, 32], 83)
+        q, qp = rnd(84, B, Hq, T, D), i32(np.full((B, T), 1000))
+        for rows, extra in ([[40, 5]], 0), ([[-3, 5]], 1), ([[2 ** 31 - 1, 8]], 2 ** 31 - 1):
+            args = (q, cache, pos, i32(rows * B), extra, qp, B, T, Hq, H, D, so)
+            out, lse = attend(K, *args)
+            with pytest.raises(K.KvcError) as ei:
+                K.kvc_check_status()
+            assert ei.value.code == K.KVC_ERR_DEVICE
+            check_attention(K, *args, out, lse, batches=[0, B - 1])
 
 
 @pytest.mark.parametrize("B,Hq,H,T", [(300, 4, 4, 1), (1, 8, 1, 1), (5, 6, 3, 4)])
@@ -514,6 +531,32 @@ def test_offsets_past_32_bits(K):
 
 
 # ------------------------------------------------------------------ as they are used
+@pytest.mark.parametrize("B,T", [(2, 1), (40, 1), (1, 20)])
+def test_two_graphs_share_a_workspace(K, B, T):
+    """Two captured calls over different caches replayed in turn on one stream, on one workspace,
+    give what the calls give alone (clusters, ranges, many rows)."""
+    H, Hq, D, n = 4, 16, 128, [300, 40, 0, 77]
+    so = K.kvc_q4_layout(H, 1000, n, 0)
+    ws = K.attention_q4_workspace(B, T, Hq, H, D)
+    calls, alone = [], []
+    for seed in (201, 301):
+        cache, pos, _, _ = filled(K, B, H, D, so, n, seed)
+        q, qp, rows = rnd(seed + 1, B, Hq, T, D), i32(np.full((B, T), 5000)), i32([n] * B)
+        out, lse = torch.empty_like(q), torch.empty((B, Hq, T), device="cuda")
+        args = (q, cache, pos, rows, 0, qp, B, T, Hq, H, D, so)
+        alone.append(attend(K, *args))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            K.kvc_attention_q4(*args, out, lse, ws)
+        calls.append((graph, out, lse, args))
+    for _ in range(3):
+        for graph, _, _, _ in calls:
+            graph.replay()
+    K.kvc_check_status()
+    for (_, out, lse, _), (o, l) in zip(calls, alone):
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
 def test_another_stream_and_a_replayed_graph(K):
     """A captured decoding step (append, attention) is replayed while the caller's row counts
     grow; it gives what the calls give one by one on another stream."""
