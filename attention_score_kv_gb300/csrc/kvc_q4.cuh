@@ -71,26 +71,37 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t amax, float* inv) {
   return two & 0xffu;
 }
 
-// x / scale as the code conversion needs it.  x has 8 significant bits, the
-// scale 4 and a border between codes 3, so x / scale either is a border
-// exactly or stays a factor of 1 + 2^-9 away from it.  x * inv is within
-// 2^-23 of the quotient; rounding it to 12 significant bits puts it back on
-// the border in the first case and crosses none in the second.
-__device__ __forceinline__ float to_code_range(uint32_t bf16_bits, float inv) {
-  const uint32_t t = __float_as_uint(__uint_as_float(bf16_bits << 16) * inv);
-  return __uint_as_float((t + 0x800u) & 0xfffff000u);
-}
-
-// Two values -> a byte of codes (nearest even, magnitudes above 6 become 6).
-__device__ __forceinline__ uint32_t code_byte(float lo, float hi) {
+// Four pairs of values (packed in two words each: lo and hi, two pairs a word)
+// -> four bytes of codes, inv the reciprocals of the pairs' two scales.
+// x has 8 significant bits, the scale 4 and a border between codes 3, so x /
+// scale either is a border exactly or stays a factor of 1 + 2^-9 away from it.
+// x * inv is within 2^-23 of the quotient; rounding it to fp16's 11 significant
+// bits puts it back on the border in the first case and crosses none in the
+// second.  Magnitudes above 6 become 6.
+__device__ __forceinline__ uint32_t code_bytes(const uint32_t* lo, const uint32_t* hi, float2 inv) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t l = lo[i >> 1], u = hi[i >> 1];
+    const float2 x = make_float2(__uint_as_float((i & 1) ? l & 0xffff0000u : l << 16),
+                                 __uint_as_float((i & 1) ? u & 0xffff0000u : u << 16));
+    float2 t;
+    asm("mul.rn.f32x2 %0, %1, %2;\n"
+        : "=l"(reinterpret_cast<uint64_t&>(t))
+        : "l"(reinterpret_cast<const uint64_t&>(x)), "l"(reinterpret_cast<const uint64_t&>(inv)));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(h[i]) : "f"(t.y), "f"(t.x));
+  }
   uint32_t r;
-  asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n cvt.u32.u8 %0, b;\n}\n"
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+      " cvt.rn.satfinite.e2m1x2.f16x2 b0, %1;\n cvt.rn.satfinite.e2m1x2.f16x2 b1, %2;\n"
+      " cvt.rn.satfinite.e2m1x2.f16x2 b2, %3;\n cvt.rn.satfinite.e2m1x2.f16x2 b3, %4;\n"
+      " mov.b32 %0, {b0, b1, b2, b3};\n}\n"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
   return r;
 }
 
-// Bit c of a uint4's values: value i (0..7) of eight packed bf16.
+// Bits of value i of packed bf16.
 __device__ __forceinline__ uint32_t bf16_of(const uint32_t* w, int i) {
   return (i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xffffu);
 }

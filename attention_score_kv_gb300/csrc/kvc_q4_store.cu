@@ -131,16 +131,7 @@ __device__ void store_block(uint8_t* rec, const __nv_bfloat16* __restrict__ k, c
     }
     uint32_t c[kB / 4];
 #pragma unroll
-    for (int b4 = 0; b4 < kB / 4; ++b4) {
-      c[b4] = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = b4 * 4 + i;
-        c[b4] |= q4::code_byte(q4::to_code_range(q4::bf16_of(w, b), inv[0]),
-                               q4::to_code_range(q4::bf16_of(w, kB + b), inv[1]))
-                 << (8 * i);
-      }
-    }
+    for (int x = 0; x < kB / 4; ++x) c[x] = q4::code_bytes(w + 2 * x, w + kB / 2 + 2 * x, make_float2(inv[0], inv[1]));
     store_bytes<kB>(rec + q4::k_codes(D) + row * (D / 2) + j * kB, c);
     if constexpr (D == 128)
       *reinterpret_cast<uint16_t*>(rec + q4::k_scales(D) + (lane * 2 + s) * 2) = (uint16_t)(sc[0] | sc[1] << 8);
@@ -172,16 +163,7 @@ __device__ void store_block(uint8_t* rec, const __nv_bfloat16* __restrict__ k, c
     uint8_t* pc = rec + q4::v_codes(D) + s * 4 * D + lane * kB;
     uint32_t c[kB / 4];
 #pragma unroll
-    for (int b4 = 0; b4 < kB / 4; ++b4) {
-      c[b4] = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int b = b4 * 4 + i;
-        c[b4] |= q4::code_byte(q4::to_code_range(q4::bf16_of(w[0], b), inv[0]),
-                               q4::to_code_range(q4::bf16_of(w[1], b), inv[1]))
-                 << (8 * i);
-      }
-    }
+    for (int x = 0; x < kB / 4; ++x) c[x] = q4::code_bytes(w[0] + 2 * x, w[1] + 2 * x, make_float2(inv[0], inv[1]));
     if (what[0] == kLeave || what[1] == kLeave) {
       const uint32_t mine = what[0] == kLeave ? 0xf0f0f0f0u : 0x0f0f0f0fu;
       uint32_t old[kB / 4];
