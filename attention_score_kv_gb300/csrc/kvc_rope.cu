@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kRopeThreads) kvc_qk_norm_rope_kernel(const __
         const uint64_t at = (uint64_t)(int64_t)a.pos[tok0 + t] * frac;
         float s, c;
         sincospif((float)(int32_t)(at >> 32) * (1.0f / 2147483648.0f), &s, &c);
-        turn[t][f] = make_float2(c, s);
+        // where the lanes of a head read side by side
+        turn[t][INTER ? (f & 3) * (2 * rot) + (f >> 2) : (f & 7) * rot + (f >> 3)] = make_float2(c, s);
       }
       __syncthreads();
     }
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kRopeThreads) kvc_qk_norm_rope_kernel(const __
           if constexpr (INTER) {
 #pragma unroll
             for (int z = 0; z < 8; ++z) {
-              const float2 t = cs[(z < 4 ? c0 : c1) * 4 + (z & 3)];
+              const float2 t = cs[(z & 3) * (2 * rot) + (z < 4 ? c0 : c1)];
               const float p = y[2 * z], r = y[2 * z + 1];
               y[2 * z] = p * t.x - r * t.y;
               y[2 * z + 1] = r * t.x + p * t.y;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kRopeThreads) kvc_qk_norm_rope_kernel(const __
           } else {
 #pragma unroll
             for (int z = 0; z < 8; ++z) {
-              const float2 t = cs[c0 * 8 + z];
+              const float2 t = cs[z * rot + c0];
               const float p = y[z], r = y[8 + z];
               y[z] = p * t.x - r * t.y;
               y[8 + z] = r * t.x + p * t.y;
