@@ -27,6 +27,13 @@
 //   rows    row k = r + 8s of block x of a warp's two is row 8 (r / 2) + 4x + 2s +
 //           r % 2 of its 32: the four rows of a value pair j, twice, side by side
 //   values  dim y of slice r is row r*D/8 + (y ^ 4 (r % 2)) of V^T
+// Measured: 512 tokens of 32 heads over 8 heads of 4.9K rows, 38.7 GFLOP, take 46.6
+// us (830 TFLOP/s), 2000 cycles a tile where the products are 1024 (the tensor
+// pipe is active 43% of the time).  The converters take 1400 of them, and a tile
+// moves 164 KB through shared memory, 1280 cycles at 128 bytes.  On the way: one
+// warp issuing both products 52.5 us, a lane polling alone 57, codes loaded ahead
+// into registers 56 (a proxy fence waits for loads in flight), eight converter
+// warps with 96 registers a thread 48.8.
 // Few row tiles leave SMs idle; then the cache rows are split over several CTAs
 // per row tile, whose parts a second kernel joins in order.
 #include <algorithm>

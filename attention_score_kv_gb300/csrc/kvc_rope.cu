@@ -14,6 +14,13 @@
 // its upper 32 bits are the angle to 2^-32 of a turn (times 2 pi), exact for
 // every int32 position.
 //
+// Memory bounds it: every value is read and written once.  A chunk of 2048
+// tokens of 32 + 2 x 8 heads of 128 takes 12.2 us (50 MB, 4.1 TB/s), one token
+// 2.8 us.  Each thread has three shares of 32 bytes on their way before the
+// angles are worked out, once per token for all of its heads (one token a CTA and
+// no loads ahead: 15.4 us; with the table in frequency order, four lanes on a
+// bank: 14.3 us).
+//
 // Eight lanes hold a head of 128 (four one of 64): 16 values each, as two
 // 16-byte vectors that hold both halves of the rotated pairs, so the only
 // exchange between lanes is the norm's sum.
