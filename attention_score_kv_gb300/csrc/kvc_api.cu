@@ -93,21 +93,21 @@ cudaError_t allow_smem(const void* kernel, size_t smem) {
     int dev;
     size_t smem;
   };
-  static std::vector<Entry> known;
+  static Entry known[64];            // the kernels that ask are a handful per device
+  static int n_known = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lk(g_mu);
-  for (Entry& x : known)
-    if (x.kernel == kernel && x.dev == dev) {
-      if (x.smem >= smem) return cudaSuccess;
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e == cudaSuccess) x.smem = smem;
-      return e;
-    }
+  Entry* at = nullptr;
+  for (int i = 0; i < n_known && !at; ++i)
+    if (known[i].kernel == kernel && known[i].dev == dev) at = &known[i];
+  if (at && at->smem >= smem) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) known.push_back({kernel, dev, smem});
-  return e;
+  if (e != cudaSuccess) return e;
+  if (!at && n_known < 64) *(at = &known[n_known++]) = Entry{kernel, dev, smem};
+  if (at) at->smem = smem;
+  return cudaSuccess;
 }
 
 uint32_t wait_limit_polls() {

@@ -355,8 +355,10 @@ def kvc_qk_norm_rope(q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleav
     """Norm of queries and keys per head and position rotation, into q_out and
     the active layer's buffers (see include/kvc.h)."""
     dev = _cur_dev()
-    bf, ok = torch.bfloat16, B > 0 and T > 0 and H_q > 0 and H_kv > 0 and D > 0
-    if ok:
+    bf = torch.bfloat16
+    if B < 1 or T < 1 or H_q < 1 or H_kv < 1 or D < 1:   # refused below
+        q, k, v = _ptr(q), _ptr(k), _ptr(v)
+    else:
         q = _tokens_arg(q, B, T, H_q * D, q_ld, "q", dev)
         k = _tokens_arg(k, B, T, H_kv * D, k_ld, "k", dev)
         v = _tokens_arg(v, B, T, H_kv * D, v_ld, "v", dev)
@@ -426,8 +428,8 @@ def kvc_compress_layer_q4(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent,
         N, layer, B, S, C, H_q, H_kv, D, W, _host(K_l, ctypes.c_int32, H_kv, "K_l"), sink, recent, pool_k, b_s,
         _arg(q_win, bf, B * H_q * W * D, "q_win", dev), _arg(k, bf, B * H_kv * S * D, "k", dev),
         _arg(v, bf, B * H_kv * S * D, "v", dev), so, _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev),
-        _arg(pos, torch.int32, n, "pos", dev), _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _event(v_ready),
-        _stream(stream)))
+        _arg(pos, torch.int32, n, "pos", dev), _arg(ws, torch.uint8, 0, "ws", dev),
+        ws.numel() if ws_bytes is None else ws_bytes, _event(v_ready), _stream(stream)))
 
 
 def kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D) -> int:
@@ -448,7 +450,8 @@ def kvc_attention_q4(q, cache, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot
                                  _arg(pos, i32, n, "pos", dev), _arg(rows, i32, B * H_kv, "rows", dev), extra,
                                  _arg(q_pos, i32, B * T, "q_pos", dev), B, T, H_q, H_kv, D, so,
                                  _arg(out, bf, nq * D, "out", dev), _arg(lse, torch.float32, nq, "lse", dev),
-                                 _ptr(ws), ws.numel() if ws_bytes is None else ws_bytes, _stream(stream)))
+                                 _arg(ws, torch.uint8, 0, "ws", dev), ws.numel() if ws_bytes is None else ws_bytes,
+                                 _stream(stream)))
 
 
 def kvc_check_status(stream=None) -> None:

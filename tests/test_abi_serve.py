@@ -137,6 +137,9 @@ def test_host_tensors_and_wrong_types_are_refused(K):
     with pytest.raises(K.KvcError) as ei:          # wrong type, before any look at the device
         K.kvc_qk_norm_rope(**{**ROPE, "q": q.float()})
     assert ei.value.code == -1 and "float32" in str(ei.value)
+    with pytest.raises(K.KvcError) as ei:          # no tokens: refused with the tensors as they are
+        K.kvc_qk_norm_rope(**{**ROPE, "q": q, "T": 0})
+    assert ei.value.code == -1
     with pytest.raises(K.KvcError) as ei:
         K.kvc_read_q4(**{**READ, "slot_off": [0, 16]})   # too short a host array
     assert ei.value.code == -1

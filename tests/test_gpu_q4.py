@@ -695,7 +695,8 @@ def test_tensors_of_another_place_or_kind_are_refused(K):
     call = lambda **o: K.kvc_attention_q4(**{**dict(q=q, cache=cache, pos=pos, rows=rows, extra=0, q_pos=qp, B=1, T=1,
                                                     H_q=2, H_kv=1, D=D, slot_off=so, out=out, lse=None, ws=ws), **o})
     for bad in (dict(q=q.cpu()), dict(rows=rows.long()), dict(cache=cache[:-1]), dict(out=out.float()),
-                dict(q=torch.stack((q, q), -1)[..., 0]), dict(pos=pos[1:]), dict(ws=ws[:256]), dict(ws=ws[1:])):
+                dict(q=torch.stack((q, q), -1)[..., 0]), dict(pos=pos[1:]), dict(ws=ws[:256]), dict(ws=ws[1:]),
+                dict(ws=ws.cpu()), dict(ws=ws.float())):
         with pytest.raises(K.KvcError):
             call(**bad)
     call()
