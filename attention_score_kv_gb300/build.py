@@ -1,8 +1,10 @@
 """Build libkvc.so in-tree from csrc/ for GB300 (sm_103a).
 
 Each translation unit is compiled by nvcc in parallel, then linked into
-``attention_score_kv_gb300/libkvc.so`` (static CUDA runtime).  Run
-``python -m attention_score_kv_gb300.build`` or call :func:`build`.
+``attention_score_kv_gb300/libkvc.so`` (static CUDA runtime); the binding's
+argument marshalling (``kvc_python.c``) is compiled by the C compiler for the
+running Python beside it.  Run ``python -m attention_score_kv_gb300.build`` or
+call :func:`build`.
 """
 
 from __future__ import annotations
@@ -12,11 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvc.so")
+BINDING = os.path.join(HERE, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr"]
@@ -33,6 +37,24 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/kvc_python.c for the running Python; returns its path."""
+    src = os.path.join(CSRC, "kvc_python.c")
+    deps = [src, os.path.join(HERE, "..", "include", "kvc.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return BINDING
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler found (set CC)")
+    tmp = BINDING + ".tmp"
+    rc, cmd, out = _run([cc, "-O2", "-shared", "-fPIC", "-Wall", "-Wextra", "-I", sysconfig.get_path("include"), src,
+                         "-o", tmp])
+    if rc:
+        raise RuntimeError(f"binding failed to compile:\n{cmd}\n{out}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def _run(cmd):
     p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     return p.returncode, " ".join(cmd), p.stdout
@@ -46,6 +68,7 @@ def build(verbose: bool = False, extra_flags=None, force: bool = False, lib_path
     ``build_dir`` place the library and objects elsewhere (default: in-tree).
     """
     nvcc = _nvcc()
+    build_binding(force)
     LIB = lib_path or globals()["LIB"]
     BUILD = build_dir or globals()["BUILD"]
     os.makedirs(BUILD, exist_ok=True)

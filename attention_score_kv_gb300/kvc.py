@@ -1,7 +1,8 @@
 """ctypes binding of libkvc.so: the C ABI of include/kvc.h, same names.
 
 Argument marshalling only: torch tensors are passed as device pointers, host
-budget arrays as int32 arrays, the stream as the caller's current CUDA stream.
+budget arrays as int32 arrays, the stream as the caller's current CUDA stream
+(the calls of a decoding step through csrc/kvc_python.c).
 Every step of the compression runs in the library's CUDA kernels; there is no
 other code path.  Importing this module fails loudly if the library has not
 been built (``python -m attention_score_kv_gb300.build``).
@@ -13,6 +14,8 @@ import ctypes
 import os
 
 import torch
+
+from . import build as _build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # KVC_LIBRARY selects another build of the same library (e.g. one compiled
@@ -45,6 +48,12 @@ class KvcError(RuntimeError):
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python -m attention_score_kv_gb300.build` (nvcc, sm_103a)")
+
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"{_build.BINDING} is missing: build it with "
+                      "`python -m attention_score_kv_gb300.build` (a C compiler and Python's headers)") from e
 
 _lib = ctypes.CDLL(LIB_PATH)
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -156,13 +165,8 @@ def _bad(msg):
     raise KvcError(KVC_ERR_INVALID_ARG, msg)
 
 
-def _arg(t, dtype, n, name, dev):
-    """Device pointer of a contiguous tensor of at least n elements on the current
-    device `dev`; a raw pointer or None passes as it is."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev:
-        return t.data_ptr()
+def _refuse(t, dtype, n, name):
+    """Says why a tensor is no device array of dtype and at least n elements here."""
     if t.dtype != dtype:
         _bad(f"{name} is {t.dtype}, not {dtype}")
     if not t.is_contiguous():
@@ -170,6 +174,16 @@ def _arg(t, dtype, n, name, dev):
     if t.numel() < n:
         _bad(f"{name} holds {t.numel()} elements, needs {n}")
     _bad(f"{name} is on {t.device}, not on the current CUDA device")
+
+
+def _arg(t, dtype, n, name, dev):
+    """Device pointer of a contiguous tensor of at least n elements on the current
+    device `dev`; a raw pointer or None passes as it is."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, dtype, n, name)
+    return t.data_ptr()
 
 
 def _tokens_arg(t, B, T, n, ld, name, dev):
@@ -204,6 +218,19 @@ def _host(arr, ctype, n, name):
     if len(arr) < n:
         _bad(f"{name} holds {len(arr)} values, needs {n}")
     return arr
+
+
+def _host_array(arr, size, n, name):
+    return _host(arr, ctypes.c_int32 if size == 4 else _I64, n, name)
+
+
+# The calls that run once per token and layer take their arguments apart in C
+# (csrc/kvc_python.c): type, size, contiguity and device of every tensor.
+_binding.init(tuple(ctypes.cast(getattr(_lib, f), _P).value for f in
+                    ("kvc_last_error", "kvc_qk_norm_rope", "kvc_gather_q4", "kvc_append_q4", "kvc_read_q4",
+                     "kvc_attention_q4")),
+              (torch.bfloat16, torch.int32, torch.uint8, torch.float32),
+              (_cur_dev, _raw_stream, _refuse, _tokens_arg, _host_array, KvcError))
 
 
 def kvc_last_error() -> str:
@@ -354,20 +381,8 @@ def kvc_qk_norm_rope(q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleav
                      inv_freq, pos, S, row0, q_out, k_act, v_act, stream=None):
     """Norm of queries and keys per head and position rotation, into q_out and
     the active layer's buffers (see include/kvc.h)."""
-    dev = _cur_dev()
-    bf = torch.bfloat16
-    if B < 1 or T < 1 or H_q < 1 or H_kv < 1 or D < 1:   # refused below
-        q, k, v = _ptr(q), _ptr(k), _ptr(v)
-    else:
-        q = _tokens_arg(q, B, T, H_q * D, q_ld, "q", dev)
-        k = _tokens_arg(k, B, T, H_kv * D, k_ld, "k", dev)
-        v = _tokens_arg(v, B, T, H_kv * D, v_ld, "v", dev)
-    _check(_lib.kvc_qk_norm_rope(
-        q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleaved, _arg(q_weight, bf, D, "q_weight", dev),
-        _arg(k_weight, bf, D, "k_weight", dev), eps, _arg(inv_freq, torch.float32, R // 2, "inv_freq", dev),
-        _arg(pos, torch.int32, B * T, "pos", dev), S, row0, _arg(q_out, bf, B * H_q * T * D, "q_out", dev),
-        _arg(k_act, bf, B * H_kv * S * D, "k_act", dev), _arg(v_act, bf, B * H_kv * S * D, "v_act", dev),
-        _stream(stream)))
+    _binding.qk_norm_rope(q, k, v, B, T, H_q, H_kv, D, q_ld, k_ld, v_ld, R, interleaved, q_weight, k_weight, eps,
+                          inv_freq, pos, S, row0, q_out, k_act, v_act, stream)
 
 
 def kvc_q4_layout(H_kv, S, K_l, extra) -> ctypes.Array:
@@ -385,37 +400,15 @@ def _q4_rows(B, H_kv, slot_off):
 
 
 def kvc_gather_q4(k, v, idx, B, H_kv, S, D, K_l, slot_off, cache, pos, stream=None):
-    dev = _cur_dev()
-    bf, i32 = torch.bfloat16, torch.int32
-    so, n = _q4_rows(B, H_kv, slot_off)
-    _check(_lib.kvc_gather_q4(_arg(k, bf, B * H_kv * S * D, "k", dev), _arg(v, bf, B * H_kv * S * D, "v", dev),
-                              _arg(idx, i32, n, "idx", dev), B, H_kv, S, D,
-                              _host(K_l, ctypes.c_int32, H_kv, "K_l"), so,
-                              _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev), _arg(pos, i32, n, "pos", dev),
-                              _stream(stream)))
+    _binding.gather_q4(k, v, idx, B, H_kv, S, D, K_l, slot_off, cache, pos, stream)
 
 
 def kvc_append_q4(k, v, pos_new, B, H_kv, T, D, slot_off, rows, cache, pos, stream=None):
-    dev = _cur_dev()
-    bf, i32 = torch.bfloat16, torch.int32
-    so, n = _q4_rows(B, H_kv, slot_off)
-    _check(_lib.kvc_append_q4(_arg(k, bf, B * H_kv * T * D, "k", dev), _arg(v, bf, B * H_kv * T * D, "v", dev),
-                              _arg(pos_new, i32, B * T, "pos_new", dev), B, H_kv, T, D, so,
-                              _arg(rows, i32, B * H_kv, "rows", dev),
-                              _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev),
-                              _arg(pos, i32, n, "pos", dev), _stream(stream)))
+    _binding.append_q4(k, v, pos_new, B, H_kv, T, D, slot_off, rows, cache, pos, stream)
 
 
 def kvc_read_q4(cache, B, H_kv, D, slot_off, first, n_rows, k_out, v_out, stream=None, out_off=None):
-    dev = _cur_dev()
-    so, n = _q4_rows(B, H_kv, slot_off)
-    nr = _host(n_rows, ctypes.c_int32, H_kv, "n_rows")
-    oo = _host(out_off, _I64, H_kv + 1, "out_off")
-    t = B * (oo[H_kv] if oo is not None else sum(nr[:H_kv]) if nr is not None else 0) * D
-    _check(_lib.kvc_read_q4(_arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev), B, H_kv, D, so,
-                            _arg(first, torch.int32, B * H_kv, "first", dev), nr, oo,
-                            _arg(k_out, torch.bfloat16, t, "k_out", dev), _arg(v_out, torch.bfloat16, t, "v_out", dev),
-                            _stream(stream)))
+    _binding.read_q4(cache, B, H_kv, D, slot_off, first, n_rows, out_off, k_out, v_out, stream)
 
 
 def kvc_compress_layer_q4(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, slot_off,
@@ -441,17 +434,8 @@ def kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D) -> int:
 
 def kvc_attention_q4(q, cache, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot_off, out, lse, ws, ws_bytes=None,
                      stream=None):
-    dev = _cur_dev()
-    bf, i32 = torch.bfloat16, torch.int32
-    so, n = _q4_rows(B, H_kv, slot_off)
-    nq = B * H_q * T
-    _check(_lib.kvc_attention_q4(_arg(q, bf, nq * D, "q", dev),
-                                 _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev),
-                                 _arg(pos, i32, n, "pos", dev), _arg(rows, i32, B * H_kv, "rows", dev), extra,
-                                 _arg(q_pos, i32, B * T, "q_pos", dev), B, T, H_q, H_kv, D, so,
-                                 _arg(out, bf, nq * D, "out", dev), _arg(lse, torch.float32, nq, "lse", dev),
-                                 _arg(ws, torch.uint8, 0, "ws", dev), ws.numel() if ws_bytes is None else ws_bytes,
-                                 _stream(stream)))
+    _binding.attention_q4(q, cache, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot_off, out, lse, ws, ws_bytes,
+                          stream)
 
 
 def kvc_check_status(stream=None) -> None:

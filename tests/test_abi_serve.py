@@ -146,3 +146,67 @@ def test_host_tensors_and_wrong_types_are_refused(K):
     with pytest.raises(K.KvcError) as ei:
         K.kvc_append_q4(**{**APPEND, "pos_new": torch.zeros(2, dtype=torch.int32)})
     assert ei.value.code == -1 and "pos_new" in str(ei.value)
+
+
+def test_host_arrays_of_every_kind_are_taken(K):
+    """Lists, tensors, arrays of the right and of another type: all reach the same check (K_l[1]
+    = 49 does not fit its slot)."""
+    import array
+    import numpy as np
+    import torch
+    for make in (list, tuple, torch.tensor, lambda x: torch.tensor(x, dtype=torch.int32), np.array,
+                 lambda x: np.array(x, dtype=np.int32), lambda x: np.array(x, dtype=np.int64), lambda x: array.array("i", x),
+                 lambda x: array.array("q", x), lambda x: (ctypes.c_int32 * 2)(*x), lambda x: (ctypes.c_int64 * 2)(*x)):
+        with pytest.raises(K.KvcError) as ei:
+            K.kvc_gather_q4(**{**GATHER, "K_l": make([16, 49])})
+        assert ei.value.code == -1 and "out_off" in str(ei.value), make
+    for make in (list, lambda x: (ctypes.c_int64 * 3)(*x), np.array, torch.tensor):
+        with pytest.raises(K.KvcError) as ei:
+            K.kvc_gather_q4(**{**GATHER, "slot_off": make([0, 16, 60])})
+        assert ei.value.code == -1 and "slot_off" in str(ei.value)
+    with pytest.raises(K.KvcError) as ei:                      # every other value of an array
+        K.kvc_gather_q4(**{**GATHER, "K_l": np.array([16, 0, 49, 0], dtype=np.int32)[::2]})
+    assert ei.value.code == -1 and "out_off" in str(ei.value)
+
+
+def test_arguments_of_another_type_are_type_errors(K):
+    for over in (dict(B="1"), dict(S=1.5), dict(k="x"), dict(K_l=3), dict(stream="s")):
+        with pytest.raises((TypeError, AttributeError)):
+            K.kvc_gather_q4(**{**GATHER, **over})
+    with pytest.raises(OverflowError):
+        K.kvc_gather_q4(**{**GATHER, "S": 1 << 40})
+    with pytest.raises(TypeError):
+        K.kvc_qk_norm_rope(**{**ROPE, "eps": "small"})
+
+
+def test_refused_calls_leave_no_references(K):
+    """Arguments are held no longer than the call, whichever check ends it."""
+    import sys
+
+    import torch
+    t = torch.zeros((2, 3, 256), dtype=torch.bfloat16)
+    slot, kl = (ctypes.c_int64 * 3)(*SLOT), [16, 49]
+
+    def calls():
+        for f, a in ((K.kvc_gather_q4, {**GATHER, "slot_off": slot, "K_l": kl}),
+                     (K.kvc_gather_q4, {**GATHER, "slot_off": slot, "k": t}),
+                     (K.kvc_gather_q4, {**GATHER, "slot_off": slot, "stream": t}),
+                     (K.kvc_append_q4, {**APPEND, "slot_off": slot, "k": t}),
+                     (K.kvc_read_q4, {**READ, "slot_off": slot, "n_rows": kl}),
+                     (K.kvc_attention_q4, {**ATTEND, "slot_off": slot, "q": t, "T": 0}),
+                     (K.kvc_qk_norm_rope, {**ROPE, "q": t, "q_ld": 256}),
+                     (K.kvc_qk_norm_rope, {**ROPE, "q": t.float()})):
+            try:
+                f(**a)
+            except (K.KvcError, AttributeError):
+                pass
+            else:
+                raise AssertionError("not refused")
+
+    calls()
+    seen = (t, slot, kl, torch.bfloat16, K.KvcError, None)
+    before = [sys.getrefcount(x) for x in seen]
+    for _ in range(50):
+        calls()
+    after = [sys.getrefcount(x) for x in seen]
+    assert all(abs(a - b) < 40 for a, b in zip(after, before)), (before, after)
