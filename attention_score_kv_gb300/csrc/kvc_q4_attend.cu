@@ -229,8 +229,8 @@ struct Segment {
   int f, bh, cnt, s0, n_rows;        // flat block it starts at; head; blocks; first block in the head; the head's rows
 };
 template <int D>
-__device__ __forceinline__ Segment segment_of(const AttendArgs& a, const SlotTable& t, int f, int f1, int bh, int before,
-                                              int n_rows) {
+__device__ __forceinline__ Segment segment_of(const AttendArgs& a, const SlotTable& t, int f, int f1, int bh,
+                                              int before, int n_rows) {
   const int b = batch_of(a, bh);
   Segment g;
   g.f = f;

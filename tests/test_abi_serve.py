@@ -155,8 +155,8 @@ def test_host_arrays_of_every_kind_are_taken(K):
     import numpy as np
     import torch
     for make in (list, tuple, torch.tensor, lambda x: torch.tensor(x, dtype=torch.int32), np.array,
-                 lambda x: np.array(x, dtype=np.int32), lambda x: np.array(x, dtype=np.int64), lambda x: array.array("i", x),
-                 lambda x: array.array("q", x), lambda x: (ctypes.c_int32 * 2)(*x), lambda x: (ctypes.c_int64 * 2)(*x)):
+                 lambda x: np.array(x, dtype=np.int32), lambda x: np.array(x, dtype=np.int64),
+                 lambda x: array.array("i", x), lambda x: array.array("q", x), lambda x: (ctypes.c_int32 * 2)(*x), lambda x: (ctypes.c_int64 * 2)(*x)):
         with pytest.raises(K.KvcError) as ei:
             K.kvc_gather_q4(**{**GATHER, "K_l": make([16, 49])})
         assert ei.value.code == -1 and "out_off" in str(ei.value), make
