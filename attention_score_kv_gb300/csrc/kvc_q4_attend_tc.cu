@@ -45,9 +45,6 @@
 namespace kvc {
 namespace {
 
-using scan::wait_bar;
-using scan::wait_bar_warp;
-
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
 constexpr int kScoreWarp = kSoftWarps + kCodeWarps, kOutWarp = kScoreWarp + 1, kLoadWarp = kOutWarp + 1;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
@@ -102,15 +99,36 @@ __device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, u
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Waits of a whole warp for several barriers at once: each look at a barrier
-// takes about as long alone as together with the others.
-__device__ __forceinline__ bool wait3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2,
-                                      volatile int* abort_flag, int* status, uint32_t limit) {
-  const bool d0 = tc::mbar_try_wait(b0, p0), d1 = tc::mbar_try_wait(b1, p1), d2 = tc::mbar_try_wait(b2, p2);
-  if (__all_sync(0xffffffffu, d0 && d1 && d2)) return true;
-  return __all_sync(0xffffffffu, wait_bar_warp(b0, p0, abort_flag, status, limit) &&
-                                     wait_bar_warp(b1, p1, abort_flag, status, limit) &&
-                                     wait_bar_warp(b2, p2, abort_flag, status, limit));
+// Bounded waits of a whole warp, as loops of a few instructions: written out by
+// the compiler, the waits made the kernel a fifth longer and 3% slower (its warps
+// run five programs at once).
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "LOOK:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra SEEN;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra LOOK;\n"
+      "SEEN:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(limit)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+// Three barriers: a look at one takes about as long alone as with the others.
+__device__ __forceinline__ bool poll3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2,
+                                      uint32_t limit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q, r;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "LOOK:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6;\n and.pred p, p, q;\n and.pred p, p, r;\n @p bra SEEN;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %7;\n @q bra LOOK;\n"
+      "SEEN:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(b2), "r"(p2), "r"(limit)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
 }
 
 // Two fp32 operations in one instruction.
@@ -137,9 +155,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The warp that brings in the cache: a tile's blocks as they are, in one copy,
 // and its positions, in the tiles' row order, with what the queries see of them.
 template <int D>
-__device__ void load_warp(const TcArgs& a, Bars* bars, uint8_t* raw, Seen* seen, const uint8_t* rec,
-                          const int32_t* pos, int n_rows, int t0, int t1, int q_lo, int q_hi,
-                          volatile int* abort_flag) {
+__device__ bool load_warp(const TcArgs& a, Bars* bars, uint8_t* raw, Seen* seen, const uint8_t* rec,
+                          const int32_t* pos, int n_rows, int t0, int t1, int q_lo, int q_hi) {
   const int lane = threadIdx.x & 31;
   const int n_blocks = (n_rows + q4::kRows - 1) / q4::kRows;
   const int n = t1 - t0;
@@ -162,9 +179,7 @@ __device__ void load_warp(const TcArgs& a, Bars* bars, uint8_t* raw, Seen* seen,
 #pragma unroll
     for (int w = 0; w < 4; ++w) p[w] = next[w];
     if (i + 1 < n) fetch(t + 1, next);
-    if (!__all_sync(0xffffffffu, wait_bar_warp(smem_u32(&bars->raw_empty[st]), ((i / kRaw) & 1) ^ 1, abort_flag,
-                                               a.status, a.wait_limit)))
-      break;
+    if (!poll(smem_u32(&bars->raw_empty[st]), ((i / kRaw) & 1) ^ 1, a.wait_limit)) break;
     Seen& s = seen[i % kSeen];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -184,6 +199,7 @@ __device__ void load_warp(const TcArgs& a, Bars* bars, uint8_t* raw, Seen* seen,
   // every copy issued has landed before the CTA may leave
   for (int y = max(0, i - kRaw); y < i; ++y)
     scan::drain_wait(smem_u32(&bars->raw_full[y % kRaw]), (y / kRaw) & 1, a.status);
+  return i >= n;
 }
 
 template <int kB>
@@ -200,16 +216,16 @@ __device__ __forceinline__ void read_codes(const uint8_t* p, uint32_t (&w)[kB / 
 // A warp of the code converters: 32 rows (two blocks) of every tile.  No load
 // from global memory may be in flight here: the proxy fences would wait for it.
 template <int D>
-__device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, const uint8_t* raw, const Seen* seen,
-                          int n, volatile int* abort_flag) {
+__device__ bool code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV, const uint8_t* raw, const Seen* seen,
+                          int n) {
   constexpr int kB = D / 8;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps, r = lane >> 2, j = lane & 3;
   for (int i = 0; i < n; ++i) {
     const int st = i & 1, rs = i % kRaw, vst = i % kV;
     const uint32_t ph = ((i >> 1) & 1) ^ 1;
-    if (!wait3(smem_u32(&bars->raw_full[rs]), (i / kRaw) & 1, smem_u32(&bars->s_full[st]), ph,
-               smem_u32(&bars->o_done[vst]), ((i / kV) & 1) ^ 1, abort_flag, a.status, a.wait_limit))
-      return;
+    if (!poll3(smem_u32(&bars->raw_full[rs]), (i / kRaw) & 1, smem_u32(&bars->s_full[st]), ph,
+               smem_u32(&bars->o_done[vst]), ((i / kV) & 1) ^ 1, a.wait_limit))
+      return false;
     const uint8_t* rec = raw + rs * raw_bytes(D) + 2 * w * q4::block_bytes(D);
     // ---- keys
     // place of (block b, half s, chunk c) for this lane: tiles are 1024-aligned, so what
@@ -276,6 +292,7 @@ __device__ void code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
       tc::mbar_arrive(smem_u32(&bars->raw_empty[rs]));
     }
   }
+  return true;
 }
 
 // A product takes the tensor core 64 cycles, and arithmetic on descriptors
@@ -301,18 +318,19 @@ __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint3
 // lane that polls alone costs 300 cycles a wait, the warp together 20 to 90);
 // lane 0 issues.
 template <int D>
-__device__ void score_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t tmem, int n, volatile int* abort_flag) {
+__device__ bool score_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t tmem, int n) {
   constexpr uint32_t kId = tc::idesc_f16(kRowsM, kKeys);
   constexpr uint64_t kStage = kKeys * D * 2 >> 4;              // descriptor units of 16 bytes
   const bool issues = (threadIdx.x & 31) == 0;
   const uint64_t k0 = tc::desc_sw128(sK);
-  const auto wait = [&](uint64_t* bar, int phase) {
-    return __all_sync(0xffffffffu, wait_bar_warp(smem_u32(bar), phase & 1, abort_flag, a.status, a.wait_limit));
-  };
-  if (wait(&bars->q_full, 0)) {
+  const auto wait = [&](uint64_t* bar, int phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
+  bool ok = wait(&bars->q_full, 0);
+  if (ok) {
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
-      if (!wait(&bars->kv_full[st], i >> 1) || !wait(&bars->s_free[st], (i >> 1) ^ 1)) break;
+      ok = wait(&bars->kv_full[st], i >> 1) && wait(&bars->s_free[st], (i >> 1) ^ 1);
+      if (!ok) break;
       tc::fence_after_sync();
       if (issues) {
         const uint64_t kd = k0 + st * kStage;
@@ -327,19 +345,20 @@ __device__ void score_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t tm
   }
   if (issues) scan::drain_mma(smem_u32(&bars->drain[0]), a.status);
   __syncwarp();
+  return ok;
 }
 template <int D>
-__device__ void out_warp(const TcArgs& a, Bars* bars, uint32_t sV, uint32_t tmem, int n, volatile int* abort_flag) {
+__device__ bool out_warp(const TcArgs& a, Bars* bars, uint32_t sV, uint32_t tmem, int n) {
   constexpr uint32_t kId = tc::idesc_f16(kRowsM, D);
   constexpr uint64_t kStage = kKeys * D * 2 >> 4;
   const bool issues = (threadIdx.x & 31) == 0;
   const uint64_t v0 = tc::desc_sw128(sV);
-  const auto wait = [&](uint64_t* bar, int phase) {
-    return __all_sync(0xffffffffu, wait_bar_warp(smem_u32(bar), phase & 1, abort_flag, a.status, a.wait_limit));
-  };
+  const auto wait = [&](uint64_t* bar, int phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
+  bool ok = true;
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const int st = i & 1;
-    if (!wait(&bars->kv_full[st], i >> 1) || !wait(&bars->p_full, i)) break;
+    ok = wait(&bars->kv_full[i & 1], i >> 1) && wait(&bars->p_full, i);
+    if (!ok) break;
     tc::fence_after_sync();
     if (issues) {
       const uint64_t vd = v0 + (i % kV) * kStage;
@@ -355,6 +374,7 @@ __device__ void out_warp(const TcArgs& a, Bars* bars, uint32_t sV, uint32_t tmem
   }
   if (issues) scan::drain_mma(smem_u32(&bars->drain[1]), a.status);
   __syncwarp();
+  return ok;
 }
 
 template <int D>
@@ -362,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort;
   __shared__ __align__(16) Seen s_seen[kSeen];
   __shared__ float s_x[2][2][kRowsM];              // what the two threads of a row tell each other
 
@@ -388,7 +407,6 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     for (int i = 0; i < kV; ++i) tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
     tc::mbar_init(smem_u32(&bars.p_full), live_warps);
     tc::mbar_init(smem_u32(&bars.q_full), live_warps);
-    s_abort = 0;
     tc::fence_barrier_init();
   }
   if (warp == kScoreWarp) {
@@ -414,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
   const int key_tiles = (n_rows + kKeys - 1) / kKeys, per = (key_tiles + a.splits - 1) / a.splits;
   const int t0 = min((int)blockIdx.y * per, key_tiles), t1 = min(t0 + per, key_tiles), n = t1 - t0;
 
+  bool ok = true;                    // false: a wait gave up
   if (warp == kLoadWarp) {
     int q_lo = INT32_MAX, q_hi = -1;
     for (int i = lane; i < kRowsM; i += 32) {
@@ -425,14 +444,14 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
     }
     q_lo = __reduce_min_sync(0xffffffffu, q_lo);
     q_hi = __reduce_max_sync(0xffffffffu, q_hi);
-    load_warp<D>(a, &bars, raw, s_seen, a.cache + row0 / q4::kRows * q4::block_bytes(D), a.pos + row0, n_rows, t0, t1,
-                 q_lo, q_hi, &s_abort);
+    ok = load_warp<D>(a, &bars, raw, s_seen, a.cache + row0 / q4::kRows * q4::block_bytes(D), a.pos + row0, n_rows, t0,
+                      t1, q_lo, q_hi);
   } else if (warp >= kSoftWarps && warp < kScoreWarp) {
-    code_warp<D>(a, &bars, sK, sV, raw, s_seen, n, &s_abort);
+    ok = code_warp<D>(a, &bars, sK, sV, raw, s_seen, n);
   } else if (warp == kScoreWarp) {
-    if (n > 0) score_warp<D>(a, &bars, sK, tmem, n, &s_abort);
+    if (n > 0) ok = score_warp<D>(a, &bars, sK, tmem, n);
   } else if (warp == kOutWarp) {
-    if (n > 0) out_warp<D>(a, &bars, sV, tmem, n, &s_abort);
+    if (n > 0) ok = out_warp<D>(a, &bars, sV, tmem, n);
   } else if ((warp & 3) < live_quarters) {
     // ---- softmax: thread (row, half): dims and scores [half * .., ..)
     constexpr int kHalfD = D / 2;
@@ -486,10 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
 
     float ref = kNoRef;
     float2 sum2[2] = {};             // the row's sum, in four parts
-    const auto wait = [&](uint64_t* bar, int phase) {
-      return __all_sync(0xffffffffu, wait_bar_warp(smem_u32(bar), phase & 1, &s_abort, a.status, a.wait_limit));
-    };
-    bool ok = true;                  // a wait that gave up: go on without waiting, so that no barrier is left alone
+    // after a wait that gave up: go on without waiting, so that no barrier is left alone
+    const auto wait = [&](uint64_t* bar, int phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       const uint32_t s_at = tmem + lanes + kColS + st * kKeys + half * 64;
@@ -619,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994530942f;
     }
   }
+  if (!ok && lane == 0) record_status(a.status, kStatusTimeout);
   tc::fence_before_sync();
   __syncthreads();
   if (warp == kScoreWarp) tc::tmem_dealloc(tmem, kCols);
