@@ -27,13 +27,18 @@
 //   rows    row k = r + 8s of block x of a warp's two is row 8 (r / 2) + 4x + 2s +
 //           r % 2 of its 32: the four rows of a value pair j, twice, side by side
 //   values  dim y of slice r is row r*D/8 + (y ^ 4 (r % 2)) of V^T
-// Measured: 512 tokens of 32 heads over 8 heads of 4.9K rows, 38.7 GFLOP, take 46.6
-// us (830 TFLOP/s), 2000 cycles a tile where the products are 1024 (the tensor
-// pipe is active 43% of the time).  The converters take 1400 of them, and a tile
-// moves 164 KB through shared memory, 1280 cycles at 128 bytes.  On the way: one
-// warp issuing both products 52.5 us, a lane polling alone 57, codes loaded ahead
-// into registers 56 (a proxy fence waits for loads in flight), eight converter
-// warps with 96 registers a thread 48.8.
+// Measured: 512 tokens of 32 heads over 8 heads of 4.9K rows, 38.7 GFLOP, take 45.2
+// us (856 TFLOP/s), 1900 to 2000 cycles a tile where the products are 1024.  No one
+// thing bounds them: the converters take 1400 and the softmax 1450 of them, a tile
+// moves 164 KB through shared memory (1280 cycles at 128 bytes), a product beside
+// the softmax's use of tensor memory takes a third longer than alone, and each
+// hand-over from warp to warp 150 to 300.  On the way: one warp issuing both
+// products 52.5 us, a lane polling alone 57, codes loaded ahead into registers 56
+// (a proxy fence waits for loads in flight), eight converter warps with 96
+// registers a thread 48.8, Q in shared memory and P twice in tensor memory 55.8.
+// Pairs of CTAs that convert half of a tile each for products of 256 rows
+// (cta_group::2) have the converters wait half of the time and gain nothing (45.4;
+// D = 64 lost 5%): the hand-overs between the two cost what the halves save.
 // Few row tiles leave SMs idle; then the cache rows are split over several CTAs
 // per row tile, whose parts a second kernel joins in order.
 #include <algorithm>
