@@ -215,6 +215,8 @@ def _host(arr, ctype, n, name):
     if not (isinstance(arr, ctypes.Array) and arr._type_ is ctype):
         vals = [int(x) for x in (arr.tolist() if hasattr(arr, "tolist") else arr)]
         arr = (ctype * len(vals))(*vals)
+        if arr[:] != vals:             # ctypes drops the upper bits
+            _bad(f"{name} holds values that do not fit {8 * ctypes.sizeof(ctype)} bits")
     if len(arr) < n:
         _bad(f"{name} holds {len(arr)} values, needs {n}")
     return arr

@@ -210,3 +210,16 @@ def test_refused_calls_leave_no_references(K):
         calls()
     after = [sys.getrefcount(x) for x in seen]
     assert all(abs(a - b) < 40 for a, b in zip(after, before)), (before, after)
+
+
+@pytest.mark.parametrize("value", [2 ** 31, -2 ** 31 - 1, 2 ** 32 + 16])
+def test_host_values_that_do_not_fit_are_refused(K, value):
+    """A list's values become 32-bit integers: none may wrap around on the way."""
+    with pytest.raises(K.KvcError) as e:
+        K.kvc_q4_layout(2, 64, [16, value], 0)
+    assert e.value.code == K.KVC_ERR_INVALID_ARG and "K_l" in str(e.value)
+    with pytest.raises(K.KvcError) as e:
+        K.kvc_read_q4(**{**READ, "n_rows": [value] * READ["H_kv"]})
+    assert e.value.code == K.KVC_ERR_INVALID_ARG and "n_rows" in str(e.value)
+    with pytest.raises(K.KvcError):
+        K.kvc_read_q4(**{**READ, "slot_off": [2 ** 64] * (READ["H_kv"] + 1)})
