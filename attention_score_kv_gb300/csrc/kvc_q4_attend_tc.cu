@@ -91,8 +91,22 @@ struct TcArgs {
 // softmax has them in registers (and has read what is seen of the tile).
 // p_full: the weights are there.  o_done: a tile's output is added up, and so
 // V's stage and the weights' columns are free.
+// A wait looks at the parity of a phase alone, so no barrier may be two phases
+// ahead of a warp that still waits for the first.  What holds each back:
+//   raw_full(i + kRaw)   raw_empty(i) of every converter, which saw raw_full(i)
+//   raw_empty(i + kRaw)  raw_full(i + kRaw), loaded after a look at raw_empty(i)
+//   k_full(i + 2)        s_full(i), issued after a look at k_full(i)
+//   v_full(i + kV)       o_done(i), issued after a look at v_full(i)
+//   s_full(i + 2)        s_free(i) of the softmax and k_full(i + 2) of the
+//                        converters, which all saw s_full(i)
+//   s_free(i + 2)        s_full(i + 2), issued after a look at s_free(i)
+//   p_full(i + 1)        o_done(i), issued after a look at p_full(i)
+//   o_done(i + kV)       p_full(i + 1) and v_full(i + kV), after looks at o_done(i)
+// K and V have as many full barriers as stages: on a barrier of K's two, V's
+// reader could be overtaken, as the converters wait for the output of kV tiles
+// before and not of two.
 struct Bars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], s_full[2], s_free[2], p_full, o_done[kV], q_full,
+  uint64_t raw_full[kRaw], raw_empty[kRaw], k_full[2], v_full[kV], s_full[2], s_free[2], p_full, o_done[kV], q_full,
       drain[2];
 };
 
@@ -293,7 +307,8 @@ __device__ bool code_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t sV,
     tc::fence_proxy_async();
     __syncwarp();
     if (lane == 0) {
-      tc::mbar_arrive(smem_u32(&bars->kv_full[st]));
+      tc::mbar_arrive(smem_u32(&bars->k_full[st]));
+      tc::mbar_arrive(smem_u32(&bars->v_full[vst]));
       tc::mbar_arrive(smem_u32(&bars->raw_empty[rs]));
     }
   }
@@ -334,7 +349,7 @@ __device__ bool score_warp(const TcArgs& a, Bars* bars, uint32_t sK, uint32_t tm
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
-      ok = wait(&bars->kv_full[st], i >> 1) && wait(&bars->s_free[st], (i >> 1) ^ 1);
+      ok = wait(&bars->k_full[st], i >> 1) && wait(&bars->s_free[st], (i >> 1) ^ 1);
       if (!ok) break;
       tc::fence_after_sync();
       if (issues) {
@@ -362,7 +377,7 @@ __device__ bool out_warp(const TcArgs& a, Bars* bars, uint32_t sV, uint32_t tmem
   bool ok = true;
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    ok = wait(&bars->kv_full[i & 1], i >> 1) && wait(&bars->p_full, i);
+    ok = wait(&bars->v_full[i % kV], i / kV) && wait(&bars->p_full, i);
     if (!ok) break;
     tc::fence_after_sync();
     if (issues) {
@@ -404,12 +419,15 @@ __global__ void __launch_bounds__(kThreads, 1) kvc_attend_q4_tc_kernel(const __g
       tc::mbar_init(smem_u32(&bars.raw_empty[i]), kCodeWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(smem_u32(&bars.kv_full[i]), kCodeWarps);
+      tc::mbar_init(smem_u32(&bars.k_full[i]), kCodeWarps);
       tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
       tc::mbar_init(smem_u32(&bars.s_free[i]), live_warps);
       tc::mbar_init(smem_u32(&bars.drain[i]), 1);
     }
-    for (int i = 0; i < kV; ++i) tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
+    for (int i = 0; i < kV; ++i) {
+      tc::mbar_init(smem_u32(&bars.v_full[i]), kCodeWarps);
+      tc::mbar_init(smem_u32(&bars.o_done[i]), 1);
+    }
     tc::mbar_init(smem_u32(&bars.p_full), live_warps);
     tc::mbar_init(smem_u32(&bars.q_full), live_warps);
     tc::fence_barrier_init();
