@@ -367,9 +367,9 @@ static PyObject* attention_q4(PyObject* self, PyObject* const* a, Py_ssize_t n_a
       as_tensor(a[1], u8, cache_bytes(n, D), "cache", dev, &cache) || as_tensor(a[2], i32, n, "pos", dev, &pos) ||
       as_tensor(a[3], i32, times(B, H), "rows", dev, &rows) || as_tensor(a[5], i32, times(B, T), "q_pos", dev, &qp) ||
       as_tensor(a[12], bf16, times(nq, D), "out", dev, &out) || as_tensor(a[13], f32, nq, "lse", dev, &lse) ||
-      as_tensor(a[14], u8, 0, "ws", dev, &ws) || as_stream(a[16], dev, &st))
+      (a[15] != Py_None ? as_i64(a[15], &ws_bytes) : call_i64(a[14], s_numel, &ws_bytes)) ||
+      as_tensor(a[14], u8, ws_bytes, "ws", dev, &ws) || as_stream(a[16], dev, &st))
     goto out;
-  if (a[15] != Py_None ? as_i64(a[15], &ws_bytes) : call_i64(a[14], s_numel, &ws_bytes)) goto out;
   RUN(rc, p_attention(q, cache, pos, rows, extra, qp, B, T, H_q, H, D, slot.p, out, lse, ws,
                       ws_bytes < 0 ? 0 : (size_t)ws_bytes, st));
   r = done(rc);

@@ -419,12 +419,14 @@ def kvc_compress_layer_q4(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent,
     dev = _cur_dev()
     bf = torch.bfloat16
     so, n = _q4_rows(B, H_kv, slot_off)
+    if ws_bytes is None:
+        ws_bytes = ws.numel()
     _check(_lib.kvc_compress_layer_q4(
         N, layer, B, S, C, H_q, H_kv, D, W, _host(K_l, ctypes.c_int32, H_kv, "K_l"), sink, recent, pool_k, b_s,
         _arg(q_win, bf, B * H_q * W * D, "q_win", dev), _arg(k, bf, B * H_kv * S * D, "k", dev),
         _arg(v, bf, B * H_kv * S * D, "v", dev), so, _arg(cache, torch.uint8, n * D * 9 // 8, "cache", dev),
-        _arg(pos, torch.int32, n, "pos", dev), _arg(ws, torch.uint8, 0, "ws", dev),
-        ws.numel() if ws_bytes is None else ws_bytes, _event(v_ready), _stream(stream)))
+        _arg(pos, torch.int32, n, "pos", dev), _arg(ws, torch.uint8, ws_bytes, "ws", dev), ws_bytes, _event(v_ready),
+        _stream(stream)))
 
 
 def kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D) -> int:

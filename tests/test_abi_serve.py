@@ -223,3 +223,16 @@ def test_host_values_that_do_not_fit_are_refused(K, value):
     assert e.value.code == K.KVC_ERR_INVALID_ARG and "n_rows" in str(e.value)
     with pytest.raises(K.KvcError):
         K.kvc_read_q4(**{**READ, "slot_off": [2 ** 64] * (READ["H_kv"] + 1)})
+
+
+def test_a_workspace_smaller_than_stated_is_refused(K):
+    """ws_bytes speaks for a raw pointer; a tensor has to hold what is stated."""
+    import torch
+    ws = torch.zeros(512, dtype=torch.uint8)
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_attention_q4(**{**ATTEND, "ws": ws, "ws_bytes": 1 << 40})
+    assert ei.value.code == K.KVC_ERR_INVALID_ARG and "ws holds 512" in str(ei.value)
+    with pytest.raises(K.KvcError) as ei:
+        K.kvc_compress_layer_q4(1, 0, 1, 512, 512, 4, 2, 64, 16, [128, 128], 4, 16, 1, 128, 0x1000, 0x2000, 0x3000,
+                                [0, 128, 256], 0x4000, 0x6000, ws, ws_bytes=1 << 40, stream=0)
+    assert ei.value.code == K.KVC_ERR_INVALID_ARG and "ws holds 512" in str(ei.value)
