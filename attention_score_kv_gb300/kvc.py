@@ -213,7 +213,13 @@ def _host(arr, ctype, n, name):
     if arr is None:
         return None
     if not (isinstance(arr, ctypes.Array) and arr._type_ is ctype):
-        vals = [int(x) for x in (arr.tolist() if hasattr(arr, "tolist") else arr)]
+        given = arr.tolist() if hasattr(arr, "tolist") else list(arr)
+        try:
+            vals = [int(x) for x in given]
+        except (ValueError, OverflowError):        # not a number, infinite
+            vals = None
+        if vals is None or any(v != x for v, x in zip(vals, given)):
+            _bad(f"{name} holds values that are no integers")
         arr = (ctype * len(vals))(*vals)
         if arr[:] != vals:             # ctypes drops the upper bits
             _bad(f"{name} holds values that do not fit {8 * ctypes.sizeof(ctype)} bits")

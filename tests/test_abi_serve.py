@@ -236,3 +236,21 @@ def test_a_workspace_smaller_than_stated_is_refused(K):
         K.kvc_compress_layer_q4(1, 0, 1, 512, 512, 4, 2, 64, 16, [128, 128], 4, 16, 1, 128, 0x1000, 0x2000, 0x3000,
                                 [0, 128, 256], 0x4000, 0x6000, ws, ws_bytes=1 << 40, stream=0)
     assert ei.value.code == K.KVC_ERR_INVALID_ARG and "ws holds 512" in str(ei.value)
+
+
+@pytest.mark.parametrize("value", [16.5, -0.25, float("nan"), float("inf")])
+def test_host_values_that_are_no_integers_are_refused(K, value):
+    """Row counts are not rounded on the way; whole numbers of another type are taken."""
+    import numpy as np
+    import torch
+    for make in (list, np.array, torch.tensor, lambda x: [np.float32(y) for y in x]):
+        with pytest.raises(K.KvcError) as e:
+            K.kvc_q4_layout(2, 64, make([16.0, value]), 0)
+        assert e.value.code == K.KVC_ERR_INVALID_ARG and "K_l" in str(e.value)
+        with pytest.raises(K.KvcError) as e:
+            K.kvc_read_q4(**{**READ, "n_rows": make([16.0, value])})
+        assert e.value.code == K.KVC_ERR_INVALID_ARG and "n_rows" in str(e.value)
+        with pytest.raises(K.KvcError) as e:
+            K.kvc_gather_q4(**{**GATHER, "slot_off": make([0.0, 16.0, value])})
+        assert e.value.code == K.KVC_ERR_INVALID_ARG and "slot_off" in str(e.value)
+        assert list(K.kvc_q4_layout(2, 64, make([16.0, 17.0]), 0)) == [0, 16, 48]
