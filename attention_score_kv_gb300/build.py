@@ -15,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -38,14 +39,18 @@ def sources():
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile csrc/kvc_python.c for the running Python; returns its path."""
+    """Compile csrc/kvc_python.c for the running Python; returns its path, or "" with a
+    warning where that is not possible (no C compiler, no Python headers): only the
+    binding's calls of a decoding step need it."""
     src = os.path.join(CSRC, "kvc_python.c")
     deps = [src, os.path.join(HERE, "..", "include", "kvc.h")]
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
         return BINDING
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
-    if not cc:
-        raise RuntimeError("no C compiler found (set CC)")
+    headers = os.path.join(sysconfig.get_path("include"), "Python.h")
+    if not cc or not os.path.exists(headers):
+        warnings.warn(f"{BINDING} is not built: " + (f"{headers} is missing" if cc else "no C compiler (set CC)"))
+        return ""
     tmp = BINDING + ".tmp"
     rc, cmd, out = _run([cc, "-O2", "-shared", "-fPIC", "-Wall", "-Wextra", "-I", sysconfig.get_path("include"), src,
                          "-o", tmp])
@@ -68,7 +73,6 @@ def build(verbose: bool = False, extra_flags=None, force: bool = False, lib_path
     ``build_dir`` place the library and objects elsewhere (default: in-tree).
     """
     nvcc = _nvcc()
-    build_binding(force)
     LIB = lib_path or globals()["LIB"]
     BUILD = build_dir or globals()["BUILD"]
     os.makedirs(BUILD, exist_ok=True)
@@ -97,6 +101,7 @@ def build(verbose: bool = False, extra_flags=None, force: bool = False, lib_path
         if rc:
             raise RuntimeError(f"link failed:\n{cmd}\n{out}")
         os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 

@@ -5,7 +5,8 @@ budget arrays as int32 arrays, the stream as the caller's current CUDA stream
 (the calls of a decoding step through csrc/kvc_python.c).
 Every step of the compression runs in the library's CUDA kernels; there is no
 other code path.  Importing this module fails loudly if the library has not
-been built (``python -m attention_score_kv_gb300.build``).
+been built (``python -m attention_score_kv_gb300.build``); without the module of
+csrc/kvc_python.c the calls of a decoding step do.
 """
 
 from __future__ import annotations
@@ -14,8 +15,6 @@ import ctypes
 import os
 
 import torch
-
-from . import build as _build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # KVC_LIBRARY selects another build of the same library (e.g. one compiled
@@ -49,11 +48,23 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python -m attention_score_kv_gb300.build` (nvcc, sm_103a)")
 
+
+class _NoBinding:
+    """In the place of csrc/kvc_python.c's module where there is none for this Python:
+    the calls that go through it raise, the rest of the library works."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name}: the module of csrc/kvc_python.c is missing ({self._why}): build it with "
+                          "`python -m attention_score_kv_gb300.build` (a C compiler and Python's headers)")
+
+
 try:
     from . import _binding
 except ImportError as e:
-    raise ImportError(f"{_build.BINDING} is missing: build it with "
-                      "`python -m attention_score_kv_gb300.build` (a C compiler and Python's headers)") from e
+    _binding = _NoBinding(e)
 
 _lib = ctypes.CDLL(LIB_PATH)
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -234,11 +245,12 @@ def _host_array(arr, size, n, name):
 
 # The calls that run once per token and layer take their arguments apart in C
 # (csrc/kvc_python.c): type, size, contiguity and device of every tensor.
-_binding.init(tuple(ctypes.cast(getattr(_lib, f), _P).value for f in
-                    ("kvc_last_error", "kvc_qk_norm_rope", "kvc_gather_q4", "kvc_append_q4", "kvc_read_q4",
-                     "kvc_attention_q4")),
-              (torch.bfloat16, torch.int32, torch.uint8, torch.float32),
-              (_cur_dev, _raw_stream, _refuse, _tokens_arg, _host_array, KvcError))
+if not isinstance(_binding, _NoBinding):
+    _binding.init(tuple(ctypes.cast(getattr(_lib, f), _P).value for f in
+                        ("kvc_last_error", "kvc_qk_norm_rope", "kvc_gather_q4", "kvc_append_q4", "kvc_read_q4",
+                         "kvc_attention_q4")),
+                  (torch.bfloat16, torch.int32, torch.uint8, torch.float32),
+                  (_cur_dev, _raw_stream, _refuse, _tokens_arg, _host_array, KvcError))
 
 
 def kvc_last_error() -> str:

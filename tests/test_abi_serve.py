@@ -254,3 +254,43 @@ def test_host_values_that_are_no_integers_are_refused(K, value):
             K.kvc_gather_q4(**{**GATHER, "slot_off": make([0.0, 16.0, value])})
         assert e.value.code == K.KVC_ERR_INVALID_ARG and "slot_off" in str(e.value)
         assert list(K.kvc_q4_layout(2, 64, make([16.0, 17.0]), 0)) == [0, 16, 48]
+
+
+def test_the_compress_needs_no_marshalling_module(K):
+    """Without the module of csrc/kvc_python.c (another Python, no headers) the library's other calls
+    work, and a decoding step's calls say what is missing."""
+    import os
+    import subprocess
+    import sys
+    code = """if True:
+        import sys
+        sys.modules["attention_score_kv_gb300._binding"] = None
+        import attention_score_kv_gb300.kvc as K
+        assert K.kvc_retained_layout(2, 100, [5, 7]) == [0, 5, 12]
+        assert list(K.kvc_q4_layout(2, 100, [5, 17], 0)) == [0, 16, 48]
+        try:
+            K.kvc_gather(*[0x1000] * 3, 0, 2, 100, 64, [5, 7], *[0x1000] * 3, stream=0)
+            raise AssertionError("not refused")
+        except K.KvcError as e:
+            assert e.code == K.KVC_ERR_INVALID_ARG
+        try:
+            K.kvc_append_q4(*[0x1000] * 3, 1, 1, 1, 64, [0, 16], *[0x1000] * 3, stream=0)
+            raise AssertionError("not refused")
+        except ImportError as e:
+            assert "attention_score_kv_gb300.build" in str(e)
+        print("fine")
+    """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert p.returncode == 0 and "fine" in p.stdout, p.stderr
+
+
+def test_the_library_is_built_without_pythons_headers(K, tmp_path, monkeypatch):
+    import sysconfig
+
+    from attention_score_kv_gb300 import build
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(sysconfig, "get_path", lambda name: str(tmp_path))
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert build.build() == build.LIB
+    assert not (tmp_path / "_binding.so").exists()
