@@ -530,6 +530,104 @@ def test_offsets_past_32_bits(K):
         assert abs(float(lse[0, h, 0]) - rl[0]) < 1e-3
 
 
+@pytest.mark.parametrize("form,B,T,n", [("cluster", 1, 1, 90), ("ranges", 40, 1, 90), ("many rows", 1, 3, 90),
+                                        ("many rows, split", 2, 50, 3000)])
+def test_odd_queries_leave_their_neighbours_alone(K, form, B, T, n):
+    """Query rows that are not finite, zero, tiny or huge beside ordinary ones, in every form of the
+    kernel: NaN and infinity stay in their rows, and every other row is right."""
+    H, Hq, D = 1, 7, 128
+    so = K.kvc_q4_layout(H, 1 << 20, [n], 0)
+    cache, pos, _, _ = filled(K, B, H, D, so, [n], 171)
+    rows, qp = i32([[n]] * B), i32(np.full((B, T), 1 << 20))
+    plain = rnd(172, B, Hq, T, D)
+    plain[:, 3, ::5] = 0
+    plain[:, 4, ::5] *= 1e-30
+    odd = plain.clone()
+    odd[:, 1, ::5, 3], odd[:, 2, ::5, 9] = float("nan"), float("inf")
+    odd[:, 5, ::5] *= 2.0 ** 20
+    args = (cache, pos, rows, 0, qp, B, T, Hq, H, D, so)
+    out, lse = attend(K, odd, *args)
+    ref, ref_lse = attend(K, plain, *args)
+    K.kvc_check_status()
+    assert torch.isnan(out[:, 1, ::5]).all() and torch.isnan(lse[:, 1, ::5]).all()
+    assert torch.isnan(out[:, 2, ::5]).any(-1).all()
+    # a huge query: one key takes it all, that of the largest score
+    kk, vv = all_rows(K, cache, B, H, D, so)
+    for b in range(B):
+        for t in range(0, T, 5):
+            best = vv[b, (kk[b, :n] @ f64(odd)[b, 5, t]).argmax()]
+            assert np.all(np.abs(f64(out)[b, 5, t] - best) <= 2.0 ** -8 * np.abs(best))
+    same = (plain == odd).all(-1)                        # the rows that are alike in both calls
+    assert not same[:, 1, ::5].any() and same[:, 0].all()
+    check_attention(K, plain, *args, torch.where(same[..., None], out, ref), torch.where(same, lse, ref_lse),
+                    batches=sorted({0, B - 1}))
+
+
+def test_a_wait_that_gives_up_is_recorded(K):
+    """With a limit of one poll some wait gives up (measured: in 56 of 100 calls), and is reported."""
+    B, T, H, Hq, D, n = 4, 40, 8, 32, 128, [6000] * 8
+    so = K.kvc_q4_layout(H, 1 << 20, n, 0)
+    cache, pos, _, _ = filled(K, B, H, D, so, n, 196)
+    q, qp = rnd(197, B, Hq, T, D), i32(np.full((B, T), 1 << 20))
+    gave_up = False
+    K.kvc_set_option(K.KVC_OPT_WAIT_LIMIT, 1)
+    try:
+        for _ in range(100):
+            attend(K, q, cache, pos, i32([n] * B), 0, qp, B, T, Hq, H, D, so)
+            try:
+                K.kvc_check_status()
+            except K.KvcError as e:
+                assert e.code == K.KVC_ERR_TIMEOUT
+                gave_up = True
+                break
+    finally:
+        K.kvc_set_option(K.KVC_OPT_WAIT_LIMIT, 0)
+    assert gave_up
+
+
+def test_offsets_past_32_bits_of_many_rows(K):
+    """The many-row form at the far end of a slot of 2^25 rows, 4.8 GB."""
+    D, cap, T, Hq = 128, 1 << 25, 9, 4
+    so = [0, cap]
+    cache = torch.zeros(cap * D * 9 // 8, dtype=torch.uint8, device="cuda")
+    pos = torch.full((cap,), -1, dtype=torch.int32, device="cuda")
+    k, v, q = rnd(1, 1, 1, 40, D), rnd(2, 1, 1, 40, D), rnd(3, 1, Hq, T, D)
+    rows, qp = i32([[cap - 43]]), 30 + np.arange(T)
+    K.kvc_append_q4(k, v, i32([np.arange(40)]), 1, 1, 40, D, so, rows, cache, pos)
+    out, lse = attend(K, q, cache, pos, rows, 43, i32([qp]), 1, T, Hq, 1, D, so)
+    K.kvc_check_status()
+    hk, hv = O.held(f64(k)[0, 0]), O.held(f64(v)[0, 0])
+    for h in range(Hq):
+        ref, rl, mag = O.attention(f64(q)[0, h], hk, hv, np.arange(40), qp)
+        A = float((np.abs(f64(q)[0, h]) @ np.abs(hk).T).max()) / math.sqrt(D)
+        tol = 2.0 ** -8 * np.abs(ref) + 2 * (2.0 ** -11 + A * 2.0 ** -18) * mag + 40 * 2.0 ** -29 * np.abs(hv).max()
+        assert np.all(np.abs(f64(out)[0, h] - ref) <= tol)
+        assert np.all(np.abs(f64(lse)[0, h] - rl) <= 2.0 ** -18 * A + 2.0 ** -20 * np.abs(rl) + 2.0 ** -20)
+
+
+def test_calls_at_the_same_time_on_two_streams(K):
+    """Calls of every form on two streams at once, each with a workspace of its own, give the bits
+    of the calls alone."""
+    H, Hq, D, n = 4, 16, 64, [700, 40, 0, 2000]
+    so = K.kvc_q4_layout(H, 1 << 20, n, 0)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    jobs = []
+    for i, (B, T) in enumerate([(2, 20), (1, 90), (2, 1), (40, 1), (1, 90), (2, 20)]):
+        cache, pos, _, _ = filled(K, B, H, D, so, n, 301 + i)
+        q, rows, qp = rnd(401 + i, B, Hq, T, D), i32([n] * B), i32(np.full((B, T), 1 << 20))
+        args = (q, cache, pos, rows, 0, qp, B, T, Hq, H, D, so)
+        jobs.append((args, attend(K, *args), torch.empty_like(q), torch.empty((B, Hq, T), device="cuda"),
+                     K.attention_q4_workspace(B, T, Hq, H, D)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, (args, _, out, lse, ws) in enumerate(jobs):
+            K.kvc_attention_q4(*args, out, lse, ws, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    K.kvc_check_status()
+    for args, (o, l), out, lse, _ in jobs:
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
 # ------------------------------------------------------------------ as they are used
 @pytest.mark.parametrize("B,T", [(2, 1), (40, 1), (1, 20)])
 def test_two_graphs_share_a_workspace(K, B, T):
