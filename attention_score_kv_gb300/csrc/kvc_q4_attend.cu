@@ -713,9 +713,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kvc_attend_q4_join_kernel(con
 }  // namespace
 
 // More query rows go to the tensor cores' other form, whose 128 rows cost the
-// same however many are used: at 8 heads of 4096 rows 20 query rows take 10.9 us
-// there and 24.6 us here in tiles of 32 (16 sequences: 41 and 62 us), 12 rows 10.4
-// and 16.4 us (16 sequences: 41 and 38 us).
+// same however many are used: at 8 heads of 4096 rows 20 query rows take 10.2 us
+// there (16 sequences: 36.6 us) and took 24.6 us here in tiles of 32 columns (62
+// us), 12 rows 9.4 us (36.6 us) and 16.4 us in tiles of 16 (38 us).
 bool attend_q4_on_tc(int H_q, int H_kv, int T) { return (int64_t)(H_q / H_kv) * T > kCols; }
 
 // Whether clusters take the heads: while two CTAs an SM hold them all and the

@@ -39,8 +39,13 @@
 // Pairs of CTAs that convert half of a tile each for products of 256 rows
 // (cta_group::2) have the converters wait half of the time and gain nothing (45.4;
 // D = 64 lost 5%): the hand-overs between the two cost what the halves save.
-// Few row tiles leave SMs idle; then the cache rows are split over several CTAs
-// per row tile, whose parts a second kernel joins in order.
+// A CTA takes a row tile of a head.  Few of them leave SMs idle; then the cache
+// rows are split over several CTAs per row tile, whose parts a second kernel joins
+// in order.  The split is the same for every head and a whole number, so SMs idle
+// where row tiles do not divide them (the turn of 512 has 128 on 152 SMs; 16 x 8
+// heads of 4096 rows take 36.6 us, 20 x 8, eight more than there are SMs, 70.3) or
+// where heads are uneven (7800 and 900 rows by turns under the turn of 512: 69 us,
+// even heads of the same sum 45).
 #include <algorithm>
 #include <cmath>
 
@@ -118,9 +123,9 @@ __device__ __forceinline__ void store16(uint32_t addr, uint32_t a, uint32_t b, u
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Bounded waits of a whole warp, as loops of a few instructions: written out by
-// the compiler, the waits made the kernel a fifth longer and 3% slower (its warps
-// run five programs at once).
+// Bounded waits of a whole warp, as loops of a few instructions (written out by
+// the compiler, the waits made the kernel 3% slower: its warps run five programs
+// at once).
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
   uint32_t ok;
   asm volatile(

@@ -9,10 +9,13 @@
 // projections does what an append of the chunk needs.
 //
 // The angle: pos * inv_freq in fp32 is 6e-3 rad off at position 10^5.  Here a
-// frequency becomes a 64-bit binary fraction of a turn, once per thread; the
-// product with the integer position drops whole turns by wrapping around, and
-// its upper 32 bits are the angle to 2^-32 of a turn (times 2 pi), exact for
-// every int32 position.
+// frequency becomes a 64-bit binary fraction of a turn; the product with the
+// integer position drops whole turns by wrapping around, and its upper 32 bits
+// go to the sine and cosine as a fp32 number.  The fraction comes from a product
+// in fp64, 2^-52 of the frequency off at most, which the position multiplies;
+// the upper bits and their rounding to fp32 leave 2^-25 of a turn: together below
+// 1e-6 rad plus pos * inv_freq * 2^-52.  The fp64 steps are done for every token
+// and frequency of a CTA, once for all of the token's heads.
 //
 // Memory bounds it: every value is read and written once.  A chunk of 2048
 // tokens of 32 + 2 x 8 heads of 128 takes 12.2 us (50 MB, 4.1 TB/s), one token

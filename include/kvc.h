@@ -534,6 +534,15 @@ int kvc_compress_layer_q4(int N, int layer, int B, int S, int C, int H_q,
  * A query that sees no row gets zeros and lse -inf.  Rows that no query of the
  * call sees may hold any bytes.  A count outside the slot is clamped to it and
  * recorded (KVC_ERR_DEVICE).  No atomics: the same call gives the same bits.
+ * Arithmetic: the products take fp16 operands and add up in fp32.  Keys and
+ * values are exact in fp16; a query row is scaled by a power of two to below 2
+ * (what is under 2^-24 of its largest value is lost); the weights p_r of the
+ * values are rounded to fp16, 2^-12 of each, while maxima, sums and lse are fp32
+ * throughout.  Against 64 bits that leaves out at its bf16 rounding (relative
+ * error 1.68e-3, 1.67e-3 with weights of 32 bits).
+ * Speed: one token of a few sequences takes the faster of two forms while no
+ * slot has room for more than 16384 rows, whatever it holds (4096 rows of 8
+ * heads: 6.4 us, in slots of 20480 rows 11.1).
  *   ws     at least kvc_attention_q4_workspace_size(...) bytes, 256-byte
  *          aligned, any content; the size does not depend on the rows
  */

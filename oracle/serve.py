@@ -56,7 +56,7 @@ def norm_rope(x, weight, eps, inv_freq, pos, R, interleaved):
         y = y / np.sqrt((y * y).mean(-1, keepdims=True) + eps) * weight
     if R:
         ang = np.asarray(pos, dtype=np.float64)[:, None] * np.asarray(inv_freq, dtype=np.float64)
-        # whole turns off first: cos and sin of the host lose nothing at far positions
+        # the product is 2^-53 of the angle off; cos and sin of the host take whole turns off exactly
         c, s = np.cos(ang), np.sin(ang)
         i = np.arange(R // 2)
         a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + R // 2)
