@@ -27,8 +27,8 @@
 //   rows    row k = r + 8s of block x of a warp's two is row 8 (r / 2) + 4x + 2s +
 //           r % 2 of its 32: the four rows of a value pair j, twice, side by side
 //   values  dim y of slice r is row r*D/8 + (y ^ 4 (r % 2)) of V^T
-// Measured: 512 tokens of 32 heads over 8 heads of 4.9K rows, 38.7 GFLOP, take 45.2
-// us (856 TFLOP/s), 1900 to 2000 cycles a tile where the products are 1024.  No one
+// Measured: 512 tokens of 32 heads over 8 heads of 4.9K rows, 38.7 GFLOP, take 45.0
+// us (860 TFLOP/s), 1900 to 2000 cycles a tile where the products are 1024.  No one
 // thing bounds them: the converters take 1400 and the softmax 1450 of them, a tile
 // moves 164 KB through shared memory (1280 cycles at 128 bytes), a product beside
 // the softmax's use of tensor memory takes a third longer than alone, and each
