@@ -306,19 +306,19 @@ int launch_status(cudaError_t e, const char* what) {
 namespace {
 
 // kvc_compress_layer with an optional event the gather waits on (the values
-// are read by the gather only).  cache given: the gather writes the 4-bit
-// cache in the slots out_off, instead of k_out and v_out.
+// are read by the gather only).  q4 or q8 given: the gather writes the 4-bit or the
+// 8-bit cache in the slots out_off, instead of k_out and v_out.
 int compress_layer(int N, int layer, int B, int S, int C, int H_q, int H_kv, int D, int W, const int32_t* K_l,
                    int sink, int recent, int pool_k, int b_s, const kvc_bf16* q_win, const kvc_bf16* k,
                    const kvc_bf16* v, kvc_bf16* k_out, kvc_bf16* v_out, int32_t* pos_out,
-                   const int64_t* out_off, uint8_t* cache, void* ws, size_t ws_bytes, cudaEvent_t v_ready,
-                   kvc_stream_t stream) {
+                   const int64_t* out_off, uint8_t* q4, const Q8Cache* q8, void* ws, size_t ws_bytes,
+                   cudaEvent_t v_ready, kvc_stream_t stream) {
   int rc;
   if (N < 1 || layer < 0 || layer >= N) return set_error(KVC_ERR_INVALID_ARG, "layer %d outside [0, N=%d)", layer, N);
   if ((rc = check_shapes(B, H_q, H_kv, S, D, W)) || (rc = check_bs(b_s)) || (rc = check_pool(pool_k))) return rc;
   if (C < W || C > S) return set_error(KVC_ERR_INVALID_ARG, "chunk C=%d must satisfy W=%d <= C <= S=%d", C, W, S);
   if ((rc = check_ptr(q_win, 16, "q_win")) || (rc = check_ptr(k, 16, "k")) || (rc = check_ptr(v, 16, "v")) ||
-      (!cache && ((rc = check_ptr(k_out, 16, "k_out")) || (rc = check_ptr(v_out, 16, "v_out")))) ||
+      (!q4 && !q8 && ((rc = check_ptr(k_out, 16, "k_out")) || (rc = check_ptr(v_out, 16, "v_out")))) ||
       (rc = check_ptr(pos_out, 4, "pos_out")))
     return rc;
   SelParams sp;
@@ -358,8 +358,10 @@ int compress_layer(int N, int layer, int B, int S, int C, int H_q, int H_kv, int
   if (ev) cudaEventRecord(ev[3], st);
   if (v_ready && (rc = launch_status(cudaStreamWaitEvent(st, v_ready, 0), "wait for v_ready")))
     return rc;
-  if (cache)
-    rc = launch_status(launch_gather_q4(kk, vv, pos_out, B, sp, D, cache, pos_out, st), "4-bit gather launch");
+  if (q4)
+    rc = launch_status(launch_gather_q4(kk, vv, pos_out, B, sp, D, q4, pos_out, st), "4-bit gather launch");
+  else if (q8)
+    rc = launch_status(launch_gather_q8(kk, vv, pos_out, B, sp, D, *q8, st), "8-bit gather launch");
   else
     rc = launch_status(launch_gather(kk, vv, pos_out, B, sp, D, reinterpret_cast<__nv_bfloat16*>(k_out),
                                      reinterpret_cast<__nv_bfloat16*>(v_out), pos_out, st),
@@ -509,7 +511,7 @@ int kvc_compress_layer(int N, int layer, int B, int S, int C, int H_q, int H_kv,
                        const kvc_bf16* v, kvc_bf16* k_out, kvc_bf16* v_out, int32_t* pos_out,
                        const int64_t* out_off, void* ws, size_t ws_bytes, kvc_stream_t stream) {
   return compress_layer(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, k_out,
-                        v_out, pos_out, out_off, nullptr, ws, ws_bytes, nullptr, stream);
+                        v_out, pos_out, out_off, nullptr, nullptr, ws, ws_bytes, nullptr, stream);
 }
 
 int kvc_compress_layer_deferred_v(int N, int layer, int B, int S, int C, int H_q, int H_kv, int D, int W,
@@ -518,7 +520,7 @@ int kvc_compress_layer_deferred_v(int N, int layer, int B, int S, int C, int H_q
                                   kvc_bf16* v_out, int32_t* pos_out, const int64_t* out_off, void* ws,
                                   size_t ws_bytes, kvc_event_t v_ready, kvc_stream_t stream) {
   return compress_layer(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, k_out,
-                        v_out, pos_out, out_off, nullptr, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready),
+                        v_out, pos_out, out_off, nullptr, nullptr, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready),
                         stream);
 }
 
@@ -530,7 +532,23 @@ int kvc_compress_layer_q4(int N, int layer, int B, int S, int C, int H_q, int H_
   if (H_kv < 1) return set_error(KVC_ERR_INVALID_ARG, "H_kv must be >= 1");
   if ((rc = check_slots(H_kv, slot_off)) || (rc = check_ptr(cache, 16, "cache"))) return rc;
   return compress_layer(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, nullptr,
-                        nullptr, pos, slot_off, cache, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready), stream);
+                        nullptr, pos, slot_off, cache, nullptr, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready),
+                        stream);
+}
+
+int kvc_compress_layer_q8(int N, int layer, int B, int S, int C, int H_q, int H_kv, int D, int W, const int32_t* K_l,
+                          int sink, int recent, int pool_k, int b_s, const kvc_bf16* q_win, const kvc_bf16* k,
+                          const kvc_bf16* v, const int64_t* slot_off, uint8_t* k8, uint8_t* v8, float* scale,
+                          int32_t* pos, void* ws, size_t ws_bytes, kvc_event_t v_ready, kvc_stream_t stream) {
+  int rc;
+  if (H_kv < 1) return set_error(KVC_ERR_INVALID_ARG, "H_kv must be >= 1");
+  if ((rc = check_slots(H_kv, slot_off)) || (rc = check_ptr(k8, 16, "k8")) || (rc = check_ptr(v8, 16, "v8")) ||
+      (rc = check_ptr(scale, 8, "scale")))
+    return rc;
+  const Q8Cache c{k8, v8, scale, pos};
+  return compress_layer(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, nullptr,
+                        nullptr, pos, slot_off, nullptr, &c, ws, ws_bytes, reinterpret_cast<cudaEvent_t>(v_ready),
+                        stream);
 }
 
 int kvc_scan_ranges(int BH, int S, int P, int64_t* starts) {

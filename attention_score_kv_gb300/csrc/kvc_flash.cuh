@@ -1,0 +1,1223 @@
+// Attention of many query rows per KV head on the tensor cores: a prompt chunk
+// over the active layer's bf16 rows, and many tokens over the 8-bit cache.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(x_j),  lse = log sum_j p_j
+//
+// One pass over the keys with a running reference r: o and the sum are kept for
+// weights 2^(x - r), and r follows the maximum only when a score passes it by
+// 2^kSlack, so the output is hardly ever rescaled.
+//
+// A CTA has two streams of 128 query rows against tiles of 128 keys (tcgen05, fp32
+// accumulators in tensor memory: S and O of both streams are its 512 columns):
+//   S = Q K^T   (both in shared memory);   O += P V   (P in tensor memory, over S)
+// One warp issues, for stream 0 and 1 in turn, the last tile's P V and the next
+// tile's Q K^T, 1024 cycles of products at D = 128, while four warps make the
+// other stream's weights: a thread has a whole row, so nothing is exchanged
+// between threads.  S is overwritten by P and P by the next S: the products of a
+// warp run in order, and the weights' barrier says that S is in registers.
+// Two ways to feed the streams:
+//   row pairs    two row tiles of a head share each tile of keys and values
+//   key pairs    one row tile (few rows: down to a single token); the streams take
+//                tiles of keys in turn, and their outputs are joined at the end
+// A row tile is nt = 128 / G tokens of all G query heads of the KV head, so a
+// causal or a document's border cuts few tiles.
+//
+// Work split: a unit is (sequence, KV head, row tile or pair), its steps the key
+// tiles (pairs of them) that some query of it sees.  A planning kernel counts them
+// from the device-held masks and row counts, lays all units end to end and gives
+// every SM's CTA an equal range, whatever the masks and lengths.  Units that a
+// range's end cuts leave partial results, which a third kernel joins in order.
+//
+// e4m3 keys and values (the 8-bit cache): the products take e4m3 operands.  A query
+// row is scaled by a power of two to below 2^8 and split into two e4m3 parts, four
+// significant bits each, so that all of a bf16's eight are there; weights are split
+// the same way: two products of twice bf16's rate each.
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+
+#include "kvc_device.cuh"
+#include "kvc_internal.cuh"
+#include "kvc_q4.cuh"
+#include "kvc_q8.cuh"
+#include "kvc_scan_common.cuh"
+#include "kvc_tc.cuh"
+
+namespace kvc {
+namespace flash {
+
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
+// Three groups of four warps: the two streams' weights, and the issuing, the loading
+// and two idle warps, whose registers the first two take (a thread's row of scores
+// alone is 128): 2 * 208 + 88 = 3 * 168, what the block is launched with.
+constexpr int kThreads = 12 * 32, kSoftRegs = 208, kOtherRegs = 88;
+constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;    // stream x: S at kColS + 128 x, O at kColO + 128 x
+constexpr float kNoRef = -1.7e38f;   // reference of a row that has seen no key
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
+constexpr float kLeastUnit = 7.8886090522101181e-31f;      // 2^-100, the smallest scale
+constexpr int kMaxStages = 11;
+constexpr int kMeta = 8;             // tiles whose positions and scales are in shared memory
+
+// What a tile of the 8-bit cache's rows is.  Its slot is written again for the
+// stream's tile of eight tiles further on, behind a stage that the ring's nine
+// loads before gave up: the products of five tiles before at least, which were
+// issued after the weights of the slot's last tile had been made.
+struct alignas(16) Meta {
+  int pos[kKeys];
+  float rel[kKeys];                  // position less the unit's last query's
+  float2 scale[kKeys / q8::kRows];   // of the blocks' keys and values
+  uint32_t some[4];                  // rows that some query of the unit may see
+  uint32_t mixed[4];                 // some query does not see all of these 32
+};
+
+// Where a CTA's range begins: a unit, and the steps of it before the range.
+struct Start { int b, h, tile, n; long long off; };
+struct Plan {                        // in the workspace
+  long long total, L;                // all steps; steps of a range
+};
+
+struct Args {
+  CUtensorMap qmap, kmap, vmap;
+  const __nv_bfloat16* q;
+  // chunk: query (b, t) at q_pos sees keys first .. last
+  const int32_t *q_pos, *first, *last;
+  // 8-bit cache
+  const int32_t *pos, *rows;
+  const float2* scale;
+  Q4Slots s;
+  const float* slopes;
+  __nv_bfloat16* out;
+  float* lse;
+  Plan* plan;
+  int2* units;                       // [B1][tiles]: first key tile, steps
+  long long* before;                 // [B1 * tiles + 1] steps before, of one head
+  Start* start;                      // [P + 1]
+  float2* part_ml;                   // [2 P][rows of a unit]: reference, sum
+  float* part_o;                     // [..][D]
+  int* status;
+  int B1, H1;                        // units are [B1][H1][tiles]: B, H_kv (chunk) or B * H_kv, 1 (cache)
+  int T, H_q, H_kv, G, S, extra;
+  int nt, tiles, P;
+  int pair_keys;                     // the streams share rows and take key tiles in turn
+  uint32_t wait_limit;
+  float scale2, cap2, inv_cap2;      // log2(e) / sqrt(D); cap in log2 units, 0: none
+};
+
+// ------------------------------------------------------------------- planning
+__device__ __forceinline__ bool key_range(const Args& a, int64_t bt, int& lo, int& hi) {
+  const int qp = __ldg(a.q_pos + bt);
+  lo = a.first ? max(__ldg(a.first + bt), 0) : 0;
+  hi = qp < 0 ? -1 : min(a.last ? __ldg(a.last + bt) : qp, a.S - 1);
+  return lo <= hi;
+}
+__device__ __forceinline__ int rows_held(const Args& a, int bh, bool* bad) {
+  const int h = bh % a.H_kv;
+  const int64_t cap = a.s.off[h + 1] - a.s.off[h], n = (int64_t)__ldg(a.rows + bh) + a.extra;
+  *bad = n < 0 || n > cap;
+  return (int)(n < 0 ? 0 : n > cap ? cap : n);
+}
+// Steps of one unit, by a warp.
+template <bool FP8>
+__device__ __forceinline__ int2 unit_steps(const Args& a, int b, int tile) {
+  const int lane = threadIdx.x & 31;
+  int k0 = 0, n = 1;
+  if constexpr (FP8) {
+    bool bad;
+    n = (rows_held(a, b, &bad) + kKeys - 1) / kKeys;
+    if (bad && lane == 0) record_status(a.status, kStatusBadInput);
+  } else {
+    const int per = a.nt * (a.pair_keys ? 1 : 2), t0 = tile * per, t1 = min(t0 + per, a.T);
+    int lo = INT_MAX, hi = -1;
+    for (int t = t0 + lane; t < t1; t += 32) {
+      int l, h;
+      if (key_range(a, (int64_t)b * a.T + t, l, h)) lo = min(lo, l), hi = max(hi, h);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lo <= hi) k0 = lo / kKeys, n = hi / kKeys - k0 + 1;
+  }
+  // a unit that sees nothing takes a step all the same, which writes its zeros
+  if (a.pair_keys) n = (n + 1) / 2;
+  return make_int2(k0, max(n, 1));
+}
+// The steps of many units, a warp each (few: the next kernel counts them itself).
+template <bool FP8>
+__global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ Args a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= a.B1 * a.tiles) return;
+  const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles);
+  if ((threadIdx.x & 31) == 0) a.units[i] = u;
+}
+// Lays the units end to end and finds where each CTA's range begins.
+template <bool FP8>
+__global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args a, int counted) {
+  __shared__ long long s_part[32], s_run;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int N = a.B1 * a.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!counted) {
+    for (int i = warp; i < N; i += 32) {
+      const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles);
+      if (lane == 0) a.units[i] = u;
+    }
+  }
+  if (threadIdx.x == 0) s_run = 0;
+  __syncthreads();
+  for (int i0 = 0; i0 < N; i0 += 1024) {
+    const int i = i0 + threadIdx.x;
+    const long long n = i < N ? a.units[i].y : 0;
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) s_part[warp] = inc;
+    __syncthreads();
+    long long run = s_run;
+    for (int w = 0; w < warp; ++w) run += s_part[w];
+    if (i < N) a.before[i] = run + inc - n;
+    __syncthreads();
+    if (threadIdx.x == 1023) s_run = run + inc;
+    __syncthreads();
+  }
+  const long long one = s_run, total = one * a.H1;
+  if (threadIdx.x == 0) a.before[N] = one;
+  const long long L = (total + a.P - 1) / a.P;
+  if (threadIdx.x == 0) a.plan->total = total, a.plan->L = L;
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.P; c += 1024) {
+    const long long f = c * L;
+    Start st{-1, 0, 0, 0, 0};
+    if (f < total) {
+      int lo = 0, hi = a.B1;         // the sequence: before[b * tiles] * H1 <= f
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.before[(int64_t)mid * a.tiles] * a.H1 <= f) lo = mid; else hi = mid;
+      }
+      const int b = lo;
+      const long long b0 = a.before[(int64_t)b * a.tiles], nb = a.before[(int64_t)(b + 1) * a.tiles] - b0;
+      const int h = (int)((f - b0 * a.H1) / nb);
+      const long long in = f - b0 * a.H1 - h * nb + b0;          // among one head's
+      lo = 0, hi = a.tiles;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.before[(int64_t)b * a.tiles + mid] <= in) lo = mid; else hi = mid;
+      }
+      st = {b, h, lo, a.units[(int64_t)b * a.tiles + lo].y, in - a.before[(int64_t)b * a.tiles + lo]};
+    }
+    a.start[c] = st;
+  }
+}
+
+// ------------------------------------------------------------------- a CTA's range
+struct Seg {
+  int b, h, tile;                    // the unit
+  int k0, n;                         // its first key tile, its steps
+  int s0, cnt;                       // steps of this range
+};
+// Walks the units of a range; every role does it by itself.
+struct Walk {
+  Seg g;
+  long long left;
+  __device__ __forceinline__ bool begin(const Args& a) {
+    const Start st = a.start[blockIdx.x];
+    if (st.b < 0) return false;
+    const Plan p = *a.plan;
+    left = min(p.L, p.total - (long long)blockIdx.x * p.L);
+    g.b = st.b, g.h = st.h, g.tile = st.tile;
+    load(a);
+    g.s0 = (int)st.off;
+    g.cnt = (int)min((long long)(g.n - g.s0), left);
+    return true;
+  }
+  __device__ __forceinline__ void load(const Args& a) {
+    const int2 u = a.units[(int64_t)g.b * a.tiles + g.tile];
+    g.k0 = u.x, g.n = u.y;
+  }
+  __device__ __forceinline__ bool next(const Args& a) {
+    left -= g.cnt;
+    if (left <= 0) return false;
+    if (++g.tile == a.tiles) {
+      g.tile = 0;
+      if (++g.h == a.H1) g.h = 0, ++g.b;
+    }
+    load(a);
+    g.s0 = 0;
+    g.cnt = (int)min((long long)g.n, left);
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------- pieces
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int kStageBytes = kKeys * D * (FP8 ? 1 : 2);
+  static constexpr int kQBytes = FP8 ? 2 * kRows * D : kRows * D * 2;       // of a stream: two parts, or bf16
+  static constexpr int kStages = FP8 ? 9 : D == 128 ? 5 : 11;
+  static constexpr int kMetaBytes = FP8 ? (int)sizeof(Meta) * kMeta : 0;
+  static constexpr int kSmem = 1024 + 2 * kQBytes + kStages * kStageBytes + kMetaBytes;
+  // bf16 reaches as far down as fp32 does, so weights may be small; e4m3's two parts
+  // end at 2^-10, so the largest weight of a row is kept between 2^6 and 2^8
+  static constexpr float kShift = FP8 ? 6.f : 0.f, kSlack = FP8 ? 2.f : 8.f;
+  static constexpr int kQSteps = FP8 ? D / 32 : D / 16, kVSteps = FP8 ? kKeys / 32 : kKeys / 16;
+};
+
+// q_full, kv_full / kv_empty (a ring over the tiles of keys and values in the order
+// of their products), s_full (a stream's scores are there; at a segment's end: its
+// output), p_full (a stream's weights are there, and its scores in registers).
+// A wait looks at the parity of a phase alone, so none may be two phases ahead of
+// a warp that still waits for the first:
+//   kv_full(i + kStages)   kv_empty(i), committed behind products that waited for kv_full(i)
+//   kv_empty(i + kStages)  kv_full(i + kStages), loaded after a look at kv_empty(i)
+//   s_full(i + 1)          p_full(i) of all four warps, which saw s_full(i); a segment's
+//                          end likewise, and the next segment's first scores come
+//                          at once: the end's barrier is another, s_end
+//   s_end(i + 1)           p_full of the next segment, made after a look at s_end(i)
+//   p_full(i + 1)          s_full(i + 1), issued after a look at p_full(i)
+//   q_full(i + 1)          q_empty(i) (bf16), committed behind products after q_full(i); or
+//                          s_end(i) (e4m3: the rows' own warps write the queries)
+//   meta_full(i + kMeta)   see Meta
+struct Bars {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], s_end[2], p_full[2], q_full, q_empty, meta_full[kMeta], drain;
+};
+
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "LOOK:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra SEEN;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra LOOK;\n"
+      "SEEN:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(limit)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two values below 448 -> two e4m3 parts each (low byte first): x = a + b to 8
+// significant bits, or to 2^-10.
+__device__ __forceinline__ void split2(float lo, float hi, uint16_t& a, uint16_t& b) {
+  uint32_t h, back, rest;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(h) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(a) : "r"(h));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(back) : "h"(a));
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(rest) : "r"(h), "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(b) : "r"(rest));
+}
+
+// Products from one thread.  A in shared memory (scores) or tensor memory (output).
+template <bool FP8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if constexpr (FP8)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+template <bool FP8>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  if constexpr (FP8)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+// Instruction descriptor: fp32 accumulator, A K-major; B K-major (keys) or, with
+// rows = contraction index, MN-major (values).
+template <bool FP8>
+__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
+  return (1u << 4) | (FP8 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(kRows >> 4) << 24);
+}
+// Rows of 128 or 64 bytes in swizzled atoms of 8 rows.  As a K-major operand: groups
+// of 8 rows `8 * row bytes` apart (stride); as an MN-major one the same groups along
+// the contraction, and `lead` bytes between panels of a row's width.
+template <int ROW>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lead >> 4) << 16;
+  d |= (uint64_t)((8 * ROW) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(ROW == 128 ? 2 : 4) << 61;      // swizzle of 128 or 64 bytes
+  return d;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// ------------------------------------------------------------------- the loads
+// Tile `t` (an index of key tiles of the unit) of keys or values into a stage.
+template <int D, bool FP8>
+__device__ __forceinline__ void load_tile(const Args& a, const Seg& g, bool vals, int t, uint32_t dst, uint32_t bar) {
+  const CUtensorMap* map = vals ? &a.vmap : &a.kmap;
+  tc::mbar_arrive_expect_tx(bar, Cfg<D, FP8>::kStageBytes);
+  if constexpr (FP8) {
+    const int b = g.b / a.H_kv, h = g.b - b * a.H_kv;
+    const int64_t row = (int64_t)b * a.s.off[a.H_kv] + a.s.off[h];
+    tc::tma_load_3d(dst, map, bar, 0, 0, (int)(row / q8::kRows) + t * (kKeys / q8::kRows));
+  } else {
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p)
+      tc::tma_load_3d(dst + p * (kKeys * 128), map, bar, p * 64, t * kKeys, g.b * a.H1 + g.h);
+  }
+}
+
+// A warp: lane 0 copies; with the 8-bit cache all lanes fetch positions and scales.
+template <int D, bool FP8>
+__device__ bool load_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring, Meta* meta) {
+  using C = Cfg<D, FP8>;
+  const int lane = threadIdx.x & 31;
+  const int subs = a.pair_keys ? 2 : 1;           // key tiles of a step
+  uint32_t it = 0, mt = 0, nq = 0;               // tiles, tiles of keys, queries asked for
+  bool ok = true;
+  Walk w;
+  if (!w.begin(a)) return true;
+  do {
+    const Seg& g = w.g;
+    int q_hi = -1, q_lo = INT_MAX;
+    int n_rows = 0, b = 0, h = 0;
+    if constexpr (FP8) {
+      bool bad;
+      n_rows = rows_held(a, g.b, &bad);
+      b = g.b / a.H_kv, h = g.b - b * a.H_kv;
+      const int per = a.nt * (a.pair_keys ? 1 : 2), t0 = g.tile * per, t1 = min(t0 + per, a.T);
+      for (int t = t0 + lane; t < t1; t += 32) {
+        const int p = __ldg(a.q_pos + (int64_t)b * a.T + t);
+        q_lo = min(q_lo, p), q_hi = max(q_hi, p);
+      }
+      q_lo = __reduce_min_sync(0xffffffffu, q_lo);
+      q_hi = __reduce_max_sync(0xffffffffu, q_hi);
+    } else {
+      if (nq > 0) ok = poll(smem_u32(&bars->q_empty), (nq - 1) & 1, a.wait_limit);
+      if (!ok) break;
+      ++nq;
+      if (lane == 0) {
+        const int rows = a.nt * a.G, qs = a.pair_keys ? 1 : 2;
+        const uint32_t bar = smem_u32(&bars->q_full);
+        tc::mbar_arrive_expect_tx(bar, (uint32_t)(qs * rows * D * 2));
+        for (int x = 0; x < qs; ++x)
+          for (int p = 0; p < D / 64; ++p)
+            tc::tma_load_3d(sQ + x * C::kQBytes + p * (kRows * 128), &a.qmap, bar, p * 64, (g.tile * qs + x) * a.nt,
+                            g.b * a.H_q + g.h * a.G);
+      }
+    }
+    const auto put = [&](bool vals, int t) {
+      const uint32_t st = it % C::kStages;
+      if (ok) ok = poll(smem_u32(&bars->kv_empty[st]), ((it / C::kStages) & 1) ^ 1, a.wait_limit);
+      if (!ok) return;
+      if constexpr (FP8) {
+        if (!vals) {                 // the tile's positions and scales with its keys
+          Meta& m = meta[mt % kMeta];
+          const int64_t row0 = (int64_t)b * a.s.off[a.H_kv] + a.s.off[h];
+          uint32_t seen = 0;         // lane y: of block y
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = t * kKeys + x * 32 + lane;
+            const int p = row < n_rows ? __ldg(a.pos + row0 + row) : -1;
+            m.pos[x * 32 + lane] = p;
+            m.rel[x * 32 + lane] = (float)(int)((uint32_t)p - (uint32_t)q_hi);
+            const uint32_t some = __ballot_sync(0xffffffffu, p >= 0 && p <= q_hi);
+            const bool all = __all_sync(0xffffffffu, p >= 0 && p <= q_lo);
+            if (lane == 0) m.some[x] = some, m.mixed[x] = all ? 0 : 1;
+            if (lane >> 1 == x) seen = some >> (lane & 1) * 16 & 0xffffu;
+          }
+          if (lane < kKeys / q8::kRows)          // a block of which nothing is seen may have anything for a scale
+            m.scale[lane] = seen ? __ldg(a.scale + row0 / q8::kRows + t * (kKeys / q8::kRows) + lane)
+                                 : make_float2(1.f, kLeastUnit);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(smem_u32(&bars->meta_full[mt % kMeta]));
+          ++mt;
+        }
+      }
+      if (lane == 0) load_tile<D, FP8>(a, g, vals, t, ring + st * C::kStageBytes, smem_u32(&bars->kv_full[st]));
+      __syncwarp();
+      ++it;
+    };
+    // in the order of the products
+    const int t0 = g.k0 + g.s0 * subs;
+    for (int i = 0; i <= g.cnt && ok; ++i)
+      for (int x = 0; x < subs; ++x) {
+        if (i > 0) put(true, t0 + (i - 1) * subs + x);
+        if (i < g.cnt) put(false, t0 + i * subs + x);
+      }
+  } while (ok && w.next(a));
+  // every copy issued has landed before the CTA may leave
+  const uint32_t lo = it > (uint32_t)C::kStages ? it - C::kStages : 0;
+  for (uint32_t i = lo; i < it; ++i)
+    scan::drain_wait(smem_u32(&bars->kv_full[i % C::kStages]), (i / C::kStages) & 1, a.status);
+  if (nq > 0) scan::drain_wait(smem_u32(&bars->q_full), (nq - 1) & 1, a.status);
+  return ok;
+}
+
+// ------------------------------------------------------------------- the products
+// Rows of a stage whose bit is not set become zeros: what no query of the unit sees
+// may hold anything, and a weight of zero times NaN would not be zero.
+template <int D, bool FP8>
+__device__ __forceinline__ void zero_rows(uint32_t stage, uint32_t keep, int word) {
+  constexpr int kRow = FP8 && D == 64 ? 64 : 128, kPanels = FP8 || D == 64 ? 1 : 2;
+  const int lane = threadIdx.x & 31;
+  if (!(keep >> lane & 1)) {
+#pragma unroll
+    for (int p = 0; p < kPanels; ++p)
+#pragma unroll
+      for (int c = 0; c < kRow / 16; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(stage + p * (kKeys * 128) +
+                                                                        (word * 32 + lane) * kRow + c * 16),
+                     "r"(0)
+                     : "memory");
+  }
+}
+
+template <int D>
+__device__ __forceinline__ uint32_t col_o(int x) { return kColO + x * D; }
+// The weights over the scores; at D = 64, where the two products have different
+// shapes and so no order of their own, in columns that are left.
+template <int D>
+__device__ __forceinline__ uint32_t col_p(int x) { return D == 64 ? kColO + 128 + x * 64 : kColS + x * 128; }
+
+template <int D, bool FP8>
+__device__ __forceinline__ void issue_scores(uint32_t tmem, int x, uint32_t q, uint32_t stage) {
+  constexpr uint32_t kId = idesc<FP8>(kKeys, false);
+  constexpr int kRow = FP8 ? D : 128;
+  const uint64_t qd = desc_rows<kRow>(q, 16), kd = desc_rows<kRow>(stage, 16);
+  const uint32_t d = tmem + kColS + x * 128;
+  if constexpr (FP8) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s)
+        mma_ss<true>(d, qd + ((p * (kRows * D) + s * 32) >> 4), kd + (s * 32 >> 4), kId, p + s > 0);
+  } else {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const uint32_t at = ((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4;
+      mma_ss<false>(d, qd + at, kd + at, kId, s > 0);
+    }
+  }
+}
+template <int D, bool FP8>
+__device__ __forceinline__ void issue_output(uint32_t tmem, int x, uint32_t stage, bool add) {
+  constexpr uint32_t kId = idesc<FP8>(D, true);
+  constexpr int kRow = FP8 ? D : 128;
+  const uint64_t vd = desc_rows<kRow>(stage, kKeys * 128);
+  const uint32_t d = tmem + col_o<D>(x), p = tmem + col_p<D>(x);
+  if constexpr (FP8) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int s = 0; s < kKeys / 32; ++s)
+        mma_ts<true>(d, p + y * 32 + s * 8, vd + (s * 32 * D >> 4), kId, add || y + s > 0);
+  } else {
+#pragma unroll
+    for (int s = 0; s < kKeys / 16; ++s) mma_ts<false>(d, p + s * 8, vd + (s * 16 * 128 >> 4), kId, add || s > 0);
+  }
+}
+
+// The warp waits as a whole; lane 0 issues.
+template <int D, bool FP8>
+__device__ bool mma_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring, const Meta* meta, uint32_t tmem) {
+  using C = Cfg<D, FP8>;
+  const int lane = threadIdx.x & 31;
+  const bool issues = lane == 0;
+  uint32_t it = 0, mt = 0, seg = 0, steps = 0;
+  bool ok = true;
+  const auto wait = [&](uint64_t* bar, uint32_t phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
+  Walk w;
+  if (w.begin(a)) do {
+    const Seg& g = w.g;
+    int lo[8], hi[8];                // what the unit's tokens see
+    if constexpr (!FP8) {
+      const int per = a.nt * (a.pair_keys ? 1 : 2);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const int in = y * 32 + lane, t = g.tile * per + in;
+        lo[y] = INT_MAX, hi[y] = -1;
+        if (in < per && t < a.T) key_range(a, (int64_t)g.b * a.T + t, lo[y], hi[y]);
+      }
+    }
+    const int t0 = g.k0 + g.s0 * (a.pair_keys ? 2 : 1);
+    // rows of tile `t` that nothing sees
+    const auto clean = [&](int t, uint32_t m, uint32_t stage) {
+      uint32_t keep[4];
+      if constexpr (FP8) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) keep[y] = meta[m % kMeta].some[y];
+      } else {
+        const int k = t * kKeys;
+        bool cover = false;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) cover |= lo[y] <= k && hi[y] >= k + kKeys - 1;
+        if (__any_sync(0xffffffffu, cover)) return;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t mask = 0;
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            const int first = max(lo[z] - k - 32 * y, 0), last = min(hi[z] - k - 32 * y, 31);
+            if (first <= last) mask |= (0xffffffffu >> (31 - last)) & (0xffffffffu << first);
+          }
+          keep[y] = __reduce_or_sync(0xffffffffu, mask);
+        }
+      }
+      if ((keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu) return;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) zero_rows<D, FP8>(stage, keep[y], y);
+      tc::fence_proxy_async();
+      __syncwarp();
+    };
+    ok = ok && wait(&bars->q_full, seg);
+    uint32_t k_st[2] = {}, v_st[2] = {};
+    for (int i = 0; i <= g.cnt && ok; ++i) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bool own = a.pair_keys || x == 0, last_use = a.pair_keys || x == 1;
+        if (i > 0) {
+          if (own) {
+            v_st[x] = it % C::kStages;
+            ok = ok && wait(&bars->kv_full[v_st[x]], it / C::kStages);
+            ++it;
+          } else {
+            v_st[1] = v_st[0];
+          }
+          const uint32_t stage = ring + v_st[x] * C::kStageBytes;
+          if (ok && own) {
+            const int sub = a.pair_keys ? 2 * (i - 1) + x : i - 1;
+            clean(t0 + sub, mt + sub, stage);
+          }
+          ok = ok && wait(&bars->p_full[x], steps + i - 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (issues) {
+            issue_output<D, FP8>(tmem, x, stage, i > 1);
+            if (last_use) tc::mma_commit(smem_u32(&bars->kv_empty[v_st[x]]));
+            if (i == g.cnt) tc::mma_commit(smem_u32(&bars->s_end[x]));
+          }
+          __syncwarp();
+        }
+        if (i < g.cnt) {
+          if (own) {
+            k_st[x] = it % C::kStages;
+            ok = ok && wait(&bars->kv_full[k_st[x]], it / C::kStages);
+            ++it;
+          } else {
+            k_st[1] = k_st[0];
+          }
+          if (!ok) break;
+          tc::fence_after_sync();
+          if (issues) {
+            issue_scores<D, FP8>(tmem, x, sQ + (a.pair_keys ? 0 : x) * C::kQBytes, ring + k_st[x] * C::kStageBytes);
+            tc::mma_commit(smem_u32(&bars->s_full[x]));
+            if (last_use) tc::mma_commit(smem_u32(&bars->kv_empty[k_st[x]]));
+            if (!FP8 && i == g.cnt - 1 && x == 1) tc::mma_commit(smem_u32(&bars->q_empty));
+          }
+          __syncwarp();
+        }
+      }
+    }
+    mt += g.cnt * (a.pair_keys ? 2 : 1);
+    steps += g.cnt;
+    ++seg;
+  } while (ok && w.next(a));
+  if (issues) scan::drain_mma(smem_u32(&bars->drain), a.status);
+  __syncwarp();
+  return ok;
+}
+
+// ------------------------------------------------------------------- the weights
+// A query row of bf16 -> two e4m3 parts in shared memory; returns the power of two
+// that was taken out.
+template <int D>
+__device__ __forceinline__ float write_query(const __nv_bfloat16* q, bool live, uint32_t sq, int row) {
+  uint4 w[D / 8];
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    w[i] = live ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+    mx = __vmaxu2(__vmaxu2(mx, w[i].x & 0x7fff7fffu), __vmaxu2(w[i].y & 0x7fff7fffu, w[i].z & 0x7fff7fffu));
+    mx = __vmaxu2(mx, w[i].w & 0x7fff7fffu);
+  }
+  mx = max(mx & 0xffffu, mx >> 16);
+  // the row's largest value into [2^7, 2^8)
+  const uint32_t e = mx >> 7, ee = e == 255 ? 134u : min(max(e, 8u), 254u);
+  const float down = __uint_as_float((261u - ee) << 23);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t p[2][4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const uint4 v = w[2 * c + (y >> 1)];
+      const uint32_t u0 = y & 1 ? v.z : v.x, u1 = y & 1 ? v.w : v.y;
+      uint16_t a[2], b[2];
+      split2(__uint_as_float(u0 << 16) * down, __uint_as_float(u0 & 0xffff0000u) * down, a[0], b[0]);
+      split2(__uint_as_float(u1 << 16) * down, __uint_as_float(u1 & 0xffff0000u) * down, a[1], b[1]);
+      p[0][y] = (uint32_t)a[0] | (uint32_t)a[1] << 16;
+      p[1][y] = (uint32_t)b[0] | (uint32_t)b[1] << 16;
+    }
+    const uint32_t at = D == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ (row >> 1 & 3)) << 4);
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(sq + y * (kRows * D) + at), "r"(p[y][0]),
+                   "r"(p[y][1]), "r"(p[y][2]), "r"(p[y][3])
+                   : "memory");
+  }
+  return __uint_as_float((ee - 7u) << 23);
+}
+
+// A score's product -> the cap's share of it: tanh.  Warps whose 32 rows have no
+// large one take the polynomial alone.
+__device__ __forceinline__ void cap_all(float (&x)[kKeys], const float2* f, bool blocks, float f1) {
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < kKeys; k += 2) {
+    const float fk = blocks ? f[k / 16].x : f1;
+    const float2 v = mul2(make_float2(x[k], x[k + 1]), make_float2(fk, fk));
+    x[k] = v.x, x[k + 1] = v.y;
+    asm("max.f32 %0, %0, %1, %2;\n" : "+f"(top) : "f"(fabsf(v.x)), "f"(fabsf(v.y)));
+  }
+  if (__all_sync(0xffffffffu, top <= kTanhNear)) {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) x[k] = tanh_near(x[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) x[k] = tanh_of(x[k]);
+  }
+}
+
+template <int D, bool FP8, bool CAP, bool BIAS>
+__device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* meta, uint32_t tmem, float* s_x) {
+  using C = Cfg<D, FP8>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 2, row = (warp & 3) * 32 + lane;
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t s_at = tmem + lanes + kColS + x * 128, p_at = tmem + lanes + col_p<D>(x), o_at = tmem + lanes;
+  const int gq = row / a.nt, tl = row - gq * a.nt;           // query head of the group, token of the tile
+  const int subs = a.pair_keys ? 2 : 1;
+  const bool any_row = (warp & 3) * 32 < a.nt * a.G;         // none of the warp's rows is one: nothing reads its part
+  uint32_t steps = 0, mt = 0, seg = 0;
+  bool ok = true;
+  // after a wait that gave up: go on without waiting, so that no barrier is left alone
+  const auto wait = [&](uint64_t* bar, uint32_t phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
+  Walk w;
+  if (!w.begin(a)) return true;
+  do {
+    const Seg& g = w.g;
+    const int bh = g.b * a.H1 + g.h, b = FP8 ? bh / a.H_kv : g.b, h = FP8 ? bh - b * a.H_kv : g.h;
+    const int t = (g.tile * (a.pair_keys ? 1 : 2) + (a.pair_keys ? 0 : x)) * a.nt + tl;
+    const bool live = gq < a.G && t < a.T;
+    const int64_t q_row = ((int64_t)b * a.H_q + h * a.G + gq) * a.T + t;
+    int lo = 0, hi = INT_MAX, qp = -1;
+    float slope = 0.f, q_rel = 0.f;
+    if (live) {
+      qp = __ldg(a.q_pos + (int64_t)b * a.T + t);
+      if constexpr (!FP8) key_range(a, (int64_t)b * a.T + t, lo, hi);
+      if constexpr (BIAS) slope = __ldg(a.slopes + h * a.G + gq) * kLog2e;
+    }
+    float c2 = a.scale2;
+    if constexpr (FP8) {
+      if constexpr (BIAS) {
+        // positions in Meta are relative to the unit's last query
+        const int per = a.nt * (a.pair_keys ? 1 : 2), t0 = g.tile * per, t1 = min(t0 + per, a.T);
+        int last = -1;
+        for (int y = t0 + lane; y < t1; y += 32) last = max(last, __ldg(a.q_pos + (int64_t)b * a.T + y));
+        q_rel = (float)(__reduce_max_sync(0xffffffffu, last) - qp);
+      }
+      if (!a.pair_keys || x == 0) {
+        c2 *= write_query<D>(a.q + (live ? q_row * D : 0), live, sQ + (a.pair_keys ? 0 : x) * C::kQBytes, row);
+        tc::fence_proxy_async();
+        if (a.pair_keys) s_x[row] = c2;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(smem_u32(&bars->q_full));
+      }
+      if (a.pair_keys) {
+        asm volatile("bar.sync 1, 256;\n" ::: "memory");
+        c2 = s_x[row];
+      }
+    }
+    float ref = kNoRef, unit = kLeastUnit;
+    float2 sum2[2] = {};
+    const int t0 = g.k0 + g.s0 * subs;
+    for (int i = 0; i < g.cnt; ++i, ++steps) {
+      const int tile = t0 + i * subs + (a.pair_keys ? x : 0);
+      const uint32_t m_at = mt + i * subs + (a.pair_keys ? x : 0);
+      const Meta& me = meta[m_at % kMeta];
+      if constexpr (FP8) ok = ok && wait(const_cast<uint64_t*>(&bars->meta_full[m_at % kMeta]), m_at / kMeta);
+      ok = ok && wait(&bars->s_full[x], steps);
+      tc::fence_after_sync();
+      if (any_row) {
+        float s[kKeys];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) tmem_ld32(s_at + 32 * y, s + 32 * y);
+        float2 f[kKeys / 16] = {};     // of 16 keys: factor to log2 units (x), of the values (y)
+        if constexpr (FP8) {
+#pragma unroll
+          for (int y = 0; y < kKeys / 16; ++y) {
+            f[y] = me.scale[y];
+            // a factor of 0 would make NaN of the masked scores
+            f[y].x = CAP ? f[y].x * c2 * a.inv_cap2 : fmaxf(f[y].x * c2, 1.2e-38f);
+          }
+        }
+        tc::tmem_wait_ld();
+        tc::reg_fence(s, kKeys);
+        if constexpr (CAP) cap_all(s, f, FP8, c2 * a.inv_cap2);
+        // ---- scores: s times f1 (or f) plus e0
+        float e0 = 0.f;
+        if constexpr (BIAS) {
+          const auto unbiased = [&](int k) { return CAP ? s[k] * a.cap2 : FP8 ? s[k] * f[k / 16].x : s[k] * c2; };
+          if constexpr (FP8) {
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k) s[k] = fmaf(slope, me.rel[k] + q_rel, unbiased(k));
+          } else {
+            const int d0 = tile * kKeys - qp;
+            if (__any_sync(0xffffffffu, d0 < 0 && d0 + kKeys > 0)) {   // the tile has keys on both sides of a query
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k) s[k] = fmaf(-slope, fabsf((float)d0 + k), unbiased(k));
+            } else {
+              const float to = d0 < 0 ? slope : -slope;
+              e0 = to * (float)d0;
+#pragma unroll
+              for (int k = 0; k < kKeys; ++k) s[k] = fmaf(to, (float)k, unbiased(k));
+            }
+          }
+        }
+        // ---- mask
+        if constexpr (FP8) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (me.mixed[y]) {
+#pragma unroll
+              for (int z = 0; z < 8; ++z) {
+                const int4 p = *reinterpret_cast<const int4*>(&me.pos[32 * y + 4 * z]);
+                if (p.x < 0 || p.x > qp) s[32 * y + 4 * z] = -INFINITY;
+                if (p.y < 0 || p.y > qp) s[32 * y + 4 * z + 1] = -INFINITY;
+                if (p.z < 0 || p.z > qp) s[32 * y + 4 * z + 2] = -INFINITY;
+                if (p.w < 0 || p.w > qp) s[32 * y + 4 * z + 3] = -INFINITY;
+              }
+            }
+        } else {
+          const int l = lo - tile * kKeys, r = hi - tile * kKeys;
+          if (__any_sync(0xffffffffu, l > 0 || r < kKeys - 1)) {
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k)
+              if (k < l || k > r) s[k] = -INFINITY;
+          }
+        }
+        // ---- the maximum, and the reference behind it
+        float m;
+        if constexpr (FP8 && !CAP && !BIAS) {
+          m = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < kKeys / 16; ++y) {
+            float v = max3(s[16 * y], s[16 * y + 1], s[16 * y + 2]);
+#pragma unroll
+            for (int k = 3; k < 15; k += 2) v = max3(v, s[16 * y + k], s[16 * y + k + 1]);
+            m = fmaxf(m, fmaxf(v, s[16 * y + 15]) * f[y].x);
+          }
+        } else {
+          float m1 = s[1];
+          m = s[0];
+#pragma unroll
+          for (int k = 2; k < 126; k += 4) m = max3(m, s[k], s[k + 1]), m1 = max3(m1, s[k + 2], s[k + 3]);
+          m = fmaxf(max3(m, s[126], s[127]), m1);
+          if constexpr (BIAS) m += e0;
+          else m *= CAP ? a.cap2 : c2;
+        }
+        bool move = m > ref + (C::kSlack + C::kShift);
+        float top = kLeastUnit;
+        if constexpr (FP8) {
+#pragma unroll
+          for (int y = 0; y < kKeys / 16; ++y) top = fmaxf(top, f[y].y);
+          move |= top > unit;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          const float to = fmaxf(ref, m - C::kShift);
+          float fo = ex2(ref - to);
+          ref = to;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) sum2[y].x *= fo, sum2[y].y *= fo;
+          if constexpr (FP8) {
+            const float u = fmaxf(unit, top);
+            fo *= unit / u;
+            unit = u;
+          }
+          if (i > 0) {
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y) {
+              float o[32];
+              tmem_ld32(o_at + col_o<D>(x) + 32 * y, o);
+              tc::tmem_wait_ld();
+              tc::reg_fence(o, 32);
+#pragma unroll
+              for (int z = 0; z < 32; ++z) o[z] *= fo;
+#pragma unroll
+              for (int z = 0; z < 2; ++z)
+                tc::tmem_st16(o_at + col_o<D>(x) + 32 * y + 16 * z, reinterpret_cast<const uint32_t*>(o) + 16 * z);
+            }
+          }
+        }
+        // ---- weights
+        const float neg = e0 - ref;
+        const float2 r2 = make_float2(neg, neg);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {  // 32 keys
+          uint32_t p[16];              // bf16: 16 columns; e4m3: 8 of the first part, 8 of the second
+          uint16_t pa[16], pb[16];
+          (void)pa, (void)pb;
+#pragma unroll
+          for (int z = 0; z < 16; ++z) {
+            const int k = 32 * y + 2 * z;
+            float2 e;
+            if constexpr (BIAS) {
+              e = add2(make_float2(s[k], s[k + 1]), r2);
+            } else {
+              const float fk = CAP ? a.cap2 : FP8 ? f[k / 16].x : c2;
+              e = fma2(make_float2(s[k], s[k + 1]), make_float2(fk, fk), r2);
+            }
+            float2 u = make_float2(ex2(e.x), ex2(e.y));
+            sum2[z & 1] = add2(sum2[z & 1], u);
+            if constexpr (FP8) {       // quotient of two powers of two, 0 below the normal numbers
+              const float fv =
+                  __int_as_float(max(__float_as_int(f[k / 16].y) - __float_as_int(unit) + 0x3f800000, 0));
+              u = mul2(u, make_float2(fv, fv));
+              split2(u.x, u.y, pa[z], pb[z]);
+            } else {
+              p[z] = bf16x2_of(u.x, u.y);
+            }
+          }
+          if constexpr (FP8) {
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+              p[z] = (uint32_t)pa[2 * z] | (uint32_t)pa[2 * z + 1] << 16;
+              p[8 + z] = (uint32_t)pb[2 * z] | (uint32_t)pb[2 * z + 1] << 16;
+            }
+            tc::tmem_st4(p_at + 8 * y, p);
+            tc::tmem_st4(p_at + 8 * y + 4, p + 4);
+            tc::tmem_st4(p_at + 32 + 8 * y, p + 8);
+            tc::tmem_st4(p_at + 32 + 8 * y + 4, p + 12);
+          } else {
+            tc::tmem_st16(p_at + 16 * y, p);
+          }
+        }
+        tc::tmem_wait_st();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(smem_u32(&bars->p_full[x]));
+    }
+    // ---- the segment's end
+    ok = ok && wait(&bars->s_end[x], seg);
+    tc::fence_after_sync();
+    float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+    const bool whole = g.s0 == 0 && g.cnt == g.n;
+    const int64_t slot = 2 * blockIdx.x + (g.s0 == 0 ? 1 : 0);
+    // row pairs: a thread writes its row.  Key pairs: both streams' threads of a row
+    // tell each other their references and sums, and take half of its dims each
+    float f0 = FP8 ? unit : 1.f, f1 = 0.f;
+    int from = 0, to = D, first = x;
+    if (a.pair_keys) {
+      tc::fence_before_sync();
+      s_x[256 + x * 128 + row] = ref;
+      s_x[512 + x * 128 + row] = sum;
+      s_x[768 + x * 128 + row] = unit;
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+      tc::fence_after_sync();
+      const float ra = s_x[256 + row], rb = s_x[384 + row], top = fmaxf(ra, rb);
+      f0 = ex2(ra - top), f1 = ex2(rb - top);
+      sum = s_x[512 + row] * f0 + s_x[640 + row] * f1;
+      ref = top;
+      if constexpr (FP8) f0 *= s_x[768 + row], f1 *= s_x[896 + row];
+      from = x * (D / 2), to = from + D / 2, first = 0;
+    }
+    if (any_row) {
+      const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      f0 *= inv, f1 *= inv;
+      const int64_t part = slot * ((a.pair_keys ? 1 : 2) * kRows) + (a.pair_keys ? 0 : x) * kRows + row;
+      for (int d = from; d < to; d += 16) {
+        float o[16];
+        tc::tmem_ld16(o_at + col_o<D>(first) + d, o);
+        tc::tmem_wait_ld();
+        tc::reg_fence(o, 16);
+        if (a.pair_keys) {
+          float o1[16];
+          tc::tmem_ld16(o_at + col_o<D>(1) + d, o1);
+          tc::tmem_wait_ld();
+          tc::reg_fence(o1, 16);
+#pragma unroll
+          for (int z = 0; z < 16; ++z) o[z] = o[z] * f0 + o1[z] * f1;
+        } else {
+#pragma unroll
+          for (int z = 0; z < 16; ++z) o[z] *= f0;
+        }
+        if (sum == 0.f) {              // a row that saw nothing
+#pragma unroll
+          for (int z = 0; z < 16; ++z) o[z] = 0.f;
+        }
+        if (!live) continue;
+        if (whole) {
+          uint32_t v[8];
+#pragma unroll
+          for (int z = 0; z < 8; ++z) v[z] = bf16x2_of(o[2 * z], o[2 * z + 1]);
+          uint4* p = reinterpret_cast<uint4*>(a.out + q_row * D + d);
+          p[0] = make_uint4(v[0], v[1], v[2], v[3]);
+          p[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        } else {
+          float4* p = reinterpret_cast<float4*>(a.part_o + part * D + d);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) p[z] = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+        }
+      }
+      if (live && (!a.pair_keys || x == 0)) {
+        if (!whole) a.part_ml[part] = make_float2(ref, sum);
+        else if (a.lse) a.lse[q_row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+      }
+    }
+    if (a.pair_keys) {                 // the next segment's weights and outputs come after everybody's reads
+      tc::fence_before_sync();
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");
+    }
+    mt += g.cnt * subs;
+    ++seg;
+  } while (w.next(a));
+  return ok;
+}
+
+template <int D, bool FP8, bool CAP, bool BIAS>
+__device__ __forceinline__ void attend(const Args& a) {
+  using C = Cfg<D, FP8>;
+  static_assert(C::kStages <= kMaxStages && (!FP8 || C::kStages <= 9), "see Meta");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t s_tmem;
+  const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, ring = sQ + 2 * C::kQBytes;
+  uint8_t* base = smem_raw + (sQ - smem_u32(smem_raw));
+  Meta* meta = reinterpret_cast<Meta*>(base + 2 * C::kQBytes + C::kStages * C::kStageBytes);
+  float* s_x = reinterpret_cast<float*>(base + C::kQBytes);       // key pairs: stream 1 has no queries of its own
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      tc::mbar_init(smem_u32(&bars.kv_full[i]), 1);
+      tc::mbar_init(smem_u32(&bars.kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
+      tc::mbar_init(smem_u32(&bars.s_end[i]), 1);
+      tc::mbar_init(smem_u32(&bars.p_full[i]), 4);
+    }
+    for (int i = 0; i < kMeta; ++i) tc::mbar_init(smem_u32(&bars.meta_full[i]), 1);
+    tc::mbar_init(smem_u32(&bars.q_full), FP8 ? (a.pair_keys ? 4 : 8) : 1);
+    tc::mbar_init(smem_u32(&bars.q_empty), 1);
+    tc::mbar_init(smem_u32(&bars.drain), 1);
+    tc::fence_barrier_init();
+    tc::tma_prefetch_desc(&a.kmap);
+    tc::tma_prefetch_desc(&a.vmap);
+    if (!FP8) tc::tma_prefetch_desc(&a.qmap);
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(smem_u32(&s_tmem), kCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  grid_dep_wait();
+  grid_dep_launch();
+  bool ok = true;
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+    ok = soft_warps<D, FP8, CAP, BIAS>(a, &bars, sQ, meta, tmem, s_x);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    if (warp == kLoadWarp) ok = load_warp<D, FP8>(a, &bars, sQ, ring, meta);
+    else if (warp == kMmaWarp) ok = mma_warp<D, FP8>(a, &bars, sQ, ring, meta, tmem);
+  }
+  if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, kStatusTimeout);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kCols);
+}
+
+// ------------------------------------------------------------------- the join
+// The CTAs of blockIdx.x = c join the unit that is cut first at the start of range
+// c, if one is: a warp a row, its parts in the order of the ranges.
+constexpr int kJoinRows = 16;        // rows of a CTA
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+  constexpr int V = D / 32;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const Start st = a.start[c];
+  const long long L = a.plan->L;
+  if (st.b < 0 || st.off == 0 || st.off > L) return;
+  const int parts = 1 + (int)((st.n - st.off + L - 1) / L);
+  const int bh = st.b * a.H1 + st.h, b = bh / a.H_kv, h = bh - b * a.H_kv, streams = a.pair_keys ? 1 : 2;
+  for (int i = threadIdx.x >> 5; i < kJoinRows; i += 8) {
+    const int in = blockIdx.y * kJoinRows + i, x = in / kRows, row = in - x * kRows, gq = row / a.nt;
+    const int t = (st.tile * streams + x) * a.nt + row - gq * a.nt;
+    if (gq >= a.G || t >= a.T) continue;
+    const int64_t q_row = ((int64_t)b * a.H_q + h * a.G + gq) * a.T + t;
+    const auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + p)) * (streams * kRows) + in; };
+    float top = kNoRef;
+    for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_ml[slot(p)].x);
+    float l = 0.f, v[V];
+#pragma unroll
+    for (int z = 0; z < V; ++z) v[z] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const int64_t s = slot(p);
+      const float2 ml = a.part_ml[s];
+      const float f = ex2(ml.x - top);
+      l = fmaf(ml.y, f, l);
+      float y[V];
+      const float* o = a.part_o + s * D + lane * V;
+      if constexpr (V == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(o);
+      else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(o);
+#pragma unroll
+      for (int z = 0; z < V; ++z) v[z] = fmaf(y[z], f, v[z]);
+    }
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int z = 0; z < V / 2; ++z)
+      w[z] = l == 0.f ? 0u : bf16x2_of(v[2 * z] / l, v[2 * z + 1] / l);
+    __nv_bfloat16* o = a.out + q_row * D + lane * V;
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(o) = w[0];
+    if (a.lse && lane == 0) a.lse[q_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------- host side
+// How a call's query rows are laid out, and its scratch.
+struct Layout {
+  int nt, tiles, pair_keys, P;
+  size_t off_units, off_before, off_start, off_ml, off_o, total;
+};
+inline Layout layout(int64_t B1, int T, int G, int D) {
+  Layout l{};
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  l.P = std::max(num_sms(), 1);
+  l.pair_keys = T <= kRows / G;
+  l.nt = l.pair_keys ? T : kRows / G;
+  const int per = l.nt * (l.pair_keys ? 1 : 2);
+  l.tiles = (T + per - 1) / per;
+  const size_t units = (size_t)B1 * l.tiles, rows = (size_t)2 * l.P * kRows * (l.pair_keys ? 1 : 2);
+  l.off_units = 256;
+  l.off_before = up(l.off_units + units * sizeof(int2));
+  l.off_start = up(l.off_before + (units + 1) * sizeof(long long));
+  l.off_ml = up(l.off_start + (size_t)(l.P + 1) * sizeof(Start));
+  l.off_o = up(l.off_ml + rows * sizeof(float2));
+  l.total = l.off_o + rows * D * sizeof(float);
+  return l;
+}
+inline void place(Args& a, const Layout& l, void* ws) {
+  char* w = static_cast<char*>(ws);
+  a.plan = reinterpret_cast<Plan*>(w);
+  a.units = reinterpret_cast<int2*>(w + l.off_units);
+  a.before = reinterpret_cast<long long*>(w + l.off_before);
+  a.start = reinterpret_cast<Start*>(w + l.off_start);
+  a.part_ml = reinterpret_cast<float2*>(w + l.off_ml);
+  a.part_o = reinterpret_cast<float*>(w + l.off_o);
+  a.nt = l.nt, a.tiles = l.tiles, a.pair_keys = l.pair_keys, a.P = l.P;
+  a.status = status_word_ptr();
+  a.wait_limit = wait_limit_polls();
+}
+
+inline bool encode3(CUtensorMap* map, CUtensorMapDataType type, const void* ptr, const cuuint64_t (&dims)[3],
+                    const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
+  auto enc = scan::get_encode();
+  if (!enc) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Queries [heads][T][D] bf16 in boxes of nt tokens of G heads: a row tile.
+inline bool map_queries(CUtensorMap* map, const void* q, int D, int T, uint64_t heads, int nt, int G) {
+  return encode3(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, {(cuuint64_t)D, (cuuint64_t)T, heads},
+                 {(cuuint64_t)D * 2, (cuuint64_t)T * D * 2}, {64, (cuuint32_t)nt, (cuuint32_t)G},
+                 CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Blocks of 16 rows of D bytes, in boxes of a key tile.
+inline bool map_blocks(CUtensorMap* map, const void* p, int D, uint64_t blocks) {
+  return encode3(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, {(cuuint64_t)D, q8::kRows, blocks},
+                 {(cuuint64_t)D, (cuuint64_t)D * q8::kRows}, {(cuuint32_t)D, q8::kRows, kKeys / q8::kRows},
+                 D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// Up to so many units the planning kernel counts the steps itself: one launch less.
+constexpr int kCountHere = 256;
+template <int D, bool FP8>
+cudaError_t launch(const Args& a, void (*kern)(Args), cudaStream_t st) {
+  using C = Cfg<D, FP8>;
+  const int64_t units = (int64_t)a.B1 * a.tiles;
+  const int counted = units > kCountHere;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem);
+  if (e == cudaSuccess && counted)
+    e = launch_pdl(count_kernel<FP8>, dim3((unsigned)((units + 7) / 8)), dim3(256), 0, st, a);
+  if (e == cudaSuccess) e = launch_pdl(plan_kernel<FP8>, dim3(1), dim3(1024), 0, st, a, counted);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(a.P), dim3(kThreads), C::kSmem, st, a);
+  if (e == cudaSuccess && a.P > 1)
+    e = launch_pdl(join_kernel<D>, dim3(a.P - 1, (a.pair_keys ? 1 : 2) * kRows / kJoinRows), dim3(256), 0, st, a);
+  note_launches(3 + counted);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace flash
+}  // namespace kvc

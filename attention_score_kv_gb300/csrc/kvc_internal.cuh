@@ -229,6 +229,50 @@ cudaError_t launch_attend_q4(const __nv_bfloat16* q, const uint8_t* cache, const
                              int extra, const int32_t* q_pos, int B, int T, int H_q, int D, const Q4Slots& slots,
                              __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st);
 
+// the 8-bit retained cache (kvc_q8.cuh): the same steps
+struct Q8Cache {
+  uint8_t *k8, *v8;    // e4m3 codes, row after row
+  float* scale;        // [block][2]: of its keys, of its values
+  int32_t* pos;
+};
+cudaError_t launch_gather_q8(const __nv_bfloat16* k, const __nv_bfloat16* v, const int32_t* idx, int B,
+                             const SelParams& sel, int D, const Q8Cache& c, cudaStream_t st);
+cudaError_t launch_append_q8(const __nv_bfloat16* k, const __nv_bfloat16* v, const int32_t* pos, int B, int T, int D,
+                             const Q4Slots& slots, const int32_t* rows, const Q8Cache& c, cudaStream_t st);
+cudaError_t launch_read_q8(const Q8Cache& c, int B, int D, const Q4Slots& slots, const int32_t* first,
+                           const SelParams& out, __nv_bfloat16* k_out, __nv_bfloat16* v_out, cudaStream_t st);
+// attention over it
+struct Q8Attend {
+  const __nv_bfloat16* q;
+  Q8Cache c;
+  const int32_t *rows, *q_pos;
+  int extra, B, T, H_q, D;
+  const Q4Slots* slots;
+  float cap;           // 0: scores are not capped
+  const float* slopes; // null: no bias by distance
+  __nv_bfloat16* out;
+  float* lse;
+  void* ws;
+};
+cudaError_t launch_attend_q8(const Q8Attend& a, cudaStream_t st);
+// the same for many query rows per KV head, on the tensor cores
+size_t attend_q8_tc_ws(int B, int T, int H_q, int H_kv, int D);
+cudaError_t launch_attend_q8_tc(const Q8Attend& a, cudaStream_t st);
+
+// attention of a prompt chunk over the active layer's buffers
+struct ChunkAttend {
+  const __nv_bfloat16 *q, *k, *v;
+  const int32_t *q_pos, *first, *last;   // first, last: may be null
+  int B, T, H_q, H_kv, S, D;
+  float cap;
+  const float* slopes;
+  __nv_bfloat16* out;
+  float* lse;
+  void* ws;
+};
+size_t attend_chunk_ws(int B, int T, int H_q, int H_kv, int D);
+cudaError_t launch_attend_chunk(const ChunkAttend& a, cudaStream_t st);
+
 int* status_word_ptr();     // device address of the status word
 void note_launches(int n);  // count kernels issued (measurement)
 

@@ -27,6 +27,11 @@ static __typeof__(&kvc_gather_q4) p_gather;
 static __typeof__(&kvc_append_q4) p_append;
 static __typeof__(&kvc_read_q4) p_read;
 static __typeof__(&kvc_attention_q4) p_attention;
+static __typeof__(&kvc_gather_q8) p_gather8;
+static __typeof__(&kvc_append_q8) p_append8;
+static __typeof__(&kvc_read_q8) p_read8;
+static __typeof__(&kvc_attention_q8) p_attention8;
+static __typeof__(&kvc_attention_chunk) p_chunk;
 
 /* ---------------------------------------------------------------- arguments */
 static int as_int(PyObject* o, int* out) {
@@ -378,13 +383,177 @@ out:
   return r;
 }
 
-/* (library: six addresses; dtypes: bf16, int32, uint8, float32; kvc.py's functions and error class) */
+/* The codes and scales of an 8-bit cache of `rows` rows. */
+typedef struct {
+  void *k8, *v8, *scale;
+} Cache8;
+static int as_cache8(PyObject* const* a, int64_t rows, int D, int64_t dev, Cache8* c) {
+  return as_tensor(a[0], u8, times(rows, D), "k8", dev, &c->k8) ||
+         as_tensor(a[1], u8, times(rows, D), "v8", dev, &c->v8) ||
+         as_tensor(a[2], f32, rows == INT64_MAX ? rows : rows / 8, "scale", dev, &c->scale);
+}
+static int as_float(PyObject* o, float* out) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) return -1;
+  *out = (float)v;
+  return 0;
+}
+/* A workspace of ws_bytes (None: all of it). */
+static int as_ws(PyObject* ws, PyObject* bytes, int64_t dev, void** p, size_t* n) {
+  int64_t v = 0;
+  if (bytes != Py_None ? as_i64(bytes, &v) : call_i64(ws, s_numel, &v)) return -1;
+  *n = v < 0 ? 0 : (size_t)v;
+  return as_tensor(ws, u8, v, "ws", dev, p);
+}
+
+/* (k, v, idx, B, H_kv, S, D, K_l, slot_off, k8, v8, scale, pos, stream) */
+static PyObject* gather_q8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  int B, H, S, D, rc;
+  int64_t dev;
+  void *k, *v, *idx, *pos;
+  Cache8 c;
+  kvc_stream_t st;
+  Host kl = {0}, slot = {0};
+  PyObject* r = NULL;
+  if (want(n_args, 14, "gather_q8") || as_int(a[3], &B) || as_int(a[4], &H) || as_int(a[5], &S) ||
+      as_int(a[6], &D) || as_device(&dev))
+    return NULL;
+  if (as_host(a[7], 4, H, "K_l", &kl) || as_host(a[8], 8, (int64_t)H + 1, "slot_off", &slot)) goto out;
+  const int64_t rows = cache_rows(B, H, &slot), kv = times(times(B, H), times(S, D));
+  if (as_tensor(a[0], bf16, kv, "k", dev, &k) || as_tensor(a[1], bf16, kv, "v", dev, &v) ||
+      as_tensor(a[2], i32, rows, "idx", dev, &idx) || as_cache8(a + 9, rows, D, dev, &c) ||
+      as_tensor(a[12], i32, rows, "pos", dev, &pos) || as_stream(a[13], dev, &st))
+    goto out;
+  RUN(rc, p_gather8(k, v, idx, B, H, S, D, kl.p, slot.p, c.k8, c.v8, c.scale, pos, st));
+  r = done(rc);
+out:
+  drop(&kl);
+  drop(&slot);
+  return r;
+}
+
+/* (k, v, pos_new, B, H_kv, T, D, slot_off, rows, k8, v8, scale, pos, stream) */
+static PyObject* append_q8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  int B, H, T, D, rc;
+  int64_t dev;
+  void *k, *v, *pn, *rows, *pos;
+  Cache8 c;
+  kvc_stream_t st;
+  Host slot = {0};
+  PyObject* r = NULL;
+  if (want(n_args, 14, "append_q8") || as_int(a[3], &B) || as_int(a[4], &H) || as_int(a[5], &T) ||
+      as_int(a[6], &D) || as_device(&dev))
+    return NULL;
+  if (as_host(a[7], 8, (int64_t)H + 1, "slot_off", &slot)) goto out;
+  const int64_t n = cache_rows(B, H, &slot), kv = times(times(B, H), times(T, D));
+  if (as_tensor(a[0], bf16, kv, "k", dev, &k) || as_tensor(a[1], bf16, kv, "v", dev, &v) ||
+      as_tensor(a[2], i32, times(B, T), "pos_new", dev, &pn) || as_tensor(a[8], i32, times(B, H), "rows", dev, &rows) ||
+      as_cache8(a + 9, n, D, dev, &c) || as_tensor(a[12], i32, n, "pos", dev, &pos) || as_stream(a[13], dev, &st))
+    goto out;
+  RUN(rc, p_append8(k, v, pn, B, H, T, D, slot.p, rows, c.k8, c.v8, c.scale, pos, st));
+  r = done(rc);
+out:
+  drop(&slot);
+  return r;
+}
+
+/* (k8, v8, scale, B, H_kv, D, slot_off, first, n_rows, out_off, k_out, v_out, stream) */
+static PyObject* read_q8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  int B, H, D, rc;
+  int64_t dev, t = 0;
+  void *first, *ko, *vo;
+  Cache8 c;
+  kvc_stream_t st;
+  Host slot = {0}, nr = {0}, off = {0};
+  PyObject* r = NULL;
+  if (want(n_args, 13, "read_q8") || as_int(a[3], &B) || as_int(a[4], &H) || as_int(a[5], &D) || as_device(&dev))
+    return NULL;
+  if (as_host(a[6], 8, (int64_t)H + 1, "slot_off", &slot) || as_host(a[8], 4, H, "n_rows", &nr) ||
+      as_host(a[9], 8, (int64_t)H + 1, "out_off", &off))
+    goto out;
+  if (off.p) t = H >= 0 ? ((const int64_t*)off.p)[H] : 0;
+  else if (nr.p)
+    for (int h = 0; h < H; ++h) t += ((const int32_t*)nr.p)[h];
+  t = times(times(B, t), D);
+  if (as_cache8(a, cache_rows(B, H, &slot), D, dev, &c) || as_tensor(a[7], i32, times(B, H), "first", dev, &first) ||
+      as_tensor(a[10], bf16, t, "k_out", dev, &ko) || as_tensor(a[11], bf16, t, "v_out", dev, &vo) ||
+      as_stream(a[12], dev, &st))
+    goto out;
+  RUN(rc, p_read8(c.k8, c.v8, c.scale, B, H, D, slot.p, first, nr.p, off.p, ko, vo, st));
+  r = done(rc);
+out:
+  drop(&slot);
+  drop(&nr);
+  drop(&off);
+  return r;
+}
+
+/* (q, k8, v8, scale, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot_off, cap, slopes, out, lse, ws, ws_bytes,
+ *  stream) */
+static PyObject* attention_q8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  int extra, B, T, H_q, H, D, rc;
+  int64_t dev;
+  size_t ws_bytes;
+  float cap;
+  void *q, *pos, *rows, *qp, *slopes, *out, *lse, *ws;
+  Cache8 c;
+  kvc_stream_t st;
+  Host slot = {0};
+  PyObject* r = NULL;
+  if (want(n_args, 21, "attention_q8") || as_int(a[6], &extra) || as_int(a[8], &B) || as_int(a[9], &T) ||
+      as_int(a[10], &H_q) || as_int(a[11], &H) || as_int(a[12], &D) || as_float(a[14], &cap) || as_device(&dev))
+    return NULL;
+  if (as_host(a[13], 8, (int64_t)H + 1, "slot_off", &slot)) goto out;
+  const int64_t n = cache_rows(B, H, &slot), nq = times(times(B, H_q), T);
+  if (as_tensor(a[0], bf16, times(nq, D), "q", dev, &q) || as_cache8(a + 1, n, D, dev, &c) ||
+      as_tensor(a[4], i32, n, "pos", dev, &pos) || as_tensor(a[5], i32, times(B, H), "rows", dev, &rows) ||
+      as_tensor(a[7], i32, times(B, T), "q_pos", dev, &qp) || as_tensor(a[15], f32, H_q, "slopes", dev, &slopes) ||
+      as_tensor(a[16], bf16, times(nq, D), "out", dev, &out) || as_tensor(a[17], f32, nq, "lse", dev, &lse) ||
+      as_ws(a[18], a[19], dev, &ws, &ws_bytes) || as_stream(a[20], dev, &st))
+    goto out;
+  RUN(rc, p_attention8(q, c.k8, c.v8, c.scale, pos, rows, extra, qp, B, T, H_q, H, D, slot.p, cap, slopes, out, lse, ws,
+                       ws_bytes, st));
+  r = done(rc);
+out:
+  drop(&slot);
+  return r;
+}
+
+/* (q, k, v, q_pos, first, last, B, T, H_q, H_kv, S, D, cap, slopes, out, lse, ws, ws_bytes, stream) */
+static PyObject* attention_chunk(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  (void)self;
+  int B, T, H_q, H, S, D, rc;
+  int64_t dev;
+  size_t ws_bytes;
+  float cap;
+  void *q, *k, *v, *qp, *first, *last, *slopes, *out, *lse, *ws;
+  kvc_stream_t st;
+  if (want(n_args, 19, "attention_chunk") || as_int(a[6], &B) || as_int(a[7], &T) || as_int(a[8], &H_q) ||
+      as_int(a[9], &H) || as_int(a[10], &S) || as_int(a[11], &D) || as_float(a[12], &cap) || as_device(&dev))
+    return NULL;
+  const int64_t nt = times(B, T), nq = times(times(B, H_q), T), kv = times(times(B, H), times(S, D));
+  if (as_tensor(a[0], bf16, times(nq, D), "q", dev, &q) || as_tensor(a[1], bf16, kv, "k", dev, &k) ||
+      as_tensor(a[2], bf16, kv, "v", dev, &v) || as_tensor(a[3], i32, nt, "q_pos", dev, &qp) ||
+      as_tensor(a[4], i32, nt, "first", dev, &first) || as_tensor(a[5], i32, nt, "last", dev, &last) ||
+      as_tensor(a[13], f32, H_q, "slopes", dev, &slopes) || as_tensor(a[14], bf16, times(nq, D), "out", dev, &out) ||
+      as_tensor(a[15], f32, nq, "lse", dev, &lse) || as_ws(a[16], a[17], dev, &ws, &ws_bytes) ||
+      as_stream(a[18], dev, &st))
+    return NULL;
+  RUN(rc, p_chunk(q, k, v, qp, first, last, B, T, H_q, H, S, D, cap, slopes, out, lse, ws, ws_bytes, st));
+  return done(rc);
+}
+
+/* (library: eleven addresses; dtypes: bf16, int32, uint8, float32; kvc.py's functions and error class) */
 static PyObject* init(PyObject* self, PyObject* args) {
   (void)self;
-  unsigned long long f[6];
+  unsigned long long f[11];
   PyObject* o[10];
-  if (!PyArg_ParseTuple(args, "(KKKKKK)(OOOO)(OOOOOO)", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &o[0], &o[1], &o[2],
-                        &o[3], &o[4], &o[5], &o[6], &o[7], &o[8], &o[9]))
+  if (!PyArg_ParseTuple(args, "(KKKKKKKKKKK)(OOOO)(OOOOOO)", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7],
+                        &f[8], &f[9], &f[10], &o[0], &o[1], &o[2], &o[3], &o[4], &o[5], &o[6], &o[7], &o[8], &o[9]))
     return NULL;
   p_last_error = (__typeof__(p_last_error))(uintptr_t)f[0];
   p_rope = (__typeof__(p_rope))(uintptr_t)f[1];
@@ -392,6 +561,11 @@ static PyObject* init(PyObject* self, PyObject* args) {
   p_append = (__typeof__(p_append))(uintptr_t)f[3];
   p_read = (__typeof__(p_read))(uintptr_t)f[4];
   p_attention = (__typeof__(p_attention))(uintptr_t)f[5];
+  p_gather8 = (__typeof__(p_gather8))(uintptr_t)f[6];
+  p_append8 = (__typeof__(p_append8))(uintptr_t)f[7];
+  p_read8 = (__typeof__(p_read8))(uintptr_t)f[8];
+  p_attention8 = (__typeof__(p_attention8))(uintptr_t)f[9];
+  p_chunk = (__typeof__(p_chunk))(uintptr_t)f[10];
   PyObject** to[10] = {&bf16, &i32, &u8, &f32, &cur_dev, &raw_stream, &refuse, &tokens_arg, &host_array, &kvc_error};
   for (int i = 0; i < 10; ++i) {
     Py_INCREF(o[i]);
@@ -407,6 +581,11 @@ static PyMethodDef methods[] = {
     {"append_q4", (PyCFunction)(void (*)(void))append_q4, METH_FASTCALL, NULL},
     {"read_q4", (PyCFunction)(void (*)(void))read_q4, METH_FASTCALL, NULL},
     {"attention_q4", (PyCFunction)(void (*)(void))attention_q4, METH_FASTCALL, NULL},
+    {"gather_q8", (PyCFunction)(void (*)(void))gather_q8, METH_FASTCALL, NULL},
+    {"append_q8", (PyCFunction)(void (*)(void))append_q8, METH_FASTCALL, NULL},
+    {"read_q8", (PyCFunction)(void (*)(void))read_q8, METH_FASTCALL, NULL},
+    {"attention_q8", (PyCFunction)(void (*)(void))attention_q8, METH_FASTCALL, NULL},
+    {"attention_chunk", (PyCFunction)(void (*)(void))attention_chunk, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -123,6 +123,17 @@ _SIGS = {
                                    _P, _P, _P, _SZ, _P, _P]),
     "kvc_attention_q4_workspace_size": (_SZ, [_I] * 5),
     "kvc_attention_q4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I64P, _P, _P, _P, _SZ, _P]),
+    "kvc_gather_q8": (_I, [_P, _P, _P, _I, _I, _I, _I, _I32P, _I64P, _P, _P, _P, _P, _P]),
+    "kvc_append_q8": (_I, [_P, _P, _P, _I, _I, _I, _I, _I64P, _P, _P, _P, _P, _P, _P]),
+    "kvc_read_q8": (_I, [_P, _P, _P, _I, _I, _I, _I64P, _P, _I32P, _I64P, _P, _P, _P]),
+    "kvc_compress_layer_q8": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I32P, _I, _I, _I, _I, _P, _P, _P, _I64P,
+                                   _P, _P, _P, _P, _P, _SZ, _P, _P]),
+    "kvc_attention_q8_workspace_size": (_SZ, [_I] * 5),
+    "kvc_attention_q8": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I64P, ctypes.c_float, _P, _P, _P,
+                              _P, _SZ, _P]),
+    "kvc_attention_chunk_workspace_size": (_SZ, [_I] * 5),
+    "kvc_attention_chunk": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _SZ,
+                                 _P]),
     "kvc_check_status": (_I, [_P]),
     "kvc_set_option": (_I, [_I, _I64]),
 }
@@ -248,7 +259,8 @@ def _host_array(arr, size, n, name):
 if not isinstance(_binding, _NoBinding):
     _binding.init(tuple(ctypes.cast(getattr(_lib, f), _P).value for f in
                         ("kvc_last_error", "kvc_qk_norm_rope", "kvc_gather_q4", "kvc_append_q4", "kvc_read_q4",
-                         "kvc_attention_q4")),
+                         "kvc_attention_q4", "kvc_gather_q8", "kvc_append_q8", "kvc_read_q8", "kvc_attention_q8",
+                         "kvc_attention_chunk")),
                   (torch.bfloat16, torch.int32, torch.uint8, torch.float32),
                   (_cur_dev, _raw_stream, _refuse, _tokens_arg, _host_array, KvcError))
 
@@ -460,6 +472,62 @@ def kvc_attention_q4(q, cache, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot
                           stream)
 
 
+def kvc_gather_q8(k, v, idx, B, H_kv, S, D, K_l, slot_off, k8, v8, scale, pos, stream=None):
+    _binding.gather_q8(k, v, idx, B, H_kv, S, D, K_l, slot_off, k8, v8, scale, pos, stream)
+
+
+def kvc_append_q8(k, v, pos_new, B, H_kv, T, D, slot_off, rows, k8, v8, scale, pos, stream=None):
+    _binding.append_q8(k, v, pos_new, B, H_kv, T, D, slot_off, rows, k8, v8, scale, pos, stream)
+
+
+def kvc_read_q8(k8, v8, scale, B, H_kv, D, slot_off, first, n_rows, k_out, v_out, stream=None, out_off=None):
+    _binding.read_q8(k8, v8, scale, B, H_kv, D, slot_off, first, n_rows, out_off, k_out, v_out, stream)
+
+
+def kvc_compress_layer_q8(N, layer, B, S, C, H_q, H_kv, D, W, K_l, sink, recent, pool_k, b_s, q_win, k, v, slot_off,
+                          k8, v8, scale, pos, ws, ws_bytes=None, v_ready=None, stream=None):
+    """kvc_compress_layer whose retained rows go into the 8-bit cache."""
+    dev = _cur_dev()
+    bf = torch.bfloat16
+    so, n = _q4_rows(B, H_kv, slot_off)
+    if ws_bytes is None:
+        ws_bytes = ws.numel()
+    _check(_lib.kvc_compress_layer_q8(
+        N, layer, B, S, C, H_q, H_kv, D, W, _host(K_l, ctypes.c_int32, H_kv, "K_l"), sink, recent, pool_k, b_s,
+        _arg(q_win, bf, B * H_q * W * D, "q_win", dev), _arg(k, bf, B * H_kv * S * D, "k", dev),
+        _arg(v, bf, B * H_kv * S * D, "v", dev), so, _arg(k8, torch.uint8, n * D, "k8", dev),
+        _arg(v8, torch.uint8, n * D, "v8", dev), _arg(scale, torch.float32, n // 8, "scale", dev),
+        _arg(pos, torch.int32, n, "pos", dev), _arg(ws, torch.uint8, ws_bytes, "ws", dev), ws_bytes, _event(v_ready),
+        _stream(stream)))
+
+
+def kvc_attention_q8_workspace_size(B, T, H_q, H_kv, D) -> int:
+    n = _lib.kvc_attention_q8_workspace_size(B, T, H_q, H_kv, D)
+    if n == 0:
+        raise KvcError(KVC_ERR_INVALID_ARG, kvc_last_error())
+    return n
+
+
+def kvc_attention_q8(q, k8, v8, scale, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot_off, cap, slopes, out, lse,
+                     ws, ws_bytes=None, stream=None):
+    _binding.attention_q8(q, k8, v8, scale, pos, rows, extra, q_pos, B, T, H_q, H_kv, D, slot_off, cap, slopes, out,
+                          lse, ws, ws_bytes, stream)
+
+
+def kvc_attention_chunk_workspace_size(B, T, H_q, H_kv, D) -> int:
+    n = _lib.kvc_attention_chunk_workspace_size(B, T, H_q, H_kv, D)
+    if n == 0:
+        raise KvcError(KVC_ERR_INVALID_ARG, kvc_last_error())
+    return n
+
+
+def kvc_attention_chunk(q, k, v, q_pos, first, last, B, T, H_q, H_kv, S, D, cap, slopes, out, lse, ws, ws_bytes=None,
+                        stream=None):
+    """Attention of a prompt chunk over the active layer's buffers (see include/kvc.h)."""
+    _binding.attention_chunk(q, k, v, q_pos, first, last, B, T, H_q, H_kv, S, D, cap, slopes, out, lse, ws, ws_bytes,
+                             stream)
+
+
 def kvc_check_status(stream=None) -> None:
     _check(_lib.kvc_check_status(_stream(stream)))
 
@@ -488,6 +556,24 @@ def retained_outputs(B, H_kv, S, D, K_l, device="cuda"):
 def attention_q4_workspace(B, T, H_q, H_kv, D, device="cuda") -> torch.Tensor:
     """A uint8 device buffer of kvc_attention_q4_workspace_size(...) bytes."""
     return torch.empty(kvc_attention_q4_workspace_size(B, T, H_q, H_kv, D), dtype=torch.uint8, device=device)
+
+
+def attention_q8_workspace(B, T, H_q, H_kv, D, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of kvc_attention_q8_workspace_size(...) bytes."""
+    return torch.empty(kvc_attention_q8_workspace_size(B, T, H_q, H_kv, D), dtype=torch.uint8, device=device)
+
+
+def attention_chunk_workspace(B, T, H_q, H_kv, D, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of kvc_attention_chunk_workspace_size(...) bytes."""
+    return torch.empty(kvc_attention_chunk_workspace_size(B, T, H_q, H_kv, D), dtype=torch.uint8, device=device)
+
+
+def q8_cache(B, D, slot_off, device="cuda"):
+    """Allocate (k8, v8, scale, pos) of an 8-bit cache; no row is visible yet (positions -1)."""
+    n = B * slot_off[len(slot_off) - 1]
+    return (torch.empty((n, D), dtype=torch.uint8, device=device), torch.empty((n, D), dtype=torch.uint8, device=device),
+            torch.empty((n // 16, 2), dtype=torch.float32, device=device),
+            torch.full((n,), -1, dtype=torch.int32, device=device))
 
 
 def q4_cache(B, D, slot_off, device="cuda"):

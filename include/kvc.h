@@ -555,6 +555,128 @@ int kvc_attention_q4(const kvc_bf16* q, const uint8_t* cache,
                      void* ws, size_t ws_bytes, kvc_stream_t stream);
 
 /*
+ * The 8-bit retained cache.  Beside the 4-bit one: e4m3 codes, 2*D bytes a row,
+ * each value within 2^-4 of itself, with one scale per block of 16 rows of a
+ * head for its keys and one for its values:
+ *   scale = 2^k, k the least integer >= -100 with max|x| <= 448 * 2^k over the
+ *   block's rows; code = x / scale, to nearest even; value = code * scale
+ * (exact in bf16).  NaN becomes zero and infinities 1.875 * 2^127, which takes the
+ * block's other values with it; both are recorded (KVC_ERR_DEVICE).  Finite
+ * magnitudes above 1.875 * 2^127 become that.
+ *
+ *   k8, v8    uint8 [B * slot_off[H_kv], D], 16-byte aligned: codes, row after row
+ *   scale     fp32 [B * slot_off[H_kv] / 16, 2], 8-byte aligned: of each block's
+ *             keys and values; powers of two
+ *   slot_off, pos, rows   as of the 4-bit cache (kvc_q4_layout makes slots for
+ *             both), with the same limits
+ */
+
+/*
+ * kvc_gather into the 8-bit cache; arguments as kvc_gather_q4.  The last block's
+ * rows behind a head's kept rows are written as zeros; other rows of the slot,
+ * and pos behind the kept rows, are left.
+ */
+int kvc_gather_q8(const kvc_bf16* k, const kvc_bf16* v, const int32_t* idx,
+                  int B, int H_kv, int S, int D, const int32_t* K_l,
+                  const int64_t* slot_off, uint8_t* k8, uint8_t* v8,
+                  float* scale, int32_t* pos, kvc_stream_t stream);
+
+/*
+ * New tokens join the 8-bit cache; arguments as kvc_append_q4 (token t becomes row
+ * rows[b, h] + t, a negative position marks an absent token).  A block in which
+ * rows are held before rows[b, h] keeps its scale unless the new rows need a larger
+ * one; then those rows are rounded anew from what they are held as (exact but
+ * for what leaves e4m3's normal numbers).  The codes of rows behind the new ones
+ * are left.  So the same append made again leaves the same cache, and rows given
+ * up by lowering `rows` can be written over; a scale that they raised stays.
+ */
+int kvc_append_q8(const kvc_bf16* k, const kvc_bf16* v, const int32_t* pos_new,
+                  int B, int H_kv, int T, int D, const int64_t* slot_off,
+                  const int32_t* rows, uint8_t* k8, uint8_t* v8, float* scale,
+                  int32_t* pos, kvc_stream_t stream);
+
+/* Rows of the 8-bit cache as bf16, exactly what is held; arguments as kvc_read_q4. */
+int kvc_read_q8(const uint8_t* k8, const uint8_t* v8, const float* scale, int B,
+                int H_kv, int D, const int64_t* slot_off, const int32_t* first,
+                const int32_t* n_rows, const int64_t* out_off, kvc_bf16* k_out,
+                kvc_bf16* v_out, kvc_stream_t stream);
+
+/* kvc_compress_layer_q4 with kvc_gather_q8 as its last step. */
+int kvc_compress_layer_q8(int N, int layer, int B, int S, int C, int H_q,
+                          int H_kv, int D, int W, const int32_t* K_l, int sink,
+                          int recent, int pool_k, int b_s,
+                          const kvc_bf16* q_win, const kvc_bf16* k,
+                          const kvc_bf16* v, const int64_t* slot_off,
+                          uint8_t* k8, uint8_t* v8, float* scale, int32_t* pos,
+                          void* ws, size_t ws_bytes, kvc_event_t v_ready,
+                          kvc_stream_t stream);
+
+/*
+ * Attention of T new tokens per sequence over the 8-bit cache; q, rows, extra,
+ * q_pos, out, lse, what a query sees, and rows and counts outside as of
+ * kvc_attention_q4.  With the score of query head hq and row r
+ *   x = q.k_r / sqrt(D);   cap > 0:  x <- cap * tanh(x / cap);
+ *   slopes:  x <- x - slopes[hq] * (q_pos[b, t] - pos[r])
+ * out = sum_r p_r v_r / sum_r p_r, p_r = exp(x); lse = log sum_r p_r.
+ *   cap     0 (none), or from 2^-20 to 2^20
+ *   slopes  [H_q] fp32, device, finite; or NULL
+ * No atomics: the same call gives the same bits.
+ * Arithmetic: keys and values as held, exact.  Up to 8 query rows per KV head (G*T),
+ * a query row is scaled by a power of two to below 2 and taken as fp16 (what is
+ * under 2^-24 of its largest value is lost), and the weights of the values are
+ * rounded to fp16.  With more rows both are split into two e4m3 parts: a query
+ * value within 2^-8 of itself plus 2^-17 of the row's largest one loses nothing
+ * that bf16 has but below that, and weights are within 2^-8 of themselves plus
+ * 2^-16 of the largest.  Scores, maxima, sums and lse are fp32 throughout; the
+ * hyperbolic tangent is within 1e-6 of itself.
+ *   ws     at least kvc_attention_q8_workspace_size(...) bytes, 256-byte
+ *          aligned, any content; the size does not depend on the rows
+ */
+size_t kvc_attention_q8_workspace_size(int B, int T, int H_q, int H_kv, int D);
+
+int kvc_attention_q8(const kvc_bf16* q, const uint8_t* k8, const uint8_t* v8,
+                     const float* scale, const int32_t* pos,
+                     const int32_t* rows, int extra, const int32_t* q_pos,
+                     int B, int T, int H_q, int H_kv, int D,
+                     const int64_t* slot_off, float cap, const float* slopes,
+                     kvc_bf16* out, float* lse, void* ws, size_t ws_bytes,
+                     kvc_stream_t stream);
+
+/*
+ * Attention of a prompt chunk over the active layer's buffers: what the
+ * layer-major schedule (TideKV, Fig. 2) runs per chunk, between
+ * kvc_qk_norm_rope or kvc_append_chunk and the layer's end.  Query head g reads
+ * KV head g / G.  Query t of sequence b sees the keys j of its sequence with
+ *   max(first[b, t], 0) <= j <= min(last[b, t], S - 1)
+ * (none where that is empty or q_pos[b, t] < 0: a padded batch); first NULL: 0, last
+ * NULL: q_pos[b, t], the causal mask.  A document mask gives each query its
+ * document's first position; a prefix mask gives last = max(q_pos, prefix - 1).
+ *   x = q.k_j / sqrt(D);   cap > 0:  x <- cap * tanh(x / cap);
+ *   slopes:  x <- x - slopes[hq] * |q_pos[b, t] - j|
+ *   out = sum_j p_j v_j / sum_j p_j, p_j = exp(x); lse = log sum_j p_j
+ *   q      [B, H_q, T, D] bf16         k, v  [B, H_kv, S, D] bf16
+ *   q_pos, first, last  [B, T] int32, device
+ *   cap, slopes         as of kvc_attention_q8
+ *   out    [B, H_q, T, D] bf16 out     lse   [B, H_q, T] fp32 out, or NULL
+ * A query that sees no key gets zeros and lse -inf.  Keys and values that no query
+ * of the call sees may hold anything (the buffer behind the chunk).  Up to 128
+ * query heads per KV head.  No atomics: the same call gives the same bits.
+ * Arithmetic: products of bf16 added up in fp32; the weights of the values are
+ * rounded to bf16, 2^-8 of each; scores, maxima, sums and lse are fp32.
+ *   ws     at least kvc_attention_chunk_workspace_size(...) bytes, 256-byte
+ *          aligned, any content; the size does not depend on S
+ */
+size_t kvc_attention_chunk_workspace_size(int B, int T, int H_q, int H_kv,
+                                          int D);
+
+int kvc_attention_chunk(const kvc_bf16* q, const kvc_bf16* k, const kvc_bf16* v,
+                        const int32_t* q_pos, const int32_t* first,
+                        const int32_t* last, int B, int T, int H_q, int H_kv,
+                        int S, int D, float cap, const float* slopes,
+                        kvc_bf16* out, float* lse, void* ws, size_t ws_bytes,
+                        kvc_stream_t stream);
+
+/*
  * Waits for `stream`, then reads and clears the device status word.
  * Returns KVC_OK, or KVC_ERR_DEVICE / KVC_ERR_TIMEOUT with a message.
  */

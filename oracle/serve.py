@@ -80,3 +80,70 @@ def attention(q, k, v, pos, q_pos):
         out[t], mag[t] = p @ v[see] / p.sum(), p @ np.abs(v[see]) / p.sum()
         lse[t] = m + math.log(p.sum())
     return out, lse, mag
+
+
+# ------------------------------------------------------------------ 8-bit rows
+TOP8 = 1.875 * 2.0 ** 127        # the largest magnitude that is held
+
+
+def finite8(x):
+    x = np.asarray(x, dtype=np.float64)
+    return np.clip(np.where(np.isnan(x), 0.0, x), -TOP8, TOP8)
+
+
+def scale8(top):
+    """2^k, k the least integer >= -100 with top <= 448 * 2^k."""
+    m, e = np.frexp(np.asarray(top, dtype=np.float64) / 448.0)        # exact where top is 448 * 2^k
+    k = np.where(m == 0.5, e - 1, e)
+    return np.where(top > 0, 2.0 ** np.maximum(k, -100), 2.0 ** -100)
+
+
+def round8(x, s):
+    """x to the nearest e4m3 multiple of s, ties to even."""
+    return np.copysign(E4M3[nearest_even(np.minimum(np.abs(x) / s, 448.0), E4M3)] * s, x)
+
+
+def held8(x):
+    """What the 8-bit cache holds for rows x [n, D] written from a block's first row on, and
+    the blocks' scales."""
+    x = finite8(x)
+    n, D = x.shape
+    blocks = np.concatenate((x, np.zeros((-n % 16, D)))).reshape(-1, 16 * D)
+    s = scale8(np.abs(blocks).max(-1))
+    return round8(blocks, s[:, None]).reshape(-1, D)[:n], s
+
+
+def append8(held, scales, x):
+    """Rows held [n0, D] with their blocks' scales, and new rows x: all rows, and scales."""
+    held, x, scales = np.asarray(held, dtype=np.float64), finite8(x), list(scales)
+    n0 = len(held)
+    first = n0 - n0 % 16
+    rows = np.concatenate((held[first:], x))
+    out, sc = [held[:first]], scales[:first // 16]
+    for i in range(0, len(rows), 16):
+        block = rows[i:i + 16]
+        new = block[n0 - first:] if i == 0 else block
+        s = float(scale8(np.abs(new).max() if new.size else 0.0))
+        if i == 0 and n0 % 16:
+            s = max(s, scales[first // 16])
+        out.append(round8(block, s))
+        sc.append(s)
+    return np.concatenate(out), np.array(sc)
+
+
+def attention_of(q, k, v, see, cap=0.0, slope=0.0, far=None):
+    """q [T, D], k and v [n, D], see [T, n], far [T, n] distances.  Returns out [T, D], lse [T],
+    sum p|v| / sum p, and the scores [T, n] (-inf where not seen)."""
+    q, k, v = (np.asarray(x, dtype=np.float64) for x in (q, k, v))
+    x = q @ k.T / math.sqrt(q.shape[1])
+    if cap:
+        x = cap * np.tanh(x / cap)
+    if slope:
+        x = x - slope * np.asarray(far, dtype=np.float64)
+    x = np.where(see, x, -np.inf)
+    some = see.any(-1)
+    m = np.where(some, x.max(-1, initial=-np.inf), 0.0)
+    p = np.exp(x - m[:, None])
+    z = np.where(some, p.sum(-1), 1.0)[:, None]
+    lse = np.where(some, m + np.log(z[:, 0]), -np.inf)
+    return p @ v / z, lse, p @ np.abs(v) / z, x
