@@ -10,10 +10,9 @@
 // A CTA has two streams of 128 query rows against tiles of 128 keys (tcgen05, fp32
 // accumulators in tensor memory: S and O of both streams are its 512 columns):
 //   S = Q K^T   (both in shared memory);   O += P V   (P in tensor memory, over S)
-// One warp issues, for stream 0 and 1 in turn, the last tile's P V and the next
-// tile's Q K^T, 1024 cycles of products at D = 128, while four warps make the
-// other stream's weights: a thread has a whole row, so nothing is exchanged
-// between threads.  S is overwritten by P and P by the next S: the products of a
+// A warp per stream issues the last tile's P V and the next tile's Q K^T, 1024 cycles
+// of products at D = 128, while eight warps make the other stream's weights, two
+// threads a row.  S is overwritten by P and P by the next S: the products of a
 // warp run in order, and the weights' barrier says that S is in registers.
 // Two ways to feed the streams:
 //   row pairs    two row tiles of a head share each tile of keys and values
@@ -48,11 +47,12 @@ namespace kvc {
 namespace flash {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
-// Three groups of four warps: the two streams' weights, and the issuing, the loading
-// and two idle warps, whose registers the first two take (a thread's row of scores
-// alone is 128): 2 * 208 + 88 = 3 * 168, what the block is launched with.
-constexpr int kThreads = 12 * 32, kSoftRegs = 208, kOtherRegs = 88;
+constexpr int kHalf = kKeys / 2;     // keys of a thread of the weights
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18;
+// Five groups of four warps: the two streams' weights, and the two issuing, the
+// loading and an idle warp, whose registers the first four groups take: 4 * 104 + 64 =
+// 5 * 96, what the block is launched with.
+constexpr int kThreads = 20 * 32, kSoftRegs = 104, kOtherRegs = 64;
 constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;    // stream x: S at kColS + 128 x, O at kColO + 128 x
 constexpr float kNoRef = -1.7e38f;   // reference of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
@@ -260,7 +260,7 @@ struct Cfg {
   static constexpr int kQBytes = FP8 ? 2 * kRows * D : kRows * D * 2;       // of a stream: two parts, or bf16
   static constexpr int kStages = FP8 ? 9 : D == 128 ? 5 : 11;
   static constexpr int kMetaBytes = FP8 ? (int)sizeof(Meta) * kMeta : 0;
-  static constexpr int kSmem = 1024 + 2 * kQBytes + kStages * kStageBytes + kMetaBytes;
+  static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMetaBytes;
   // bf16 reaches as far down as fp32 does, so weights may be small; e4m3's two parts
   // end at 2^-10, so the largest weight of a row is kept between 2^6 and 2^8
   static constexpr float kShift = FP8 ? 6.f : 0.f, kSlack = FP8 ? 2.f : 8.f;
@@ -274,16 +274,17 @@ struct Cfg {
 // a warp that still waits for the first:
 //   kv_full(i + kStages)   kv_empty(i), committed behind products that waited for kv_full(i)
 //   kv_empty(i + kStages)  kv_full(i + kStages), loaded after a look at kv_empty(i)
-//   s_full(i + 1)          p_full(i) of all four warps, which saw s_full(i); a segment's
+//   s_full(i + 1)          p_full(i) of all eight warps, which saw s_full(i); a segment's
 //                          end likewise, and the next segment's first scores come
 //                          at once: the end's barrier is another, s_end
 //   s_end(i + 1)           p_full of the next segment, made after a look at s_end(i)
 //   p_full(i + 1)          s_full(i + 1), issued after a look at p_full(i)
 //   q_full(i + 1)          q_empty(i) (bf16), committed behind products after q_full(i); or
 //                          s_end(i) (e4m3: the rows' own warps write the queries)
+//   turn(i + 1)            the other stream's warp issues in between, after a look at turn(i)
 //   meta_full(i + kMeta)   see Meta
 struct Bars {
-  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], s_end[2], p_full[2], q_full, q_empty, meta_full[kMeta], drain;
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], s_end[2], p_full[2], q_full, q_empty, meta_full[kMeta], turn[2], drain[2];
 };
 
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
@@ -295,6 +296,20 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t lim
       "SEEN:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(limit)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+// Two barriers: a look at one takes about as long alone as with the other.
+__device__ __forceinline__ bool poll2(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t limit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "LOOK:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n @p bra SEEN;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %5;\n @q bra LOOK;\n"
+      "SEEN:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(limit)
       : "memory");
   return __all_sync(0xffffffffu, ok != 0);
 }
@@ -338,6 +353,15 @@ __device__ __forceinline__ void split2(float lo, float hi, uint16_t& a, uint16_t
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(back) : "h"(a));
   asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(rest) : "r"(h), "r"(back));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(b) : "r"(rest));
+}
+
+// One lane of the warp, the same each time.  A branch on it, unlike one on the lane's
+// number, tells the compiler that a single thread is left, whose operands then stay in
+// uniform registers: a product's issue costs 64 cycles less.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 
 // Products from one thread.  A in shared memory (scores) or tensor memory (output).
@@ -572,51 +596,46 @@ __device__ __forceinline__ void issue_output(uint32_t tmem, int x, uint32_t stag
   }
 }
 
-// The warp waits as a whole; lane 0 issues.
+// A warp per stream; it waits as a whole, lane 0 issues.  Two, as an issuer spends
+// about as long on its waits and hand-overs as its products run, which the other
+// stream's products cover.  They take turns: products issued at once share the
+// tensor core and end together, and then both streams make weights at once, with
+// the tensor core idle, and wait for it at once.
 template <int D, bool FP8>
-__device__ bool mma_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring, const Meta* meta, uint32_t tmem) {
+__device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t ring, const Meta* meta, uint32_t tmem) {
   using C = Cfg<D, FP8>;
   const int lane = threadIdx.x & 31;
-  const bool issues = lane == 0;
-  uint32_t it = 0, mt = 0, seg = 0, steps = 0;
+  const int subs = a.pair_keys ? 2 : 1;
+  const uint32_t q_at = sQ + (a.pair_keys ? 0 : x) * C::kQBytes;
+  uint32_t it = 0, mt = 0, seg = 0, steps = 0, turns = 0;
   bool ok = true;
   const auto wait = [&](uint64_t* bar, uint32_t phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
   Walk w;
   if (w.begin(a)) do {
     const Seg& g = w.g;
-    int lo[8], hi[8];                // what the unit's tokens see
-    if constexpr (!FP8) {
-      const int per = a.nt * (a.pair_keys ? 1 : 2);
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const int in = y * 32 + lane, t = g.tile * per + in;
-        lo[y] = INT_MAX, hi[y] = -1;
-        if (in < per && t < a.T) key_range(a, (int64_t)g.b * a.T + t, lo[y], hi[y]);
-      }
-    }
-    const int t0 = g.k0 + g.s0 * (a.pair_keys ? 2 : 1);
-    // rows of tile `t` that nothing sees
+    const int t0 = g.k0 + g.s0 * subs;
+    // rows of tile `t` that no query of the unit sees become zeros (both streams' warps
+    // may write the same ones)
     const auto clean = [&](int t, uint32_t m, uint32_t stage) {
       uint32_t keep[4];
       if constexpr (FP8) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) keep[y] = meta[m % kMeta].some[y];
       } else {
-        const int k = t * kKeys;
-        bool cover = false;
+        const int k = t * kKeys, per = a.nt * (a.pair_keys ? 1 : 2), t1 = min((g.tile + 1) * per, a.T);
 #pragma unroll
-        for (int y = 0; y < 8; ++y) cover |= lo[y] <= k && hi[y] >= k + kKeys - 1;
-        if (__any_sync(0xffffffffu, cover)) return;
+        for (int y = 0; y < 4; ++y) keep[y] = 0;
+        for (int tk = g.tile * per + lane; tk < t1; tk += 32) {
+          int lo, hi;
+          if (!key_range(a, (int64_t)g.b * a.T + tk, lo, hi)) continue;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t mask = 0;
-#pragma unroll
-          for (int z = 0; z < 8; ++z) {
-            const int first = max(lo[z] - k - 32 * y, 0), last = min(hi[z] - k - 32 * y, 31);
-            if (first <= last) mask |= (0xffffffffu >> (31 - last)) & (0xffffffffu << first);
+          for (int y = 0; y < 4; ++y) {
+            const int first = max(lo - k - 32 * y, 0), last = min(hi - k - 32 * y, 31);
+            if (first <= last) keep[y] |= (0xffffffffu >> (31 - last)) & (0xffffffffu << first);
           }
-          keep[y] = __reduce_or_sync(0xffffffffu, mask);
         }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) keep[y] = __reduce_or_sync(0xffffffffu, keep[y]);
       }
       if ((keep[0] & keep[1] & keep[2] & keep[3]) == 0xffffffffu) return;
 #pragma unroll
@@ -624,60 +643,53 @@ __device__ bool mma_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring, 
       tc::fence_proxy_async();
       __syncwarp();
     };
+    // keys that all of some query's range covers: tiles within need no look
+    int in_lo = 0, in_hi = -1;
+    if constexpr (!FP8) {
+      const int per = a.nt * (a.pair_keys ? 1 : 2), tk = g.tile * per + per / 2;
+      if (tk < a.T) key_range(a, (int64_t)g.b * a.T + tk, in_lo, in_hi);
+    }
     ok = ok && wait(&bars->q_full, seg);
-    uint32_t k_st[2] = {}, v_st[2] = {};
-    for (int i = 0; i <= g.cnt && ok; ++i) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bool own = a.pair_keys || x == 0, last_use = a.pair_keys || x == 1;
+    for (int i = 0; i <= g.cnt && ok; ++i, ++turns) {
+      // places in the ring: K(0), then V(i - 1), K(i), ..; key pairs: both streams' in turn
+      const uint32_t v_it = it + (a.pair_keys ? 4 * i - 2 + (i == g.cnt ? x : 2 * x) : 2 * i - 1);
+      const uint32_t k_it = it + (a.pair_keys ? (i == 0 ? x : 4 * i - 1 + 2 * x) : 2 * i);
+      const uint32_t v_st = v_it % C::kStages, k_st = k_it % C::kStages;
+      if (i > 0) {
+        ok = ok && wait(&bars->kv_full[v_st], v_it / C::kStages);
+        if (!ok) break;
+        const int sub = a.pair_keys ? 2 * (i - 1) + x : i - 1, k = (t0 + sub) * kKeys;
+        if (FP8 || in_lo > k || in_hi < k + kKeys - 1) clean(t0 + sub, mt + sub, ring + v_st * C::kStageBytes);
+      }
+      if (i < g.cnt) ok = ok && wait(&bars->kv_full[k_st], k_it / C::kStages);
+      // at a segment's start: the turn alone, twice
+      const uint32_t turn = smem_u32(&bars->turn[x]), turn_ph = (x == 0 ? turns - 1 : turns) & 1;
+      ok = ok && poll2(i > 0 ? smem_u32(&bars->p_full[x]) : turn, i > 0 ? (steps + i - 1) & 1 : turn_ph, turn, turn_ph,
+                       a.wait_limit);
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (elect_one()) {
         if (i > 0) {
-          if (own) {
-            v_st[x] = it % C::kStages;
-            ok = ok && wait(&bars->kv_full[v_st[x]], it / C::kStages);
-            ++it;
-          } else {
-            v_st[1] = v_st[0];
-          }
-          const uint32_t stage = ring + v_st[x] * C::kStageBytes;
-          if (ok && own) {
-            const int sub = a.pair_keys ? 2 * (i - 1) + x : i - 1;
-            clean(t0 + sub, mt + sub, stage);
-          }
-          ok = ok && wait(&bars->p_full[x], steps + i - 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          if (issues) {
-            issue_output<D, FP8>(tmem, x, stage, i > 1);
-            if (last_use) tc::mma_commit(smem_u32(&bars->kv_empty[v_st[x]]));
-            if (i == g.cnt) tc::mma_commit(smem_u32(&bars->s_end[x]));
-          }
-          __syncwarp();
+          issue_output<D, FP8>(tmem, x, ring + v_st * C::kStageBytes, i > 1);
+          tc::mma_commit(smem_u32(&bars->kv_empty[v_st]));
+          if (i == g.cnt) tc::mma_commit(smem_u32(&bars->s_end[x]));
         }
         if (i < g.cnt) {
-          if (own) {
-            k_st[x] = it % C::kStages;
-            ok = ok && wait(&bars->kv_full[k_st[x]], it / C::kStages);
-            ++it;
-          } else {
-            k_st[1] = k_st[0];
-          }
-          if (!ok) break;
-          tc::fence_after_sync();
-          if (issues) {
-            issue_scores<D, FP8>(tmem, x, sQ + (a.pair_keys ? 0 : x) * C::kQBytes, ring + k_st[x] * C::kStageBytes);
-            tc::mma_commit(smem_u32(&bars->s_full[x]));
-            if (last_use) tc::mma_commit(smem_u32(&bars->kv_empty[k_st[x]]));
-            if (!FP8 && i == g.cnt - 1 && x == 1) tc::mma_commit(smem_u32(&bars->q_empty));
-          }
-          __syncwarp();
+          issue_scores<D, FP8>(tmem, x, q_at, ring + k_st * C::kStageBytes);
+          tc::mma_commit(smem_u32(&bars->s_full[x]));
+          tc::mma_commit(smem_u32(&bars->kv_empty[k_st]));
+          if (!FP8 && i == g.cnt - 1) tc::mma_commit(smem_u32(&bars->q_empty));
         }
+        tc::mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
       }
+      __syncwarp();
     }
-    mt += g.cnt * (a.pair_keys ? 2 : 1);
+    it += g.cnt * 2 * subs;
+    mt += g.cnt * subs;
     steps += g.cnt;
     ++seg;
   } while (ok && w.next(a));
-  if (issues) scan::drain_mma(smem_u32(&bars->drain), a.status);
+  if (elect_one()) scan::drain_mma(smem_u32(&bars->drain[x]), a.status);
   __syncwarp();
   return ok;
 }
@@ -724,10 +736,10 @@ __device__ __forceinline__ float write_query(const __nv_bfloat16* q, bool live, 
 
 // A score's product -> the cap's share of it: tanh.  Warps whose 32 rows have no
 // large one take the polynomial alone.
-__device__ __forceinline__ void cap_all(float (&x)[kKeys], const float2* f, bool blocks, float f1) {
+__device__ __forceinline__ void cap_all(float (&x)[kHalf], const float2* f, bool blocks, float f1) {
   float top = 0.f;
 #pragma unroll
-  for (int k = 0; k < kKeys; k += 2) {
+  for (int k = 0; k < kHalf; k += 2) {
     const float fk = blocks ? f[k / 16].x : f1;
     const float2 v = mul2(make_float2(x[k], x[k + 1]), make_float2(fk, fk));
     x[k] = v.x, x[k + 1] = v.y;
@@ -735,26 +747,34 @@ __device__ __forceinline__ void cap_all(float (&x)[kKeys], const float2* f, bool
   }
   if (__all_sync(0xffffffffu, top <= kTanhNear)) {
 #pragma unroll
-    for (int k = 0; k < kKeys; ++k) x[k] = tanh_near(x[k]);
+    for (int k = 0; k < kHalf; ++k) x[k] = tanh_near(x[k]);
   } else {
 #pragma unroll
-    for (int k = 0; k < kKeys; ++k) x[k] = tanh_of(x[k]);
+    for (int k = 0; k < kHalf; ++k) x[k] = tanh_of(x[k]);
   }
 }
 
+// A thread has a row's scores of half a tile; the two threads of a row tell each
+// other their maxima (both need one reference: the row has one output).
 template <int D, bool FP8, bool CAP, bool BIAS>
-__device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* meta, uint32_t tmem, float* s_x) {
+__device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ, const Meta* meta, uint32_t tmem,
+                           float* s_x) {
   using C = Cfg<D, FP8>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 2, row = (warp & 3) * 32 + lane;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 3, half = warp >> 2 & 1;
+  const int row = (warp & 3) * 32 + lane;
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-  const uint32_t s_at = tmem + lanes + kColS + x * 128, p_at = tmem + lanes + col_p<D>(x), o_at = tmem + lanes;
+  const uint32_t s_at = tmem + lanes + kColS + x * 128 + half * kHalf, o_at = tmem + lanes;
+  const uint32_t p_at = tmem + lanes + col_p<D>(x) + half * (FP8 ? 16 : 32);
+  float* my_max = s_max + (x * 2 + half) * kRows + row;
+  const float* its_max = s_max + (x * 2 + (half ^ 1)) * kRows + row;
+  const int pair = 2 + x * 4 + (warp & 3);                   // the barrier of a row's two warps
   const int gq = row / a.nt, tl = row - gq * a.nt;           // query head of the group, token of the tile
   const int subs = a.pair_keys ? 2 : 1;
   const bool any_row = (warp & 3) * 32 < a.nt * a.G;         // none of the warp's rows is one: nothing reads its part
   uint32_t steps = 0, mt = 0, seg = 0;
   bool ok = true;
   // after a wait that gave up: go on without waiting, so that no barrier is left alone
-  const auto wait = [&](uint64_t* bar, uint32_t phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
+  const auto wait = [&](const uint64_t* bar, uint32_t phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
   Walk w;
   if (!w.begin(a)) return true;
   do {
@@ -779,17 +799,16 @@ __device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* m
         for (int y = t0 + lane; y < t1; y += 32) last = max(last, __ldg(a.q_pos + (int64_t)b * a.T + y));
         q_rel = (float)(__reduce_max_sync(0xffffffffu, last) - qp);
       }
-      if (!a.pair_keys || x == 0) {
+      if (half == 0 && (!a.pair_keys || x == 0)) {
         c2 *= write_query<D>(a.q + (live ? q_row * D : 0), live, sQ + (a.pair_keys ? 0 : x) * C::kQBytes, row);
         tc::fence_proxy_async();
-        if (a.pair_keys) s_x[row] = c2;
+        s_max[(a.pair_keys ? 0 : x) * 2 * kRows + row] = c2;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(smem_u32(&bars->q_full));
       }
-      if (a.pair_keys) {
-        asm volatile("bar.sync 1, 256;\n" ::: "memory");
-        c2 = s_x[row];
-      }
+      asm volatile("bar.sync 1, 512;\n" ::: "memory");
+      c2 = s_max[(a.pair_keys ? 0 : x) * 2 * kRows + row];
+      asm volatile("bar.sync 1, 512;\n" ::: "memory");       // read before the first maxima are written there
     }
     float ref = kNoRef, unit = kLeastUnit;
     float2 sum2[2] = {};
@@ -798,24 +817,27 @@ __device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* m
       const int tile = t0 + i * subs + (a.pair_keys ? x : 0);
       const uint32_t m_at = mt + i * subs + (a.pair_keys ? x : 0);
       const Meta& me = meta[m_at % kMeta];
-      if constexpr (FP8) ok = ok && wait(const_cast<uint64_t*>(&bars->meta_full[m_at % kMeta]), m_at / kMeta);
+      if constexpr (FP8) ok = ok && wait(&bars->meta_full[m_at % kMeta], m_at / kMeta);
       ok = ok && wait(&bars->s_full[x], steps);
       tc::fence_after_sync();
-      if (any_row) {
-        float s[kKeys];
+      // The weights are made against the reference as it is, while the maximum is still
+      // being found: it hardly ever moves.  Where it has to, the scores, which are still in
+      // tensor memory, are taken again.
+      for (bool again = false; any_row;) {
+        float s[kHalf];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) tmem_ld32(s_at + 32 * y, s + 32 * y);
-        float2 f[kKeys / 16] = {};     // of 16 keys: factor to log2 units (x), of the values (y)
+        for (int y = 0; y < 2; ++y) tmem_ld32(s_at + 32 * y, s + 32 * y);
+        float2 f[kHalf / 16] = {};     // of 16 keys: factor to log2 units (x), of the values (y)
         if constexpr (FP8) {
 #pragma unroll
-          for (int y = 0; y < kKeys / 16; ++y) {
-            f[y] = me.scale[y];
+          for (int y = 0; y < kHalf / 16; ++y) {
+            f[y] = me.scale[half * (kHalf / 16) + y];
             // a factor of 0 would make NaN of the masked scores
             f[y].x = CAP ? f[y].x * c2 * a.inv_cap2 : fmaxf(f[y].x * c2, 1.2e-38f);
           }
         }
         tc::tmem_wait_ld();
-        tc::reg_fence(s, kKeys);
+        tc::reg_fence(s, kHalf);
         if constexpr (CAP) cap_all(s, f, FP8, c2 * a.inv_cap2);
         // ---- scores: s times f1 (or f) plus e0
         float e0 = 0.f;
@@ -823,28 +845,29 @@ __device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* m
           const auto unbiased = [&](int k) { return CAP ? s[k] * a.cap2 : FP8 ? s[k] * f[k / 16].x : s[k] * c2; };
           if constexpr (FP8) {
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k) s[k] = fmaf(slope, me.rel[k] + q_rel, unbiased(k));
+            for (int k = 0; k < kHalf; ++k) s[k] = fmaf(slope, me.rel[half * kHalf + k] + q_rel, unbiased(k));
           } else {
-            const int d0 = tile * kKeys - qp;
-            if (__any_sync(0xffffffffu, d0 < 0 && d0 + kKeys > 0)) {   // the tile has keys on both sides of a query
+            int d0 = tile * kKeys + half * kHalf - qp;
+            asm volatile("" : "+r"(d0));             // as l and r below
+            if (__any_sync(0xffffffffu, d0 < 0 && d0 + kHalf > 0)) {   // keys on both sides of a query
 #pragma unroll
-              for (int k = 0; k < kKeys; ++k) s[k] = fmaf(-slope, fabsf((float)d0 + k), unbiased(k));
+              for (int k = 0; k < kHalf; ++k) s[k] = fmaf(-slope, fabsf((float)d0 + k), unbiased(k));
             } else {
               const float to = d0 < 0 ? slope : -slope;
               e0 = to * (float)d0;
 #pragma unroll
-              for (int k = 0; k < kKeys; ++k) s[k] = fmaf(to, (float)k, unbiased(k));
+              for (int k = 0; k < kHalf; ++k) s[k] = fmaf(to, (float)k, unbiased(k));
             }
           }
         }
         // ---- mask
         if constexpr (FP8) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (me.mixed[y]) {
+          for (int y = 0; y < 2; ++y)
+            if (me.mixed[2 * half + y]) {
 #pragma unroll
               for (int z = 0; z < 8; ++z) {
-                const int4 p = *reinterpret_cast<const int4*>(&me.pos[32 * y + 4 * z]);
+                const int4 p = *reinterpret_cast<const int4*>(&me.pos[half * kHalf + 32 * y + 4 * z]);
                 if (p.x < 0 || p.x > qp) s[32 * y + 4 * z] = -INFINITY;
                 if (p.y < 0 || p.y > qp) s[32 * y + 4 * z + 1] = -INFINITY;
                 if (p.z < 0 || p.z > qp) s[32 * y + 4 * z + 2] = -INFINITY;
@@ -852,77 +875,37 @@ __device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* m
               }
             }
         } else {
-          const int l = lo - tile * kKeys, r = hi - tile * kKeys;
-          if (__any_sync(0xffffffffu, l > 0 || r < kKeys - 1)) {
+          int l = lo - tile * kKeys - half * kHalf, r = hi - tile * kKeys - half * kHalf;
+          // as far as the compiler sees, no two rounds have the same: it would work the 64
+          // comparisons out ahead of the loop, for every tile
+          asm volatile("" : "+r"(l), "+r"(r));
+          if (__any_sync(0xffffffffu, l > 0 || r < kHalf - 1)) {
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k)
+            for (int k = 0; k < kHalf; ++k)
               if (k < l || k > r) s[k] = -INFINITY;
           }
         }
-        // ---- the maximum, and the reference behind it
-        float m;
-        if constexpr (FP8 && !CAP && !BIAS) {
-          m = -INFINITY;
-#pragma unroll
-          for (int y = 0; y < kKeys / 16; ++y) {
-            float v = max3(s[16 * y], s[16 * y + 1], s[16 * y + 2]);
-#pragma unroll
-            for (int k = 3; k < 15; k += 2) v = max3(v, s[16 * y + k], s[16 * y + k + 1]);
-            m = fmaxf(m, fmaxf(v, s[16 * y + 15]) * f[y].x);
-          }
-        } else {
-          float m1 = s[1];
-          m = s[0];
-#pragma unroll
-          for (int k = 2; k < 126; k += 4) m = max3(m, s[k], s[k + 1]), m1 = max3(m1, s[k + 2], s[k + 3]);
-          m = fmaxf(max3(m, s[126], s[127]), m1);
-          if constexpr (BIAS) m += e0;
-          else m *= CAP ? a.cap2 : c2;
-        }
-        bool move = m > ref + (C::kSlack + C::kShift);
-        float top = kLeastUnit;
-        if constexpr (FP8) {
-#pragma unroll
-          for (int y = 0; y < kKeys / 16; ++y) top = fmaxf(top, f[y].y);
-          move |= top > unit;
-        }
-        if (__any_sync(0xffffffffu, move)) {
-          const float to = fmaxf(ref, m - C::kShift);
-          float fo = ex2(ref - to);
-          ref = to;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) sum2[y].x *= fo, sum2[y].y *= fo;
-          if constexpr (FP8) {
-            const float u = fmaxf(unit, top);
-            fo *= unit / u;
-            unit = u;
-          }
-          if (i > 0) {
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y) {
-              float o[32];
-              tmem_ld32(o_at + col_o<D>(x) + 32 * y, o);
-              tc::tmem_wait_ld();
-              tc::reg_fence(o, 32);
-#pragma unroll
-              for (int z = 0; z < 32; ++z) o[z] *= fo;
-#pragma unroll
-              for (int z = 0; z < 2; ++z)
-                tc::tmem_st16(o_at + col_o<D>(x) + 32 * y + 16 * z, reinterpret_cast<const uint32_t*>(o) + 16 * z);
-            }
-          }
-        }
-        // ---- weights
+        // ---- weights, and the maximum beside them: the exponentials' unit is the narrow one
         const float neg = e0 - ref;
         const float2 r2 = make_float2(neg, neg);
+        uint32_t p[kHalf / 2];         // bf16: pairs; e4m3: fours of the first part, then of the second
+        float2 part[2] = {};
+        float v[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {  // 32 keys
-          uint32_t p[16];              // bf16: 16 columns; e4m3: 8 of the first part, 8 of the second
-          uint16_t pa[16], pb[16];
+        for (int y = 0; y < kHalf / 4; ++y) {
+          uint16_t pa[2], pb[2];
           (void)pa, (void)pb;
+          if constexpr (FP8 && !CAP && !BIAS) {        // a block's maximum, then times its factor
+            v[0] = y % 4 == 0 ? fmaxf(s[4 * y], s[4 * y + 1]) : max3(v[0], s[4 * y], s[4 * y + 1]);
+            v[0] = max3(v[0], s[4 * y + 2], s[4 * y + 3]);
+            if (y % 4 == 3) v[1] = fmaxf(v[1], v[0] * f[y / 4].x);
+          } else {
+            v[0] = max3(v[0], s[4 * y], s[4 * y + 1]);
+            v[1] = max3(v[1], s[4 * y + 2], s[4 * y + 3]);
+          }
 #pragma unroll
-          for (int z = 0; z < 16; ++z) {
-            const int k = 32 * y + 2 * z;
+          for (int z = 0; z < 2; ++z) {
+            const int k = 4 * y + 2 * z;
             float2 e;
             if constexpr (BIAS) {
               e = add2(make_float2(s[k], s[k + 1]), r2);
@@ -931,65 +914,103 @@ __device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* m
               e = fma2(make_float2(s[k], s[k + 1]), make_float2(fk, fk), r2);
             }
             float2 u = make_float2(ex2(e.x), ex2(e.y));
-            sum2[z & 1] = add2(sum2[z & 1], u);
+            part[z] = add2(part[z], u);
             if constexpr (FP8) {       // quotient of two powers of two, 0 below the normal numbers
               const float fv =
                   __int_as_float(max(__float_as_int(f[k / 16].y) - __float_as_int(unit) + 0x3f800000, 0));
               u = mul2(u, make_float2(fv, fv));
               split2(u.x, u.y, pa[z], pb[z]);
             } else {
-              p[z] = bf16x2_of(u.x, u.y);
+              p[2 * y + z] = bf16x2_of(u.x, u.y);
             }
           }
           if constexpr (FP8) {
-#pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              p[z] = (uint32_t)pa[2 * z] | (uint32_t)pa[2 * z + 1] << 16;
-              p[8 + z] = (uint32_t)pb[2 * z] | (uint32_t)pb[2 * z + 1] << 16;
-            }
-            tc::tmem_st4(p_at + 8 * y, p);
-            tc::tmem_st4(p_at + 8 * y + 4, p + 4);
-            tc::tmem_st4(p_at + 32 + 8 * y, p + 8);
-            tc::tmem_st4(p_at + 32 + 8 * y + 4, p + 12);
-          } else {
-            tc::tmem_st16(p_at + 16 * y, p);
+            p[y] = (uint32_t)pa[0] | (uint32_t)pa[1] << 16;
+            p[kHalf / 4 + y] = (uint32_t)pb[0] | (uint32_t)pb[1] << 16;
           }
         }
+        float m;
+        if constexpr (FP8 && !CAP && !BIAS) m = v[1];
+        else if constexpr (BIAS) m = fmaxf(v[0], v[1]) + e0;
+        else m = fmaxf(v[0], v[1]) * (CAP ? a.cap2 : c2);
+        // ---- did the reference hold?
+        if (!again) {
+          *my_max = m;
+          asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory");
+          m = fmaxf(m, *its_max);
+          bool move = m > ref + (C::kSlack + C::kShift);
+          float top = kLeastUnit;
+          if constexpr (FP8) {         // of the whole tile: both halves need one unit
+#pragma unroll
+            for (int y = 0; y < kKeys / q8::kRows; ++y) top = fmaxf(top, me.scale[y].y);
+            move |= top > unit;
+          }
+          if (__any_sync(0xffffffffu, move)) {
+            const float to = fmaxf(ref, m - C::kShift);
+            float fo = ex2(ref - to);
+            ref = to;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) sum2[y].x *= fo, sum2[y].y *= fo;
+            if constexpr (FP8) {
+              const float u = fmaxf(unit, top);
+              fo *= unit / u;
+              unit = u;
+            }
+            if (i > 0) {               // half of the row's output
+#pragma unroll
+              for (int y = 0; y < D / 32; ++y) {
+                float o[16];
+                const uint32_t at = o_at + col_o<D>(x) + half * (D / 2) + 16 * y;
+                tc::tmem_ld16(at, o);
+                tc::tmem_wait_ld();
+                tc::reg_fence(o, 16);
+#pragma unroll
+                for (int z = 0; z < 16; ++z) o[z] *= fo;
+                tc::tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
+              }
+            }
+            again = true;
+            continue;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) sum2[y] = add2(sum2[y], part[y]);
+        tc::tmem_st16(p_at, p);
+        tc::tmem_st16(p_at + (FP8 ? 32 : 16), p + 16);
         tc::tmem_wait_st();
+        break;
       }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(smem_u32(&bars->p_full[x]));
     }
-    // ---- the segment's end
+    // ---- the segment's end: the threads of a row tell each other their sums (and, key
+    // pairs, the streams' references), and share out its dims
     ok = ok && wait(&bars->s_end[x], seg);
-    tc::fence_after_sync();
     float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     const bool whole = g.s0 == 0 && g.cnt == g.n;
     const int64_t slot = 2 * blockIdx.x + (g.s0 == 0 ? 1 : 0);
-    // row pairs: a thread writes its row.  Key pairs: both streams' threads of a row
-    // tell each other their references and sums, and take half of its dims each
+    tc::fence_before_sync();
+    *my_max = sum;
+    if (a.pair_keys && half == 0) s_x[x * kRows + row] = ref, s_x[(2 + x) * kRows + row] = unit;
+    asm volatile("bar.sync 1, 512;\n" ::: "memory");
+    tc::fence_after_sync();
+    sum = s_max[x * 2 * kRows + row] + s_max[(x * 2 + 1) * kRows + row];
     float f0 = FP8 ? unit : 1.f, f1 = 0.f;
-    int from = 0, to = D, first = x;
+    int from = half * (D / 2), dims = D / 2, first = x;
     if (a.pair_keys) {
-      tc::fence_before_sync();
-      s_x[256 + x * 128 + row] = ref;
-      s_x[512 + x * 128 + row] = sum;
-      s_x[768 + x * 128 + row] = unit;
-      asm volatile("bar.sync 1, 256;\n" ::: "memory");
-      tc::fence_after_sync();
-      const float ra = s_x[256 + row], rb = s_x[384 + row], top = fmaxf(ra, rb);
+      const float ra = s_x[row], rb = s_x[kRows + row], top = fmaxf(ra, rb);
       f0 = ex2(ra - top), f1 = ex2(rb - top);
-      sum = s_x[512 + row] * f0 + s_x[640 + row] * f1;
+      sum = (s_max[row] + s_max[kRows + row]) * f0 + (s_max[2 * kRows + row] + s_max[3 * kRows + row]) * f1;
       ref = top;
-      if constexpr (FP8) f0 *= s_x[768 + row], f1 *= s_x[896 + row];
-      from = x * (D / 2), to = from + D / 2, first = 0;
+      if constexpr (FP8) f0 *= s_x[2 * kRows + row], f1 *= s_x[3 * kRows + row];
+      from = (2 * x + half) * (D / 4), dims = D / 4, first = 0;
     }
     if (any_row) {
       const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
       f0 *= inv, f1 *= inv;
       const int64_t part = slot * ((a.pair_keys ? 1 : 2) * kRows) + (a.pair_keys ? 0 : x) * kRows + row;
-      for (int d = from; d < to; d += 16) {
+      for (int d = from; d < from + dims; d += 16) {
         float o[16];
         tc::tmem_ld16(o_at + col_o<D>(first) + d, o);
         tc::tmem_wait_ld();
@@ -1023,15 +1044,14 @@ __device__ bool soft_warps(const Args& a, Bars* bars, uint32_t sQ, const Meta* m
           for (int z = 0; z < 4; ++z) p[z] = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
         }
       }
-      if (live && (!a.pair_keys || x == 0)) {
+      if (live && from == 0) {
         if (!whole) a.part_ml[part] = make_float2(ref, sum);
         else if (a.lse) a.lse[q_row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
       }
     }
-    if (a.pair_keys) {                 // the next segment's weights and outputs come after everybody's reads
-      tc::fence_before_sync();
-      asm volatile("bar.sync 1, 256;\n" ::: "memory");
-    }
+    // the next segment's weights, outputs and what is told come after everybody's reads
+    tc::fence_before_sync();
+    asm volatile("bar.sync 1, 512;\n" ::: "memory");
     mt += g.cnt * subs;
     ++seg;
   } while (w.next(a));
@@ -1042,28 +1062,44 @@ template <int D, bool FP8, bool CAP, bool BIAS>
 __device__ __forceinline__ void attend(const Args& a) {
   using C = Cfg<D, FP8>;
   static_assert(C::kStages <= kMaxStages && (!FP8 || C::kStages <= 9), "see Meta");
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars bars;
-  __shared__ uint32_t s_tmem;
-  const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u, ring = sQ + 2 * C::kQBytes;
-  uint8_t* base = smem_raw + (sQ - smem_u32(smem_raw));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // a whole number of 1024 bytes, so that what follows is aligned without a gap: at
+  // D = 128 the two fill a CTA's 227 KB
+  struct alignas(1024) Small {
+    Bars bars;
+    uint32_t tmem;
+    float max[4 * kRows];
+  };
+  static_assert(sizeof(Small) == 3072 && C::kSmem + sizeof(Small) <= 232448, "shared memory of a CTA");
+  __shared__ Small small;
+  Bars& bars = small.bars;
+  uint32_t& s_tmem = small.tmem;
+  uint8_t* const base = smem_raw;
+  const uint32_t sQ = smem_u32(base), ring = sQ + 2 * C::kQBytes;
+  if (sQ % 1024 != 0) {              // no placement does this; the products need it
+    record_status(a.status, kStatusTimeout);
+    return;
+  }
   Meta* meta = reinterpret_cast<Meta*>(base + 2 * C::kQBytes + C::kStages * C::kStageBytes);
   float* s_x = reinterpret_cast<float*>(base + C::kQBytes);       // key pairs: stream 1 has no queries of its own
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       tc::mbar_init(smem_u32(&bars.kv_full[i]), 1);
-      tc::mbar_init(smem_u32(&bars.kv_empty[i]), 1);
+      tc::mbar_init(smem_u32(&bars.kv_empty[i]), a.pair_keys ? 1 : 2);   // streams that multiply a tile
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(smem_u32(&bars.s_full[i]), 1);
       tc::mbar_init(smem_u32(&bars.s_end[i]), 1);
-      tc::mbar_init(smem_u32(&bars.p_full[i]), 4);
+      tc::mbar_init(smem_u32(&bars.p_full[i]), 8);
     }
     for (int i = 0; i < kMeta; ++i) tc::mbar_init(smem_u32(&bars.meta_full[i]), 1);
     tc::mbar_init(smem_u32(&bars.q_full), FP8 ? (a.pair_keys ? 4 : 8) : 1);
-    tc::mbar_init(smem_u32(&bars.q_empty), 1);
-    tc::mbar_init(smem_u32(&bars.drain), 1);
+    tc::mbar_init(smem_u32(&bars.q_empty), 2);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(smem_u32(&bars.turn[i]), 1);
+      tc::mbar_init(smem_u32(&bars.drain[i]), 1);
+    }
     tc::fence_barrier_init();
     tc::tma_prefetch_desc(&a.kmap);
     tc::tma_prefetch_desc(&a.vmap);
@@ -1082,11 +1118,11 @@ __device__ __forceinline__ void attend(const Args& a) {
   bool ok = true;
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
-    ok = soft_warps<D, FP8, CAP, BIAS>(a, &bars, sQ, meta, tmem, s_x);
+    ok = soft_warps<D, FP8, CAP, BIAS>(a, &bars, small.max, sQ, meta, tmem, s_x);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) ok = load_warp<D, FP8>(a, &bars, sQ, ring, meta);
-    else if (warp == kMmaWarp) ok = mma_warp<D, FP8>(a, &bars, sQ, ring, meta, tmem);
+    else if (warp < kLoadWarp) ok = mma_warp<D, FP8>(a, &bars, warp - kMmaWarp, sQ, ring, meta, tmem);
   }
   if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, kStatusTimeout);
   tc::fence_before_sync();

@@ -464,19 +464,28 @@ def test_two_streams_at_once(K, T):
 
 
 def test_a_wait_that_gives_up(K):
-    B, T, Hq, H, D, n = 1, 40, 8, 2, 128, [3000, 3000]
+    """With a limit of one poll a wait may give up: the call ends all the same and says so, a call
+    in which none did is right, and so is the next one."""
+    B, T, Hq, H, D, n = 4, 40, 32, 8, 128, [6000] * 8
     so = K.kvc_q4_layout(H, 1 << 20, n, 0)
     c, _, _ = filled(K, B, H, D, so, n, 44)
-    rows, qp, q = i32([n]), i32(np.full((B, T), 1 << 20)), rnd(45, B, Hq, T, D)
+    rows, qp, q = i32([n] * B), i32(np.full((B, T), 1 << 20)), rnd(45, B, Hq, T, D)
     want, lse = attend(K, q, c, rows, 0, qp, H, so)
+    gave_up = False
     K.kvc_set_option(K.KVC_OPT_WAIT_LIMIT, 1)
     try:
-        attend(K, q, c, rows, 0, qp, H, so)
-        with pytest.raises(K.KvcError) as e:
-            K.kvc_check_status()
-        assert e.value.code == K.KVC_ERR_TIMEOUT
+        for _ in range(300):
+            out, _ = attend(K, q, c, rows, 0, qp, H, so)
+            try:
+                K.kvc_check_status()
+                assert torch.equal(out, want)
+            except K.KvcError as e:
+                assert e.code == K.KVC_ERR_TIMEOUT
+                gave_up = True
+                break
     finally:
         K.kvc_set_option(K.KVC_OPT_WAIT_LIMIT, 0)
+    assert gave_up
     out, _ = attend(K, q, c, rows, 0, qp, H, so)
     K.kvc_check_status()
     assert torch.equal(out, want)
