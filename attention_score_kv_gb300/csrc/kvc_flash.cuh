@@ -73,7 +73,7 @@ struct alignas(16) Meta {
 };
 
 // Where a CTA's range begins: a unit, and the steps of it before the range.
-struct Start { int b, h, tile, n; long long off; };
+struct Start { int b, h, tile, n, k0; long long off; };
 struct Plan {                        // in the workspace
   long long total, L;                // all steps; steps of a range
 };
@@ -152,24 +152,32 @@ __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ Args
   const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles);
   if ((threadIdx.x & 31) == 0) a.units[i] = u;
 }
-// Lays the units end to end and finds where each CTA's range begins.
+// Lays the units end to end and finds where each CTA's range begins.  Up to kPlanned
+// units its searches stay in shared memory.
+constexpr int kPlanned = 2048;
 template <bool FP8>
 __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args a, int counted) {
-  __shared__ long long s_part[32], s_run;
+  __shared__ long long s_part[32], s_run, s_before[kPlanned + 1];
+  __shared__ int2 s_units[kPlanned];
+  const int N = a.B1 * a.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool here = N <= kPlanned;
+  long long* const before = here ? s_before : a.before;
   grid_dep_wait();
   grid_dep_launch();
-  const int N = a.B1 * a.tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (!counted) {
     for (int i = warp; i < N; i += 32) {
       const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles);
-      if (lane == 0) a.units[i] = u;
+      if (lane == 0) a.units[i] = s_units[i] = u;
     }
+  } else if (here) {
+    for (int i = threadIdx.x; i < N; i += 1024) s_units[i] = a.units[i];
   }
+  const int2* const units = here ? s_units : a.units;
   if (threadIdx.x == 0) s_run = 0;
   __syncthreads();
   for (int i0 = 0; i0 < N; i0 += 1024) {
     const int i = i0 + threadIdx.x;
-    const long long n = i < N ? a.units[i].y : 0;
+    const long long n = i < N ? units[i].y : 0;
     long long inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,35 +188,36 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
     __syncthreads();
     long long run = s_run;
     for (int w = 0; w < warp; ++w) run += s_part[w];
-    if (i < N) a.before[i] = run + inc - n;
+    if (i < N) before[i] = run + inc - n;
     __syncthreads();
     if (threadIdx.x == 1023) s_run = run + inc;
     __syncthreads();
   }
   const long long one = s_run, total = one * a.H1;
-  if (threadIdx.x == 0) a.before[N] = one;
+  if (threadIdx.x == 0) before[N] = one;
   const long long L = (total + a.P - 1) / a.P;
   if (threadIdx.x == 0) a.plan->total = total, a.plan->L = L;
   __syncthreads();
   for (int c = threadIdx.x; c < a.P; c += 1024) {
     const long long f = c * L;
-    Start st{-1, 0, 0, 0, 0};
+    Start st{-1, 0, 0, 0, 0, 0};
     if (f < total) {
       int lo = 0, hi = a.B1;         // the sequence: before[b * tiles] * H1 <= f
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (a.before[(int64_t)mid * a.tiles] * a.H1 <= f) lo = mid; else hi = mid;
+        if (before[(int64_t)mid * a.tiles] * a.H1 <= f) lo = mid; else hi = mid;
       }
       const int b = lo;
-      const long long b0 = a.before[(int64_t)b * a.tiles], nb = a.before[(int64_t)(b + 1) * a.tiles] - b0;
+      const long long b0 = before[(int64_t)b * a.tiles], nb = before[(int64_t)(b + 1) * a.tiles] - b0;
       const int h = (int)((f - b0 * a.H1) / nb);
       const long long in = f - b0 * a.H1 - h * nb + b0;          // among one head's
       lo = 0, hi = a.tiles;
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (a.before[(int64_t)b * a.tiles + mid] <= in) lo = mid; else hi = mid;
+        if (before[(int64_t)b * a.tiles + mid] <= in) lo = mid; else hi = mid;
       }
-      st = {b, h, lo, a.units[(int64_t)b * a.tiles + lo].y, in - a.before[(int64_t)b * a.tiles + lo]};
+      const int64_t at = (int64_t)b * a.tiles + lo;
+      st = {b, h, lo, units[at].y, units[at].x, in - before[at]};
     }
     a.start[c] = st;
   }
@@ -220,35 +229,43 @@ struct Seg {
   int k0, n;                         // its first key tile, its steps
   int s0, cnt;                       // steps of this range
 };
-// Walks the units of a range; every role does it by itself.
+// Walks the units of a range; every role does it by itself, the next unit's place
+// asked for ahead.
 struct Walk {
   Seg g;
   long long left;
+  int2 ahead;
   __device__ __forceinline__ bool begin(const Args& a) {
     const Start st = a.start[blockIdx.x];
-    if (st.b < 0) return false;
     const Plan p = *a.plan;
+    if (st.b < 0) return false;
     left = min(p.L, p.total - (long long)blockIdx.x * p.L);
     g.b = st.b, g.h = st.h, g.tile = st.tile;
-    load(a);
+    g.k0 = st.k0, g.n = st.n;
     g.s0 = (int)st.off;
     g.cnt = (int)min((long long)(g.n - g.s0), left);
+    look(a);
     return true;
   }
-  __device__ __forceinline__ void load(const Args& a) {
-    const int2 u = a.units[(int64_t)g.b * a.tiles + g.tile];
-    g.k0 = u.x, g.n = u.y;
+  __device__ __forceinline__ void step(const Args& a, int& b, int& h, int& tile) const {
+    if (++tile == a.tiles) {
+      tile = 0;
+      if (++h == a.H1) h = 0, ++b;
+    }
+  }
+  __device__ __forceinline__ void look(const Args& a) {
+    int b = g.b, h = g.h, tile = g.tile;
+    step(a, b, h, tile);
+    ahead = left > g.cnt ? a.units[(int64_t)b * a.tiles + tile] : make_int2(0, 0);
   }
   __device__ __forceinline__ bool next(const Args& a) {
     left -= g.cnt;
     if (left <= 0) return false;
-    if (++g.tile == a.tiles) {
-      g.tile = 0;
-      if (++g.h == a.H1) g.h = 0, ++g.b;
-    }
-    load(a);
+    step(a, g.b, g.h, g.tile);
+    g.k0 = ahead.x, g.n = ahead.y;
     g.s0 = 0;
     g.cnt = (int)min((long long)g.n, left);
+    look(a);
     return true;
   }
 };
@@ -296,20 +313,6 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t lim
       "SEEN:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(limit)
-      : "memory");
-  return __all_sync(0xffffffffu, ok != 0);
-}
-// Two barriers: a look at one takes about as long alone as with the other.
-__device__ __forceinline__ bool poll2(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t limit) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-      "LOOK:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n @p bra SEEN;\n"
-      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %5;\n @q bra LOOK;\n"
-      "SEEN:\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(limit)
       : "memory");
   return __all_sync(0xffffffffu, ok != 0);
 }
@@ -470,19 +473,6 @@ __device__ bool load_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring,
       }
       q_lo = __reduce_min_sync(0xffffffffu, q_lo);
       q_hi = __reduce_max_sync(0xffffffffu, q_hi);
-    } else {
-      if (nq > 0) ok = poll(smem_u32(&bars->q_empty), (nq - 1) & 1, a.wait_limit);
-      if (!ok) break;
-      ++nq;
-      if (lane == 0) {
-        const int rows = a.nt * a.G, qs = a.pair_keys ? 1 : 2;
-        const uint32_t bar = smem_u32(&bars->q_full);
-        tc::mbar_arrive_expect_tx(bar, (uint32_t)(qs * rows * D * 2));
-        for (int x = 0; x < qs; ++x)
-          for (int p = 0; p < D / 64; ++p)
-            tc::tma_load_3d(sQ + x * C::kQBytes + p * (kRows * 128), &a.qmap, bar, p * 64, (g.tile * qs + x) * a.nt,
-                            g.b * a.H_q + g.h * a.G);
-      }
     }
     const auto put = [&](bool vals, int t) {
       const uint32_t st = it % C::kStages;
@@ -516,13 +506,28 @@ __device__ bool load_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring,
       __syncwarp();
       ++it;
     };
-    // in the order of the products
+    // in the order of the products; the first keys need not wait for the queries' room
     const int t0 = g.k0 + g.s0 * subs;
-    for (int i = 0; i <= g.cnt && ok; ++i)
+    for (int i = 0; i <= g.cnt && ok; ++i) {
       for (int x = 0; x < subs; ++x) {
         if (i > 0) put(true, t0 + (i - 1) * subs + x);
         if (i < g.cnt) put(false, t0 + i * subs + x);
       }
+      if (FP8 || i > 0 || !ok) continue;
+      if (nq > 0) ok = poll(smem_u32(&bars->q_empty), (nq - 1) & 1, a.wait_limit);
+      if (!ok) break;
+      ++nq;
+      if (lane == 0) {
+        const int rows = a.nt * a.G, qs = a.pair_keys ? 1 : 2;
+        const uint32_t bar = smem_u32(&bars->q_full);
+        tc::mbar_arrive_expect_tx(bar, (uint32_t)(qs * rows * D * 2));
+        for (int x = 0; x < qs; ++x)
+          for (int p = 0; p < D / 64; ++p)
+            tc::tma_load_3d(sQ + x * C::kQBytes + p * (kRows * 128), &a.qmap, bar, p * 64, (g.tile * qs + x) * a.nt,
+                            g.b * a.H_q + g.h * a.G);
+      }
+      __syncwarp();
+    }
   } while (ok && w.next(a));
   // every copy issued has landed before the CTA may leave
   const uint32_t lo = it > (uint32_t)C::kStages ? it - C::kStages : 0;
@@ -614,25 +619,45 @@ __device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t
   if (w.begin(a)) do {
     const Seg& g = w.g;
     const int t0 = g.k0 + g.s0 * subs;
+    // What the unit's queries see between them: as a rule one range, each token's touching
+    // the next one's (whole: no holes; tokens that see nothing only behind the others).
+    int lo = INT_MAX, hi = -1;
+    bool holes = false;
+    const int per = a.nt * (a.pair_keys ? 1 : 2), tk0 = g.tile * per, tk1 = min(tk0 + per, a.T);
+    if constexpr (!FP8) {
+      for (int tk = tk0 + lane; tk < tk1; tk += 32) {
+        int l, h, l1 = 0, h1 = -1;
+        const bool some = key_range(a, (int64_t)g.b * a.T + tk, l, h);
+        const bool next = tk + 1 < tk1 && key_range(a, (int64_t)g.b * a.T + tk + 1, l1, h1);
+        if (some) lo = min(lo, l), hi = max(hi, h);
+        holes |= next && (!some || l1 > h + 1 || l > h1 + 1);
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      holes = __any_sync(0xffffffffu, holes);
+    }
     // rows of tile `t` that no query of the unit sees become zeros (both streams' warps
     // may write the same ones)
     const auto clean = [&](int t, uint32_t m, uint32_t stage) {
-      uint32_t keep[4];
+      uint32_t keep[4] = {};
+      const int k = t * kKeys;
+      const auto add = [&](int l, int h) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int first = max(l - k - 32 * y, 0), last = min(h - k - 32 * y, 31);
+          if (first <= last) keep[y] |= (0xffffffffu >> (31 - last)) & (0xffffffffu << first);
+        }
+      };
       if constexpr (FP8) {
 #pragma unroll
         for (int y = 0; y < 4; ++y) keep[y] = meta[m % kMeta].some[y];
+      } else if (!holes) {
+        if (lo <= k && hi >= k + kKeys - 1) return;
+        add(lo, hi);
       } else {
-        const int k = t * kKeys, per = a.nt * (a.pair_keys ? 1 : 2), t1 = min((g.tile + 1) * per, a.T);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) keep[y] = 0;
-        for (int tk = g.tile * per + lane; tk < t1; tk += 32) {
-          int lo, hi;
-          if (!key_range(a, (int64_t)g.b * a.T + tk, lo, hi)) continue;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int first = max(lo - k - 32 * y, 0), last = min(hi - k - 32 * y, 31);
-            if (first <= last) keep[y] |= (0xffffffffu >> (31 - last)) & (0xffffffffu << first);
-          }
+        for (int tk = tk0 + lane; tk < tk1; tk += 32) {
+          int l, h;
+          if (key_range(a, (int64_t)g.b * a.T + tk, l, h)) add(l, h);
         }
 #pragma unroll
         for (int y = 0; y < 4; ++y) keep[y] = __reduce_or_sync(0xffffffffu, keep[y]);
@@ -643,12 +668,6 @@ __device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t
       tc::fence_proxy_async();
       __syncwarp();
     };
-    // keys that all of some query's range covers: tiles within need no look
-    int in_lo = 0, in_hi = -1;
-    if constexpr (!FP8) {
-      const int per = a.nt * (a.pair_keys ? 1 : 2), tk = g.tile * per + per / 2;
-      if (tk < a.T) key_range(a, (int64_t)g.b * a.T + tk, in_lo, in_hi);
-    }
     ok = ok && wait(&bars->q_full, seg);
     for (int i = 0; i <= g.cnt && ok; ++i, ++turns) {
       // places in the ring: K(0), then V(i - 1), K(i), ..; key pairs: both streams' in turn
@@ -658,14 +677,12 @@ __device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t
       if (i > 0) {
         ok = ok && wait(&bars->kv_full[v_st], v_it / C::kStages);
         if (!ok) break;
-        const int sub = a.pair_keys ? 2 * (i - 1) + x : i - 1, k = (t0 + sub) * kKeys;
-        if (FP8 || in_lo > k || in_hi < k + kKeys - 1) clean(t0 + sub, mt + sub, ring + v_st * C::kStageBytes);
+        const int sub = a.pair_keys ? 2 * (i - 1) + x : i - 1;
+        clean(t0 + sub, mt + sub, ring + v_st * C::kStageBytes);
       }
       if (i < g.cnt) ok = ok && wait(&bars->kv_full[k_st], k_it / C::kStages);
-      // at a segment's start: the turn alone, twice
-      const uint32_t turn = smem_u32(&bars->turn[x]), turn_ph = (x == 0 ? turns - 1 : turns) & 1;
-      ok = ok && poll2(i > 0 ? smem_u32(&bars->p_full[x]) : turn, i > 0 ? (steps + i - 1) & 1 : turn_ph, turn, turn_ph,
-                       a.wait_limit);
+      ok = ok && wait(&bars->turn[x], x == 0 ? turns - 1 : turns);
+      if (i > 0) ok = ok && wait(&bars->p_full[x], steps + i - 1);
       if (!ok) break;
       tc::fence_after_sync();
       if (elect_one()) {
@@ -734,6 +751,16 @@ __device__ __forceinline__ float write_query(const __nv_bfloat16* q, bool live, 
   return __uint_as_float((ee - 7u) << 23);
 }
 
+// tanh of a pair, |x| <= kTanhNear: tanh_near.
+__device__ __forceinline__ float2 tanh_near2(float2 x) {
+  const auto both = [](float c) { return make_float2(c, c); };
+  const float2 w = mul2(x, x);
+  float2 p = fma2(w, both(0.015050944872200489f), both(-0.051821865141391754f));
+  p = fma2(w, p, both(0.1330452561378479f));
+  p = fma2(w, p, both(-0.3333195447921753f));
+  p = fma2(w, p, both(0.9999998807907104f));
+  return mul2(x, p);
+}
 // A score's product -> the cap's share of it: tanh.  Warps whose 32 rows have no
 // large one take the polynomial alone.
 __device__ __forceinline__ void cap_all(float (&x)[kHalf], const float2* f, bool blocks, float f1) {
@@ -747,11 +774,26 @@ __device__ __forceinline__ void cap_all(float (&x)[kHalf], const float2* f, bool
   }
   if (__all_sync(0xffffffffu, top <= kTanhNear)) {
 #pragma unroll
-    for (int k = 0; k < kHalf; ++k) x[k] = tanh_near(x[k]);
+    for (int k = 0; k < kHalf; k += 2) {
+      const float2 v = tanh_near2(make_float2(x[k], x[k + 1]));
+      x[k] = v.x, x[k + 1] = v.y;
+    }
   } else {
 #pragma unroll
     for (int k = 0; k < kHalf; ++k) x[k] = tanh_of(x[k]);
   }
+}
+// Four weights, fp16 pairs of 2^-8 of them, below 2^-8 * 448 and not negative -> the
+// e4m3 codes of their two parts.  Times 2^-8 the exponents of e4m3 and fp16 are the
+// same, subnormal numbers' too, so a code is bits 7 to 14: the first part is the weight
+// cut off there, the second the rest, rounded.  The conversion instructions would
+// take eight times as long as these few of the integer unit.
+__device__ __forceinline__ void split4(uint32_t h0, uint32_t h1, uint32_t& a, uint32_t& b) {
+  uint32_t r0, r1;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r0) : "r"(h0), "r"(h0 & 0xff80ff80u));
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r1) : "r"(h1), "r"(h1 & 0xff80ff80u));
+  a = __byte_perm(h0 >> 7, h1 >> 7, 0x6420);
+  b = __byte_perm((r0 + 0x00400040u) >> 7, (r1 + 0x00400040u) >> 7, 0x6420);
 }
 
 // A thread has a row's scores of half a tile; the two threads of a row tell each
@@ -810,7 +852,8 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
       c2 = s_max[(a.pair_keys ? 0 : x) * 2 * kRows + row];
       asm volatile("bar.sync 1, 512;\n" ::: "memory");       // read before the first maxima are written there
     }
-    float ref = kNoRef, unit = kLeastUnit;
+    float ref = 0.f, unit = kLeastUnit;        // the first keys that the row sees set the reference
+    bool seen = false;
     float2 sum2[2] = {};
     const int t0 = g.k0 + g.s0 * subs;
     for (int i = 0; i < g.cnt; ++i, ++steps) {
@@ -839,27 +882,6 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
         tc::tmem_wait_ld();
         tc::reg_fence(s, kHalf);
         if constexpr (CAP) cap_all(s, f, FP8, c2 * a.inv_cap2);
-        // ---- scores: s times f1 (or f) plus e0
-        float e0 = 0.f;
-        if constexpr (BIAS) {
-          const auto unbiased = [&](int k) { return CAP ? s[k] * a.cap2 : FP8 ? s[k] * f[k / 16].x : s[k] * c2; };
-          if constexpr (FP8) {
-#pragma unroll
-            for (int k = 0; k < kHalf; ++k) s[k] = fmaf(slope, me.rel[half * kHalf + k] + q_rel, unbiased(k));
-          } else {
-            int d0 = tile * kKeys + half * kHalf - qp;
-            asm volatile("" : "+r"(d0));             // as l and r below
-            if (__any_sync(0xffffffffu, d0 < 0 && d0 + kHalf > 0)) {   // keys on both sides of a query
-#pragma unroll
-              for (int k = 0; k < kHalf; ++k) s[k] = fmaf(-slope, fabsf((float)d0 + k), unbiased(k));
-            } else {
-              const float to = d0 < 0 ? slope : -slope;
-              e0 = to * (float)d0;
-#pragma unroll
-              for (int k = 0; k < kHalf; ++k) s[k] = fmaf(to, (float)k, unbiased(k));
-            }
-          }
-        }
         // ---- mask
         if constexpr (FP8) {
 #pragma unroll
@@ -885,60 +907,72 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
               if (k < l || k > r) s[k] = -INFINITY;
           }
         }
+        // ---- the scores less the reference: s times a factor plus `neg` and the bias.  The bias
+        // of key k is `to` * (d0 + k) where the half tile lies on one side of the query
+        float neg = -ref, to = 0.f;
+        bool cross = false;
+        int d0 = 0;
+        if constexpr (BIAS && !FP8) {
+          d0 = tile * kKeys + half * kHalf - qp;
+          asm volatile("" : "+r"(d0));             // as l and r above
+          cross = __any_sync(0xffffffffu, d0 < 0 && d0 + kHalf > 0);
+          to = d0 < 0 ? slope : -slope;
+          if (!cross) neg = fmaf(to, (float)d0, neg);
+        }
+        const auto both = [](float v) { return make_float2(v, v); };
+        const auto scores = [&](int k, bool crossing) {            // of keys k and k + 1
+          const float2 fk = both(CAP ? a.cap2 : FP8 ? f[k / 16].x : c2);
+          float2 c = both(neg);
+          if constexpr (BIAS && FP8) {
+            const float2 rel = *reinterpret_cast<const float2*>(&me.rel[half * kHalf + k]);
+            c = fma2(both(slope), add2(rel, both(q_rel)), c);
+          } else if constexpr (BIAS) {
+            c = crossing ? make_float2(fmaf(-slope, fabsf((float)d0 + k), neg), fmaf(-slope, fabsf((float)d0 + k + 1), neg))
+                         : fma2(both(to), make_float2(k, k + 1), c);
+          }
+          return fma2(make_float2(s[k], s[k + 1]), fk, c);
+        };
+        if (BIAS && !FP8 && cross) {
+#pragma unroll
+          for (int k = 0; k < kHalf; k += 2) {
+            const float2 e = scores(k, true);
+            s[k] = e.x, s[k + 1] = e.y;
+          }
+        }
         // ---- weights, and the maximum beside them: the exponentials' unit is the narrow one
-        const float neg = e0 - ref;
-        const float2 r2 = make_float2(neg, neg);
         uint32_t p[kHalf / 2];         // bf16: pairs; e4m3: fours of the first part, then of the second
         float2 part[2] = {};
         float v[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int y = 0; y < kHalf / 4; ++y) {
-          uint16_t pa[2], pb[2];
-          (void)pa, (void)pb;
-          if constexpr (FP8 && !CAP && !BIAS) {        // a block's maximum, then times its factor
-            v[0] = y % 4 == 0 ? fmaxf(s[4 * y], s[4 * y + 1]) : max3(v[0], s[4 * y], s[4 * y + 1]);
-            v[0] = max3(v[0], s[4 * y + 2], s[4 * y + 3]);
-            if (y % 4 == 3) v[1] = fmaxf(v[1], v[0] * f[y / 4].x);
-          } else {
-            v[0] = max3(v[0], s[4 * y], s[4 * y + 1]);
-            v[1] = max3(v[1], s[4 * y + 2], s[4 * y + 3]);
-          }
+          uint32_t h[2];
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             const int k = 4 * y + 2 * z;
-            float2 e;
-            if constexpr (BIAS) {
-              e = add2(make_float2(s[k], s[k + 1]), r2);
-            } else {
-              const float fk = CAP ? a.cap2 : FP8 ? f[k / 16].x : c2;
-              e = fma2(make_float2(s[k], s[k + 1]), make_float2(fk, fk), r2);
-            }
+            float2 e = make_float2(s[k], s[k + 1]);
+            if (!(BIAS && !FP8 && cross)) e = scores(k, false);
+            v[z] = max3(v[z], e.x, e.y);
             float2 u = make_float2(ex2(e.x), ex2(e.y));
             part[z] = add2(part[z], u);
-            if constexpr (FP8) {       // quotient of two powers of two, 0 below the normal numbers
+            if constexpr (FP8) {
+              // times the values' scale over the unit and 2^-8: of two powers of two, 0 below the normal numbers
               const float fv =
-                  __int_as_float(max(__float_as_int(f[k / 16].y) - __float_as_int(unit) + 0x3f800000, 0));
-              u = mul2(u, make_float2(fv, fv));
-              split2(u.x, u.y, pa[z], pb[z]);
+                  __int_as_float(max(__float_as_int(f[k / 16].y) - __float_as_int(unit) + 0x3b800000, 0));
+              u = mul2(u, both(fv));
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(h[z]) : "f"(u.y), "f"(u.x));
             } else {
               p[2 * y + z] = bf16x2_of(u.x, u.y);
             }
           }
-          if constexpr (FP8) {
-            p[y] = (uint32_t)pa[0] | (uint32_t)pa[1] << 16;
-            p[kHalf / 4 + y] = (uint32_t)pb[0] | (uint32_t)pb[1] << 16;
-          }
+          if constexpr (FP8) split4(h[0], h[1], p[y], p[kHalf / 4 + y]);
         }
-        float m;
-        if constexpr (FP8 && !CAP && !BIAS) m = v[1];
-        else if constexpr (BIAS) m = fmaxf(v[0], v[1]) + e0;
-        else m = fmaxf(v[0], v[1]) * (CAP ? a.cap2 : c2);
-        // ---- did the reference hold?
+        // ---- did the reference hold?  (m: the row's maximum less the reference)
         if (!again) {
-          *my_max = m;
+          *my_max = fmaxf(v[0], v[1]);
           asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory");
-          m = fmaxf(m, *its_max);
-          bool move = m > ref + (C::kSlack + C::kShift);
+          const float m = max3(v[0], v[1], *its_max);
+          const bool first = !seen && m > -INFINITY;               // the row's first keys
+          bool move = first || m > C::kSlack + C::kShift;
           float top = kLeastUnit;
           if constexpr (FP8) {         // of the whole tile: both halves need one unit
 #pragma unroll
@@ -946,9 +980,10 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
             move |= top > unit;
           }
           if (__any_sync(0xffffffffu, move)) {
-            const float to = fmaxf(ref, m - C::kShift);
-            float fo = ex2(ref - to);
-            ref = to;
+            const float up = first ? m - C::kShift : fmaxf(0.f, m - C::kShift);
+            float fo = first ? 1.f : ex2(-up);     // nothing has been added up before the first
+            if (first || m > -INFINITY) ref += up;
+            seen |= first;
 #pragma unroll
             for (int y = 0; y < 2; ++y) sum2[y].x *= fo, sum2[y].y *= fo;
             if constexpr (FP8) {
@@ -990,6 +1025,7 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
     float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     const bool whole = g.s0 == 0 && g.cnt == g.n;
     const int64_t slot = 2 * blockIdx.x + (g.s0 == 0 ? 1 : 0);
+    if (!seen) ref = kNoRef;
     tc::fence_before_sync();
     *my_max = sum;
     if (a.pair_keys && half == 0) s_x[x * kRows + row] = ref, s_x[(2 + x) * kRows + row] = unit;
@@ -1132,52 +1168,61 @@ __device__ __forceinline__ void attend(const Args& a) {
 
 // ------------------------------------------------------------------- the join
 // The CTAs of blockIdx.x = c join the unit that is cut first at the start of range
-// c, if one is: a warp a row, its parts in the order of the ranges.
-constexpr int kJoinRows = 16;        // rows of a CTA
+// c + 1, if one is: a warp a row, its parts in the order of the ranges.
+constexpr int kJoinRows = 8;         // rows of a CTA
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const __grid_constant__ Args a) {
   constexpr int V = D / 32;
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, streams = a.pair_keys ? 1 : 2, rows = a.nt * a.G;
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), x = r / rows, row = r - x * rows, gq = row / a.nt;
   grid_dep_wait();
   grid_dep_launch();
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
   const Start st = a.start[c];
   const long long L = a.plan->L;
-  if (st.b < 0 || st.off == 0 || st.off > L) return;
+  if (x >= streams || st.b < 0 || st.off == 0 || st.off > L) return;
+  const int t = (st.tile * streams + x) * a.nt + row - gq * a.nt;
+  if (t >= a.T) return;
   const int parts = 1 + (int)((st.n - st.off + L - 1) / L);
-  const int bh = st.b * a.H1 + st.h, b = bh / a.H_kv, h = bh - b * a.H_kv, streams = a.pair_keys ? 1 : 2;
-  for (int i = threadIdx.x >> 5; i < kJoinRows; i += 8) {
-    const int in = blockIdx.y * kJoinRows + i, x = in / kRows, row = in - x * kRows, gq = row / a.nt;
-    const int t = (st.tile * streams + x) * a.nt + row - gq * a.nt;
-    if (gq >= a.G || t >= a.T) continue;
-    const int64_t q_row = ((int64_t)b * a.H_q + h * a.G + gq) * a.T + t;
-    const auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + p)) * (streams * kRows) + in; };
-    float top = kNoRef;
-    for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_ml[slot(p)].x);
-    float l = 0.f, v[V];
+  const int bh = st.b * a.H1 + st.h, b = bh / a.H_kv, h = bh - b * a.H_kv;
+  const int64_t q_row = ((int64_t)b * a.H_q + h * a.G + gq) * a.T + t;
+  const auto slot = [&](int p) {
+    return (int64_t)(p == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + p)) * (streams * kRows) + x * kRows + row;
+  };
+  float top = kNoRef, l = 0.f, v[V];
 #pragma unroll
-    for (int z = 0; z < V; ++z) v[z] = 0.f;
+  for (int z = 0; z < V; ++z) v[z] = 0.f;
+  for (int p0 = 0; p0 < parts; p0 += 32) {        // 32 parts at a time: a lane has one's reference and sum
+    const float2 ml = p0 + lane < parts ? a.part_ml[slot(p0 + lane)] : make_float2(kNoRef, 0.f);
+    float next = fmaxf(top, ml.x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, o));
+    const float f0 = ex2(top - next), f = ex2(ml.x - next);
+    top = next;
+    float sum = ml.y * f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = fmaf(l, f0, sum);
+#pragma unroll
+    for (int z = 0; z < V; ++z) v[z] *= f0;
+    const int n = min(32, parts - p0);
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const int64_t s = slot(p);
-      const float2 ml = a.part_ml[s];
-      const float f = ex2(ml.x - top);
-      l = fmaf(ml.y, f, l);
+    for (int p = 0; p < n; ++p) {
+      const float fp = __shfl_sync(0xffffffffu, f, p);
       float y[V];
-      const float* o = a.part_o + s * D + lane * V;
+      const float* o = a.part_o + slot(p0 + p) * D + lane * V;
       if constexpr (V == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(o);
       else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(o);
 #pragma unroll
-      for (int z = 0; z < V; ++z) v[z] = fmaf(y[z], f, v[z]);
+      for (int z = 0; z < V; ++z) v[z] = fmaf(y[z], fp, v[z]);
     }
-    uint32_t w[V / 2];
-#pragma unroll
-    for (int z = 0; z < V / 2; ++z)
-      w[z] = l == 0.f ? 0u : bf16x2_of(v[2 * z] / l, v[2 * z + 1] / l);
-    __nv_bfloat16* o = a.out + q_row * D + lane * V;
-    if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(o) = w[0];
-    if (a.lse && lane == 0) a.lse[q_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
   }
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int z = 0; z < V / 2; ++z) w[z] = l == 0.f ? 0u : bf16x2_of(v[2 * z] / l, v[2 * z + 1] / l);
+  __nv_bfloat16* o = a.out + q_row * D + lane * V;
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(o) = w[0];
+  if (a.lse && lane == 0) a.lse[q_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host side
@@ -1250,7 +1295,9 @@ cudaError_t launch(const Args& a, void (*kern)(Args), cudaStream_t st) {
   if (e == cudaSuccess) e = launch_pdl(plan_kernel<FP8>, dim3(1), dim3(1024), 0, st, a, counted);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(a.P), dim3(kThreads), C::kSmem, st, a);
   if (e == cudaSuccess && a.P > 1)
-    e = launch_pdl(join_kernel<D>, dim3(a.P - 1, (a.pair_keys ? 1 : 2) * kRows / kJoinRows), dim3(256), 0, st, a);
+    e = launch_pdl(join_kernel<D>,
+                   dim3(a.P - 1, ((a.pair_keys ? 1 : 2) * a.nt * a.G + kJoinRows - 1) / kJoinRows),
+                   dim3(kJoinRows * 32), 0, st, a);
   note_launches(3 + counted);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
