@@ -228,6 +228,10 @@ struct Seg {
   int b, h, tile;                    // the unit
   int k0, n;                         // its first key tile, its steps
   int s0, cnt;                       // steps of this range
+  // The key tile that comes first, of `subs` a step.  The last keys do: with a bias by
+  // distance they have the largest scores, and the reference would move at every tile
+  // the other way round (2048 tokens over 8K: 315 us).
+  __device__ __forceinline__ int last(int subs) const { return k0 + (n - s0) * subs - 1; }
 };
 // Walks the units of a range; every role does it by itself, the next unit's place
 // asked for ahead.
@@ -507,11 +511,11 @@ __device__ bool load_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring,
       ++it;
     };
     // in the order of the products; the first keys need not wait for the queries' room
-    const int t0 = g.k0 + g.s0 * subs;
+    const int t1 = g.last(subs);
     for (int i = 0; i <= g.cnt && ok; ++i) {
       for (int x = 0; x < subs; ++x) {
-        if (i > 0) put(true, t0 + (i - 1) * subs + x);
-        if (i < g.cnt) put(false, t0 + i * subs + x);
+        if (i > 0) put(true, t1 - (i - 1) * subs - x);
+        if (i < g.cnt) put(false, t1 - i * subs - x);
       }
       if (FP8 || i > 0 || !ok) continue;
       if (nq > 0) ok = poll(smem_u32(&bars->q_empty), (nq - 1) & 1, a.wait_limit);
@@ -618,7 +622,7 @@ __device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t
   Walk w;
   if (w.begin(a)) do {
     const Seg& g = w.g;
-    const int t0 = g.k0 + g.s0 * subs;
+    const int t1 = g.last(subs);
     // What the unit's queries see between them: as a rule one range, each token's touching
     // the next one's (whole: no holes; tokens that see nothing only behind the others).
     int lo = INT_MAX, hi = -1;
@@ -678,7 +682,7 @@ __device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t
         ok = ok && wait(&bars->kv_full[v_st], v_it / C::kStages);
         if (!ok) break;
         const int sub = a.pair_keys ? 2 * (i - 1) + x : i - 1;
-        clean(t0 + sub, mt + sub, ring + v_st * C::kStageBytes);
+        clean(t1 - sub, mt + sub, ring + v_st * C::kStageBytes);
       }
       if (i < g.cnt) ok = ok && wait(&bars->kv_full[k_st], k_it / C::kStages);
       ok = ok && wait(&bars->turn[x], x == 0 ? turns - 1 : turns);
@@ -855,9 +859,9 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
     float ref = 0.f, unit = kLeastUnit;        // the first keys that the row sees set the reference
     bool seen = false;
     float2 sum2[2] = {};
-    const int t0 = g.k0 + g.s0 * subs;
+    const int t1 = g.last(subs);
     for (int i = 0; i < g.cnt; ++i, ++steps) {
-      const int tile = t0 + i * subs + (a.pair_keys ? x : 0);
+      const int tile = t1 - i * subs - (a.pair_keys ? x : 0);
       const uint32_t m_at = mt + i * subs + (a.pair_keys ? x : 0);
       const Meta& me = meta[m_at % kMeta];
       if constexpr (FP8) ok = ok && wait(&bars->meta_full[m_at % kMeta], m_at / kMeta);
@@ -932,11 +936,19 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
           }
           return fma2(make_float2(s[k], s[k + 1]), fk, c);
         };
-        if (BIAS && !FP8 && cross) {
+        if constexpr (BIAS && !FP8) {  // one or the other for the whole half tile
+          if (cross) {
 #pragma unroll
-          for (int k = 0; k < kHalf; k += 2) {
-            const float2 e = scores(k, true);
-            s[k] = e.x, s[k + 1] = e.y;
+            for (int k = 0; k < kHalf; k += 2) {
+              const float2 e = scores(k, true);
+              s[k] = e.x, s[k + 1] = e.y;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kHalf; k += 2) {
+              const float2 e = scores(k, false);
+              s[k] = e.x, s[k + 1] = e.y;
+            }
           }
         }
         // ---- weights, and the maximum beside them: the exponentials' unit is the narrow one
@@ -950,7 +962,7 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
           for (int z = 0; z < 2; ++z) {
             const int k = 4 * y + 2 * z;
             float2 e = make_float2(s[k], s[k + 1]);
-            if (!(BIAS && !FP8 && cross)) e = scores(k, false);
+            if constexpr (!BIAS || FP8) e = scores(k, false);
             v[z] = max3(v[z], e.x, e.y);
             float2 u = make_float2(ex2(e.x), ex2(e.y));
             part[z] = add2(part[z], u);
