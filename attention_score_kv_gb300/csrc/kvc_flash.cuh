@@ -283,8 +283,11 @@ struct Cfg {
   static constexpr int kMetaBytes = FP8 ? (int)sizeof(Meta) * kMeta : 0;
   static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMetaBytes;
   // bf16 reaches as far down as fp32 does, so weights may be small; e4m3's two parts
-  // end at 2^-10, so the largest weight of a row is kept between 2^6 and 2^8
-  static constexpr float kShift = FP8 ? 6.f : 0.f, kSlack = FP8 ? 2.f : 8.f;
+  // end at 2^-10, so the largest weight of a row is kept between 2^5 and 2^8 (from 2^6 on,
+  // twice as many tiles move the reference)
+  static constexpr float kShift = FP8 ? 5.f : 0.f, kSlack = FP8 ? 3.f : 8.f;
+  // a row's first maximum that leaves the reference where it is
+  static constexpr float kLow = FP8 ? 5.f : -24.f;
   static constexpr int kQSteps = FP8 ? D / 32 : D / 16, kVSteps = FP8 ? kKeys / 32 : kKeys / 16;
 };
 
@@ -478,8 +481,30 @@ __device__ bool load_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring,
       q_lo = __reduce_min_sync(0xffffffffu, q_lo);
       q_hi = __reduce_max_sync(0xffffffffu, q_hi);
     }
+    bool wants_q = !FP8;               // the segment's queries are not asked for yet
+    const auto ask_q = [&] {
+      ++nq;
+      wants_q = false;
+      if (lane == 0) {
+        const int rows = a.nt * a.G, qs = a.pair_keys ? 1 : 2;
+        const uint32_t bar = smem_u32(&bars->q_full);
+        tc::mbar_arrive_expect_tx(bar, (uint32_t)(qs * rows * D * 2));
+        for (int x = 0; x < qs; ++x)
+          for (int p = 0; p < D / 64; ++p)
+            tc::tma_load_3d(sQ + x * C::kQBytes + p * (kRows * 128), &a.qmap, bar, p * 64, (g.tile * qs + x) * a.nt,
+                            g.b * a.H_q + g.h * a.G);
+      }
+      __syncwarp();
+    };
     const auto put = [&](bool vals, int t) {
       const uint32_t st = it % C::kStages;
+      // keys and values run ahead of the queries, which wait for the last segment's products
+      for (uint32_t n = 0; wants_q; ++n) {
+        if (nq == 0 || __all_sync(0xffffffffu, tc::mbar_try_wait(smem_u32(&bars->q_empty), (nq - 1) & 1))) ask_q();
+        else if (__all_sync(0xffffffffu, tc::mbar_try_wait(smem_u32(&bars->kv_empty[st]), ((it / C::kStages) & 1) ^ 1))) break;
+        else if (n >= a.wait_limit) ok = false;
+        if (!ok) return;
+      }
       if (ok) ok = poll(smem_u32(&bars->kv_empty[st]), ((it / C::kStages) & 1) ^ 1, a.wait_limit);
       if (!ok) return;
       if constexpr (FP8) {
@@ -510,27 +535,17 @@ __device__ bool load_warp(const Args& a, Bars* bars, uint32_t sQ, uint32_t ring,
       __syncwarp();
       ++it;
     };
-    // in the order of the products; the first keys need not wait for the queries' room
+    // in the order of the products
     const int t1 = g.last(subs);
     for (int i = 0; i <= g.cnt && ok; ++i) {
       for (int x = 0; x < subs; ++x) {
         if (i > 0) put(true, t1 - (i - 1) * subs - x);
         if (i < g.cnt) put(false, t1 - i * subs - x);
       }
-      if (FP8 || i > 0 || !ok) continue;
-      if (nq > 0) ok = poll(smem_u32(&bars->q_empty), (nq - 1) & 1, a.wait_limit);
-      if (!ok) break;
-      ++nq;
-      if (lane == 0) {
-        const int rows = a.nt * a.G, qs = a.pair_keys ? 1 : 2;
-        const uint32_t bar = smem_u32(&bars->q_full);
-        tc::mbar_arrive_expect_tx(bar, (uint32_t)(qs * rows * D * 2));
-        for (int x = 0; x < qs; ++x)
-          for (int p = 0; p < D / 64; ++p)
-            tc::tma_load_3d(sQ + x * C::kQBytes + p * (kRows * 128), &a.qmap, bar, p * 64, (g.tile * qs + x) * a.nt,
-                            g.b * a.H_q + g.h * a.G);
-      }
-      __syncwarp();
+    }
+    if (wants_q && ok) {
+      ok = poll(smem_u32(&bars->q_empty), (nq - 1) & 1, a.wait_limit);
+      if (ok) ask_q();
     }
   } while (ok && w.next(a));
   // every copy issued has landed before the CTA may leave
@@ -628,18 +643,6 @@ __device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t
     int lo = INT_MAX, hi = -1;
     bool holes = false;
     const int per = a.nt * (a.pair_keys ? 1 : 2), tk0 = g.tile * per, tk1 = min(tk0 + per, a.T);
-    if constexpr (!FP8) {
-      for (int tk = tk0 + lane; tk < tk1; tk += 32) {
-        int l, h, l1 = 0, h1 = -1;
-        const bool some = key_range(a, (int64_t)g.b * a.T + tk, l, h);
-        const bool next = tk + 1 < tk1 && key_range(a, (int64_t)g.b * a.T + tk + 1, l1, h1);
-        if (some) lo = min(lo, l), hi = max(hi, h);
-        holes |= next && (!some || l1 > h + 1 || l > h1 + 1);
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      holes = __any_sync(0xffffffffu, holes);
-    }
     // rows of tile `t` that no query of the unit sees become zeros (both streams' warps
     // may write the same ones)
     const auto clean = [&](int t, uint32_t m, uint32_t stage) {
@@ -704,6 +707,19 @@ __device__ bool mma_warp(const Args& a, Bars* bars, int x, uint32_t sQ, uint32_t
         tc::mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
       }
       __syncwarp();
+      // behind the first scores, which need not wait for it
+      if (!FP8 && i == 0) {
+        for (int tk = tk0 + lane; tk < tk1; tk += 32) {
+          int l, h, l1 = 0, h1 = -1;
+          const bool some = key_range(a, (int64_t)g.b * a.T + tk, l, h);
+          const bool next = tk + 1 < tk1 && key_range(a, (int64_t)g.b * a.T + tk + 1, l1, h1);
+          if (some) lo = min(lo, l), hi = max(hi, h);
+          holes |= next && (!some || l1 > h + 1 || l > h1 + 1);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        holes = __any_sync(0xffffffffu, holes);
+      }
     }
     it += g.cnt * 2 * subs;
     mt += g.cnt * subs;
@@ -818,6 +834,7 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
   const int subs = a.pair_keys ? 2 : 1;
   const bool any_row = (warp & 3) * 32 < a.nt * a.G;         // none of the warp's rows is one: nothing reads its part
   uint32_t steps = 0, mt = 0, seg = 0;
+  float ref = 0.f;
   bool ok = true;
   // after a wait that gave up: go on without waiting, so that no barrier is left alone
   const auto wait = [&](const uint64_t* bar, uint32_t phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
@@ -856,7 +873,9 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
       c2 = s_max[(a.pair_keys ? 0 : x) * 2 * kRows + row];
       asm volatile("bar.sync 1, 512;\n" ::: "memory");       // read before the first maxima are written there
     }
-    float ref = 0.f, unit = kLeastUnit;        // the first keys that the row sees set the reference
+    // the last segment's reference, another row's, stands in until the row sees keys
+    if (!(fabsf(ref) < 1e30f)) ref = 0.f;
+    float unit = kLeastUnit;
     bool seen = false;
     float2 sum2[2] = {};
     const int t1 = g.last(subs);
@@ -901,14 +920,18 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
               }
             }
         } else {
-          int l = lo - tile * kKeys - half * kHalf, r = hi - tile * kKeys - half * kHalf;
-          // as far as the compiler sees, no two rounds have the same: it would work the 64
-          // comparisons out ahead of the loop, for every tile
-          asm volatile("" : "+r"(l), "+r"(r));
-          if (__any_sync(0xffffffffu, l > 0 || r < kHalf - 1)) {
+          const int l = max(lo - tile * kKeys - half * kHalf, 0), r = min(hi - tile * kKeys - half * kHalf, kHalf - 1);
+          if (__any_sync(0xffffffffu, r - l < kHalf - 1)) {
+            unsigned long long in = l > r ? 0 : (~0ull >> (63 - (r - l))) << l;
+            // as far as the compiler sees, no two rounds have the same: it would work the 64
+            // bits out ahead of the loop, for every tile
+            asm volatile("" : "+l"(in));
+            const uint32_t in0 = (uint32_t)in, in1 = (uint32_t)(in >> 32);
 #pragma unroll
-            for (int k = 0; k < kHalf; ++k)
-              if (k < l || k > r) s[k] = -INFINITY;
+            for (int k = 0; k < 32; ++k) {
+              if (!(in0 & 1u << k)) s[k] = -INFINITY;
+              if (!(in1 & 1u << k)) s[32 + k] = -INFINITY;
+            }
           }
         }
         // ---- the scores less the reference: s times a factor plus `neg` and the bias.  The bias
@@ -983,8 +1006,10 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
           *my_max = fmaxf(v[0], v[1]);
           asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory");
           const float m = max3(v[0], v[1], *its_max);
-          const bool first = !seen && m > -INFINITY;               // the row's first keys
+          // the row's first keys, and the reference, which is another row's, far above them
+          const bool first = !seen && m > -INFINITY && !(m >= C::kLow && m <= C::kSlack + C::kShift);
           bool move = first || m > C::kSlack + C::kShift;
+          seen |= m > -INFINITY;
           float top = kLeastUnit;
           if constexpr (FP8) {         // of the whole tile: both halves need one unit
 #pragma unroll
@@ -994,8 +1019,7 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
           if (__any_sync(0xffffffffu, move)) {
             const float up = first ? m - C::kShift : fmaxf(0.f, m - C::kShift);
             float fo = first ? 1.f : ex2(-up);     // nothing has been added up before the first
-            if (first || m > -INFINITY) ref += up;
-            seen |= first;
+            if (m > -INFINITY) ref += up;
 #pragma unroll
             for (int y = 0; y < 2; ++y) sum2[y].x *= fo, sum2[y].y *= fo;
             if constexpr (FP8) {
@@ -1037,10 +1061,10 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
     float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
     const bool whole = g.s0 == 0 && g.cnt == g.n;
     const int64_t slot = 2 * blockIdx.x + (g.s0 == 0 ? 1 : 0);
-    if (!seen) ref = kNoRef;
+    float said = seen ? ref : kNoRef;
     tc::fence_before_sync();
     *my_max = sum;
-    if (a.pair_keys && half == 0) s_x[x * kRows + row] = ref, s_x[(2 + x) * kRows + row] = unit;
+    if (a.pair_keys && half == 0) s_x[x * kRows + row] = said, s_x[(2 + x) * kRows + row] = unit;
     asm volatile("bar.sync 1, 512;\n" ::: "memory");
     tc::fence_after_sync();
     sum = s_max[x * 2 * kRows + row] + s_max[(x * 2 + 1) * kRows + row];
@@ -1050,7 +1074,7 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
       const float ra = s_x[row], rb = s_x[kRows + row], top = fmaxf(ra, rb);
       f0 = ex2(ra - top), f1 = ex2(rb - top);
       sum = (s_max[row] + s_max[kRows + row]) * f0 + (s_max[2 * kRows + row] + s_max[3 * kRows + row]) * f1;
-      ref = top;
+      said = top;
       if constexpr (FP8) f0 *= s_x[2 * kRows + row], f1 *= s_x[3 * kRows + row];
       from = (2 * x + half) * (D / 4), dims = D / 4, first = 0;
     }
@@ -1093,8 +1117,8 @@ __device__ bool soft_warps(const Args& a, Bars* bars, float* s_max, uint32_t sQ,
         }
       }
       if (live && from == 0) {
-        if (!whole) a.part_ml[part] = make_float2(ref, sum);
-        else if (a.lse) a.lse[q_row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+        if (!whole) a.part_ml[part] = make_float2(said, sum);
+        else if (a.lse) a.lse[q_row] = sum == 0.f ? -INFINITY : (said + log2f(sum)) * kLn2;
       }
     }
     // the next segment's weights, outputs and what is told come after everybody's reads
