@@ -20,7 +20,7 @@
 // from accumulator to operand layout with movmatrix.
 //
 // A format F has:
-//   kD; kScaled: the values of a block have one scale, a power of two; kMods: scores
+//   kD; kJoinInRing: a ring stage has room for a warp's outputs; kScaled: the values of a block have one scale, a power of two; kMods: scores
 //   may be capped and biased (then its scales give the keys' scale too)
 //   Source, Cursor, cursor(source, row), touch(source): where a row's block is
 //   kStageBytes, kPosAt, copy(stage, cursor, block, pos, lane): a block in a ring
@@ -229,12 +229,24 @@ __device__ __forceinline__ void fetch_block(const Segment<F>& x, int in, uint32_
   copies_commit();
 }
 
-// Shared memory: the warps' outputs, then their rings.
-// Position d' = 16 m + 2 r + e of a row there holds dim r*D/8 + 2m + e: a lane
+// Shared memory: the warps' outputs (kJoinInRing: in the stage of a warp's ring that
+// is not being filled, which leaves room for a second CTA), then their rings.
+// Position d' = 16 m + 2 r + e of an output row holds dim r*D/8 + 2m + e: a lane
 // of the output fragments stores pairs side by side with its neighbours', and
 // rows D + 4 apart keep the four columns of a store on different banks.
 __host__ __device__ constexpr int o_stride(int D) { return D + 4; }
-__host__ __device__ constexpr int o_bytes(int D, int R) { return kWarps * R * o_stride(D) * (int)sizeof(float); }
+template <class F>
+__host__ __device__ constexpr int o_bytes(int R) {
+  return F::kJoinInRing ? 0 : kWarps * R * o_stride(F::kD) * (int)sizeof(float);
+}
+// Where a warp's outputs go, and its ring.
+template <class F>
+__device__ __forceinline__ float* outputs_of(uint8_t* dyn, int R, int warp, int stage_out) {
+  static_assert(!F::kJoinInRing || F::kStageBytes >= kCols * o_stride(F::kD) * (int)sizeof(float), "a stage holds them");
+  if constexpr (F::kJoinInRing)
+    return reinterpret_cast<float*>(dyn + (warp * kStages + (stage_out + kStages - 1) % kStages) * F::kStageBytes);
+  return reinterpret_cast<float*>(dyn) + warp * R * o_stride(F::kD);
+}
 template <int D>
 __device__ __forceinline__ int dim_of(int at) { return (at >> 1 & 7) * (D / 8) + (at >> 4) * 2 + (at & 1); }
 
@@ -414,8 +426,9 @@ __device__ __forceinline__ void attend_segment(const Args<F>& a, const Segment<F
 // Joins the CTA's warps, in warp order, into sum_o [R][D] and sum_ml [R]: shared
 // or global memory.
 template <class F>
-__device__ __forceinline__ void join_warps(const Acc<F>& x, int R, float2 (*s_ml)[kCols], float* s_o, float* sum_o,
+__device__ __forceinline__ void join_warps(const Acc<F>& x, int R, float2 (*s_ml)[kCols], float* mine, float* sum_o,
                                            float2* sum_ml) {
+  __shared__ const float* s_at[kWarps];
   constexpr int D = F::kD, KS = D / 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
 #pragma unroll
@@ -426,6 +439,7 @@ __device__ __forceinline__ void join_warps(const Acc<F>& x, int R, float2 (*s_ml
     v += __shfl_xor_sync(0xffffffffu, v, 16);
     if (r == 0) s_ml[warp][2 * j + y] = make_float2(x.ref[y], v);
   }
+  if (lane == 0) s_at[warp] = mine;
   __syncthreads();
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
@@ -436,7 +450,7 @@ __device__ __forceinline__ void join_warps(const Acc<F>& x, int R, float2 (*s_ml
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][col].x);
     float f = ex2(x.ref[y] - top);
     if constexpr (F::kScaled) f *= x.unit;
-    float* to = s_o + (warp * R + col) * o_stride(D) + 2 * r;
+    float* to = mine + col * o_stride(D) + 2 * r;
 #pragma unroll
     for (int m = 0; m < KS; ++m)
       *reinterpret_cast<float2*>(to + 16 * m) = make_float2(x.o[m][y] * f, x.o[m][2 + y] * f);
@@ -447,7 +461,7 @@ __device__ __forceinline__ void join_warps(const Acc<F>& x, int R, float2 (*s_ml
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float4 z = *reinterpret_cast<const float4*>(s_o + (w * R + col) * o_stride(D) + at);
+      const float4 z = *reinterpret_cast<const float4*>(s_at[w] + col * o_stride(D) + at);
       v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
     }
     *reinterpret_cast<float4*>(sum_o + col * D + at) = v;
@@ -485,8 +499,7 @@ __device__ __forceinline__ void scan_ranges(const Args<F>& a) {
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int R = a.G * a.T;           // query rows, at most kCols
-  float* s_o = reinterpret_cast<float*>(dyn);              // [kWarps][R][o_stride]
-  uint8_t* ring = dyn + o_bytes(D, R) + warp * kStages * F::kStageBytes;
+  uint8_t* ring = dyn + o_bytes<F>(R) + warp * kStages * F::kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
 
   // the CTA's range [f0, f1) of the blocks laid end to end
@@ -520,7 +533,7 @@ __device__ __forceinline__ void scan_ranges(const Args<F>& a) {
     if (more)
       for (int i = 0; i < kStages - 1; ++i) fetch(next, i);
     const int64_t part = ((int64_t)blockIdx.x + g.bh) * R;
-    join_warps<F>(acc, R, s_ml, s_o, a.part_o + part * D, a.part_ml + part);
+    join_warps<F>(acc, R, s_ml, outputs_of<F>(dyn, R, warp, stage_out), a.part_o + part * D, a.part_ml + part);
     __syncthreads();
     g = next;
   }
@@ -554,8 +567,7 @@ __device__ __forceinline__ void scan_cluster(const Args<F>& a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = a.G * a.T, H = a.s.H_kv;
   const int bh = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = bh / H, h = bh - b * H;
   const int64_t cap = a.s.off[h + 1] - a.s.off[h], row0 = (int64_t)b * a.s.off[H] + a.s.off[h];
-  float* s_o = reinterpret_cast<float*>(dyn);
-  uint8_t* ring = dyn + o_bytes(D, R) + warp * kStages * F::kStageBytes;
+  uint8_t* ring = dyn + o_bytes<F>(R) + warp * kStages * F::kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
   grid_dep_wait();
   grid_dep_launch();
@@ -583,7 +595,7 @@ __device__ __forceinline__ void scan_cluster(const Args<F>& a) {
   };
   Acc<F> acc;
   attend_segment<F>(a, g, b, t_of, ring, stage_out, start, fetch, acc);
-  join_warps<F>(acc, R, s_ml, s_o, s_sum, s_sum_ml);
+  join_warps<F>(acc, R, s_ml, outputs_of<F>(dyn, R, warp, stage_out), s_sum, s_sum_ml);
   cluster_sync();
   for (int i = rank * kThreads + threadIdx.x; i < R * D; i += kCluster * kThreads) {
     const int row = i / D, d = i % D;
@@ -709,7 +721,7 @@ template <class F>
 cudaError_t launch(const Args<F>& a, bool clusters, void (*scan)(Args<F>), void (*cluster)(Args<F>),
                    void (*join)(Args<F>), cudaStream_t st) {
   const int H = a.s.H_kv, R = a.G * a.T;
-  const size_t smem = o_bytes(F::kD, R) + kWarps * kStages * F::kStageBytes;
+  const size_t smem = o_bytes<F>(R) + kWarps * kStages * F::kStageBytes;
   if (clusters) {
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(cluster), smem);
     if (e != cudaSuccess) return e;

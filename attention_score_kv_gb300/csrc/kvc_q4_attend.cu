@@ -48,7 +48,7 @@ __device__ __forceinline__ Codes<kB / 4> load_codes(const uint8_t* p) {
 template <int D>
 struct Q4Rows {
   static constexpr int kD = D, kB = D / 8;
-  static constexpr bool kScaled = false, kMods = false;
+  static constexpr bool kJoinInRing = false, kScaled = false, kMods = false;
   using Source = const uint8_t*;
   using Cursor = const uint8_t*;
   static __device__ __forceinline__ void touch(Source s) { asm volatile("" ::"l"(s)); }

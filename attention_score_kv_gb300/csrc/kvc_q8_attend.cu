@@ -27,7 +27,7 @@ struct Q8Source { const uint8_t *k8, *v8; const float* scale; };
 template <int D>
 struct Q8Rows {
   static constexpr int kD = D;
-  static constexpr bool kScaled = true, kMods = true;
+  static constexpr bool kJoinInRing = true, kScaled = true, kMods = true;
   using Source = Q8Source;
   using Cursor = Q8Source;
   static __device__ __forceinline__ void touch(const Source& s) {
