@@ -11,9 +11,9 @@
 // running maximum, sum and unnormalised output, and a second kernel joins the
 // parts in order.
 //
-// A warp takes one block at a time, and every lane copies its share of the
-// blocks ahead into shared memory asynchronously and reads it back itself, so
-// the copies need no barrier.  The products are
+// A warp takes one block at a time and copies blocks ahead into shared memory
+// asynchronously, a ring of its own, so the copies need no barrier of the CTA (and
+// none at all where every lane reads back what it copied).  The products are
 //   S^T (16 rows x 8 queries) = K Q^T,   O^T (D x 8 queries) += V^T P^T,
 // with up to 8 query rows as the narrow N side, so that no row of the
 // matrix instruction is wasted when a KV head has 4 or 5 query heads.  P goes
@@ -23,9 +23,10 @@
 //   kD; kJoinInRing: a ring stage has room for a warp's outputs; kScaled: the values of a block have one scale, a power of two; kMods: scores
 //   may be capped and biased (then its scales give the keys' scale too)
 //   Source, Cursor, cursor(source, row), touch(source): where a row's block is
-//   kStageBytes, kPosAt, copy(stage, cursor, block, pos, lane): a block in a ring
+//   kStageBytes, copy(stage, cursor, block, pos, lane): a block in a ring; kCross: lanes
+//   read what others copied
 //   q_at(j, i): dims of the i-th 8 of lane quarter j; q_pair(w, s, y, lo, hi)
-//   scales, mask, scores, outputs: a block's products
+//   positions, scales, mask, scores, outputs: a block's products
 #pragma once
 
 #include <algorithm>
@@ -339,12 +340,14 @@ __device__ __forceinline__ void attend_segment(const Args<F>& a, const Segment<F
   const int mine = (g.cnt - warp + kWarps - 1) / kWarps;       // blocks of this warp (may be <= 0)
   for (int i = 0; i < mine; ++i) {
     const int blk = g.s0 + warp + i * kWarps;
+    if constexpr (F::kCross) __syncwarp();         // all have read the stage that is filled now
     fetch(g, i + kStages - 1);
     copies_wait<kStages - 1>();
+    if constexpr (F::kCross) __syncwarp();
     const uint8_t* st = ring + stage_out * F::kStageBytes;
     stage_out = stage_out + 1 == kStages ? 0 : stage_out + 1;
     auto sc = F::scales(st, lane);
-    const int2 xp = *reinterpret_cast<const int2*>(st + F::kPosAt + lane * 8);
+    const int2 xp = F::positions(st, lane);        // of rows r and r + 8
     // ---- scores
     float acc[4] = {};
     F::scores(st, lane, sc, qf, acc);

@@ -48,7 +48,7 @@ __device__ __forceinline__ Codes<kB / 4> load_codes(const uint8_t* p) {
 template <int D>
 struct Q4Rows {
   static constexpr int kD = D, kB = D / 8;
-  static constexpr bool kJoinInRing = false, kScaled = false, kMods = false;
+  static constexpr bool kJoinInRing = false, kCross = false, kScaled = false, kMods = false;
   using Source = const uint8_t*;
   using Cursor = const uint8_t*;
   static __device__ __forceinline__ void touch(Source s) { asm volatile("" ::"l"(s)); }
@@ -80,6 +80,10 @@ struct Q4Rows {
     }
     few::copy_small<4>(dst + kPosAt + lane * 8, pos + r);
     few::copy_small<4>(dst + kPosAt + lane * 8 + 4, pos + r + 8);
+  }
+
+  static __device__ __forceinline__ int2 positions(const uint8_t* st, int lane) {
+    return *reinterpret_cast<const int2*>(st + kPosAt + lane * 8);
   }
 
   // quarter j of a row, pairs of dims D/8 apart

@@ -5,12 +5,11 @@
 //   o = sum p v / sum p,  p = exp(x)
 //
 // One read of the cache bounds it: 2D + 4.5 bytes a row.  How the rows are shared
-// out and the products made: kvc_few_rows.cuh.  Rows are held row after row; a
-// lane's share of a block is 16 bytes of a row at a time, four lanes (keys) or
-// eight (values) on the same 64 or 128 bytes, so whole sectors move.  The order
-// of a contraction is free, so keys go from a row's bytes through one conversion
-// into mma operands, with the queries laid out alike; values, whose rows are the
-// contraction's index, take a byte permutation first (two rows in one operand).
+// out and the products made: kvc_few_rows.cuh.  Rows are held row after row, and
+// go into shared memory 512 bytes a copy.  The order of a contraction is free, so
+// keys go from a row's bytes through one conversion into mma operands, with the
+// queries laid out alike; values, whose rows are the contraction's index, take a
+// byte permutation first (two rows in one operand).
 // Codes are exact in fp16.  A block's scale of the keys multiplies its scores,
 // that of the values the block's weights, in units of the largest scale that the
 // warp has met, so that fp16 holds the weights.
@@ -27,7 +26,7 @@ struct Q8Source { const uint8_t *k8, *v8; const float* scale; };
 template <int D>
 struct Q8Rows {
   static constexpr int kD = D;
-  static constexpr bool kJoinInRing = true, kScaled = true, kMods = true;
+  static constexpr bool kJoinInRing = true, kCross = true, kScaled = true, kMods = true;
   using Source = Q8Source;
   using Cursor = Q8Source;
   static __device__ __forceinline__ void touch(const Source& s) {
@@ -37,41 +36,43 @@ struct Q8Rows {
     return {s.k8 + row * D, s.v8 + row * D, s.scale + row / q8::kRows * 2};
   }
 
-  // A stage of a warp's ring, in the order in which the lanes read it.  Lane
-  // 4r + j has rows r and r + 8 of the keys, 16 bytes at 16 j (and 64 + 16 j); slice
-  // r of rows 2j, 2j + 1, 2j + 8 and 2j + 9 of the values; the two scales; and the
-  // positions of rows r and r + 8.
-  static constexpr int kV = D / 8;                 // bytes of a slice
-  static constexpr int kValuesAt = 16 * D, kScaleAt = 32 * D, kPosAt = kScaleAt + 32 * 8, kStageBytes = kPosAt + 32 * 8;
+  // A stage of a warp's ring: the keys, the values, 16 positions, the two scales.  A copy
+  // of the warp takes 512 bytes in a row.  Lines of 128 bytes (a row, or two of D = 64)
+  // have their eight pieces of 16 bytes swapped about, so that the eight lanes of a
+  // read's phase find theirs on different banks: keys, two rows' even or odd pieces, by
+  // the row; values, two pieces of every other row, by the pair of rows.
+  static constexpr int kV = D / 8;                 // bytes of a slice of a value row
+  static constexpr int kValuesAt = 16 * D, kPosAt = 32 * D, kScaleAt = kPosAt + 64, kStageBytes = kPosAt + 128;
+  static __device__ __forceinline__ int at_line(int line, int piece, bool vals) {
+    const int flip = D == 128 ? (vals ? 2 * (line >> 1 & 3) : line & 7) : (vals ? 2 * (line & 3) : 0);
+    return line * 128 + ((piece ^ flip) << 4);
+  }
   static __device__ __forceinline__ void copy(uint32_t dst, const Cursor& at, int in, const int32_t* pos, int lane) {
-    const int r = lane >> 2, j = lane & 3;
-    const uint8_t* k = at.k8 + (int64_t)in * (16 * D) + r * D + 16 * j;
-    const uint8_t* v = at.v8 + (int64_t)in * (16 * D) + 2 * j * D + r * kV;
+    const uint8_t* k = at.k8 + (int64_t)in * (16 * D) + lane * 16;
+    const uint8_t* v = at.v8 + (int64_t)in * (16 * D) + lane * 16;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const int row = i / (D / 64) * 8, part = i % (D / 64) * 64;
-      few::copy16(dst + i * 512 + lane * 16, k + row * D + part);
+      const int line = 4 * i + (lane >> 3), piece = lane & 7;
+      few::copy16(dst + at_line(line, piece, false), k + i * 512);
+      few::copy16(dst + kValuesAt + at_line(line, piece, true), v + i * 512);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint8_t* p = v + ((e & 1) + (e >> 1) * 8) * D;
-      const uint32_t to = dst + kValuesAt + (e * 32 + lane) * kV;
-      if constexpr (kV == 16) few::copy16(to, p);
-      else few::copy_small<8>(to, p);
-    }
-    few::copy_small<8>(dst + kScaleAt + lane * 8, at.scale + (int64_t)in * 2);
-    few::copy_small<4>(dst + kPosAt + lane * 8, pos + r);
-    few::copy_small<4>(dst + kPosAt + lane * 8 + 4, pos + r + 8);
+    if (lane < 16) few::copy_small<4>(dst + kPosAt + lane * 4, pos + lane);
+    else if (lane == 16) few::copy_small<8>(dst + kScaleAt, at.scale + (int64_t)in * 2);
+  }
+  static __device__ __forceinline__ int2 positions(const uint8_t* st, int lane) {
+    const int* p = reinterpret_cast<const int*>(st + kPosAt);
+    return make_int2(p[lane >> 2], p[(lane >> 2) + 8]);
   }
 
-  static __device__ __forceinline__ int q_at(int j, int i) { return 16 * j + i / 2 * 64 + i % 2 * 8; }
+  // a lane's quarter of a row, pairs of dims side by side
+  static __device__ __forceinline__ int q_at(int j, int i) { return j * (D / 4) + 8 * i; }
   static __device__ __forceinline__ void q_pair(const uint32_t* w, int s, int y, uint32_t& lo, uint32_t& hi) {
     lo = w[2 * s + y] & 0xffffu, hi = w[2 * s + y] >> 16;
   }
 
   struct Scales { float k, v; uint32_t keep; };
-  static __device__ __forceinline__ Scales scales(const uint8_t* st, int lane) {
-    const float2 s = *reinterpret_cast<const float2*>(st + kScaleAt + lane * 8);
+  static __device__ __forceinline__ Scales scales(const uint8_t* st, int) {
+    const float2 s = *reinterpret_cast<const float2*>(st + kScaleAt);
     return {s.x, s.y, 0xffffffffu};
   }
   // keep: a byte each for rows 2j, 2j + 1, 2j + 8, 2j + 9
@@ -84,10 +85,12 @@ struct Q8Rows {
   static __device__ __forceinline__ void scores(const uint8_t* st, int lane, const Scales&,
                                                 const uint32_t (&qf)[D / 16][2], float (&acc)[4]) {
     float odd[4] = {};
+    const int r = lane >> 2, j = lane & 3;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const uint4 a4 = *reinterpret_cast<const uint4*>(st + i * 512 + lane * 16);
-      const uint4 b4 = *reinterpret_cast<const uint4*>(st + (i + D / 64) * 512 + lane * 16);
+    for (int i = 0; i < D / 64; ++i) {             // rows r and r + 8, 16 dims
+      const int at = D == 128 ? at_line(r, 2 * j + i, false) : at_line(r >> 1, (r & 1) * 4 + j, false);
+      const uint4 a4 = *reinterpret_cast<const uint4*>(st + at);
+      const uint4 b4 = *reinterpret_cast<const uint4*>(st + 8 * D + at);       // the same place: rows r and r + 8 flip alike
       const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -104,9 +107,12 @@ struct Q8Rows {
   static __device__ __forceinline__ void outputs(const uint8_t* st, int lane, const Scales& sc, uint32_t pf0,
                                                  uint32_t pf1, float (&o)[D / 16][4]) {
     uint32_t v[4][kV / 4];
+    const int r = lane >> 2, j = lane & 3;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint8_t* p = st + kValuesAt + (e * 32 + lane) * kV;
+    for (int e = 0; e < 4; ++e) {                  // slice r of rows 2j, 2j + 1, 2j + 8, 2j + 9
+      const int row = 2 * j + (e & 1) + (e >> 1) * 8;
+      const uint8_t* p = st + kValuesAt + (D == 128 ? at_line(row, r, true)
+                                                    : at_line(row >> 1, (row & 1) * 4 + (r >> 1), true) + (r & 1) * 8);
       if constexpr (kV == 16) {
         const uint4 x = *reinterpret_cast<const uint4*>(p);
         v[e][0] = x.x, v[e][1] = x.y, v[e][2] = x.z, v[e][3] = x.w;
