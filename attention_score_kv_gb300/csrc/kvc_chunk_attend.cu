@@ -17,7 +17,7 @@ __global__ void __launch_bounds__(flash::kThreads, 1) kvc_attend_chunk_kernel(co
 }
 
 template <int D>
-cudaError_t launch_of(const flash::Args& a, cudaStream_t st) {
+cudaError_t launch_of(flash::Args& a, cudaStream_t st) {
   auto* kern = a.cap2 > 0.f ? (a.slopes ? kvc_attend_chunk_kernel<D, true, true> : kvc_attend_chunk_kernel<D, true, false>)
                             : (a.slopes ? kvc_attend_chunk_kernel<D, false, true>
                                         : kvc_attend_chunk_kernel<D, false, false>);
