@@ -235,7 +235,7 @@ struct Seg {
   __device__ __forceinline__ int last(int subs) const { return k0 + (n - s0) * subs - 1; }
 };
 // Few units: every CTA counts all of them and finds its own range, a launch less
-// (8 units of a single token over 8K: 18.4 -> 15.7 us).
+// (8 units of a single token over 8K: 18.5 -> 17.2 us).
 constexpr int kPlanHere = 38;
 struct Here {
   Start start;
@@ -517,6 +517,29 @@ __device__ bool load_warp(const Args& a, const Here& here, Bars* bars, uint32_t 
       q_lo = __reduce_min_sync(0xffffffffu, q_lo);
       q_hi = __reduce_max_sync(0xffffffffu, q_hi);
     }
+    // positions and scales of the next tiles (which go downward), on their way: asked for
+    // when a tile's turn comes, they held every tile up by two trips to memory
+    constexpr int kAhead = FP8 ? 3 : 1;
+    struct Rows { int pos[4]; float2 scale; };
+    Rows ahead[kAhead];
+    const int64_t row0 = FP8 ? (int64_t)b * a.s.off[a.H_kv] + a.s.off[h] : 0;
+    const int t_end = g.last(subs) - g.cnt * subs;             // the tile behind the segment's last
+    const auto fetch = [&](int t) {
+      Rows r;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = t * kKeys + x * 32 + lane;
+        r.pos[x] = t > t_end && row < n_rows ? __ldg(a.pos + row0 + row) : -1;
+      }
+      r.scale = make_float2(1.f, kLeastUnit);
+      const int block = t * (kKeys / q8::kRows) + lane;
+      if (t > t_end && lane < kKeys / q8::kRows && block * q8::kRows < n_rows)
+        r.scale = __ldg(a.scale + row0 / q8::kRows + block);
+      return r;
+    };
+    if constexpr (FP8)
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) ahead[x] = fetch(g.last(subs) - x);
     bool wants_q = !FP8;               // the segment's queries are not asked for yet
     const auto ask_q = [&] {
       ++nq;
@@ -543,15 +566,20 @@ __device__ bool load_warp(const Args& a, const Here& here, Bars* bars, uint32_t 
       }
       if (ok) ok = poll(smem_u32(&bars->kv_empty[st]), ((it / C::kStages) & 1) ^ 1, a.wait_limit);
       if (!ok) return;
+      if (lane == 0) load_tile<D, FP8>(a, g, vals, t, ring + st * C::kStageBytes, smem_u32(&bars->kv_full[st]));
+      __syncwarp();
+      ++it;
       if constexpr (FP8) {
-        if (!vals) {                 // the tile's positions and scales with its keys
+        if (!vals) {                 // the tile's positions and scales
           Meta& m = meta[mt % kMeta];
-          const int64_t row0 = (int64_t)b * a.s.off[a.H_kv] + a.s.off[h];
+          const Rows r = ahead[0];
+#pragma unroll
+          for (int x = 0; x + 1 < kAhead; ++x) ahead[x] = ahead[x + 1];
+          ahead[kAhead - 1] = fetch(t - kAhead);
           uint32_t seen = 0;         // lane y: of block y
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int row = t * kKeys + x * 32 + lane;
-            const int p = row < n_rows ? __ldg(a.pos + row0 + row) : -1;
+            const int p = r.pos[x];
             m.pos[x * 32 + lane] = p;
             m.rel[x * 32 + lane] = (float)(int)((uint32_t)p - (uint32_t)q_hi);
             const uint32_t some = __ballot_sync(0xffffffffu, p >= 0 && p <= q_hi);
@@ -560,16 +588,12 @@ __device__ bool load_warp(const Args& a, const Here& here, Bars* bars, uint32_t 
             if (lane >> 1 == x) seen = some >> (lane & 1) * 16 & 0xffffu;
           }
           if (lane < kKeys / q8::kRows)          // a block of which nothing is seen may have anything for a scale
-            m.scale[lane] = seen ? __ldg(a.scale + row0 / q8::kRows + t * (kKeys / q8::kRows) + lane)
-                                 : make_float2(1.f, kLeastUnit);
+            m.scale[lane] = seen ? r.scale : make_float2(1.f, kLeastUnit);
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(smem_u32(&bars->meta_full[mt % kMeta]));
           ++mt;
         }
       }
-      if (lane == 0) load_tile<D, FP8>(a, g, vals, t, ring + st * C::kStageBytes, smem_u32(&bars->kv_full[st]));
-      __syncwarp();
-      ++it;
     };
     // in the order of the products
     const int t1 = g.last(subs);
@@ -693,6 +717,7 @@ __device__ bool mma_warp(const Args& a, const Here& here, Bars* bars, int x, uin
         }
       };
       if constexpr (FP8) {
+        ok = ok && wait(&bars->meta_full[m % kMeta], m / kMeta);
 #pragma unroll
         for (int y = 0; y < 4; ++y) keep[y] = meta[m % kMeta].some[y];
       } else if (!holes) {
