@@ -48,9 +48,9 @@ namespace flash {
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kHalf = kKeys / 2;     // keys of a thread of the weights
-constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18;
+constexpr int kSoftWarps = 16, kMmaWarp = 16, kLoadWarp = 18, kMetaWarp = 19;
 // Five groups of four warps: the two streams' weights, and the two issuing, the
-// loading and an idle warp, whose registers the first four groups take: 4 * 104 + 64 =
+// loading and the 8-bit cache's warp, whose registers the first four groups take: 4 * 104 + 64 =
 // 5 * 96, what the block is launched with.
 constexpr int kThreads = 20 * 32, kSoftRegs = 104, kOtherRegs = 64;
 constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;    // stream x: S at kColS + 128 x, O at kColO + 128 x
@@ -60,15 +60,12 @@ constexpr float kLeastUnit = 7.8886090522101181e-31f;      // 2^-100, the smalle
 constexpr int kMaxStages = 11;
 constexpr int kMeta = 8;             // tiles whose positions and scales are in shared memory
 
-// What a tile of the 8-bit cache's rows is.  Its slot is written again for the
-// stream's tile of eight tiles further on, behind a stage that the ring's nine
-// loads before gave up: the products of five tiles before at least, which were
-// issued after the weights of the slot's last tile had been made.
+// What a tile of the 8-bit cache's rows is.
 struct alignas(16) Meta {
   int pos[kKeys];
   float rel[kKeys];                  // position less the unit's last query's
   float2 scale[kKeys / q8::kRows];   // of the blocks' keys and values
-  uint32_t some[4];                  // rows that some query of the unit may see
+  uint32_t some[4];                  // rows that some query of the call may see
   uint32_t mixed[4];                 // some query does not see all of these 32
 };
 
@@ -92,6 +89,7 @@ struct Args {
   float* lse;
   Plan* plan;
   int2* units;                       // [B1][tiles]: first key tile, steps
+  int2 *sees, *seen;                 // [B1][tiles], [B1]: what units and sequences see
   long long* before;                 // [B1 * tiles + 1] steps before, of one head
   Start* start;                      // [P + 1]
   float2* part_ml;                   // [2 P][rows of a unit]: reference, sum
@@ -119,29 +117,53 @@ __device__ __forceinline__ int rows_held(const Args& a, int bh, bool* bad) {
   *bad = n < 0 || n > cap;
   return (int)(n < 0 ? 0 : n > cap ? cap : n);
 }
-// Steps of one unit, by a warp.
+// One unit, by a warp: its first key tile and steps, and what its tokens see: the first
+// and last key, and whether their ranges leave holes between them or to the next
+// unit's (each token's touches the next one's, and those that see nothing come last).
+// 8-bit cache: the last position that a token of it may see.  Packed: the first key, -1
+// with holes, and the last.
 template <bool FP8>
-__device__ __forceinline__ int2 unit_steps(const Args& a, int b, int tile) {
-  const int lane = threadIdx.x & 31;
-  int k0 = 0, n = 1;
+__device__ __forceinline__ int2 unit_steps(const Args& a, int b, int tile, int2& sees) {
+  const int lane = threadIdx.x & 31, per = a.nt * (a.pair_keys ? 1 : 2), t0 = tile * per, t1 = min(t0 + per, a.T);
+  int k0 = 0, n = 1, lo = INT_MAX, hi = -1;
+  bool holes = false;
   if constexpr (FP8) {
     bool bad;
     n = (rows_held(a, b, &bad) + kKeys - 1) / kKeys;
     if (bad && lane == 0) record_status(a.status, kStatusBadInput);
+    for (int t = t0 + lane; t < t1; t += 32) hi = max(hi, __ldg(a.q_pos + (int64_t)(b / a.H_kv) * a.T + t));
+    hi = __reduce_max_sync(0xffffffffu, hi);
   } else {
-    const int per = a.nt * (a.pair_keys ? 1 : 2), t0 = tile * per, t1 = min(t0 + per, a.T);
-    int lo = INT_MAX, hi = -1;
     for (int t = t0 + lane; t < t1; t += 32) {
-      int l, h;
-      if (key_range(a, (int64_t)b * a.T + t, l, h)) lo = min(lo, l), hi = max(hi, h);
+      int l, h, l1 = 0, h1 = -1;
+      const bool some = key_range(a, (int64_t)b * a.T + t, l, h);
+      const bool next = t + 1 < a.T && key_range(a, (int64_t)b * a.T + t + 1, l1, h1);
+      if (some) lo = min(lo, l), hi = max(hi, h);
+      holes |= next && (!some || l1 > h + 1 || l > h1 + 1);
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
+    holes = __any_sync(0xffffffffu, holes);
     if (lo <= hi) k0 = lo / kKeys, n = hi / kKeys - k0 + 1;
   }
+  sees = make_int2(holes ? -1 : lo, hi);
   // a unit that sees nothing takes a step all the same, which writes its zeros
   if (a.pair_keys) n = (n + 1) / 2;
   return make_int2(k0, max(n, 1));
+}
+// The same of a whole sequence, from its units', a warp each.
+__device__ __forceinline__ void join_sees(const Args& a, const int2* sees, int2* seen) {
+  const int lane = threadIdx.x & 31;
+  for (int b = threadIdx.x >> 5; b < a.B1; b += blockDim.x >> 5) {
+    int lo = INT_MAX, hi = -1;
+    for (int t = lane; t < a.tiles; t += 32) {
+      const int2 x = sees[(int64_t)b * a.tiles + t];
+      lo = min(lo, x.x), hi = max(hi, x.y);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) seen[b] = make_int2(lo, hi);
+  }
 }
 // The steps of many units, a warp each (few: the next kernel counts them itself).
 template <bool FP8>
@@ -150,8 +172,9 @@ __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ Args
   grid_dep_launch();
   const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= a.B1 * a.tiles) return;
-  const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles);
-  if ((threadIdx.x & 31) == 0) a.units[i] = u;
+  int2 sees;
+  const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles, sees);
+  if ((threadIdx.x & 31) == 0) a.units[i] = u, a.sees[i] = sees;
 }
 // Where the range that begins with step f does.
 __device__ __forceinline__ Start find_start(const Args& a, long long f, long long total, const long long* before,
@@ -189,8 +212,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
   grid_dep_launch();
   if (!counted) {
     for (int i = warp; i < N; i += 32) {
-      const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles);
-      if (lane == 0) a.units[i] = s_units[i] = u;
+      int2 sees;
+      const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles, sees);
+      if (lane == 0) a.units[i] = s_units[i] = u, a.sees[i] = sees;
     }
   } else if (here) {
     for (int i = threadIdx.x; i < N; i += 1024) s_units[i] = a.units[i];
@@ -198,6 +222,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const __grid_constant__ Args
   const int2* const units = here ? s_units : a.units;
   if (threadIdx.x == 0) s_run = 0;
   __syncthreads();
+  join_sees(a, a.sees, a.seen);
   for (int i0 = 0; i0 < N; i0 += 1024) {
     const int i = i0 + threadIdx.x;
     const long long n = i < N ? units[i].y : 0;
@@ -236,34 +261,40 @@ struct Seg {
 };
 // Few units: every CTA counts all of them and finds its own range, a launch less
 // (8 units of a single token over 8K: 18.5 -> 17.2 us).
-constexpr int kPlanHere = 38;
+constexpr int kPlanHere = 34;
 struct Here {
   Start start;
   Plan plan;
+  int2 units[kPlanHere], seen[kPlanHere];
+};
+struct Scratch {                     // where the ring will be
   long long before[kPlanHere + 1];
-  int2 units[kPlanHere];
+  int2 sees[kPlanHere];
 };
 template <bool FP8>
-__device__ __forceinline__ void plan_here(const Args& a, Here& here) {
+__device__ __forceinline__ void plan_here(const Args& a, Here& here, Scratch& tmp) {
   const int N = a.B1 * a.tiles, lane = threadIdx.x & 31;
   for (int i = threadIdx.x >> 5; i < N; i += blockDim.x >> 5) {
-    const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles);
-    if (lane == 0) here.units[i] = u;
+    int2 sees;
+    const int2 u = unit_steps<FP8>(a, i / a.tiles, i % a.tiles, sees);
+    if (lane == 0) here.units[i] = u, tmp.sees[i] = sees;
   }
   __syncthreads();
+  join_sees(a, tmp.sees, here.seen);
   if (threadIdx.x == 0) {
     long long run = 0;
     for (int i = 0; i < N; ++i) {
-      here.before[i] = run;
+      tmp.before[i] = run;
       run += here.units[i].y;
     }
-    here.before[N] = run;
+    tmp.before[N] = run;
     const long long total = run * a.H1, L = (total + a.P - 1) / a.P;
     here.plan = {total, L};
-    here.start = find_start(a, blockIdx.x * L, total, here.before, here.units);
+    here.start = find_start(a, blockIdx.x * L, total, tmp.before, here.units);
     a.start[blockIdx.x] = here.start;  // for the join
     if (blockIdx.x == 0) *a.plan = here.plan;
   }
+  tc::fence_proxy_async();           // the copies write there next
   __syncthreads();
 }
 
@@ -273,11 +304,12 @@ struct Walk {
   Seg g;
   long long left;
   int2 ahead;
-  const int2* units;
+  const int2 *units, *seen;
   __device__ __forceinline__ bool begin(const Args& a, const Here& here) {
     const Start st = a.planned ? a.start[blockIdx.x] : here.start;
     const Plan p = a.planned ? *a.plan : here.plan;
     units = a.planned ? a.units : here.units;
+    seen = a.planned ? a.seen : here.seen;
     if (st.b < 0) return false;
     left = min(p.L, p.total - (long long)blockIdx.x * p.L);
     g.b = st.b, g.h = st.h, g.tile = st.tile;
@@ -342,9 +374,10 @@ struct Cfg {
 //   q_full(i + 1)          q_empty(i) (bf16), committed behind products after q_full(i); or
 //                          s_end(i) (e4m3: the rows' own warps write the queries)
 //   turn(i + 1)            the other stream's warp issues in between, after a look at turn(i)
-//   meta_full(i + kMeta)   see Meta
+//   meta_full(i + kMeta)   meta_empty(i) of every warp that reads the tile's, after meta_full(i)
+//   meta_empty(i + kMeta)  meta_full(i + kMeta), written after a look at meta_empty(i)
 struct Bars {
-  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], s_end[2], p_full[2], q_full, q_empty, meta_full[kMeta], turn[2], drain[2];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], s_full[2], s_end[2], p_full[2], q_full, q_empty, meta_full[kMeta], meta_empty[kMeta], turn[2], drain[2];
 };
 
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint32_t limit) {
@@ -491,55 +524,18 @@ __device__ __forceinline__ void load_tile(const Args& a, const Seg& g, bool vals
   }
 }
 
-// A warp: lane 0 copies; with the 8-bit cache all lanes fetch positions and scales.
+// The warp that copies (lane 0).
 template <int D, bool FP8>
-__device__ bool load_warp(const Args& a, const Here& here, Bars* bars, uint32_t sQ, uint32_t ring, Meta* meta) {
+__device__ bool load_warp(const Args& a, const Here& here, Bars* bars, uint32_t sQ, uint32_t ring) {
   using C = Cfg<D, FP8>;
   const int lane = threadIdx.x & 31;
   const int subs = a.pair_keys ? 2 : 1;           // key tiles of a step
-  uint32_t it = 0, mt = 0, nq = 0;               // tiles, tiles of keys, queries asked for
+  uint32_t it = 0, nq = 0;                       // tiles, queries asked for
   bool ok = true;
   Walk w;
   if (!w.begin(a, here)) return true;
   do {
     const Seg& g = w.g;
-    int q_hi = -1, q_lo = INT_MAX;
-    int n_rows = 0, b = 0, h = 0;
-    if constexpr (FP8) {
-      bool bad;
-      n_rows = rows_held(a, g.b, &bad);
-      b = g.b / a.H_kv, h = g.b - b * a.H_kv;
-      const int per = a.nt * (a.pair_keys ? 1 : 2), t0 = g.tile * per, t1 = min(t0 + per, a.T);
-      for (int t = t0 + lane; t < t1; t += 32) {
-        const int p = __ldg(a.q_pos + (int64_t)b * a.T + t);
-        q_lo = min(q_lo, p), q_hi = max(q_hi, p);
-      }
-      q_lo = __reduce_min_sync(0xffffffffu, q_lo);
-      q_hi = __reduce_max_sync(0xffffffffu, q_hi);
-    }
-    // positions and scales of the next tiles (which go downward), on their way: asked for
-    // when a tile's turn comes, they held every tile up by two trips to memory
-    constexpr int kAhead = FP8 ? 3 : 1;
-    struct Rows { int pos[4]; float2 scale; };
-    Rows ahead[kAhead];
-    const int64_t row0 = FP8 ? (int64_t)b * a.s.off[a.H_kv] + a.s.off[h] : 0;
-    const int t_end = g.last(subs) - g.cnt * subs;             // the tile behind the segment's last
-    const auto fetch = [&](int t) {
-      Rows r;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = t * kKeys + x * 32 + lane;
-        r.pos[x] = t > t_end && row < n_rows ? __ldg(a.pos + row0 + row) : -1;
-      }
-      r.scale = make_float2(1.f, kLeastUnit);
-      const int block = t * (kKeys / q8::kRows) + lane;
-      if (t > t_end && lane < kKeys / q8::kRows && block * q8::kRows < n_rows)
-        r.scale = __ldg(a.scale + row0 / q8::kRows + block);
-      return r;
-    };
-    if constexpr (FP8)
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) ahead[x] = fetch(g.last(subs) - x);
     bool wants_q = !FP8;               // the segment's queries are not asked for yet
     const auto ask_q = [&] {
       ++nq;
@@ -569,31 +565,6 @@ __device__ bool load_warp(const Args& a, const Here& here, Bars* bars, uint32_t 
       if (lane == 0) load_tile<D, FP8>(a, g, vals, t, ring + st * C::kStageBytes, smem_u32(&bars->kv_full[st]));
       __syncwarp();
       ++it;
-      if constexpr (FP8) {
-        if (!vals) {                 // the tile's positions and scales
-          Meta& m = meta[mt % kMeta];
-          const Rows r = ahead[0];
-#pragma unroll
-          for (int x = 0; x + 1 < kAhead; ++x) ahead[x] = ahead[x + 1];
-          ahead[kAhead - 1] = fetch(t - kAhead);
-          uint32_t seen = 0;         // lane y: of block y
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int p = r.pos[x];
-            m.pos[x * 32 + lane] = p;
-            m.rel[x * 32 + lane] = (float)(int)((uint32_t)p - (uint32_t)q_hi);
-            const uint32_t some = __ballot_sync(0xffffffffu, p >= 0 && p <= q_hi);
-            const bool all = __all_sync(0xffffffffu, p >= 0 && p <= q_lo);
-            if (lane == 0) m.some[x] = some, m.mixed[x] = all ? 0 : 1;
-            if (lane >> 1 == x) seen = some >> (lane & 1) * 16 & 0xffffu;
-          }
-          if (lane < kKeys / q8::kRows)          // a block of which nothing is seen may have anything for a scale
-            m.scale[lane] = seen ? r.scale : make_float2(1.f, kLeastUnit);
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(smem_u32(&bars->meta_full[mt % kMeta]));
-          ++mt;
-        }
-      }
     };
     // in the order of the products
     const int t1 = g.last(subs);
@@ -616,23 +587,96 @@ __device__ bool load_warp(const Args& a, const Here& here, Bars* bars, uint32_t 
   return ok;
 }
 
+// 8-bit cache: the warp that brings in a tile's positions and scales, and what the
+// queries see of them.  A warp of its own: beside the copies it took as long as the
+// products of a pair of tiles.
+template <bool BIAS>
+__device__ bool meta_warp(const Args& a, const Here& here, Bars* bars, Meta* meta) {
+  const int lane = threadIdx.x & 31, subs = a.pair_keys ? 2 : 1;
+  uint32_t mt = 0;
+  bool ok = true;
+  Walk w;
+  if (!w.begin(a, here)) return true;
+  do {
+    const Seg& g = w.g;
+    bool bad;
+    const int n_rows = rows_held(a, g.b, &bad), b = g.b / a.H_kv, h = g.b - b * a.H_kv;
+    const int per = a.nt * (a.pair_keys ? 1 : 2), tk0 = g.tile * per, tk1 = min(tk0 + per, a.T);
+    const int q_seen = w.seen[g.b].y;
+    int q_hi = -1, q_lo = INT_MAX;
+    for (int t = tk0 + lane; t < tk1; t += 32) {
+      const int p = __ldg(a.q_pos + (int64_t)b * a.T + t);
+      q_lo = min(q_lo, p), q_hi = max(q_hi, p);
+    }
+    q_lo = __reduce_min_sync(0xffffffffu, q_lo);
+    q_hi = __reduce_max_sync(0xffffffffu, q_hi);
+    // the next tiles' are on their way
+    constexpr int kAhead = 3;
+    struct Rows { int pos[4]; float2 scale; };
+    Rows ahead[kAhead];
+    const int64_t row0 = (int64_t)b * a.s.off[a.H_kv] + a.s.off[h];
+    const int t1 = g.last(subs), t_end = t1 - g.cnt * subs;    // the tiles go downward
+    const auto fetch = [&](int t) {
+      Rows r;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = t * kKeys + x * 32 + lane;
+        r.pos[x] = t > t_end && row < n_rows ? __ldg(a.pos + row0 + row) : -1;
+      }
+      r.scale = make_float2(1.f, kLeastUnit);
+      const int block = t * (kKeys / q8::kRows) + lane;
+      if (t > t_end && lane < kKeys / q8::kRows && block * q8::kRows < n_rows)
+        r.scale = __ldg(a.scale + row0 / q8::kRows + block);
+      return r;
+    };
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) ahead[x] = fetch(t1 - x);
+    for (int t = t1; t > t_end; --t, ++mt) {
+      const Rows r = ahead[0];
+#pragma unroll
+      for (int x = 0; x + 1 < kAhead; ++x) ahead[x] = ahead[x + 1];
+      ahead[kAhead - 1] = fetch(t - kAhead);
+      ok = poll(smem_u32(&bars->meta_empty[mt % kMeta]), ((mt / kMeta) & 1) ^ 1, a.wait_limit);
+      if (!ok) return false;
+      Meta& m = meta[mt % kMeta];
+      uint32_t seen = 0;             // lane y: of block y
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int p = r.pos[x];
+        m.pos[x * 32 + lane] = p;
+        if constexpr (BIAS) m.rel[x * 32 + lane] = (float)(int)((uint32_t)p - (uint32_t)q_hi);
+        const uint32_t some = __ballot_sync(0xffffffffu, p >= 0 && p <= q_seen);
+        const bool all = __all_sync(0xffffffffu, p >= 0 && p <= q_lo);
+        if (lane == 0) m.some[x] = some, m.mixed[x] = all ? 0 : 1;
+        if (lane >> 1 == x) seen = some >> (lane & 1) * 16 & 0xffffu;
+      }
+      if (lane < kKeys / q8::kRows)  // a block of which nothing is seen may have anything for a scale
+        m.scale[lane] = seen ? r.scale : make_float2(1.f, kLeastUnit);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(smem_u32(&bars->meta_full[mt % kMeta]));
+    }
+  } while (w.next(a));
+  return ok;
+}
+
 // ------------------------------------------------------------------- the products
 // Rows of a stage whose bit is not set become zeros: what no query of the unit sees
 // may hold anything, and a weight of zero times NaN would not be zero.
 template <int D, bool FP8>
 __device__ __forceinline__ void zero_rows(uint32_t stage, uint32_t keep, int word) {
   constexpr int kRow = FP8 && D == 64 ? 64 : 128, kPanels = FP8 || D == 64 ? 1 : 2;
-  const int lane = threadIdx.x & 31;
-  if (!(keep >> lane & 1)) {
+  constexpr int kAtOnce = 512 / kRow;              // rows of a store of the warp
+  const int lane = threadIdx.x & 31, row = lane / (kRow / 16);
 #pragma unroll
-    for (int p = 0; p < kPanels; ++p)
+  for (int y = 0; y < 32; y += kAtOnce)
+    if (!(keep >> (y + row) & 1)) {
 #pragma unroll
-      for (int c = 0; c < kRow / 16; ++c)
+      for (int p = 0; p < kPanels; ++p)
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(stage + p * (kKeys * 128) +
-                                                                        (word * 32 + lane) * kRow + c * 16),
+                                                                        (word * 32 + y) * kRow + lane * 16),
                      "r"(0)
                      : "memory");
-  }
+    }
 }
 
 template <int D>
@@ -699,13 +743,11 @@ __device__ bool mma_warp(const Args& a, const Here& here, Bars* bars, int x, uin
   if (w.begin(a, here)) do {
     const Seg& g = w.g;
     const int t1 = g.last(subs);
-    // What the unit's queries see between them: as a rule one range, each token's touching
-    // the next one's (whole: no holes; tokens that see nothing only behind the others).
-    int lo = INT_MAX, hi = -1;
-    bool holes = false;
-    const int per = a.nt * (a.pair_keys ? 1 : 2), tk0 = g.tile * per, tk1 = min(tk0 + per, a.T);
-    // rows of tile `t` that no query of the unit sees become zeros (both streams' warps
-    // may write the same ones)
+    const int2 seen = w.seen[g.b];
+    // Rows of tile `t` that no query of the call sees become zeros (both streams' warps may
+    // write the same ones).  Only those may hold anything: where the sequence's queries
+    // see one range between them (no holes), tiles within need no look; else what no query
+    // of the unit sees does.
     const auto clean = [&](int t, uint32_t m, uint32_t stage) {
       uint32_t keep[4] = {};
       const int k = t * kKeys;
@@ -720,10 +762,11 @@ __device__ bool mma_warp(const Args& a, const Here& here, Bars* bars, int x, uin
         ok = ok && wait(&bars->meta_full[m % kMeta], m / kMeta);
 #pragma unroll
         for (int y = 0; y < 4; ++y) keep[y] = meta[m % kMeta].some[y];
-      } else if (!holes) {
-        if (lo <= k && hi >= k + kKeys - 1) return;
-        add(lo, hi);
+      } else if (seen.x >= 0) {
+        if (seen.x <= k && seen.y >= k + kKeys - 1) return;
+        add(seen.x, seen.y);
       } else {
+        const int per = a.nt * (a.pair_keys ? 1 : 2), tk0 = g.tile * per, tk1 = min(tk0 + per, a.T);
         for (int tk = tk0 + lane; tk < tk1; tk += 32) {
           int l, h;
           if (key_range(a, (int64_t)g.b * a.T + tk, l, h)) add(l, h);
@@ -748,6 +791,7 @@ __device__ bool mma_warp(const Args& a, const Here& here, Bars* bars, int x, uin
         if (!ok) break;
         const int sub = a.pair_keys ? 2 * (i - 1) + x : i - 1;
         clean(t1 - sub, mt + sub, ring + v_st * C::kStageBytes);
+        if (FP8 && lane == 0) tc::mbar_arrive(smem_u32(&bars->meta_empty[(mt + sub) % kMeta]));
       }
       if (i < g.cnt) ok = ok && wait(&bars->kv_full[k_st], k_it / C::kStages);
       ok = ok && wait(&bars->turn[x], x == 0 ? turns - 1 : turns);
@@ -769,19 +813,6 @@ __device__ bool mma_warp(const Args& a, const Here& here, Bars* bars, int x, uin
         tc::mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
       }
       __syncwarp();
-      // behind the first scores, which need not wait for it
-      if (!FP8 && i == 0) {
-        for (int tk = tk0 + lane; tk < tk1; tk += 32) {
-          int l, h, l1 = 0, h1 = -1;
-          const bool some = key_range(a, (int64_t)g.b * a.T + tk, l, h);
-          const bool next = tk + 1 < tk1 && key_range(a, (int64_t)g.b * a.T + tk + 1, l1, h1);
-          if (some) lo = min(lo, l), hi = max(hi, h);
-          holes |= next && (!some || l1 > h + 1 || l > h1 + 1);
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        holes = __any_sync(0xffffffffu, holes);
-      }
     }
     it += g.cnt * 2 * subs;
     mt += g.cnt * subs;
@@ -1116,6 +1147,7 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(smem_u32(&bars->p_full[x]));
+      if (FP8 && lane == 0) tc::mbar_arrive(smem_u32(&bars->meta_empty[m_at % kMeta]));
     }
     // ---- the segment's end: the threads of a row tell each other their sums (and, key
     // pairs, the streams' references), and share out its dims
@@ -1195,7 +1227,7 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
 template <int D, bool FP8, bool CAP, bool BIAS>
 __device__ __forceinline__ void attend(const Args& a) {
   using C = Cfg<D, FP8>;
-  static_assert(C::kStages <= kMaxStages && (!FP8 || C::kStages <= 9), "see Meta");
+  static_assert(C::kStages <= kMaxStages, "barriers of the ring");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // a whole number of 1024 bytes, so that what follows is aligned without a gap: at
   // D = 128 the two fill a CTA's 227 KB
@@ -1228,7 +1260,10 @@ __device__ __forceinline__ void attend(const Args& a) {
       tc::mbar_init(smem_u32(&bars.s_end[i]), 1);
       tc::mbar_init(smem_u32(&bars.p_full[i]), 8);
     }
-    for (int i = 0; i < kMeta; ++i) tc::mbar_init(smem_u32(&bars.meta_full[i]), 1);
+    for (int i = 0; i < kMeta; ++i) {
+      tc::mbar_init(smem_u32(&bars.meta_full[i]), 1);
+      tc::mbar_init(smem_u32(&bars.meta_empty[i]), a.pair_keys ? 9 : 18);      // eight warps of weights and an issuer a stream
+    }
     tc::mbar_init(smem_u32(&bars.q_full), FP8 ? (a.pair_keys ? 4 : 8) : 1);
     tc::mbar_init(smem_u32(&bars.q_empty), 2);
     for (int i = 0; i < 2; ++i) {
@@ -1251,14 +1286,15 @@ __device__ __forceinline__ void attend(const Args& a) {
   grid_dep_wait();
   grid_dep_launch();
   Here& here = small.here;
-  if (!a.planned) plan_here<FP8>(a, here);
+  if (!a.planned) plan_here<FP8>(a, here, *reinterpret_cast<Scratch*>(base));
   bool ok = true;
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     ok = soft_warps<D, FP8, CAP, BIAS>(a, here, &bars, small.max, sQ, meta, tmem, s_x);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp) ok = load_warp<D, FP8>(a, here, &bars, sQ, ring, meta);
+    if (warp == kLoadWarp) ok = load_warp<D, FP8>(a, here, &bars, sQ, ring);
+    else if (FP8 && warp == kMetaWarp) ok = meta_warp<BIAS>(a, here, &bars, meta);
     else if (warp < kLoadWarp) ok = mma_warp<D, FP8>(a, here, &bars, warp - kMmaWarp, sQ, ring, meta, tmem);
   }
   if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, kStatusTimeout);
@@ -1330,7 +1366,7 @@ __global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const __grid_const
 // How a call's query rows are laid out, and its scratch.
 struct Layout {
   int nt, tiles, pair_keys, P;
-  size_t off_units, off_before, off_start, off_ml, off_o, total;
+  size_t off_units, off_sees, off_seen, off_before, off_start, off_ml, off_o, total;
 };
 inline Layout layout(int64_t B1, int T, int G, int D) {
   Layout l{};
@@ -1342,7 +1378,9 @@ inline Layout layout(int64_t B1, int T, int G, int D) {
   l.tiles = (T + per - 1) / per;
   const size_t units = (size_t)B1 * l.tiles, rows = (size_t)2 * l.P * kRows * (l.pair_keys ? 1 : 2);
   l.off_units = 256;
-  l.off_before = up(l.off_units + units * sizeof(int2));
+  l.off_sees = up(l.off_units + units * sizeof(int2));
+  l.off_seen = up(l.off_sees + units * sizeof(int2));
+  l.off_before = up(l.off_seen + (size_t)B1 * sizeof(int2));
   l.off_start = up(l.off_before + (units + 1) * sizeof(long long));
   l.off_ml = up(l.off_start + (size_t)(l.P + 1) * sizeof(Start));
   l.off_o = up(l.off_ml + rows * sizeof(float2));
@@ -1353,6 +1391,8 @@ inline void place(Args& a, const Layout& l, void* ws) {
   char* w = static_cast<char*>(ws);
   a.plan = reinterpret_cast<Plan*>(w);
   a.units = reinterpret_cast<int2*>(w + l.off_units);
+  a.sees = reinterpret_cast<int2*>(w + l.off_sees);
+  a.seen = reinterpret_cast<int2*>(w + l.off_seen);
   a.before = reinterpret_cast<long long*>(w + l.off_before);
   a.start = reinterpret_cast<Start*>(w + l.off_start);
   a.part_ml = reinterpret_cast<float2*>(w + l.off_ml);
