@@ -43,14 +43,14 @@ def seen(qp, first, last, S):
     return (j >= lo[..., None]) & (j <= hi[..., None]) & (qp >= 0)[..., None]
 
 
-def verify(q, k, v, qp, first, last, S, cap, slopes, out, lse, heads=None):
+def verify(q, k, v, qp, first, last, S, cap, slopes, out, lse, heads=None, batches=None):
     B, Hq, T, D = q.shape
     H = k.shape[1]
     see = seen(qp, first, last, S)
     far = np.abs(qp.cpu().numpy()[..., None].astype(np.int64) - np.arange(S))
     qn, kn, vn, on, ln = f64(q), f64(k), f64(v), f64(out), f64(lse)
     sl = np.zeros(Hq) if slopes is None else f64(slopes)
-    for b in range(B):
+    for b in batches if batches is not None else range(B):
         for hq in heads if heads is not None else range(Hq):
             h = hq // (Hq // H)
             check(qn[b, hq], kn[b, h], vn[b, h], see[b], far[b], cap, sl[hq], on[b, hq], ln[b, hq], 2.0 ** -8, 0.0, 0.0,
@@ -147,14 +147,19 @@ def test_many_parts(K, T):
            out[:, :, pick].contiguous(), lse[:, :, pick].contiguous(), heads=[0, 3, 5])
 
 
-def test_many_units(K):
-    """More units than the planning kernel counts itself, and than ranges."""
-    B, T, Hq, H, S, D = 40, 150, 6, 2, 260, 64
+@pytest.mark.parametrize("B,T", [(12, 40), (20, 250), (150, 250), (1100, 250)])
+def test_many_units(K, B, T):
+    """Few units, which every CTA plans; more; more than the planning kernel counts itself; more than
+    its shared memory holds.  And more than ranges, in each."""
+    Hq, H, S, D = 6, 2, 260, 64
     q, k, v = rnd(14, B, Hq, T, D), rnd(15, B, H, S, D), rnd(16, B, H, S, D)
     qp = i32(np.random.default_rng(0).integers(-40, 110, (B, 1)) + np.arange(T)[None])
     out, lse = run(K, q, k, v, qp, None, None, S)
     K.kvc_check_status()
-    verify(q, k, v, qp, None, None, S, 0.0, None, out, lse, heads=[1, 4])
+    pick = sorted({0, 1, B // 2, B - 2, B - 1})
+    at = [x[pick].contiguous() for x in (q, k, v, qp, out, lse)]
+    verify(*at[:4], None, None, S, 0.0, None, *at[4:], heads=[1, 4])
+    assert torch.isfinite(out).all()
 
 
 def test_scores_that_grow(K):
@@ -235,6 +240,46 @@ def test_captured(K):
         want2, _ = run(K, q2, k, v, qp, first, None, S)
         assert torch.equal(out, want) and torch.equal(two, want2)
         verify(q, k, v, qp, first, None, S, 0.0, None, want, lse, heads=[0, 7])
+
+
+def test_offsets_past_32_bits(K):
+    """Buffers of 2^32 elements and more: the last head's keys, and queries at the far end of a sequence."""
+    B, T, Hq, H, S, D = 1, 3, 3, 3, 12 << 20, 128
+    k, v = (torch.zeros((B, H, S, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, tail = rnd(50, B, Hq, T, D, scale=2.0), 300
+    k[0, :, S - tail:], v[0, :, S - tail:] = rnd(51, H, tail, D), rnd(52, H, tail, D)
+    qp, first = i32([[S - 3, S - 2, S - 1]]), i32([[S - 200, S - 290, S - 1]])
+    out, lse = run(K, q, k, v, qp, first, None, S)
+    K.kvc_check_status()
+    at = S - tail
+    verify(q, k[:, :, at:], v[:, :, at:], qp - at, first - at, None, tail, 0.0, None, out, lse)
+
+
+@pytest.mark.parametrize("mask", ["first", "last"])
+def test_steep_and_negative_slopes(K, mask):
+    """Slopes from 2^-20 to 8, and negative ones, which favour far keys; keys ahead of the query."""
+    B, T, Hq, H, S, D = 1, 70, 8, 2, 1500, 64
+    q, k, v = rnd(53, B, Hq, T, D), rnd(54, B, H, S, D), rnd(55, B, H, S, D)
+    qp = i32(np.arange(800, 800 + T)[None])
+    first, last = (i32(np.arange(300, 300 + T)[None]), None) if mask == "first" else (None, i32(np.full((B, T), 1400)))
+    sl = torch.tensor([2.0 ** -20, 2.0 ** -10, 0.01, 0.5, 2.0, 8.0, 0.0, -0.02], device="cuda")
+    out, lse = run(K, q, k, v, qp, first, last, S, 0.0, sl)
+    K.kvc_check_status()
+    verify(q, k, v, qp, first, last, S, 0.0, sl, out, lse)
+
+
+@pytest.mark.parametrize("level", [-3000.0, -100.0, 100.0, 3000.0])
+def test_scores_of_every_level(K, level):
+    """Rows whose scores all lie far from the last row's: the reference that a segment starts from is
+    another row's, and has to move either way; many segments a range."""
+    B, T, Hq, H, S, D = 6, 200, 4, 2, 200, 64
+    q, k, v = rnd(56, B, Hq, T, D), rnd(57, B, H, S, D), rnd(58, B, H, S, D)
+    q[..., 0] = 8.0
+    k[..., 0] = torch.where(torch.arange(B, device="cuda") % 2 == 0, level, -level)[:, None, None].to(torch.bfloat16)
+    qp = i32(np.arange(T)[None].repeat(B, 0))
+    out, lse = run(K, q, k, v, qp, None, None, S)
+    K.kvc_check_status()
+    verify(q, k, v, qp, None, None, S, 0.0, None, out, lse, heads=[0, 3])
 
 
 def test_a_wait_that_gives_up(K):

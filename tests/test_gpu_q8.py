@@ -6,7 +6,10 @@ roundings of the two forms: up to 8 query rows per KV head fp16 (w = 2^-11; weig
 below fp16's normal numbers half a step, 2^-25, where the largest is at least 2^4 less the
 values' scales, which the blocks of normal values here leave within 2^4 of one
 another: floor = 2^-25; queries 2^-24 of the row's largest), more rows two e4m3
-parts (w = 2^-8, floor = 2^-16, by the same scales 2^-12; queries 2^-17)."""
+parts (w = 2^-8: the first is cut to 4 significant bits, the rest, at most 2^-3 of the
+weight, is rounded to 4 of its own, half a step of which is 2^-8 of the weight's binade;
+floor: half of e4m3's smallest step, 2^-10, where the row's largest weight is at least
+2^5, so 2^-15, and by the same scales 2^-11; queries 2^-17)."""
 
 import math
 
@@ -281,7 +284,7 @@ def verify(K, q, c, rows, extra, qp, H, so, cap, slopes, out, lse, heads=None):
             p = K_pos[b, so[h]:so[h] + n].astype(np.int64)
             see = (p >= 0) & (p <= qp[b][:, None])
             check(qn[b, hq], kk[b, so[h]:so[h] + n], vv[b, so[h]:so[h] + n], see, qp[b][:, None].astype(np.int64) - p,
-                  cap, sl[hq], on[b, hq], ln[b, hq], 2.0 ** -11 if few else 2.0 ** -8, 2.0 ** -25 if few else 2.0 ** -12,
+                  cap, sl[hq], on[b, hq], ln[b, hq], 2.0 ** -11 if few else 2.0 ** -8, 2.0 ** -25 if few else 2.0 ** -11,
                   2.0 ** -24 if few else 2.0 ** -17, (b, hq))
 
 
@@ -364,9 +367,9 @@ def test_scales_far_apart(K, T):
         for hq in range(Hq):
             h = hq // 4
             sl = slice(so[h], so[h + 1])
-            # floor: 2^-25 or 2^-16 of the largest weight times the largest scale, which vmax stands for
+            # floor: 2^-25 or 2^-15 of the largest weight times the largest scale, which vmax stands for
             check(f64(q)[0, hq], kk[0, sl], vv[0, sl], np.ones((T, N), bool), None, 0.0, 0.0, f64(out)[0, hq],
-                  f64(lse)[0, hq], 2.0 ** -11 if few else 2.0 ** -8, 2.0 ** -25 if few else 2.0 ** -16,
+                  f64(lse)[0, hq], 2.0 ** -11 if few else 2.0 ** -8, 2.0 ** -25 if few else 2.0 ** -15,
                   2.0 ** -24 if few else 2.0 ** -17, hq)
 
 
@@ -461,6 +464,59 @@ def test_two_streams_at_once(K, T):
             K.kvc_attention_q8(qs[i], *c, rows, 0, qp, B, T, Hq, H, D, so, 0.0, None, got[i], None, ws[i], stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_offsets_past_32_bits(K, T):
+    """A slot of 2^25 rows, 8.6 GB: append and both forms of the attention at its far end."""
+    D, cap, Hq = 128, 1 << 25, 4
+    so = [0, cap]
+    c = (torch.zeros((cap, D), dtype=torch.uint8, device="cuda"), torch.zeros((cap, D), dtype=torch.uint8, device="cuda"),
+         torch.ones((cap // 16, 2), device="cuda"), torch.full((cap,), -1, dtype=torch.int32, device="cuda"))
+    k, v, q = rnd(1, 1, 1, 40, D), rnd(2, 1, 1, 40, D), rnd(3, 1, Hq, T, D)
+    rows, qp = i32([[cap - 43]]), i32([30 + np.arange(T)])
+    K.kvc_append_q8(k, v, i32([np.arange(40)]), 1, 1, 40, D, so, rows, *c)
+    out, lse = attend(K, q, c, rows, 43, qp, 1, so)
+    K.kvc_check_status()
+    n = 48                                                        # the slot's last rows, as a cache of their own
+    tail = tuple(t[cap - n:].contiguous() for t in c[:2]) + (c[2][-n // 16:].contiguous(), c[3][cap - n:].contiguous())
+    few = T == 1
+    kk, vv = read_all(K, tail, 1, 1, D, [0, n])
+    p = tail[3].cpu().numpy().astype(np.int64)
+    see = (p >= 0) & (p <= qp.cpu().numpy()[0][:, None])
+    for hq in range(Hq):
+        check(f64(q)[0, hq], kk[0], vv[0], see, None, 0.0, 0.0, f64(out)[0, hq], f64(lse)[0, hq],
+              2.0 ** -11 if few else 2.0 ** -8, 2.0 ** -25 if few else 2.0 ** -11, 2.0 ** -24 if few else 2.0 ** -17, hq)
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_neighbours_may_hold_anything(K, T):
+    """Rows of other sequences' slots, of unheld blocks and of tokens that come later in the call are
+    NaN codes with NaN and infinite scales; slots without rows; uneven sequences."""
+    B, Hq, H, D = 3, 8, 2, 64
+    so = [0, 160, 176]
+    c = empty_cache(K, B, D, so)
+    c[2][::3] = float("inf")
+    c[3].fill_(5)                                                 # stale positions
+    n = np.array([[130, 0], [0, 16], [7, 3]])
+    k, v = rnd(70, B, H, 160, D), rnd(71, B, H, 160, D)
+    for b in range(B):
+        for h in range(H):
+            m = int(n[b, h])
+            if not m:
+                continue
+            part = tuple(t.view(B, -1, *t.shape[1:])[b] for t in c)
+            sub = tuple(t.contiguous() for t in part)
+            K.kvc_append_q8(k[b:b + 1, :, :m].contiguous(), v[b:b + 1, :, :m].contiguous(), i32([np.arange(m)]), 1, H, m,
+                            D, so, i32([[0 if x == h else 1 << 20 for x in range(H)]]), *sub)
+            with pytest.raises(K.KvcError):                       # the other head has no room: left as it was
+                K.kvc_check_status()
+            for t, x in zip(part, sub):
+                t.copy_(x)
+    q, qp = rnd(72, B, Hq, T, D), i32(np.sort(np.random.default_rng(5).integers(0, 140, (B, T)), 1))
+    out, lse = attend(K, q, c, i32(n), 0, qp, H, so)
+    K.kvc_check_status()
+    verify(K, q, c, i32(n), 0, qp, H, so, 0.0, None, out, lse)
 
 
 def test_a_wait_that_gives_up(K):
