@@ -27,6 +27,12 @@
 // every SM's CTA an equal range, whatever the masks and lengths.  Units that a
 // range's end cuts leave partial results, which a third kernel joins in order.
 //
+// Measured (D = 128, 32/8 heads): 2048 tokens over 32K behind a prefix 760 us (1416
+// TFLOP/s; the products alone, without weights, 575), over 8K 190, with a bias 215,
+// with a cap 260; one token over 8K 16.5, of 16 sequences 86.8 (6.2 TB/s); 512 tokens over
+// 4.8K rows of the 8-bit cache 102.  A tile's chain bounds it: weights 1300 to 1570
+// cycles, products 920, hand-overs 750 to 1000.
+//
 // e4m3 keys and values (the 8-bit cache): the products take e4m3 operands.  A query
 // row is scaled by a power of two to below 2^8 and split into two e4m3 parts, four
 // significant bits each, so that all of a bf16's eight are there; weights are split

@@ -3,10 +3,12 @@
 //   scale = 2^ceil(log2(max |x| / 448)),  code = e4m3(x / scale)   per block of 16 rows
 //
 // A warp takes the keys or the values of one block of 16 rows and has them in
-// registers whole (D / 4 words a lane... 16 D values), so the block's maximum is
-// one warp reduction and every byte moves once.  D / 16 lanes share a row, 32
-// bytes of bf16 and 16 bytes of codes each: loads and stores of whole sectors.
-// The scattered rows of 2 D bytes bound a gather, latency an append.
+// registers whole (D / 2 values a lane), so the block's maximum is one warp
+// reduction and every byte moves once.  D / 16 lanes share a row, 32 bytes of bf16
+// and 16 bytes of codes each: loads and stores of whole sectors.
+// The scattered rows of 2 D bytes bound a gather, latency an append.  Measured at 315K
+// of 1M rows of 128: gather and read-back 74 us (486 MB, 6.55 TB/s, 97% of a plain
+// copy); one token appended to 8 heads and read back 4.5 us, five to 512 heads 6.2.
 #include <algorithm>
 
 #include "kvc_device.cuh"

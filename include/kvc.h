@@ -624,11 +624,11 @@ int kvc_compress_layer_q8(int N, int layer, int B, int S, int C, int H_q,
  * Arithmetic: keys and values as held, exact.  Up to 8 query rows per KV head (G*T),
  * a query row is scaled by a power of two to below 2 and taken as fp16 (what is
  * under 2^-24 of its largest value is lost), and the weights of the values are
- * rounded to fp16.  With more rows both are split into two e4m3 parts: a query
- * value within 2^-8 of itself plus 2^-17 of the row's largest one loses nothing
- * that bf16 has but below that, and weights are within 2^-8 of themselves plus
- * 2^-16 of the largest.  Scores, maxima, sums and lse are fp32 throughout; the
- * hyperbolic tangent is within 1e-6 of itself.
+ * rounded to fp16.  With more rows both are split into two e4m3 parts: of a query
+ * value what is under 2^-17 of the row's largest is lost, and weights are within
+ * 2^-8 of themselves plus 2^-15 of the largest.  Scores, maxima, sums and lse are
+ * fp32 throughout; the hyperbolic tangent is within 1e-6 of itself, distances above
+ * 2^24 within 2^-24.  Up to 128 query heads per KV head.
  *   ws     at least kvc_attention_q8_workspace_size(...) bytes, 256-byte
  *          aligned, any content; the size does not depend on the rows
  */
@@ -659,8 +659,8 @@ int kvc_attention_q8(const kvc_bf16* q, const uint8_t* k8, const uint8_t* v8,
  *   cap, slopes         as of kvc_attention_q8
  *   out    [B, H_q, T, D] bf16 out     lse   [B, H_q, T] fp32 out, or NULL
  * A query that sees no key gets zeros and lse -inf.  Keys and values that no query
- * of the call sees may hold anything (the buffer behind the chunk).  Up to 128
- * query heads per KV head.  No atomics: the same call gives the same bits.
+ * of the call sees may hold anything (the buffer behind the chunk); values that some
+ * query sees are finite.  Up to 128 query heads per KV head.  No atomics: the same call gives the same bits.
  * Arithmetic: products of bf16 added up in fp32; the weights of the values are
  * rounded to bf16, 2^-8 of each; scores, maxima, sums and lse are fp32.
  *   ws     at least kvc_attention_chunk_workspace_size(...) bytes, 256-byte
