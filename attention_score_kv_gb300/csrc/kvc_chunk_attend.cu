@@ -37,7 +37,7 @@ cudaError_t launch_attend_chunk(const ChunkAttend& x, cudaStream_t st) {
   a.scale2 = (float)(1.4426950408889634 / std::sqrt((double)x.D));
   a.cap2 = x.cap * flash::kLog2e;
   a.inv_cap2 = x.cap > 0.f ? 1.f / a.cap2 : 0.f;
-  flash::place(a, l, x.ws);
+  flash::place(a, l, x.D, x.ws);
   if (!flash::map_queries(&a.qmap, x.q, x.D, x.T, (uint64_t)x.B * x.H_q, l.nt, G) ||
       !scan::make_map(&a.kmap, x.k, x.D, x.S, (uint64_t)x.B * x.H_kv, flash::kKeys) ||
       !scan::make_map(&a.vmap, x.v, x.D, x.S, (uint64_t)x.B * x.H_kv, flash::kKeys))

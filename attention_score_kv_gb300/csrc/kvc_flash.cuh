@@ -99,13 +99,20 @@ struct Args {
   long long* before;                 // [B1 * tiles + 1] steps before, of one head
   Start* start;                      // [P + 1]
   float2* part_ml;                   // [2 P][rows of a unit]: reference, sum
-  float* part_o;                     // [..][D]
+  float* part_o;                     // [2 P][rows of a unit x D], see part_row
   int* status;
   int B1, H1;                        // units are [B1][H1][tiles]: B, H_kv (chunk) or B * H_kv, 1 (cache)
   int T, H_q, H_kv, G, S, extra;
   int nt, tiles, P;
   int planned;                       // by a kernel of its own; else every CTA does it
   int pair_keys;                     // the streams share rows and take key tiles in turn
+  // Where four dims of a row of partial results lie: row * part_row + d / 4 * part_step.
+  // Row after row when a unit has less than a warp's rows, or when four CTAs and more
+  // share a unit, so that a row has many parts and reading them counts; else four dims
+  // of all rows side by side, as a warp (a row a lane) writes them.  Row after row, and
+  // side by side: one token over 8K 16.4 and 20.2 us, 32 tokens 23.0 and 26.2; a turn
+  // of 512 102.7 and 97.6, causal at D = 64 136.5 and 133.6, documents 106.4 and 104.7.
+  int part_row, part_step;
   uint32_t wait_limit;
   float scale2, cap2, inv_cap2;      // log2(e) / sqrt(D); cap in log2 units, 0: none
 };
@@ -1211,9 +1218,11 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
           p[0] = make_uint4(v[0], v[1], v[2], v[3]);
           p[1] = make_uint4(v[4], v[5], v[6], v[7]);
         } else {
-          float4* p = reinterpret_cast<float4*>(a.part_o + part * D + d);
+          float* p = a.part_o + slot * ((a.pair_keys ? 1 : 2) * kRows * D) +
+                     ((a.pair_keys ? 0 : x) * kRows + row) * a.part_row + d / 4 * a.part_step;
 #pragma unroll
-          for (int z = 0; z < 4; ++z) p[z] = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
+          for (int z = 0; z < 4; ++z)
+            *reinterpret_cast<float4*>(p + z * a.part_step) = make_float4(o[4 * z], o[4 * z + 1], o[4 * z + 2], o[4 * z + 3]);
         }
       }
       if (live && from == 0) {
@@ -1243,7 +1252,7 @@ __device__ __forceinline__ void attend(const Args& a) {
     float max[4 * kRows];
     Here here;
   };
-  static_assert(sizeof(Small) == 3072 && C::kSmem + sizeof(Small) <= 232448, "shared memory of a CTA");
+  static_assert(sizeof(Small) == 3 * 1024 && C::kSmem + sizeof(Small) <= 232448, "shared memory of a CTA");
   __shared__ Small small;
   Bars& bars = small.bars;
   uint32_t& s_tmem = small.tmem;
@@ -1328,14 +1337,13 @@ __global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const __grid_const
   const int parts = 1 + (int)((st.n - st.off + L - 1) / L);
   const int bh = st.b * a.H1 + st.h, b = bh / a.H_kv, h = bh - b * a.H_kv;
   const int64_t q_row = ((int64_t)b * a.H_q + h * a.G + gq) * a.T + t;
-  const auto slot = [&](int p) {
-    return (int64_t)(p == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + p)) * (streams * kRows) + x * kRows + row;
-  };
+  const auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * (c - 1) + 1 : 2 * (c - 1 + p)); };
+  const int unit_rows = streams * kRows, in = x * kRows + row;
   float top = kNoRef, l = 0.f, v[V];
 #pragma unroll
   for (int z = 0; z < V; ++z) v[z] = 0.f;
   for (int p0 = 0; p0 < parts; p0 += 32) {        // 32 parts at a time: a lane has one's reference and sum
-    const float2 ml = p0 + lane < parts ? a.part_ml[slot(p0 + lane)] : make_float2(kNoRef, 0.f);
+    const float2 ml = p0 + lane < parts ? a.part_ml[slot(p0 + lane) * unit_rows + in] : make_float2(kNoRef, 0.f);
     float next = fmaxf(top, ml.x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, o));
@@ -1352,7 +1360,7 @@ __global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const __grid_const
     for (int p = 0; p < n; ++p) {
       const float fp = __shfl_sync(0xffffffffu, f, p);
       float y[V];
-      const float* o = a.part_o + slot(p0 + p) * D + lane * V;
+      const float* o = a.part_o + slot(p0 + p) * (unit_rows * D) + in * a.part_row + lane * V / 4 * a.part_step + lane * V % 4;
       if constexpr (V == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(o);
       else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(o);
 #pragma unroll
@@ -1393,7 +1401,7 @@ inline Layout layout(int64_t B1, int T, int G, int D) {
   l.total = l.off_o + rows * D * sizeof(float);
   return l;
 }
-inline void place(Args& a, const Layout& l, void* ws) {
+inline void place(Args& a, const Layout& l, int D, void* ws) {
   char* w = static_cast<char*>(ws);
   a.plan = reinterpret_cast<Plan*>(w);
   a.units = reinterpret_cast<int2*>(w + l.off_units);
@@ -1404,6 +1412,8 @@ inline void place(Args& a, const Layout& l, void* ws) {
   a.part_ml = reinterpret_cast<float2*>(w + l.off_ml);
   a.part_o = reinterpret_cast<float*>(w + l.off_o);
   a.nt = l.nt, a.tiles = l.tiles, a.pair_keys = l.pair_keys, a.P = l.P;
+  const bool spread = l.nt * a.G < 32 || (int64_t)a.B1 * a.H1 * l.tiles * 4 < l.P;
+  a.part_row = spread ? D : 4, a.part_step = spread ? 4 : 4 * kRows * (l.pair_keys ? 1 : 2);
   a.status = status_word_ptr();
   a.wait_limit = wait_limit_polls();
 }

@@ -41,7 +41,7 @@ cudaError_t launch_attend_q8_tc(const Q8Attend& x, cudaStream_t st) {
   a.scale2 = (float)(1.4426950408889634 / std::sqrt((double)x.D));
   a.cap2 = x.cap * flash::kLog2e;
   a.inv_cap2 = x.cap > 0.f ? 1.f / a.cap2 : 0.f;
-  flash::place(a, l, x.ws);
+  flash::place(a, l, x.D, x.ws);
   const uint64_t blocks = (uint64_t)x.B * (uint64_t)(x.slots->off[H] / q8::kRows);
   if (!flash::map_blocks(&a.kmap, x.c.k8, x.D, blocks) || !flash::map_blocks(&a.vmap, x.c.v8, x.D, blocks))
     return cudaErrorInvalidValue;
