@@ -28,9 +28,9 @@
 // range's end cuts leave partial results, which a third kernel joins in order.
 //
 // Measured (D = 128, 32/8 heads): 2048 tokens over 32K behind a prefix 760 us (1416
-// TFLOP/s; the products alone, without weights, 575), over 8K 190, with a bias 215,
-// with a cap 260; one token over 8K 16.5, of 16 sequences 86.8 (6.2 TB/s); 512 tokens over
-// 4.8K rows of the 8-bit cache 102.  A tile's chain bounds it: weights 1300 to 1570
+// TFLOP/s; the products alone, without weights, 575), over 8K 184, with a bias 209,
+// with a cap 234; one token over 8K 16.5, of 16 sequences 86.8 (6.2 TB/s); 512 tokens over
+// 4.8K rows of the 8-bit cache 97.  A tile's chain bounds it: weights 1300 to 1570
 // cycles, products 920, hand-overs 750 to 1000.
 //
 // e4m3 keys and values (the 8-bit cache): the products take e4m3 operands.  A query
@@ -887,16 +887,39 @@ __device__ __forceinline__ float2 tanh_near2(float2 x) {
   p = fma2(w, p, both(0.9999998807907104f));
   return mul2(x, p);
 }
-// A score's product -> the cap's share of it: tanh.  Warps whose 32 rows have no
-// large one take the polynomial alone.
-__device__ __forceinline__ void cap_all(float (&x)[kHalf], const float2* f, bool blocks, float f1) {
+// A score's product -> the cap's share of it, tanh, up to the factor returned.  Warps
+// whose 32 rows have no large one take a polynomial alone: up to kTanhLow one of three
+// terms (relative error 5e-7, fitted as tanh_near), which without block scales has the
+// score's factor in its coefficients (2048 tokens behind 6K: 234 us; with tanh_near
+// for all 260).  Factors whose powers could leave the range take the general way.
+constexpr float kTanhLow = 0.25f;
+template <bool BLOCKS>
+__device__ __forceinline__ float cap_all(float (&x)[kHalf], const float2* f, float f1, float cap2) {
+  constexpr float c0 = 0.9999995827674866f, c1 = -0.33321908116340637f, c2 = 0.12841613590717316f;
+  const auto both = [](float c) { return make_float2(c, c); };
   float top = 0.f;
 #pragma unroll
   for (int k = 0; k < kHalf; k += 2) {
-    const float fk = blocks ? f[k / 16].x : f1;
-    const float2 v = mul2(make_float2(x[k], x[k + 1]), make_float2(fk, fk));
-    x[k] = v.x, x[k + 1] = v.y;
-    asm("max.f32 %0, %0, %1, %2;\n" : "+f"(top) : "f"(fabsf(v.x)), "f"(fabsf(v.y)));
+    if constexpr (BLOCKS) {
+      const float2 v = mul2(make_float2(x[k], x[k + 1]), both(f[k / 16].x));
+      x[k] = v.x, x[k + 1] = v.y;
+    }
+    asm("max.f32 %0, %0, %1, %2;\n" : "+f"(top) : "f"(fabsf(x[k])), "f"(fabsf(x[k + 1])));
+  }
+  if (!BLOCKS) top *= f1;
+  if (__all_sync(0xffffffffu, top <= kTanhLow) && (BLOCKS || (f1 > 1e-6f && f1 < 1e3f))) {
+    const float ff = BLOCKS ? 1.f : f1 * f1;
+    const float2 d1 = both(c1 * ff), d2 = both(c2 * ff * ff);
+#pragma unroll
+    for (int k = 0; k < kHalf; k += 2) {
+      const float2 v = make_float2(x[k], x[k + 1]), w = mul2(v, v), y = mul2(v, fma2(w, fma2(w, d2, d1), both(c0)));
+      x[k] = y.x, x[k + 1] = y.y;
+    }
+    return BLOCKS ? cap2 : cap2 * f1;
+  }
+  if constexpr (!BLOCKS) {
+#pragma unroll
+    for (int k = 0; k < kHalf; ++k) x[k] *= f1;
   }
   if (__all_sync(0xffffffffu, top <= kTanhNear)) {
 #pragma unroll
@@ -908,6 +931,7 @@ __device__ __forceinline__ void cap_all(float (&x)[kHalf], const float2* f, bool
 #pragma unroll
     for (int k = 0; k < kHalf; ++k) x[k] = tanh_of(x[k]);
   }
+  return cap2;
 }
 // Four weights, fp16 pairs of 2^-8 of them, below 2^-8 * 448 and not negative -> the
 // e4m3 codes of their two parts.  Times 2^-8 the exponents of e4m3 and fp16 are the
@@ -1010,7 +1034,8 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
         }
         tc::tmem_wait_ld();
         tc::reg_fence(s, kHalf);
-        if constexpr (CAP) cap_all(s, f, FP8, c2 * a.inv_cap2);
+        float cap2 = 0.f;
+        if constexpr (CAP) cap2 = cap_all<FP8>(s, f, c2 * a.inv_cap2, a.cap2);
         // ---- mask
         if constexpr (FP8) {
 #pragma unroll
@@ -1054,7 +1079,7 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
         }
         const auto both = [](float v) { return make_float2(v, v); };
         const auto scores = [&](int k, bool crossing) {            // of keys k and k + 1
-          const float2 fk = both(CAP ? a.cap2 : FP8 ? f[k / 16].x : c2);
+          const float2 fk = both(CAP ? cap2 : FP8 ? f[k / 16].x : c2);
           float2 c = both(neg);
           if constexpr (BIAS && FP8) {
             const float2 rel = *reinterpret_cast<const float2*>(&me.rel[half * kHalf + k]);
