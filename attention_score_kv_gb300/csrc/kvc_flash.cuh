@@ -27,8 +27,8 @@
 // every SM's CTA an equal range, whatever the masks and lengths.  Units that a
 // range's end cuts leave partial results, which a third kernel joins in order.
 //
-// Measured (D = 128, 32/8 heads): 2048 tokens over 32K behind a prefix 760 us (1416
-// TFLOP/s; the products alone, without weights, 575), over 8K 184, with a bias 209,
+// Measured (D = 128, 32/8 heads): 2048 tokens over 32K behind a prefix 700 to 760 us (1420 to 1540
+// TFLOP/s; the products alone, without weights, 575), over 8K 184, with a bias 208,
 // with a cap 234; one token over 8K 16.5, of 16 sequences 86.8 (6.2 TB/s); 512 tokens over
 // 4.8K rows of the 8-bit cache 97.  A tile's chain bounds it: weights 1300 to 1570
 // cycles, products 920, hand-overs 750 to 1000.
@@ -887,11 +887,28 @@ __device__ __forceinline__ float2 tanh_near2(float2 x) {
   p = fma2(w, p, both(0.9999998807907104f));
   return mul2(x, p);
 }
+// The same for |x| <= kTanhMid: eight terms, relative error 1.8e-7.
+constexpr float kTanhMid = 1.25f;
+__device__ __forceinline__ float2 tanh_mid2(float2 x) {
+  const auto both = [](float c) { return make_float2(c, c); };
+  const float2 w = mul2(x, x);
+  float2 p = fma2(w, both(-0.000182598116225563f), both(0.0015881144208833575f));
+  p = fma2(w, p, both(-0.0067961555905640125f));
+  p = fma2(w, p, both(0.02055717259645462f));
+  p = fma2(w, p, both(-0.05349034070968628f));
+  p = fma2(w, p, both(0.1332450658082962f));
+  p = fma2(w, p, both(-0.3333269953727722f));
+  p = fma2(w, p, both(0.9999999403953552f));
+  return mul2(x, p);
+}
 // A score's product -> the cap's share of it, tanh, up to the factor returned.  Warps
 // whose 32 rows have no large one take a polynomial alone: up to kTanhLow one of three
 // terms (relative error 5e-7, fitted as tanh_near), which without block scales has the
 // score's factor in its coefficients (2048 tokens behind 6K: 234 us; with tanh_near
-// for all 260).  Factors whose powers could leave the range take the general way.
+// for all 260), then tanh_near and tanh_mid2, and only above those the special
+// functions (largest scores 0.7, 1.4 and 7 times the cap: 280, 330, 377 us; without
+// tanh_mid2 336, 389, 396).  Factors whose powers could leave the range take no
+// coefficients of their own.
 constexpr float kTanhLow = 0.25f;
 template <bool BLOCKS>
 __device__ __forceinline__ float cap_all(float (&x)[kHalf], const float2* f, float f1, float cap2) {
@@ -919,7 +936,10 @@ __device__ __forceinline__ float cap_all(float (&x)[kHalf], const float2* f, flo
   }
   if constexpr (!BLOCKS) {
 #pragma unroll
-    for (int k = 0; k < kHalf; ++k) x[k] *= f1;
+    for (int k = 0; k < kHalf; k += 2) {
+      const float2 v = mul2(make_float2(x[k], x[k + 1]), both(f1));
+      x[k] = v.x, x[k + 1] = v.y;
+    }
   }
   if (__all_sync(0xffffffffu, top <= kTanhNear)) {
 #pragma unroll
@@ -927,9 +947,19 @@ __device__ __forceinline__ float cap_all(float (&x)[kHalf], const float2* f, flo
       const float2 v = tanh_near2(make_float2(x[k], x[k + 1]));
       x[k] = v.x, x[k + 1] = v.y;
     }
+  } else if (__all_sync(0xffffffffu, top <= kTanhMid)) {
+#pragma unroll
+    for (int k = 0; k < kHalf; k += 2) {
+      const float2 v = tanh_mid2(make_float2(x[k], x[k + 1]));
+      x[k] = v.x, x[k + 1] = v.y;
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < kHalf; ++k) x[k] = tanh_of(x[k]);
+    for (int k = 0; k < kHalf; k += 2) {
+      const float2 v = tanh_near2(make_float2(x[k], x[k + 1]));
+      x[k] = fabsf(x[k]) <= kTanhNear ? v.x : tanh_far(x[k]);
+      x[k + 1] = fabsf(x[k + 1]) <= kTanhNear ? v.y : tanh_far(x[k + 1]);
+    }
   }
   return cap2;
 }

@@ -188,10 +188,10 @@ def test_cap_of_every_size(K, cap, scale):
     K.kvc_check_status()
 
 
-@pytest.mark.parametrize("cap,scale", [(50.0, 0.3), (1.0, 0.02), (2.0 ** -6, 0.0005), (1e4, 1.0)])
+@pytest.mark.parametrize("cap,scale", [(50.0, 0.3), (1.0, 0.02), (2.0 ** -6, 0.0005), (1e4, 1.0), (8.0, 1.0), (4.5, 1.0)])
 @pytest.mark.parametrize("S,D", [(130, 128), (1500, 64)])
-def test_cap_of_small_scores(K, S, D, cap, scale):
-    """Scores far below the cap, but for the queries of a few tokens: tiles of both forms of the tangent."""
+def test_cap_above_most_scores(K, S, D, cap, scale):
+    """Scores below the cap, but for the queries of a few tokens: tiles of each form of the tangent."""
     B, T, Hq, H = 2, 130, 4, 2
     q, k, v = rnd(23, B, Hq, T, D, scale=scale), rnd(24, B, H, S, D), rnd(25, B, H, S, D)
     q[:, 1:, 100:103] *= 32
