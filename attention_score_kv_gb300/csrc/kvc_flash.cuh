@@ -13,7 +13,9 @@
 // A warp per stream issues the last tile's P V and the next tile's Q K^T, 1024 cycles
 // of products at D = 128, while eight warps make the other stream's weights, two
 // threads a row.  S is overwritten by P and P by the next S: the products of a
-// warp run in order, and the weights' barrier says that S is in registers.
+// warp run in order, and the two threads of a row, one of which writes P where the
+// other's scores were, meet at a barrier of theirs with S in registers, each time that
+// they take it.
 // Two ways to feed the streams:
 //   row pairs    two row tiles of a head share each tile of keys and values
 //   key pairs    one row tile (few rows: down to a single token); the streams take
@@ -1064,6 +1066,11 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
         }
         tc::tmem_wait_ld();
         tc::reg_fence(s, kHalf);
+        if (again) {                   // the second time nobody has to wait for a maximum
+          tc::fence_before_sync();
+          asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory");
+          tc::fence_after_sync();
+        }
         float cap2 = 0.f;
         if constexpr (CAP) cap2 = cap_all<FP8>(s, f, c2 * a.inv_cap2, a.cap2);
         // ---- mask
@@ -1165,7 +1172,9 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
         // ---- did the reference hold?  (m: the row's maximum less the reference)
         if (!again) {
           *my_max = fmaxf(v[0], v[1]);
+          tc::fence_before_sync();
           asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory");
+          tc::fence_after_sync();
           const float m = max3(v[0], v[1], *its_max);
           // the row's first keys, and the reference, which is another row's, far above them
           const bool first = !seen && m > -INFINITY && !(m >= C::kLow && m <= C::kSlack + C::kShift);

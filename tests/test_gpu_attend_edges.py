@@ -1,0 +1,67 @@
+"""Edges of the attentions on the tensor cores (a prompt chunk's, and the 8-bit cache's with
+many query rows) that go across their warps, streams and segments.  Bounds: attend_util,
+and those written beside a test."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests import test_gpu_chunk as C
+from tests import test_gpu_q8 as Q
+from tests.attend_util import i32, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def K():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from attention_score_kv_gb300 import build
+    build.build()
+    import attention_score_kv_gb300.kvc as kvc
+    return kvc
+
+
+# ------------------------------------------------------- scores that are taken a second time
+@pytest.mark.parametrize("T", [40, 200])                           # key pairs, row pairs
+@pytest.mark.parametrize("cap", [0.0, 300.0])
+def test_moving_references_give_the_same_bits(K, T, cap):
+    """The reference moves in nearly every tile (the last keys come first, and scores grow towards the
+    first), so both threads of a row take their scores again, and one's weights go where the other's
+    scores are: hundreds of calls have to agree bit by bit."""
+    B, Hq, H, S, D = 4, 16, 4, 2048, 128
+    q, v = rnd(1, B, Hq, T, D, scale=3.0), rnd(3, B, H, S, D)
+    k = (rnd(2, B, H, S, D).float() * torch.linspace(12, 0.01, S, device="cuda")[None, None, :, None]).to(torch.bfloat16)
+    qp = i32(np.arange(S - T, S)[None].repeat(B, 0))
+    ws = K.attention_chunk_workspace(B, T, Hq, H, D)
+    want, lse = C.run(K, q, k, v, qp, None, None, S, cap, ws=ws)
+    C.verify(q, k, v, qp, None, None, S, cap, None, want, lse, heads=[0, 7], batches=[0, 3])
+    out, wrong = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        C.run(K, q, k, v, qp, None, None, S, cap, ws=ws, out=out, lse=False)
+        wrong += (out.view(torch.int16) != want.view(torch.int16)).sum()
+    K.kvc_check_status()
+    assert int(wrong) == 0
+
+
+@pytest.mark.parametrize("T", [20, 200])
+@pytest.mark.parametrize("bias", [False, True])
+def test_moving_units_give_the_same_bits(K, T, bias):
+    """The same over the 8-bit cache, where the scales of both keys and values grow as well."""
+    B, Hq, H, D, N = 4, 16, 4, 128, 2048
+    so = [h * N for h in range(H + 1)]
+    g = torch.exp2(torch.linspace(4, -4, N, device="cuda"))[None, None, :, None]
+    k, v = ((rnd(s, B, H, N, D).float() * g).to(torch.bfloat16) for s in (4, 5))
+    c = Q.empty_cache(K, B, D, so)
+    K.kvc_gather_q8(k, v, torch.arange(N, dtype=torch.int32, device="cuda").repeat(B * H), B, H, N, D, [N] * H, so, *c)
+    q, rows, qp = rnd(6, B, Hq, T, D), i32([[N] * H] * B), i32(np.arange(N, N + T)[None].repeat(B, 0))
+    sl = Q.slopes_of(Hq, bias)
+    ws = K.attention_q8_workspace(B, T, Hq, H, D)
+    want, _ = Q.attend(K, q, c, rows, 0, qp, H, so, 0.0, sl, ws=ws)
+    out, wrong = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        Q.attend(K, q, c, rows, 0, qp, H, so, 0.0, sl, ws=ws, out=out, lse=False)
+        wrong += (out.view(torch.int16) != want.view(torch.int16)).sum()
+    K.kvc_check_status()
+    assert torch.isfinite(want).all() and int(wrong) == 0
