@@ -1303,6 +1303,23 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
   return ok;
 }
 
+// Rows of the streams' tiles that are no query, bf16: the copies of the queries never
+// write them, so they are made zeros once.  Their scores take part where a warp decides for
+// its rows together (does a reference move, which form of the tangent), and what an
+// earlier kernel left there would decide with them.
+template <int D>
+__device__ __forceinline__ void clear_rows(const Args& a, uint32_t sQ) {
+  const int rows = a.nt * a.G, pieces = (kRows - rows) * 8;  // of 16 bytes; a row of a panel is 128 bytes
+  for (int x = 0; x < (a.pair_keys ? 1 : 2); ++x)
+    for (int p = 0; p < D / 64; ++p)
+      for (int i = threadIdx.x; i < pieces; i += kThreads)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(sQ + x * Cfg<D, false>::kQBytes +
+                                                                        p * (kRows * 128) + rows * 128 + i * 16),
+                     "r"(0)
+                     : "memory");
+  tc::fence_proxy_async();
+}
+
 template <int D, bool FP8, bool CAP, bool BIAS>
 __device__ __forceinline__ void attend(const Args& a) {
   using C = Cfg<D, FP8>;
@@ -1358,6 +1375,7 @@ __device__ __forceinline__ void attend(const Args& a) {
     tc::tmem_alloc(smem_u32(&s_tmem), kCols);
     tc::tmem_relinquish();
   }
+  if constexpr (!FP8) clear_rows<D>(a, sQ);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -1365,7 +1383,7 @@ __device__ __forceinline__ void attend(const Args& a) {
   grid_dep_wait();
   grid_dep_launch();
   Here& here = small.here;
-  if (!a.planned) plan_here<FP8>(a, here, *reinterpret_cast<Scratch*>(base));
+  if (!a.planned) plan_here<FP8>(a, here, *reinterpret_cast<Scratch*>(base + 2 * C::kQBytes));
   bool ok = true;
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));

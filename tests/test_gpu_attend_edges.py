@@ -65,3 +65,32 @@ def test_moving_units_give_the_same_bits(K, T, bias):
         wrong += (out.view(torch.int16) != want.view(torch.int16)).sum()
     K.kvc_check_status()
     assert torch.isfinite(want).all() and int(wrong) == 0
+
+
+# ------------------------------------------------------- rows of a tile that are no query
+def leave_behind(K, value):
+    """Another call of each form leaves full tiles of large queries in shared memory."""
+    B, T, Hq, H, D = 8, 256, 32, 8, 128
+    q = torch.full((B, Hq, T, D), value, dtype=torch.bfloat16, device="cuda")
+    k = rnd(9, B, H, 512, D)
+    C.run(K, q, k, k, i32(np.arange(256, 512)[None].repeat(B, 0)), None, None, 512)
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (1, 1), (3, 7), (60, 5), (130, 3), (50, 7)])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_was_in_shared_memory_does_not_matter(K, T, G, cap, D):
+    """A tile whose last rows are no query's: what an earlier call left there must not decide when the
+    others' reference moves, or which form of the tangent they take."""
+    B, H, S = 2, 2, 1500
+    Hq = G * H
+    q, k, v = rnd(10, B, Hq, T, D), rnd(11, B, H, S, D), rnd(12, B, H, S, D)
+    qp = i32(np.arange(S - T, S)[None].repeat(B, 0))
+    got = []
+    for value in (0.0, 3.0, -40.0, 3e38):
+        leave_behind(K, value)
+        got.append(C.run(K, q, k, v, qp, None, None, S, cap))
+    C.verify(q, k, v, qp, None, None, S, cap, None, *got[0])
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    K.kvc_check_status()
