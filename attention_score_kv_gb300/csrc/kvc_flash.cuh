@@ -120,10 +120,11 @@ struct Args {
 };
 
 // ------------------------------------------------------------------- planning
+// The keys a query sees: 0 <= lo, -1 <= hi < S, so that differences to a tile's keys fit ints.
 __device__ __forceinline__ bool key_range(const Args& a, int64_t bt, int& lo, int& hi) {
   const int qp = __ldg(a.q_pos + bt);
   lo = a.first ? max(__ldg(a.first + bt), 0) : 0;
-  hi = qp < 0 ? -1 : min(a.last ? __ldg(a.last + bt) : qp, a.S - 1);
+  hi = qp < 0 ? -1 : max(min(a.last ? __ldg(a.last + bt) : qp, a.S - 1), -1);
   return lo <= hi;
 }
 __device__ __forceinline__ int rows_held(const Args& a, int bh, bool* bad) {
@@ -1011,7 +1012,7 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
     int lo = 0, hi = INT_MAX, qp = -1;
     float slope = 0.f, q_rel = 0.f;
     if (live) {
-      qp = __ldg(a.q_pos + (int64_t)b * a.T + t);
+      qp = max(__ldg(a.q_pos + (int64_t)b * a.T + t), -1);
       if constexpr (!FP8) key_range(a, (int64_t)b * a.T + t, lo, hi);
       if constexpr (BIAS) slope = __ldg(a.slopes + h * a.G + gq) * kLog2e;
     }

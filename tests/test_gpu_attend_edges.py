@@ -94,3 +94,43 @@ def test_what_was_in_shared_memory_does_not_matter(K, T, G, cap, D):
     for out, lse in got[1:]:
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
     K.kvc_check_status()
+
+
+# ------------------------------------------------------- masks
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T", [3, 200])
+def test_ranges_at_the_ends_of_their_type(K, T, bias):
+    """`last` of -2^31 sees nothing, of 2^31 - 1 all that `first` leaves, `first` of 2^31 - 1 nothing; among
+    queries of the same tile that see several tiles of keys."""
+    B, Hq, H, S, D = 2, 8, 2, 900, 64
+    lo, hi = -(1 << 31), (1 << 31) - 1
+    q, k, v = rnd(13, B, Hq, T, D), rnd(14, B, H, S, D), rnd(15, B, H, S, D)
+    qp = i32(np.arange(S - T, S)[None].repeat(B, 0))
+    first, last = np.zeros((B, T), np.int64), np.full((B, T), S - 1)
+    last[:, 0::3] = lo
+    last[:, 1::3] = hi
+    first[1, :T // 2] = lo
+    first[1, T - 1] = hi
+    if T > 10:
+        first[0, 10], last[0, 10] = hi, lo
+        qp[0, 7] = lo                                             # an absent token, whatever its position says
+    first, last = i32(first), i32(last)
+    sl = C.slopes_of(Hq, bias)
+    out, lse = C.run(K, q, k, v, qp, first, last, S, 0.0, sl)
+    K.kvc_check_status()
+    C.verify(q, k, v, qp, first, last, S, 0.0, sl, out, lse)
+
+
+def test_queries_before_everything_over_the_cache(K):
+    """Positions of -2^31 mark absent tokens too."""
+    B, Hq, H, D, T = 2, 8, 2, 64, 40
+    n = [300, 200]
+    so = K.kvc_q4_layout(H, 1 << 20, n, 0)
+    c, _, _ = Q.filled(K, B, H, D, so, n, 16)
+    qp = np.arange(800, 800 + T)[None].repeat(B, 0)
+    qp[:, ::3] = -(1 << 31)
+    qp[1, :] = -(1 << 31)
+    qp, rows, q, sl = i32(qp), i32([n] * B), rnd(18, B, Hq, T, D), Q.slopes_of(Hq, True)
+    out, lse = Q.attend(K, q, c, rows, 0, qp, H, so, 0.0, sl)
+    K.kvc_check_status()
+    Q.verify(K, q, c, rows, 0, qp, H, so, 0.0, sl, out, lse)
