@@ -38,7 +38,10 @@
 // e4m3 keys and values (the 8-bit cache): the products take e4m3 operands.  A query
 // row is scaled by a power of two to below 2^8 and split into two e4m3 parts, four
 // significant bits each, so that all of a bf16's eight are there; weights are split
-// the same way: two products of twice bf16's rate each.
+// the same way: two products of twice bf16's rate each.  What is split is a weight times the
+// scale of its block of values, a contribution, in a unit of the row's own, 2^unit, which
+// follows the row's largest contribution as the reference follows its largest score: e4m3
+// reaches 2^-10 down, so a unit that other rows' blocks decided would lose a row's own.
 #pragma once
 
 #include <algorithm>
@@ -65,6 +68,8 @@ constexpr uint32_t kCols = 512, kColS = 0, kColO = 256;    // stream x: S at kCo
 constexpr float kNoRef = -1.7e38f;   // reference of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994530942f;
 constexpr float kLeastUnit = 7.8886090522101181e-31f;      // 2^-100, the smallest scale
+constexpr int kPasses = 3;           // times that a tile's maximum is looked at
+constexpr float kExact = 8192.f;     // below it steps of fp32 are 2^-11 at most
 constexpr int kMaxStages = 11;
 constexpr int kMeta = 8;             // tiles whose positions and scales are in shared memory
 
@@ -100,8 +105,8 @@ struct Args {
   int2 *sees, *seen;                 // [B1][tiles], [B1]: what units and sequences see
   long long* before;                 // [B1 * tiles + 1] steps before, of one head
   Start* start;                      // [P + 1]
-  float2* part_ml;                   // [2 P][rows of a unit]: reference, sum
-  float* part_o;                     // [2 P][rows of a unit x D], see part_row
+  float2* part_ml;                   // [2 P][rows of a unit]: reference, sum of the weights
+  float* part_o;                     // [2 P][rows of a unit x D], see part_row; divided by the sum
   int* status;
   int B1, H1;                        // units are [B1][H1][tiles]: B, H_kv (chunk) or B * H_kv, 1 (cache)
   int T, H_q, H_kv, G, S, extra;
@@ -365,13 +370,13 @@ struct Cfg {
   static constexpr int kQBytes = FP8 ? 2 * kRows * D : kRows * D * 2;       // of a stream: two parts, or bf16
   static constexpr int kStages = FP8 ? 9 : D == 128 ? 5 : 11;
   static constexpr int kMetaBytes = FP8 ? (int)sizeof(Meta) * kMeta : 0;
-  static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMetaBytes;
-  // bf16 reaches as far down as fp32 does, so weights may be small; e4m3's two parts
-  // end at 2^-10, so the largest weight of a row is kept between 2^5 and 2^8 (from 2^6 on,
-  // twice as many tiles move the reference)
-  static constexpr float kShift = FP8 ? 5.f : 0.f, kSlack = FP8 ? 3.f : 8.f;
-  // a row's first maximum that leaves the reference where it is
-  static constexpr float kLow = FP8 ? 5.f : -24.f;
+  static constexpr int kMostBytes = FP8 ? 4 * kRows * (int)sizeof(float) : 0;   // largest contributions
+  static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + kMetaBytes + kMostBytes;
+  // A row's largest weight may be up to 2^kHigh, and the first tile's as small as 2^kLow:
+  // bf16 and fp32 reach as far down as they have to.  e4m3's two parts end at 2^-10, so
+  // the largest contribution of a row is kept between 2^kLeast and 2^kMost units (from 2^6
+  // on, twice as many tiles move it).
+  static constexpr float kLow = -24.f, kHigh = FP8 ? 16.f : 8.f, kLeast = 5.f, kMost = 8.f;
   static constexpr int kQSteps = FP8 ? D / 32 : D / 16, kVSteps = FP8 ? kKeys / 32 : kKeys / 16;
 };
 
@@ -966,6 +971,10 @@ __device__ __forceinline__ float cap_all(float (&x)[kHalf], const float2* f, flo
   }
   return cap2;
 }
+// log2 of a power of two: its exponent in the lowest bits of 2^23.
+__device__ __forceinline__ float log2_of(float s) {
+  return __uint_as_float(__float_as_uint(s) >> 23 | 0x4b000000u) - (8388608.f + 127.f);
+}
 // Four weights, fp16 pairs of 2^-8 of them, below 2^-8 * 448 and not negative -> the
 // e4m3 codes of their two parts.  Times 2^-8 the exponents of e4m3 and fp16 are the
 // same, subnormal numbers' too, so a code is bits 7 to 14: the first part is the weight
@@ -982,22 +991,24 @@ __device__ __forceinline__ void split4(uint32_t h0, uint32_t h1, uint32_t& a, ui
 // A thread has a row's scores of half a tile; the two threads of a row tell each
 // other their maxima (both need one reference: the row has one output).
 template <int D, bool FP8, bool CAP, bool BIAS>
-__device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s_max, uint32_t sQ, const Meta* meta, uint32_t tmem,
-                           float* s_x) {
+__device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s_max, float* s_most, uint32_t sQ,
+                           const Meta* meta, uint32_t tmem, float* s_x) {
   using C = Cfg<D, FP8>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = warp >> 3, half = warp >> 2 & 1;
   const int row = (warp & 3) * 32 + lane;
   const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t s_at = tmem + lanes + kColS + x * 128 + half * kHalf, o_at = tmem + lanes;
   const uint32_t p_at = tmem + lanes + col_p<D>(x) + half * (FP8 ? 16 : 32);
-  float* my_max = s_max + (x * 2 + half) * kRows + row;
-  const float* its_max = s_max + (x * 2 + (half ^ 1)) * kRows + row;
+  const int mine = (x * 2 + half) * kRows + row, its = (x * 2 + (half ^ 1)) * kRows + row;
+  float* my_max = s_max + mine;
+  const float* its_max = s_max + its;
   const int pair = 2 + x * 4 + (warp & 3);                   // the barrier of a row's two warps
   const int gq = row / a.nt, tl = row - gq * a.nt;           // query head of the group, token of the tile
   const int subs = a.pair_keys ? 2 : 1;
   const bool any_row = (warp & 3) * 32 < a.nt * a.G;         // none of the warp's rows is one: nothing reads its part
   uint32_t steps = 0, mt = 0, seg = 0;
   float ref = 0.f;
+  int unit = 0;                        // 8-bit cache: outputs are in 2^unit
   bool ok = true;
   // after a wait that gave up: go on without waiting, so that no barrier is left alone
   const auto wait = [&](const uint64_t* bar, uint32_t phase) { return poll(smem_u32(bar), phase & 1, a.wait_limit); };
@@ -1038,7 +1049,6 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
     }
     // the last segment's reference, another row's, stands in until the row sees keys
     if (!(fabsf(ref) < 1e30f)) ref = 0.f;
-    float unit = kLeastUnit;
     bool seen = false;
     float2 sum2[2] = {};
     const int t1 = g.last(subs);
@@ -1051,8 +1061,10 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
       tc::fence_after_sync();
       // The weights are made against the reference as it is, while the maximum is still
       // being found: it hardly ever moves.  Where it has to, the scores, which are still in
-      // tensor memory, are taken again.
-      for (bool again = false; any_row;) {
+      // tensor memory, are taken again; and looked at again after a step of large numbers,
+      // which are not exact where scores differ by a few.
+      const bool fresh = !seen;        // nothing has been added up for the row
+      for (int pass = 0; any_row; ++pass) {
         float s[kHalf];
 #pragma unroll
         for (int y = 0; y < 2; ++y) tmem_ld32(s_at + 32 * y, s + 32 * y);
@@ -1067,7 +1079,7 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
         }
         tc::tmem_wait_ld();
         tc::reg_fence(s, kHalf);
-        if (again) {                   // the second time nobody has to wait for a maximum
+        if (pass) {                    // and the other's maxima of the last pass have been read
           tc::fence_before_sync();
           asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory");
           tc::fence_after_sync();
@@ -1146,7 +1158,7 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
         // ---- weights, and the maximum beside them: the exponentials' unit is the narrow one
         uint32_t p[kHalf / 2];         // bf16: pairs; e4m3: fours of the first part, then of the second
         float2 part[2] = {};
-        float v[2] = {-INFINITY, -INFINITY};
+        float v[2] = {-INFINITY, -INFINITY}, top = -INFINITY, most = -INFINITY;
 #pragma unroll
         for (int y = 0; y < kHalf / 4; ++y) {
           uint32_t h[2];
@@ -1159,44 +1171,54 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
             float2 u = make_float2(ex2(e.x), ex2(e.y));
             part[z] = add2(part[z], u);
             if constexpr (FP8) {
-              // times the values' scale over the unit and 2^-8: of two powers of two, 0 below the normal numbers
-              const float fv =
-                  __int_as_float(max(__float_as_int(f[k / 16].y) - __float_as_int(unit) + 0x3b800000, 0));
-              u = mul2(u, both(fv));
+              // times the values' scale over 2^unit and 2^-8.  0 below the normal numbers; above them
+              // the weight is 0, or the tile is taken again
+              const int e = (int)(__float_as_uint(f[k / 16].y) >> 23) - unit - 8;
+              u = mul2(u, both(__int_as_float(min(max(e, 0), 254) << 23)));
               asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(h[z]) : "f"(u.y), "f"(u.x));
             } else {
               p[2 * y + z] = bf16x2_of(u.x, u.y);
             }
           }
           if constexpr (FP8) split4(h[0], h[1], p[y], p[kHalf / 4 + y]);
+          if (FP8 && y % 4 == 3) {     // the end of a block
+            const float b = fmaxf(v[0], v[1]);
+            top = fmaxf(top, b);
+            most = fmaxf(most, b + log2_of(f[y / 4].y));
+            v[0] = v[1] = -INFINITY;
+          }
         }
-        // ---- did the reference hold?  (m: the row's maximum less the reference)
-        if (!again) {
-          *my_max = fmaxf(v[0], v[1]);
+        if constexpr (!FP8) top = fmaxf(v[0], v[1]);
+        // ---- did the reference and the unit hold?  (m: the row's largest score less the
+        // reference, c: log2 of its largest contribution, in units)
+        if (pass < kPasses) {
+          *my_max = top;
+          if constexpr (FP8) s_most[mine] = most;
           tc::fence_before_sync();
           asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory");
           tc::fence_after_sync();
-          const float m = max3(v[0], v[1], *its_max);
-          // the row's first keys, and the reference, which is another row's, far above them
-          const bool first = !seen && m > -INFINITY && !(m >= C::kLow && m <= C::kSlack + C::kShift);
-          bool move = first || m > C::kSlack + C::kShift;
+          const float m = fmaxf(top, *its_max);
+          float c = C::kLeast;
+          if constexpr (FP8) c = fmaxf(most, s_most[its]) - (float)unit;
+          // the row's first keys, and the reference and the unit, which are another row's, far from them
+          const bool first =
+              fresh && m > -INFINITY && !(m >= C::kLow && m <= C::kHigh && c >= C::kLeast && c <= C::kMost);
+          const bool move = first || m > C::kHigh || c > C::kMost;
           seen |= m > -INFINITY;
-          float top = kLeastUnit;
-          if constexpr (FP8) {         // of the whole tile: both halves need one unit
-#pragma unroll
-            for (int y = 0; y < kKeys / q8::kRows; ++y) top = fmaxf(top, me.scale[y].y);
-            move |= top > unit;
-          }
           if (__any_sync(0xffffffffu, move)) {
-            const float up = first ? m - C::kShift : fmaxf(0.f, m - C::kShift);
-            float fo = first ? 1.f : ex2(-up);     // nothing has been added up before the first
-            if (m > -INFINITY) ref += up;
+            // whole steps, so that a unit can follow them: weights are 2^(x - ref), contributions
+            // in 2^(ref + unit)
+            const float was = ref;
+            ref += first ? floorf(m) : fmaxf(0.f, floorf(m));
+            const float up = ref - was;
+            if (!__any_sync(0xffffffffu, fabsf(was) > kExact || fabsf(up) > kExact)) pass = kPasses;
+            float fo = fresh ? 1.f : ex2(-up);
 #pragma unroll
             for (int y = 0; y < 2; ++y) sum2[y].x *= fo, sum2[y].y *= fo;
             if constexpr (FP8) {
-              const float u = fmaxf(unit, top);
-              fo *= unit / u;
-              unit = u;
+              const float more = first ? floorf(c) - C::kLeast : fmaxf(0.f, floorf(c) - C::kLeast);
+              unit = max(-126, min((int)((float)unit + (more - up)), 127));
+              if (!fresh) fo = ex2(-more);
             }
             if (i > 0) {               // half of the row's output
 #pragma unroll
@@ -1211,7 +1233,6 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
                 tc::tmem_st16(at, reinterpret_cast<const uint32_t*>(o));
               }
             }
-            again = true;
             continue;
           }
         }
@@ -1236,11 +1257,11 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
     float said = seen ? ref : kNoRef;
     tc::fence_before_sync();
     *my_max = sum;
-    if (a.pair_keys && half == 0) s_x[x * kRows + row] = said, s_x[(2 + x) * kRows + row] = unit;
+    if (a.pair_keys && half == 0) s_x[x * kRows + row] = said, s_x[(2 + x) * kRows + row] = FP8 ? q8::pow2(unit + 127) : 1.f;
     asm volatile("bar.sync 1, 512;\n" ::: "memory");
     tc::fence_after_sync();
     sum = s_max[x * 2 * kRows + row] + s_max[(x * 2 + 1) * kRows + row];
-    float f0 = FP8 ? unit : 1.f, f1 = 0.f;
+    float f0 = FP8 ? q8::pow2(unit + 127) : 1.f, f1 = 0.f;
     int from = half * (D / 2), dims = D / 2, first = x;
     if (a.pair_keys) {
       const float ra = s_x[row], rb = s_x[kRows + row], top = fmaxf(ra, rb);
@@ -1251,7 +1272,8 @@ __device__ bool soft_warps(const Args& a, const Here& here, Bars* bars, float* s
       from = (2 * x + half) * (D / 4), dims = D / 4, first = 0;
     }
     if (any_row) {
-      const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      // a part of a unit is divided by its own sum, and joined by it: no larger than a value
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       f0 *= inv, f1 *= inv;
       const int64_t part = slot * ((a.pair_keys ? 1 : 2) * kRows) + (a.pair_keys ? 0 : x) * kRows + row;
       for (int d = from; d < from + dims; d += 16) {
@@ -1345,6 +1367,7 @@ __device__ __forceinline__ void attend(const Args& a) {
     return;
   }
   Meta* meta = reinterpret_cast<Meta*>(base + 2 * C::kQBytes + C::kStages * C::kStageBytes);
+  float* s_most = reinterpret_cast<float*>(base + C::kSmem - C::kMostBytes);
   float* s_x = reinterpret_cast<float*>(base + C::kQBytes);       // key pairs: stream 1 has no queries of its own
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -1388,7 +1411,7 @@ __device__ __forceinline__ void attend(const Args& a) {
   bool ok = true;
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
-    ok = soft_warps<D, FP8, CAP, BIAS>(a, here, &bars, small.max, sQ, meta, tmem, s_x);
+    ok = soft_warps<D, FP8, CAP, BIAS>(a, here, &bars, small.max, s_most, sQ, meta, tmem, s_x);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) ok = load_warp<D, FP8>(a, here, &bars, sQ, ring);
@@ -1430,9 +1453,9 @@ __global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const __grid_const
     float next = fmaxf(top, ml.x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, o));
-    const float f0 = ex2(top - next), f = ex2(ml.x - next);
+    const float f0 = ex2(top - next), f = ml.y * ex2(ml.x - next);
     top = next;
-    float sum = ml.y * f;
+    float sum = f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l = fmaf(l, f0, sum);

@@ -134,3 +134,120 @@ def test_queries_before_everything_over_the_cache(K):
     out, lse = Q.attend(K, q, c, rows, 0, qp, H, so, 0.0, sl)
     K.kvc_check_status()
     Q.verify(K, q, c, rows, 0, qp, H, so, 0.0, sl, out, lse)
+
+
+# ------------------------------------------------------- blocks of values with other scales
+def against_own_rows(K, q, c, qp, H, so, out, lse, floor, cap=0.0, slopes=None):
+    """Every query against the rows that it sees itself.  A weight times its block's scale (a contribution) is
+    off by `floor` of the query's own largest contribution at most, beside the relative roundings of
+    attend_util: of row j's output that is floor * max(p s) * |code_j|."""
+    B, Hq, T, D = q.shape
+    few = Hq // H * T <= 8
+    kk, vv = Q.read_all(K, c, B, H, D, so)
+    sc = Q.f64(c[2]).reshape(B, -1, 2)[..., 1]
+    pos, qpn = c[3].view(B, -1).cpu().numpy(), qp.cpu().numpy()
+    qn, on, ln = Q.f64(q), Q.f64(out), Q.f64(lse)
+    sl = np.zeros(Hq) if slopes is None else Q.f64(slopes)
+    w, qr = (2.0 ** -11, 2.0 ** -24) if few else (2.0 ** -8, 2.0 ** -17)
+    for b in range(B):
+        for hq in range(Hq):
+            h = hq // (Hq // H)
+            r = slice(so[h], so[h + 1])
+            s = sc[b, so[h] // 16:so[h + 1] // 16].repeat(16)
+            k, v, p = kk[b, r], vv[b, r], pos[b, r].astype(np.int64)
+            see = (p >= 0) & (p <= qpn[b][:, None])
+            far = qpn[b][:, None].astype(np.int64) - p
+            ref, rl, mag, x = Q.O.attention_of(qn[b, hq], k, v, see, cap, sl[hq], far)
+            some = see.any(1)
+            A = float((np.abs(qn[b, hq]) @ np.abs(k).T).max()) / D ** 0.5
+            Aq = float(np.abs(qn[b, hq]).max() * np.abs(k).sum(1).max()) / D ** 0.5
+            dx = A * 2.0 ** -18 + Aq * qr + 2.0 ** -20 + cap * 2.0 ** -20 + abs(sl[hq]) * float(far.max()) * 2.0 ** -22
+            prob = np.where(see, np.exp(x - np.where(some, rl, 0.0)[:, None]), 0.0)
+            most = (prob * s).max(1)[:, None]
+            codes = see.astype(float) @ (np.abs(v) / s[:, None])
+            tol = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * ((w + 2 * dx) * mag + floor * most * codes) + 1e-38
+            err = np.abs(on[b, hq] - ref)
+            assert np.all(err <= tol), (b, hq, float((err / tol).max()))
+            assert np.array_equal(np.isneginf(ln[b, hq]), ~some)
+            le = np.abs(ln[b, hq][some] - rl[some])
+            assert np.all(le <= dx + 2.0 ** -20 * np.abs(rl[some]) + 2.0 ** -20), (b, hq, float(le.max()))
+
+
+# The tensor cores' form keeps the largest contribution at 2^5 at least, and half a step of its second part is
+# 2^-10 (fp16 before it: 2^-17).
+MANY_FLOOR = 2.0 ** -15 * (1 + 2.0 ** -7)
+
+
+@pytest.mark.parametrize("up", [2.0 ** 6, 2.0 ** 9, 2.0 ** 12, 2.0 ** 30])
+@pytest.mark.parametrize("T,G", [(9, 1), (40, 4), (5, 4)])
+@pytest.mark.parametrize("what", ["unseen", "negligible", "weighty"])
+def test_blocks_of_large_values(K, up, T, G, what):
+    """Some blocks' values are 2^6 to 2^30 times the others': in rows that come after some of the call's
+    queries; with scores that leave them next to no weight; and with weight."""
+    B, H, D, N = 2, 2, 64, 1200
+    Hq, so = G * H, [0, N, 2 * N]
+    q, k, v = rnd(20, B, Hq, T, D, scale=1.5), rnd(21, B, H, N, D), rnd(22, B, H, N, D)
+    # of query heads' common direction: what a key has there, a score of 12 / 8 * that
+    q[..., 0] = 12.0
+    k[..., 0] = 0.0
+    big = [(64, 80), (560, 592), (N - 16, N)]
+    qp = np.arange(N, N + T)[None].repeat(B, 0)
+    for a, e in big if what != "unseen" else big[2:]:
+        v[:, :, a:e] = (v[:, :, a:e].float() * up).to(torch.bfloat16)
+        if what == "negligible":
+            k[:, :, a:e, 0] = -30.0                               # 45 below: e^-45
+        elif what == "weighty":
+            k[:, :, a:e, 0] = -2.0
+    if what == "unseen":
+        qp[:, :T // 2] = N - 17 - np.arange(T // 2)               # the first half do not see the last block
+    c = Q.empty_cache(K, B, D, so)
+    K.kvc_gather_q8(k, v, torch.arange(N, dtype=torch.int32, device="cuda").repeat(2 * B), B, H, N, D, [N, N], so, *c)
+    qp = i32(qp)
+    out, lse = Q.attend(K, q, c, i32([[N, N]] * B), 0, qp, H, so)
+    K.kvc_check_status()
+    against_own_rows(K, q, c, qp, H, so, out, lse, MANY_FLOOR)
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (0.0, True)])
+@pytest.mark.parametrize("T", [20, 150])
+def test_scales_of_values_over_forty_binades(K, order, cap, bias, T):
+    """Values that grow and fall by 2^40 over the cache, scores that run against them or with them, a block
+    of zeros among them: a reference and a unit that both move, and seldom together."""
+    B, Hq, H, D, N = 1, 8, 2, 128, 1600
+    so = [0, N, 2 * N]
+    g = torch.exp2(torch.linspace(-20, 20, N, device="cuda"))[None, None, :, None]
+    q, k = rnd(23, B, Hq, T, D), rnd(24, B, H, N, D)
+    v = (rnd(25, B, H, N, D).float() * (g if order == 1 else g.flip(2))).to(torch.bfloat16)
+    v[:, :, 800:816] = 0
+    q[..., 0] = 4.0
+    k[:, 0, :, 0] = torch.linspace(12, -12, N, device="cuda").to(torch.bfloat16)
+    k[:, 1, :, 0] = torch.linspace(-40, 40, N, device="cuda").to(torch.bfloat16)
+    c = Q.empty_cache(K, B, D, so)
+    K.kvc_gather_q8(k, v, torch.arange(N, dtype=torch.int32, device="cuda").repeat(2), B, H, N, D, [N, N], so, *c)
+    qp = np.random.default_rng(3).integers(0, N + 50, (B, T))
+    qp[0, 3] = -1
+    qp, sl = i32(qp), Q.slopes_of(Hq, bias)
+    out, lse = Q.attend(K, q, c, i32([[N, N]]), 0, qp, H, so, cap, sl)
+    K.kvc_check_status()
+    against_own_rows(K, q, c, qp, H, so, out, lse, MANY_FLOOR, cap, sl)
+
+
+def test_later_tokens_do_not_change_a_query(K):
+    """The tokens of a call that come later, with values 2^12 times as large, leave a query's output within
+    the bounds of what it sees itself."""
+    B, Hq, H, D, N, T = 1, 8, 2, 64, 512, 32
+    so = [0, N + T, 2 * (N + T)]
+    k, v = rnd(26, B, H, N, D), rnd(27, B, H, N, D)
+    nk, nv, q = rnd(28, B, H, T, D), rnd(29, B, H, T, D), rnd(30, B, Hq, T, D)
+    qp = i32(np.arange(N, N + T)[None])
+    for up in (1.0, 2.0 ** 12):
+        nv2 = nv.clone()
+        nv2[:, :, 16:] = (nv2[:, :, 16:].float() * up).to(torch.bfloat16)
+        c = Q.empty_cache(K, B, D, so)
+        idx = torch.arange(N + T, dtype=torch.int32, device="cuda").repeat(2)
+        K.kvc_gather_q8(k, v, idx, B, H, N, D, [N, N], so, *c)
+        K.kvc_append_q8(nk, nv2, qp, B, H, T, D, so, i32([[N, N]]), *c)
+        out, lse = Q.attend(K, q, c, i32([[N, N]]), T, qp, H, so)
+        K.kvc_check_status()
+        against_own_rows(K, q, c, qp, H, so, out, lse, MANY_FLOOR)
