@@ -620,6 +620,7 @@ int kvc_compress_layer_q8(int N, int layer, int B, int S, int C, int H_q,
  * out = sum_r p_r v_r / sum_r p_r, p_r = exp(x); lse = log sum_r p_r.
  *   cap     0 (none), or from 2^-20 to 2^20
  *   slopes  [H_q] fp32, device, finite; or NULL
+ * Scores, with their bias, below 2^27 in magnitude, and values below 2^96.
  * No atomics: the same call gives the same bits.
  * Arithmetic: keys and values as held, exact.  Up to 8 query rows per KV head (G*T),
  * a query row is scaled by a power of two to below 2 and taken as fp16 (what is
@@ -657,7 +658,7 @@ int kvc_attention_q8(const kvc_bf16* q, const uint8_t* k8, const uint8_t* v8,
  *   out = sum_j p_j v_j / sum_j p_j, p_j = exp(x); lse = log sum_j p_j
  *   q      [B, H_q, T, D] bf16         k, v  [B, H_kv, S, D] bf16
  *   q_pos, first, last  [B, T] int32, device
- *   cap, slopes         as of kvc_attention_q8
+ *   cap, slopes, and the magnitudes of scores and values   as of kvc_attention_q8
  *   out    [B, H_q, T, D] bf16 out     lse   [B, H_q, T] fp32 out, or NULL
  * A query that sees no key gets zeros and lse -inf.  Keys and values that no query
  * of the call sees may hold anything (the buffer behind the chunk); values that some

@@ -251,3 +251,63 @@ def test_later_tokens_do_not_change_a_query(K):
         out, lse = Q.attend(K, q, c, i32([[N, N]]), T, qp, H, so)
         K.kvc_check_status()
         against_own_rows(K, q, c, qp, H, so, out, lse, MANY_FLOOR)
+
+
+# ------------------------------------------------------- scores of other magnitudes before
+@pytest.mark.parametrize("small", [7.0, 100.0, 400.0, -400.0])
+@pytest.mark.parametrize("T", [5, 200])
+def test_small_scores_behind_far_larger_ones(K, small, T):
+    """Sequences with scores around 2^34 in turn with sequences of ordinary ones: a segment's first reference is
+    the last one's, whose steps are larger than the scores."""
+    B, Hq, H, S, D = 300, 4, 1, 120 if T == 5 else 250, 64
+    q, k, v = rnd(31, B, Hq, T, D), rnd(32, B, H, S, D), rnd(33, B, H, S, D)
+    q[..., 0] = 2.0 ** 10
+    k[..., 0] = small * 8 / 2.0 ** 10
+    k[::2, ..., 0] = 2.0 ** 27
+    qp = i32(np.arange(S - T, S)[None].repeat(B, 0))
+    out, lse = C.run(K, q, k, v, qp, None, None, S)
+    K.kvc_check_status()
+    C.verify(q, k, v, qp, None, None, S, 0.0, None, out, lse, heads=[0, 3], batches=range(1, B, 26))
+
+
+@pytest.mark.parametrize("small", [7.0, 100.0, -400.0])
+@pytest.mark.parametrize("T", [5, 100])
+@pytest.mark.parametrize("level", [2.0 ** 20, 2.0 ** 27])
+def test_small_scores_behind_far_larger_ones_over_the_cache(K, small, T, level):
+    B, Hq, H, D, N = 300, 4, 1, 64, 112
+    so = [0, N]
+    q, k, v = rnd(34, B, Hq, T, D), rnd(35, B, H, N, D), rnd(36, B, H, N, D)
+    q[..., 0] = 64.0
+    k[..., 0] = small * 8 / 64.0
+    k[::2, ..., 0] = level * 8 / 64.0
+    c = Q.empty_cache(K, B, D, so)
+    K.kvc_gather_q8(k, v, torch.arange(N, dtype=torch.int32, device="cuda").repeat(B), B, H, N, D, [N], so, *c)
+    qp = i32(np.arange(N, N + T)[None].repeat(B, 0))
+    out, lse = Q.attend(K, q, c, i32([[N]] * B), 0, qp, H, so)
+    K.kvc_check_status()
+    assert torch.isfinite(out).all()
+    for b in range(1, B, 26):
+        sub = tuple(t.view(B, -1, *t.shape[1:])[b].contiguous() for t in c)
+        against_own_rows(K, q[b:b + 1], sub, qp[b:b + 1], H, so, out[b:b + 1], lse[b:b + 1], MANY_FLOOR)
+
+
+@pytest.mark.parametrize("T", [9, 60])
+@pytest.mark.parametrize("level", [2.0 ** 12, 2.0 ** 20, 2.0 ** 27])
+def test_large_scores_close_to_one_another(K, T, level):
+    """Scores as far up as single steps of fp32 are 2^-11, 2^-3 and 2^4: as good as those steps allow."""
+    B, Hq, H, D, N = 2, 4, 2, 128, 700
+    so = K.kvc_q4_layout(H, N, [N, N], 0)
+    q, k, v = rnd(37, B, Hq, T, D, scale=0.1), rnd(38, B, H, N, D), rnd(39, B, H, N, D)
+    q[..., 0] = 16.0
+    k[..., 0] = level * 128 ** 0.5 / 16
+    # keys of one row in three differ by steps of bf16 in that direction, which decide
+    k[:, :, ::3, 0] *= 1 - 2.0 ** -7
+    c = Q.empty_cache(K, B, D, so)
+    idx = torch.arange(so[1], dtype=torch.int32, device="cuda").clamp(max=N - 1).repeat(2 * B)
+    K.kvc_gather_q8(k, v, idx, B, H, N, D, [N, N], so, *c)
+    qp = i32(np.arange(N, N + T)[None].repeat(B, 0))
+    out, lse = Q.attend(K, q, c, i32([[N, N]] * B), 0, qp, H, so)
+    Q.verify(K, q, c, i32([[N, N]] * B), 0, qp, H, so, 0.0, None, out, lse)
+    out, lse = C.run(K, q, k, v, qp, None, None, N)
+    C.verify(q, k, v, qp, None, None, N, 0.0, None, out, lse)
+    K.kvc_check_status()
