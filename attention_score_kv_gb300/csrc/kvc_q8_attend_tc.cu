@@ -43,7 +43,11 @@ cudaError_t launch_attend_q8_tc(const Q8Attend& x, cudaStream_t st) {
   a.inv_cap2 = x.cap > 0.f ? 1.f / a.cap2 : 0.f;
   flash::place(a, l, x.D, x.ws);
   const uint64_t blocks = (uint64_t)x.B * (uint64_t)(x.slots->off[H] / q8::kRows);
-  if (!flash::map_blocks(&a.kmap, x.c.k8, x.D, blocks) || !flash::map_blocks(&a.vmap, x.c.v8, x.D, blocks))
+  // Slots without any row: there is no block to map, and a unit's one tile, of which no row is
+  // looked at, comes from the queries (more than eight rows of 2 D bytes: a block).
+  const void *k8 = blocks ? x.c.k8 : (const void*)x.q, *v8 = blocks ? x.c.v8 : (const void*)x.q;
+  if (!flash::map_blocks(&a.kmap, k8, x.D, std::max<uint64_t>(blocks, 1)) ||
+      !flash::map_blocks(&a.vmap, v8, x.D, std::max<uint64_t>(blocks, 1)))
     return cudaErrorInvalidValue;
   return x.D == 128 ? launch_of<128>(a, st) : launch_of<64>(a, st);
 }

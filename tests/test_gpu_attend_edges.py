@@ -311,3 +311,22 @@ def test_large_scores_close_to_one_another(K, T, level):
     out, lse = C.run(K, q, k, v, qp, None, None, N)
     C.verify(q, k, v, qp, None, None, N, 0.0, None, out, lse)
     K.kvc_check_status()
+
+
+# ------------------------------------------------------- caches without room
+@pytest.mark.parametrize("T", [1, 40])
+def test_slots_without_any_row(K, T):
+    """A slot table of which no head has a row (budgets of 0 before the first token): zeros, and -inf; counts
+    above that are recorded."""
+    B, Hq, H, D = 2, 8, 2, 64
+    so = [0, 0, 0]
+    c = Q.empty_cache(K, 1, D, [0, 16])
+    q, qp = rnd(40, B, Hq, T, D), i32(np.arange(T)[None].repeat(B, 0))
+    out, lse = Q.attend(K, q, c, i32([[0, 0]] * B), 0, qp, H, so)
+    K.kvc_check_status()
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    out, lse = Q.attend(K, q, c, i32([[0, 3]] * B), 0, qp, H, so)
+    with pytest.raises(K.KvcError) as e:
+        K.kvc_check_status()
+    assert e.value.code == K.KVC_ERR_DEVICE
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
