@@ -252,14 +252,17 @@ template <int D>
 __device__ __forceinline__ int dim_of(int at) { return (at >> 1 & 7) * (D / 8) + (at >> 4) * 2 + (at & 1); }
 
 // What a warp has of a head: output fragments (columns 2j and 2j + 1 of dims
-// dim_of), per column the reference and the sum, and with the values' scales
-// of kScaled formats, what one of its units is worth.
+// dim_of), per column the reference and the sum; with kScaled formats the fragments
+// are in units of 2^unit, which follow a column's largest contribution (weight times
+// the scale of the block's values) as the reference follows its largest score, so
+// that fp16 holds it whatever scales there are in rows of no weight to the column.
 template <class F>
 struct Acc {
   static constexpr int D = F::kD;
-  float o[D / 16][4], ref[2], sum[2], unit;
+  float o[D / 16][4], ref[2], sum[2];
+  int unit[2];
   __device__ __forceinline__ void clear() {
-    unit = kLeastUnit;
+    unit[0] = unit[1] = 0;
 #pragma unroll
     for (int m = 0; m < D / 16; ++m)
 #pragma unroll
@@ -383,27 +386,33 @@ __device__ __forceinline__ void attend_segment(const Args<F>& a, const Segment<F
     }
     // ---- weights
     bool above = false;
+    float lv = 0.f;
+    if constexpr (F::kScaled) lv = log2_of(sc.v);
 #pragma unroll
-    for (int y = 0; y < 2; ++y) above |= fmaxf(acc[y], acc[2 + y]) * u[y] > ref[y] + (kSlack + kShift);
-    if constexpr (F::kScaled) above |= sc.v > acc_out.unit;
+    for (int y = 0; y < 2; ++y) {
+      const float m = fmaxf(acc[y], acc[2 + y]) * u[y];
+      above |= m > ref[y] + (kSlack + kShift);
+      if constexpr (F::kScaled) above |= m - ref[y] + lv > (float)acc_out.unit[y] + (kSlack + kShift);
+    }
     if (__any_sync(0xffffffffu, above)) {
-      float g2 = 1.f;
-      if constexpr (F::kScaled) {
-        const float unit = fmaxf(acc_out.unit, sc.v);
-        g2 = acc_out.unit / unit;  // powers of two
-        acc_out.unit = unit;
-      }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         float m = fmaxf(acc[y], acc[2 + y]) * u[y];
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        const float next = fmaxf(ref[y], m - kShift);
+        // whole steps with kScaled: what the reference rises, the unit falls, and then rises to
+        // where the block's largest contribution is 2^kShift of it
+        const float next = fmaxf(ref[y], (F::kScaled ? floorf(m) : m) - kShift);
         float f = ex2(ref[y] - next);
-        ref[y] = next;
         sum[y] *= f;
-        if constexpr (F::kScaled) f *= g2;
+        if constexpr (F::kScaled) {
+          const float was = (float)acc_out.unit[y] - (next - ref[y]);
+          const float now = fmaxf(was, floorf((m - next) + lv) - kShift);
+          acc_out.unit[y] = max(-126, min((int)now, 127));
+          f = ex2(was - now);
+        }
+        ref[y] = next;
 #pragma unroll
         for (int m2 = 0; m2 < KS; ++m2) o[m2][y] *= f, o[m2][2 + y] *= f;
       }
@@ -414,11 +423,14 @@ __device__ __forceinline__ void attend_segment(const Args<F>& a, const Segment<F
       p[y] = ex2(fmaf(acc[y], u[y & 1], -ref[y & 1]));
       sum[y & 1] += p[y];
     }
-    if constexpr (F::kScaled) {    // the block's values in units of the largest scale so far
-      // quotient of two powers of two, 0 below the normal numbers
-      const float f = __int_as_float(max(__float_as_int(sc.v) - __float_as_int(acc_out.unit) + 0x3f800000, 0));
+    if constexpr (F::kScaled) {    // contributions in the columns' units
 #pragma unroll
-      for (int y = 0; y < 4; ++y) p[y] *= f;
+      for (int y = 0; y < 2; ++y) {
+        // quotient of two powers of two, 0 below the normal numbers; above them the weight is 0
+        const int e = (int)(__float_as_uint(sc.v) >> 23) - acc_out.unit[y];
+        const float f = __int_as_float(min(max(e, 0), 254) << 23);
+        p[y] *= f, p[2 + y] *= f;
+      }
     }
     const uint32_t pf0 = transpose8(pack_half2(p[0], p[1])), pf1 = transpose8(pack_half2(p[2], p[3]));
     // ---- output
@@ -452,7 +464,7 @@ __device__ __forceinline__ void join_warps(const Acc<F>& x, int R, float2 (*s_ml
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][col].x);
     float f = ex2(x.ref[y] - top);
-    if constexpr (F::kScaled) f *= x.unit;
+    if constexpr (F::kScaled) f *= __int_as_float((x.unit[y] + 127) << 23);
     float* to = mine + col * o_stride(D) + 2 * r;
 #pragma unroll
     for (int m = 0; m < KS; ++m)

@@ -971,10 +971,6 @@ __device__ __forceinline__ float cap_all(float (&x)[kHalf], const float2* f, flo
   }
   return cap2;
 }
-// log2 of a power of two: its exponent in the lowest bits of 2^23.
-__device__ __forceinline__ float log2_of(float s) {
-  return __uint_as_float(__float_as_uint(s) >> 23 | 0x4b000000u) - (8388608.f + 127.f);
-}
 // Four weights, fp16 pairs of 2^-8 of them, below 2^-8 * 448 and not negative -> the
 // e4m3 codes of their two parts.  Times 2^-8 the exponents of e4m3 and fp16 are the
 // same, subnormal numbers' too, so a code is bits 7 to 14: the first part is the weight

@@ -624,13 +624,13 @@ int kvc_compress_layer_q8(int N, int layer, int B, int S, int C, int H_q,
  * No atomics: the same call gives the same bits.
  * Arithmetic: keys and values as held, exact.  Up to 8 query rows per KV head (G*T),
  * a query row is scaled by a power of two to below 2 and taken as fp16 (what is
- * under 2^-24 of its largest value is lost), and the weights of the values are
- * rounded to fp16.  With more rows both are split into two e4m3 parts: of a query
- * value what is under 2^-17 of the row's largest is lost, and a weight times the
- * scale of its block of values is within 2^-8 of itself plus 2^-15 of the largest such
- * product among the rows that the query sees.  Scores, maxima, sums and lse are
- * fp32 throughout; the hyperbolic tangent is within 1e-6 of itself, distances above
- * 2^24 within 2^-24.  Up to 128 query heads per KV head.
+ * under 2^-24 of its largest value is lost), and a weight times the scale of its block
+ * of values is rounded to fp16: 2^-11 of itself plus 2^-29 of the largest such product
+ * among the rows that the query sees.  With more rows both are split into two e4m3
+ * parts: of a query value what is under 2^-17 of the row's largest is lost, and a weight
+ * times its scale is within 2^-8 of itself plus 2^-15 of the largest.  Scores, maxima,
+ * sums and lse are fp32 throughout; the hyperbolic tangent is within 1e-6 of itself,
+ * distances above 2^24 within 2^-24.  Up to 128 query heads per KV head.
  *   ws     at least kvc_attention_q8_workspace_size(...) bytes, 256-byte
  *          aligned, any content; the size does not depend on the rows
  */

@@ -184,7 +184,11 @@ MANY_FLOOR = 2.0 ** -15 * (1 + 2.0 ** -7)
 def test_blocks_of_large_values(K, up, T, G, what):
     """Some blocks' values are 2^6 to 2^30 times the others': in rows that come after some of the call's
     queries; with scores that leave them next to no weight; and with weight."""
-    B, H, D, N = 2, 2, 64, 1200
+    blocks_of_large_values(K, up, T, G, what, 2, MANY_FLOOR)
+
+
+def blocks_of_large_values(K, up, T, G, what, B, floor):
+    H, D, N = 2, 64, 1200
     Hq, so = G * H, [0, N, 2 * N]
     q, k, v = rnd(20, B, Hq, T, D, scale=1.5), rnd(21, B, H, N, D), rnd(22, B, H, N, D)
     # of query heads' common direction: what a key has there, a score of 12 / 8 * that
@@ -205,7 +209,7 @@ def test_blocks_of_large_values(K, up, T, G, what):
     qp = i32(qp)
     out, lse = Q.attend(K, q, c, i32([[N, N]] * B), 0, qp, H, so)
     K.kvc_check_status()
-    against_own_rows(K, q, c, qp, H, so, out, lse, MANY_FLOOR)
+    against_own_rows(K, q, c, qp, H, so, out, lse, floor)
 
 
 @pytest.mark.parametrize("order", [1, -1])
@@ -330,3 +334,18 @@ def test_slots_without_any_row(K, T):
         K.kvc_check_status()
     assert e.value.code == K.KVC_ERR_DEVICE
     assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+# The form for up to 8 query rows: the largest contribution 2^4 units at least, half of fp16's last step.
+FEW_FLOOR = 2.0 ** -29
+
+
+@pytest.mark.parametrize("up", [2.0 ** 9, 2.0 ** 16, 2.0 ** 22, 2.0 ** 40])
+@pytest.mark.parametrize("T,G", [(2, 4), (1, 8), (8, 1)])
+@pytest.mark.parametrize("what", ["unseen", "negligible", "weighty"])
+@pytest.mark.parametrize("B", [2, 24])                             # clusters of CTAs, ranges
+def test_blocks_of_large_values_few_rows(K, up, T, G, what, B):
+    """The same with up to 8 query rows."""
+    if what == "unseen" and T == 1:
+        pytest.skip("one token")
+    blocks_of_large_values(K, up, T, G, what, B, FEW_FLOOR)
