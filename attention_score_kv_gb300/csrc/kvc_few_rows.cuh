@@ -319,7 +319,9 @@ __device__ __forceinline__ void attend_segment(const Args<F>& a, const Segment<F
   mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   // scale by the power of two that brings the row's largest value into [1, 2)
   const uint32_t e = mx >> 7, ee = (e == 0 || e == 255) ? 127u : min(e, 253u);
-  const float down = __uint_as_float((254u - ee) << 23);
+  float down = __uint_as_float((254u - ee) << 23);
+  if constexpr (F::kMods)            // a row that is not finite becomes NaN, capped or not, as with many rows
+    if (e == 255) down = __uint_as_float(0x7fffffffu);
   const float c = __uint_as_float(ee << 23) * a.scale;
   uint32_t qf[KS][2];
 #pragma unroll

@@ -861,7 +861,8 @@ __device__ __forceinline__ float write_query(const __nv_bfloat16* q, bool live, 
   mx = max(mx & 0xffffu, mx >> 16);
   // the row's largest value into [2^7, 2^8)
   const uint32_t e = mx >> 7, ee = e == 255 ? 134u : min(max(e, 8u), 254u);
-  const float down = __uint_as_float((261u - ee) << 23);
+  // a row that is not finite becomes NaN: the conversions would make an infinity a number
+  const float down = __uint_as_float(e == 255 ? 0x7fffffffu : (261u - ee) << 23);
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     uint32_t p[2][4];

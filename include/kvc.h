@@ -620,7 +620,8 @@ int kvc_compress_layer_q8(int N, int layer, int B, int S, int C, int H_q,
  * out = sum_r p_r v_r / sum_r p_r, p_r = exp(x); lse = log sum_r p_r.
  *   cap     0 (none), or from 2^-20 to 2^20
  *   slopes  [H_q] fp32, device, finite; or NULL
- * Scores, with their bias, below 2^27 in magnitude, and values below 2^96.
+ * Scores, with their bias, below 2^27 in magnitude, and values below 2^96.  A query
+ * row that is not finite gives NaN where it sees a row, and leaves the others as they are.
  * No atomics: the same call gives the same bits.
  * Arithmetic: keys and values as held, exact.  Up to 8 query rows per KV head (G*T),
  * a query row is scaled by a power of two to below 2 and taken as fp16 (what is

@@ -349,3 +349,30 @@ def test_blocks_of_large_values_few_rows(K, up, T, G, what, B):
     if what == "unseen" and T == 1:
         pytest.skip("one token")
     blocks_of_large_values(K, up, T, G, what, B, FEW_FLOOR)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 60])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_non_finite_queries_over_the_cache(K, T, cap, value):
+    """A query row that is not finite gives NaN whatever the form, where it sees a row, and leaves the others'."""
+    B, Hq, H, D = 2, 8, 2, 64
+    n = [300, 200]
+    so = K.kvc_q4_layout(H, 1 << 20, n, 0)
+    c, _, _ = Q.filled(K, B, H, D, so, n, 50)
+    q, rows = rnd(52, B, Hq, T, D), i32([n, [300, 0]])
+    qp = np.full((B, T), 5000)
+    qp[0, 0] = 0 if T > 1 else 5000                               # sees the first row alone
+    qp = i32(qp)
+    bad = q.clone()
+    bad[:, 2::4, T - 1, 5] = value
+    out, lse = Q.attend(K, bad, c, rows, 0, qp, H, so, cap)
+    K.kvc_check_status()
+    assert torch.isnan(out[:, 2, T - 1]).all() and torch.isnan(out[0, 6, T - 1]).all()
+    assert torch.isnan(lse[:, 2, T - 1]).all()
+    assert torch.all(out[1, 6, T - 1] == 0) and torch.isneginf(lse[1, 6, T - 1])      # no rows
+    good = torch.ones((B, Hq, T), dtype=torch.bool, device="cuda")
+    good[:, 2::4, T - 1] = False
+    want, want_lse = Q.attend(K, q, c, rows, 0, qp, H, so, cap)
+    out[~good], lse[~good] = want[~good], want_lse[~good]
+    Q.verify(K, q, c, rows, 0, qp, H, so, cap, None, out, lse)
