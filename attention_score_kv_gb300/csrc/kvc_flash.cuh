@@ -29,11 +29,12 @@
 // every SM's CTA an equal range, whatever the masks and lengths.  Units that a
 // range's end cuts leave partial results, which a third kernel joins in order.
 //
-// Measured (D = 128, 32/8 heads): 2048 tokens over 32K behind a prefix 700 to 760 us (1420 to 1540
-// TFLOP/s; the products alone, without weights, 575), over 8K 184, with a bias 208,
-// with a cap 234; one token over 8K 16.5, of 16 sequences 86.8 (6.2 TB/s); 512 tokens over
-// 4.8K rows of the 8-bit cache 97.  A tile's chain bounds it: weights 1300 to 1570
-// cycles, products 920, hand-overs 750 to 1000.
+// Measured (D = 128, 32/8 heads): 2048 tokens over 32K behind a prefix 743 to 783 us by the
+// clocks under load (1375 to 1450 TFLOP/s; the products alone, without weights, 575),
+// over 8K 186, with a bias 213, with a cap 238 to 387 by how large the scores are against
+// it; one token over 8K 16.5, of 16 sequences 85.9 (6.3 TB/s); 512 tokens over 4.8K rows
+// of the 8-bit cache 96.5.  A tile's chain bounds it: weights 1300 to 1570 cycles,
+// products 920, hand-overs 750 to 1000.
 //
 // e4m3 keys and values (the 8-bit cache): the products take e4m3 operands.  A query
 // row is scaled by a power of two to below 2^8 and split into two e4m3 parts, four
@@ -896,7 +897,7 @@ __device__ __forceinline__ float2 tanh_near2(float2 x) {
   p = fma2(w, p, both(0.9999998807907104f));
   return mul2(x, p);
 }
-// The same for |x| <= kTanhMid: eight terms, relative error 1.8e-7.
+// The same for |x| <= kTanhMid: eight terms, relative error 1.9e-7 with fp32's roundings.
 constexpr float kTanhMid = 1.25f;
 __device__ __forceinline__ float2 tanh_mid2(float2 x) {
   const auto both = [](float c) { return make_float2(c, c); };
@@ -913,11 +914,12 @@ __device__ __forceinline__ float2 tanh_mid2(float2 x) {
 // A score's product -> the cap's share of it, tanh, up to the factor returned.  Warps
 // whose 32 rows have no large one take a polynomial alone: up to kTanhLow one of three
 // terms (relative error 5e-7, fitted as tanh_near), which without block scales has the
-// score's factor in its coefficients (2048 tokens behind 6K: 234 us; with tanh_near
-// for all 260), then tanh_near and tanh_mid2, and only above those the special
-// functions (largest scores 0.7, 1.4 and 7 times the cap: 280, 330, 377 us; without
-// tanh_mid2 336, 389, 396).  Factors whose powers could leave the range take no
-// coefficients of their own.
+// score's factor in its coefficients, then tanh_near and tanh_mid2, and only above those
+// the special functions.  So a cap's cost goes by the scores: 2048 tokens behind 6K take
+// 238 us where warps' largest scores are at 0.2 of the cap (260 with tanh_near for all,
+// 186 without a cap), and 285, 332 and 387 at 0.7, 1.4 and 7 times the cap (336, 389, 396
+// without tanh_mid2, before later steps).  Factors whose powers could leave the range
+// take no coefficients of their own.
 constexpr float kTanhLow = 0.25f;
 template <bool BLOCKS>
 __device__ __forceinline__ float cap_all(float (&x)[kHalf], const float2* f, float f1, float cap2) {

@@ -17,7 +17,7 @@
 // Numerics: codes times scales are exact in fp16; q is scaled by a power of
 // two per row into fp16's range (values below 2^-24 of the row's largest round
 // off there); sums, maxima and outputs are fp32; p is rounded to fp16
-// (2^-12 relative; the reference point leaves it below 2^12, so that steps below
+// (2^-11 relative; the reference point leaves it below 2^12, so that steps below
 // fp16's normal numbers are 2^-28 of the largest weight or less).
 #include <algorithm>
 #include <cmath>

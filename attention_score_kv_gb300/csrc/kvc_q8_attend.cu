@@ -13,8 +13,8 @@
 // Codes are exact in fp16.  A block's scale of the keys multiplies its scores,
 // that of the values the block's weights, in units that follow the query's own
 // largest product of the two, so that fp16 holds it.
-// Measured: one token of 64 sequences over 8 heads of 4.3K rows (582 MB) 95.7 us, 6.1
-// TB/s (97.5 with capped scores); one token over 8 heads of 4096 rows 7.5 us.  Copies
+// Measured: one token of 64 sequences over 8 heads of 4.3K rows (582 MB) 96.5 us, 6.0
+// TB/s (97 with capped scores); one token over 8 heads of 4096 rows 7.5 us.  Copies
 // of 16 bytes a lane in the order of the fragments (two lines of 64 bytes a row) left
 // it at 4.75 TB/s; one CTA an SM, with the joins' room beside the rings, took 35
 // instead of 29 us over uneven heads.

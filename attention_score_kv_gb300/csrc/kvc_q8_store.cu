@@ -23,7 +23,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
 // A lane's share of a row: 16 values from dim 16 * (lane % (D / 16)).  Step i
-// takes rows i * rows_at_once(D) + lane / (D / 16).
+// takes rows i * kAtOnce + lane / kLanes.
 template <int D>
 struct Lay {
   static constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes, kSteps = q8::kRows / kAtOnce;

@@ -537,7 +537,7 @@ int kvc_compress_layer_q4(int N, int layer, int B, int S, int C, int H_q,
  * Arithmetic: the products take fp16 operands and add up in fp32.  Keys and
  * values are exact in fp16; a query row is scaled by a power of two to below 2
  * (what is under 2^-24 of its largest value is lost); the weights p_r of the
- * values are rounded to fp16, 2^-12 of each, while maxima, sums and lse are fp32
+ * values are rounded to fp16, 2^-11 of each, while maxima, sums and lse are fp32
  * throughout.  Against 64 bits that leaves out at its bf16 rounding (relative
  * error 1.68e-3, 1.67e-3 with weights of 32 bits).
  * Speed: one token of a few sequences takes the faster of two forms while no
@@ -631,7 +631,8 @@ int kvc_compress_layer_q8(int N, int layer, int B, int S, int C, int H_q,
  * parts: of a query value what is under 2^-17 of the row's largest is lost, and a weight
  * times its scale is within 2^-8 of itself plus 2^-15 of the largest.  Scores, maxima,
  * sums and lse are fp32 throughout; the hyperbolic tangent is within 1e-6 of itself,
- * distances above 2^24 within 2^-24.  Up to 128 query heads per KV head.
+ * distances above 2^24 within 2^-24.  Up to 128 query heads and 2^20 query rows per
+ * KV head.
  *   ws     at least kvc_attention_q8_workspace_size(...) bytes, 256-byte
  *          aligned, any content; the size does not depend on the rows
  */
@@ -651,8 +652,8 @@ int kvc_attention_q8(const kvc_bf16* q, const uint8_t* k8, const uint8_t* v8,
  * kvc_qk_norm_rope or kvc_append_chunk and the layer's end.  Query head g reads
  * KV head g / G.  Query t of sequence b sees the keys j of its sequence with
  *   max(first[b, t], 0) <= j <= min(last[b, t], S - 1)
- * (none where that is empty or q_pos[b, t] < 0: a padded batch); first NULL: 0, last
- * NULL: q_pos[b, t], the causal mask.  A document mask gives each query its
+ * (none where that is empty or q_pos[b, t] < 0: a padded batch; any ints); first NULL: 0,
+ * last NULL: q_pos[b, t], the causal mask.  A document mask gives each query its
  * document's first position; a prefix mask gives last = max(q_pos, prefix - 1).
  *   x = q.k_j / sqrt(D);   cap > 0:  x <- cap * tanh(x / cap);
  *   slopes:  x <- x - slopes[hq] * |q_pos[b, t] - j|
@@ -663,7 +664,8 @@ int kvc_attention_q8(const kvc_bf16* q, const uint8_t* k8, const uint8_t* v8,
  *   out    [B, H_q, T, D] bf16 out     lse   [B, H_q, T] fp32 out, or NULL
  * A query that sees no key gets zeros and lse -inf.  Keys and values that no query
  * of the call sees may hold anything (the buffer behind the chunk); values that some
- * query sees are finite.  Up to 128 query heads per KV head.  No atomics: the same call gives the same bits.
+ * query sees are finite.  Up to 128 query heads and 2^20 query rows (G*T) per KV head.
+ * No atomics: the same call gives the same bits.
  * Arithmetic: products of bf16 added up in fp32; the weights of the values are
  * rounded to bf16, 2^-8 of each; scores, maxima, sums and lse are fp32.
  *   ws     at least kvc_attention_chunk_workspace_size(...) bytes, 256-byte
